@@ -14,6 +14,11 @@
  *   gptq_pack                 codes -> LSB-first bitstream of b-bit unsigned codes
  *   gptq_dequant_matmul       Y = X Wq^T read straight from the packed codes, scales,
  *                             zeros and g_idx (the consumer of the stored form)
+ *   gptq_fp4_*                the microscaled 4-bit form (e2m1 codes, one scale per 32 or 16
+ *                             columns): quantise, dequantise, and the product of two such
+ *                             matrices, dense or with one weight per expert
+ *   gptq_expert_*             tokens sorted by expert, their rows gathered and brought back
+ *                             with the router's weights, and the gradients of both
  *   gptq_set_status_mode,     device-side errors reported by each call (synchronising)
  *   gptq_status_sync          or deferred to one check (calls only enqueue work)
  *
@@ -251,6 +256,124 @@ enum { GPTQ_DQ_RELU = 1, GPTQ_DQ_BF16_OUT = 2 };
 int gptq_dequant_matmul(const void* X, int64_t T, int64_t K, int64_t ldx, const uint32_t* packed,
                         const float* scales, const uint8_t* zeros, const int32_t* g_idx, int64_t N,
                         int64_t G, int bits, int flags, void* Y, int64_t ldy, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The microscaled 4-bit form (no counterpart on the pages). e2m1 codes (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and negatives; the code's low three bits in that order, the fourth the sign) with
+ * one scale per block of columns:
+ *   GPTQ_MXFP4   blocks of 32; scale byte c = 2^(c - 127), c = 255 NaN (OCP microscaling)
+ *   GPTQ_NVFP4   blocks of 16; scale byte = e4m3, times one fp32 scale g > 0 per matrix
+ * A stored matrix (rows, cols) is two 16-byte-aligned device buffers and, for NVFP4, g:
+ *   codes   rows * gptq_fp4_code_pitch(cols) bytes (pitch 16 * ceil(cols / 32)): column 2i
+ *           of a row in the low half of byte i; codes past cols are zero
+ *   scales  gptq_fp4_scale_bytes(rows, cols, format) bytes: tiles of 128 rows x 4 blocks,
+ *           512 bytes each, the tiles of one row block adjacent; scale b of row r is byte
+ *           (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile (r / 128, b / 4). Blocks past
+ *           cols hold 0 in every row of the matrix; rows past the last are not read into
+ *           any result.
+ * ------------------------------------------------------------------------------------ */
+typedef enum gptq_fp4_format { GPTQ_MXFP4 = 0, GPTQ_NVFP4 = 1 } gptq_fp4_format;
+int64_t gptq_fp4_code_pitch(int64_t cols);
+int64_t gptq_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
+
+/* *g (device) = the least power of two for which no NVFP4 block scale of X saturates:
+ * max|x| <= 448 * 6 * g; 1 where X is all zeros. A power of two keeps block scale * g exact.
+ * X (rows, cols) bf16 or fp32, row stride ldx. Synchronises `stream` to report a NaN or
+ * infinity in X as NONFINITE (not in the deferred status mode). Errors: INVALID_ARG,
+ * NONFINITE, CUDA. */
+int gptq_fp4_tensor_scale(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                          float* g, void* stream);
+
+/* X (src_rows, cols) bf16 or fp32, row stride ldx -> codes, scales of `rows` rows. index
+ * (device, int32, rows; may be NULL): row r is X row index[r] / per, a row of zeros where
+ * index[r] < 0 (gptq_expert_sort's src with per = its top gathers and quantises the experts'
+ * rows in one pass); NULL: rows == src_rows, in order. Per block, with a = max|x|:
+ *   MXFP4  c = max(floor(log2 a) - 2 + 127, 0), s = 2^(c - 127) (c = 0 where a = 0)
+ *   NVFP4  c = e4m3(min(a / (6 g), 448)) to nearest even, s = c * g (g: device, 1 fp32)
+ * and code = the e2m1 number nearest to x / s (the fp32 quotient), ties to even, saturating
+ * at 6; zeros where s = 0. Synchronises `stream` to report a NaN or infinity in X as
+ * NONFINITE (its block's scale is then NaN) or an index past X's rows as INVALID_ARG (read as
+ * negative); not in the deferred status mode. Allocates nothing.
+ * Errors: INVALID_ARG, NONFINITE, CUDA. */
+int gptq_fp4_quantize(const void* X, int dtype, int64_t src_rows, int64_t cols, int64_t ldx,
+                      const int32_t* index, int64_t per, int64_t rows, int format,
+                      const float* g, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The inverse: Y (rows, cols) bf16 (rounded to nearest even) or fp32 = code * scale, row
+ * stride ldy. Asynchronous. Errors: INVALID_ARG, CUDA. */
+int gptq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* g,
+                        int64_t rows, int64_t cols, int format, void* Y, int dtype,
+                        int64_t ldy, void* stream);
+
+/* Row-major scale bytes (rows, ceil(cols / block), row stride lds), as checkpoints store
+ * them -> the tiled order above, zeros outside the matrix. Asynchronous.
+ * Errors: INVALID_ARG, CUDA. */
+int gptq_fp4_tile_scales(const uint8_t* src, int64_t rows, int64_t cols, int64_t lds,
+                         int format, uint8_t* scales, void* stream);
+
+/* Y[t][o] = act(sum_k X[t][k] W_e[o][k]) for X (T, K) and W_e (N, K), both stored in the
+ * form above with the same format.
+ *   offsets  NULL: one weight for all rows (experts = 1). Otherwise device, int32,
+ *            experts + 1, non-decreasing: rows offsets[e] .. offsets[e + 1] - 1 use weight e
+ *            (gptq_expert_sort's offsets); rows in none of the ranges get Y = 0. Values out
+ *            of order or of range are clamped and reported as INVALID_ARG.
+ *   w_codes, w_scales  the experts' stored matrices one after another
+ *   x_g, w_g device fp32, NVFP4 only: x_g one number, w_g one, or `experts` numbers with
+ *            GPTQ_FP4_EXPERT_G
+ *   flags    GPTQ_DQ_RELU, GPTQ_DQ_BF16_OUT (else fp32), GPTQ_FP4_EXPERT_G
+ *   Y        device, (T, N) row-major, row stride ldy elements
+ * Sums are fp32; the result is rounded once. Allocates nothing. Synchronises `stream` and
+ * returns the device status (in the deferred status mode neither).
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 65536 experts), TIMEOUT, CUDA. */
+enum { GPTQ_FP4_EXPERT_G = 4 };
+int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_g, int64_t T,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const float* w_g, int64_t N,
+                    int64_t K, int format, const int32_t* offsets, int64_t experts, int flags,
+                    void* Y, int64_t ldy, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Tokens sorted by expert and back (no counterpart on the pages). Token t has `top` slots;
+ * slot i = t * top + j goes to expert ids[i], or nowhere (negative: dropped). One Hessian per
+ * expert is gptq_hessian_accumulate on its contiguous rows of the gathered matrix.
+ *
+ * gptq_expert_sort: ids (device, int32, tokens * top) ->
+ *   offsets  experts + 1 int32: expert e's places are offsets[e] .. offsets[e + 1] - 1
+ *   pos      tokens * top int32: each slot's place, -1 where dropped; slots of one expert
+ *            keep their order
+ *   src      tokens * top int32: the slot in each place, -1 past the last live place
+ * ws: device, gptq_expert_sort_workspace_bytes(tokens, top, experts) bytes (may be 0).
+ * Synchronises `stream` to report an id >= experts as INVALID_ARG (it counts as dropped);
+ * not in the deferred status mode. Errors: INVALID_ARG, UNSUPPORTED (experts > 1024),
+ * WORKSPACE, CUDA. */
+size_t gptq_expert_sort_workspace_bytes(int64_t tokens, int64_t top, int64_t experts);
+int gptq_expert_sort(const int32_t* ids, int64_t tokens, int64_t top, int64_t experts,
+                     int32_t* offsets, int32_t* src, int32_t* pos, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* Xs[pos[t][j]] = X[t] (bf16 or fp32, d columns); rows of Xs (tokens * top) past
+ * offsets[experts] are zero. All three below: pos and offsets as gptq_expert_sort leaves
+ * them; a place past tokens * top is reported as INVALID_ARG (synchronising, not in the
+ * deferred status mode) and counts as dropped. Errors: INVALID_ARG, UNSUPPORTED (more than
+ * 2^31 thread blocks), CUDA. */
+int gptq_expert_gather(const void* X, int dtype, int64_t tokens, int64_t d, int64_t ldx,
+                       const int32_t* pos, int64_t top, const int32_t* offsets,
+                       int64_t experts, void* Xs, int64_t lds, void* stream);
+
+/* Y[t] = sum_j weights[t][j] Ys[pos[t][j]] over the slots that are not dropped, j in order, in
+ * fp32, rounded once. weights: device fp32 (tokens, top), or NULL for 1: then this is the
+ * gradient of gptq_expert_gather (Ys its output's gradient, Y its input's). */
+int gptq_expert_combine(const void* Ys, int dtype, int64_t tokens, int64_t d, int64_t ldys,
+                        const int32_t* pos, int64_t top, const float* weights, void* Y,
+                        int64_t ldy, void* stream);
+
+/* The gradients of gptq_expert_combine, from dY (tokens, d): dYs[pos[t][j]] = weights[t][j]
+ * dY[t] (rows past offsets[experts] zero) and dW[t][j] = <dY[t], Ys[pos[t][j]]> (fp32; 0
+ * where dropped). */
+int gptq_expert_combine_grad(const void* dY, int64_t lddy, const void* Ys, int64_t ldys,
+                             int dtype, int64_t tokens, int64_t d, const int32_t* pos,
+                             int64_t top, const int32_t* offsets, int64_t experts,
+                             const float* weights, void* dYs, int64_t lddys, float* dW,
+                             void* stream);
 
 /* Static text for a status code. */
 const char* gptq_status_string(int status);

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional, Tuple
+from typing import Dict, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -32,6 +32,9 @@ EXPORTS = [
     "gptq_hessian_destroy", "gptq_prepare_workspace_bytes", "gptq_prepare", "gptq_prepare_noalloc",
     "gptq_quantize_workspace_bytes",
     "gptq_quantize", "gptq_prune_workspace_bytes", "gptq_prune", "rtn_quantize", "gptq_packed_words_per_row", "gptq_pack", "gptq_dequant_matmul",
+    "gptq_fp4_code_pitch", "gptq_fp4_scale_bytes", "gptq_fp4_tensor_scale", "gptq_fp4_quantize", "gptq_fp4_dequantize",
+    "gptq_fp4_tile_scales", "gptq_fp4_matmul", "gptq_expert_sort_workspace_bytes", "gptq_expert_sort",
+    "gptq_expert_gather", "gptq_expert_combine", "gptq_expert_combine_grad",
     "gptq_status_string", "gptq_set_status_mode", "gptq_status_mode", "gptq_status_sync",
     "gptq_launch_count", "gptq_profile_enable", "gptq_profile_read", "gptq_profile_kernel_count",
     "gptq_profile_kernel_name",
@@ -76,6 +79,18 @@ def _declare(lib: ctypes.CDLL) -> None:
         "gptq_packed_words_per_row": (_I64, [_I64, _I]),
         "gptq_pack": (_I, [_P, _I64, _I64, _I, _I, _P, _P]),
         "gptq_dequant_matmul": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I64, _I64, _I, _I, _P, _I64, _P]),
+        "gptq_fp4_code_pitch": (_I64, [_I64]),
+        "gptq_fp4_scale_bytes": (_I64, [_I64, _I64, _I]),
+        "gptq_fp4_tensor_scale": (_I, [_P, _I, _I64, _I64, _I64, _P, _P]),
+        "gptq_fp4_quantize": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _I64, _I, _P, _P, _P, _P]),
+        "gptq_fp4_dequantize": (_I, [_P, _P, _P, _I64, _I64, _I, _P, _I, _I64, _P]),
+        "gptq_fp4_tile_scales": (_I, [_P, _I64, _I64, _I64, _I, _P, _P]),
+        "gptq_fp4_matmul": (_I, [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I, _P, _I64, _I, _P, _I64, _P]),
+        "gptq_expert_sort_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+        "gptq_expert_sort": (_I, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+        "gptq_expert_gather": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+        "gptq_expert_combine": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P]),
+        "gptq_expert_combine_grad": (_I, [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P]),
         "gptq_status_string": (ctypes.c_char_p, [_I]),
         "gptq_set_status_mode": (_I, [_I]),
         "gptq_status_mode": (_I, []),
@@ -416,6 +431,279 @@ def gptq_layerwise(X: torch.Tensor, Ws, bits: int = 4, group: int = 0, sym: bool
     return layers, h
 
 
+# -------------------------------------------------- the microscaled 4-bit form (e2m1 codes)
+
+MXFP4, NVFP4 = 0, 1
+_FP4 = {"mx": MXFP4, "nv": NVFP4}
+FP4_EXPERT_G = 4
+
+
+class Fp4(NamedTuple):
+    """A matrix (rows, cols), or one per expert, in the microscaled 4-bit form: codes uint8
+    ([experts,] rows, gptq_fp4_code_pitch(cols)), scales uint8 ([experts,] row tiles, column
+    tiles, 512), the format ("mx" or "nv") and, for "nv", the fp32 tensor scale (one, or one
+    per expert). Layouts: include/gptq.h."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+    format: str
+    tensor_scale: Optional[torch.Tensor] = None
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+
+def _fp4_format(format: str) -> int:
+    if format not in _FP4:
+        raise ValueError(f"format must be 'mx' or 'nv', got {format!r}")
+    return _FP4[format]
+
+
+def gptq_fp4_code_pitch(cols: int) -> int:
+    return (cols + 31) // 32 * 16
+
+
+def _fp4_scale_shape(rows: int, cols: int, format: str) -> Tuple[int, int, int]:
+    return ((rows + 127) // 128, -(-cols // (128 if format == "mx" else 64)), 512)
+
+
+def gptq_fp4_scale_bytes(rows: int, cols: int, format: str) -> int:
+    return int(load().gptq_fp4_scale_bytes(rows, cols, _fp4_format(format)))
+
+
+def _rows_of(t: torch.Tensor, name: str) -> int:
+    """The dtype code of a matrix whose rows are contiguous (any row stride)."""
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a 2-D CUDA bf16 or fp32 tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} rows must not overlap")
+    return GPTQ_BF16 if t.dtype == torch.bfloat16 else GPTQ_F32
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _check_fp4(q: Fp4, name: str, dims: int) -> int:
+    f = _fp4_format(q.format)
+    lead = tuple(q.codes.shape[:-2])
+    if q.codes.dim() != dims:
+        raise ValueError(f"{name}.codes must have {dims} dimensions")
+    _dev(q.codes, torch.uint8, name + ".codes", (*lead, q.rows, gptq_fp4_code_pitch(q.cols)))
+    _dev(q.scales, torch.uint8, name + ".scales", (*lead, *_fp4_scale_shape(q.rows, q.cols, q.format)))
+    if f == NVFP4:
+        if q.tensor_scale is None:
+            raise ValueError(f"{name}: format 'nv' needs a tensor scale")
+        _dev(q.tensor_scale, torch.float32, name + ".tensor_scale")
+        if q.tensor_scale.numel() not in (1, lead[0] if lead else 1):
+            raise ValueError(f"{name}.tensor_scale must hold one number, or one per expert")
+    return f
+
+
+def gptq_fp4_tensor_scale(X: torch.Tensor, stream=None) -> torch.Tensor:
+    """The "nv" tensor scale of X: the least power of two for which no block scale saturates."""
+    dt = _rows_of(X, "X")
+    g = torch.empty(1, dtype=torch.float32, device=X.device)
+    _check("gptq_fp4_tensor_scale", load().gptq_fp4_tensor_scale(_ptr(X), dt, X.shape[0], X.shape[1], _ld(X), _ptr(g),
+                                                                 _stream(stream)))
+    return g
+
+
+def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optional[torch.Tensor] = None,
+                      index: Optional[torch.Tensor] = None, per: int = 1, out: Optional[Fp4] = None,
+                      stream=None) -> Fp4:
+    """X (bf16 or fp32, any row stride) in the microscaled 4-bit form. index (int32): row r is X row
+    index[r] // per, zeros where index[r] < 0 (a Route's src with per = top gathers the experts' rows
+    in the same pass). "nv" without a tensor scale takes gptq_fp4_tensor_scale(X)."""
+    f, dt = _fp4_format(format), _rows_of(X, "X")
+    n, cols = X.shape
+    rows = n
+    if index is not None:
+        _dev(index, torch.int32, "index")
+        rows = index.numel()
+    if f == NVFP4:
+        if tensor_scale is None:
+            tensor_scale = gptq_fp4_tensor_scale(X, stream)
+        _dev(tensor_scale, torch.float32, "tensor_scale", (1,))
+    else:
+        tensor_scale = None
+    if out is None:
+        out = Fp4(torch.empty(rows, gptq_fp4_code_pitch(cols), dtype=torch.uint8, device=X.device),
+                  torch.empty(_fp4_scale_shape(rows, cols, format), dtype=torch.uint8, device=X.device), cols, format,
+                  tensor_scale)
+    else:
+        if out.cols != cols or out.format != format or out.codes.shape[-2] != rows:
+            raise ValueError("out has another shape or format")
+        out = out._replace(tensor_scale=tensor_scale)
+        _check_fp4(out, "out", 2)
+    _check("gptq_fp4_quantize", load().gptq_fp4_quantize(
+        _ptr(X), dt, n, cols, _ld(X), _ptr(index), per, rows, f, _ptr(tensor_scale), _ptr(out.codes), _ptr(out.scales),
+        _stream(stream)))
+    return out
+
+
+def gptq_fp4_dequantize(q: Fp4, dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values that q's codes and scales stand for."""
+    f = _check_fp4(q, "q", 2)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dtype must be float32 or bfloat16")
+    Y = out if out is not None else torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
+    dt = _rows_of(Y, "out")
+    if Y.dtype != dtype or tuple(Y.shape) != (q.rows, q.cols):
+        raise ValueError(f"out must be {dtype} of shape {(q.rows, q.cols)}")
+    _check("gptq_fp4_dequantize", load().gptq_fp4_dequantize(
+        _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale), q.rows, q.cols, f, _ptr(Y), dt, _ld(Y), _stream(stream)))
+    return Y
+
+
+def gptq_fp4_tile_scales(scales: torch.Tensor, cols: int, format: str, stream=None) -> torch.Tensor:
+    """Row-major scale bytes (rows, blocks) of a checkpoint, in the tiled order of Fp4.scales."""
+    f = _fp4_format(format)
+    rows = scales.shape[0]
+    _dev(scales, torch.uint8, "scales", (rows, -(-cols // (32 if f == MXFP4 else 16))))
+    out = torch.empty(_fp4_scale_shape(rows, cols, format), dtype=torch.uint8, device=scales.device)
+    _check("gptq_fp4_tile_scales", load().gptq_fp4_tile_scales(_ptr(scales), rows, cols, scales.shape[1], f, _ptr(out),
+                                                               _stream(stream)))
+    return out
+
+
+def gptq_fp4_matmul(X: Fp4, W: Fp4, offsets: Optional[torch.Tensor] = None, relu: bool = False,
+                    out_dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W^T (optionally max(., 0)) of two matrices in the microscaled 4-bit form. With offsets
+    (int32, experts + 1, a Route's) W holds one weight per expert and rows offsets[e]..offsets[e+1]
+    of X use weight e; rows in no expert's range give zeros."""
+    f = _check_fp4(X, "X", 2)
+    _check_fp4(W, "W", 2 if offsets is None else 3)
+    if X.format != W.format or X.cols != W.cols:
+        raise ValueError("X and W must have the same format and columns")
+    experts = 1 if offsets is None else W.codes.shape[0]
+    if offsets is not None:
+        _dev(offsets, torch.int32, "offsets", (experts + 1,))
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    T, N = X.rows, W.rows
+    Y = out if out is not None else torch.empty(T, N, dtype=out_dtype, device=X.codes.device)
+    _rows_of(Y, "out")
+    if Y.dtype != out_dtype or tuple(Y.shape) != (T, N):
+        raise ValueError(f"out must be {out_dtype} of shape {(T, N)}")
+    if X.tensor_scale is not None and X.tensor_scale.numel() != 1:
+        raise ValueError("X.tensor_scale must hold one number")
+    flags = (DQ_RELU if relu else 0) | (DQ_BF16_OUT if out_dtype == torch.bfloat16 else 0)
+    if f == NVFP4 and experts > 1 and W.tensor_scale.numel() == experts:
+        flags |= FP4_EXPERT_G
+    _check("gptq_fp4_matmul", load().gptq_fp4_matmul(
+        _ptr(X.codes), _ptr(X.scales), _ptr(X.tensor_scale), T, _ptr(W.codes), _ptr(W.scales), _ptr(W.tensor_scale), N,
+        X.cols, f, _ptr(offsets), experts, flags, _ptr(Y), _ld(Y), _stream(stream)))
+    return Y
+
+
+# ------------------------------------------------------- tokens sorted by expert, and back
+
+class Route(NamedTuple):
+    """Where each token's slots go (gptq_expert_sort): offsets int32 (experts + 1), src int32
+    (tokens * top), pos int32 (tokens, top)."""
+    offsets: torch.Tensor
+    src: torch.Tensor
+    pos: torch.Tensor
+
+    @property
+    def experts(self) -> int:
+        return self.offsets.numel() - 1
+
+
+def gptq_expert_sort_workspace_bytes(tokens: int, top: int, experts: int) -> int:
+    return int(load().gptq_expert_sort_workspace_bytes(tokens, top, experts))
+
+
+def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor] = None, stream=None) -> Route:
+    """ids (tokens, top) int32, each slot's expert (negative: dropped) -> the slots' places, stably
+    sorted by expert."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be (tokens, top)")
+    _dev(ids, torch.int32, "ids")
+    tokens, top = ids.shape
+    route = Route(torch.empty(experts + 1, dtype=torch.int32, device=ids.device),
+                  torch.empty(tokens * top, dtype=torch.int32, device=ids.device), torch.empty_like(ids))
+    if ws is None:
+        nb = gptq_expert_sort_workspace_bytes(tokens, top, experts)
+        ws = torch.empty(nb, dtype=torch.uint8, device=ids.device) if nb else None
+    _check("gptq_expert_sort", load().gptq_expert_sort(
+        _ptr(ids), tokens, top, experts, _ptr(route.offsets), _ptr(route.src), _ptr(route.pos), _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
+    return route
+
+
+def _check_route(route: Route) -> Tuple[int, int]:
+    tokens, top = route.pos.shape
+    _dev(route.pos, torch.int32, "route.pos")
+    _dev(route.src, torch.int32, "route.src", (tokens * top,))
+    _dev(route.offsets, torch.int32, "route.offsets")
+    return tokens, top
+
+
+def _like(t: torch.Tensor, name: str, dtype, shape) -> int:
+    dt = _rows_of(t, name)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return dt
+
+
+def gptq_expert_gather(X: torch.Tensor, route: Route, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The tokens' rows in the order of their experts (tokens * top rows, zeros past the live ones)."""
+    tokens, top = _check_route(route)
+    d = X.shape[1]
+    dt = _like(X, "X", X.dtype, (tokens, d))
+    Xs = out if out is not None else torch.empty(tokens * top, d, dtype=X.dtype, device=X.device)
+    _like(Xs, "out", X.dtype, (tokens * top, d))
+    _check("gptq_expert_gather", load().gptq_expert_gather(
+        _ptr(X), dt, tokens, d, _ld(X), _ptr(route.pos), top, _ptr(route.offsets), route.experts, _ptr(Xs), _ld(Xs),
+        _stream(stream)))
+    return Xs
+
+
+def gptq_expert_combine(Ys: torch.Tensor, route: Route, weights: Optional[torch.Tensor],
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t][j] * the row of slot (t, j), in fp32, rounded once; weights None: 1."""
+    tokens, top = _check_route(route)
+    d = Ys.shape[1]
+    dt = _like(Ys, "Ys", Ys.dtype, (tokens * top, d))
+    if weights is not None:
+        _dev(weights, torch.float32, "weights", (tokens, top))
+    Y = out if out is not None else torch.empty(tokens, d, dtype=Ys.dtype, device=Ys.device)
+    _like(Y, "out", Ys.dtype, (tokens, d))
+    _check("gptq_expert_combine", load().gptq_expert_combine(
+        _ptr(Ys), dt, tokens, d, _ld(Ys), _ptr(route.pos), top, _ptr(weights), _ptr(Y), _ld(Y), _stream(stream)))
+    return Y
+
+
+def gptq_expert_gather_grad(dXs: torch.Tensor, route: Route, out: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """The gradient of gptq_expert_gather's input: each token's rows of dXs summed."""
+    return gptq_expert_combine(dXs, route, None, out, stream)
+
+
+def gptq_expert_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, route: Route, weights: torch.Tensor,
+                             out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gradients of gptq_expert_combine: (dYs, dweights)."""
+    tokens, top = _check_route(route)
+    d = Ys.shape[1]
+    dt = _like(Ys, "Ys", Ys.dtype, (tokens * top, d))
+    _like(dY, "dY", Ys.dtype, (tokens, d))
+    _dev(weights, torch.float32, "weights", (tokens, top))
+    dYs, dW = out if out is not None else (torch.empty(tokens * top, d, dtype=Ys.dtype, device=Ys.device),
+                                           torch.empty_like(weights))
+    _like(dYs, "out[0]", Ys.dtype, (tokens * top, d))
+    _dev(dW, torch.float32, "out[1]", (tokens, top))
+    _check("gptq_expert_combine_grad", load().gptq_expert_combine_grad(
+        _ptr(dY), _ld(dY), _ptr(Ys), _ld(Ys), dt, tokens, d, _ptr(route.pos), top, _ptr(route.offsets), route.experts,
+        _ptr(weights), _ptr(dYs), _ld(dYs), _ptr(dW), _stream(stream)))
+    return dYs, dW
+
+
 def gptq_status_string(status: int) -> str:
     return _str(status)
 
@@ -445,6 +733,10 @@ __all__ = [
     "gptq_hessian_finalize", "gptq_prepare", "gptq_prepare_workspace_bytes", "gptq_quantize",
     "gptq_quantize_workspace_bytes", "rtn_quantize", "gptq_pack", "gptq_packed_words_per_row",
     "gptq_dequant_matmul", "gptq_layerwise", "gptq_status_string", "gptq_launch_count", "gptq_profile_enable", "gptq_profile_read",
+    "Fp4", "MXFP4", "NVFP4", "gptq_fp4_code_pitch", "gptq_fp4_scale_bytes", "gptq_fp4_tensor_scale", "gptq_fp4_quantize",
+    "gptq_fp4_dequantize", "gptq_fp4_tile_scales", "gptq_fp4_matmul", "Route", "gptq_expert_sort",
+    "gptq_expert_sort_workspace_bytes", "gptq_expert_gather", "gptq_expert_gather_grad", "gptq_expert_combine",
+    "gptq_expert_combine_grad",
     "set_status_mode", "status_sync", "deferred_status", "STATUS_SYNC", "STATUS_DEFERRED",
     "EXPORTS", "LIB_PATH",
 ]

@@ -31,7 +31,8 @@ namespace gptq {
 enum KernelId {
     K_HESS_TC, K_HESS_SIMT, K_FINALIZE, K_PREP_DIAG, K_PREP_PERM, K_PREP_GATHER, K_POTRF, K_SGEMM_PREP,
     K_EYE, K_SCATTER, K_INIT_WORK, K_ROW_PARAMS, K_BLOCK, K_SGEMM_TRAIL, K_G_IDX, K_PACK, K_RTN,
-    K_SPLIT, K_TC_PREP, K_TC_TRAIL, K_DEQUANT_MM, K_STATUS, K_TC_CHAIN, K_COUNT
+    K_SPLIT, K_TC_PREP, K_TC_TRAIL, K_DEQUANT_MM, K_STATUS, K_TC_CHAIN, K_FP4_AMAX, K_FP4_QUANT, K_FP4_DEQUANT,
+    K_FP4_TILE, K_FP4_MM, K_EXPERT_SORT, K_EXPERT_GATHER, K_EXPERT_COMBINE, K_EXPERT_GRAD, K_COUNT
 };
 void prof_begin(int id, cudaStream_t s);
 void prof_end(int id, cudaStream_t s);
@@ -87,6 +88,17 @@ struct ContextPtrCache {
 // (nothing is allocated), cleared on `s`. Calls in flight at the same time get different
 // words unless a few hundred calls are issued while one is still running.
 cudaError_t call_status_word(cudaStream_t s, int** out);
+
+// The status word of a call whose kernels only ever record into it with set_status. In deferred
+// mode that is the device's sticky status itself (set_status keeps the first error, as the
+// fold at the end of a call would), so the call needs no clearing and no folding launch;
+// otherwise it is a word from call_status_word's ring, which finish() reads.
+struct CallStatus {
+    int* word = nullptr;
+    bool deferred = false;
+    cudaError_t begin(cudaStream_t s);
+    int finish(cudaStream_t s) const { return deferred ? GPTQ_OK : finish_call(word, s); }
+};
 
 // Test hook support: sets this library's limit on pipeline mbarrier waits (mbar_wait) in
 // every translation unit that has such waits; the drain waits keep kWaitLimitNs.

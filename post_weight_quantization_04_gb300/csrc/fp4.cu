@@ -1,0 +1,344 @@
+// fp4.cu — quantisation to the microscaled 4-bit form (fp4.cuh) and its inverse.
+//
+// For a block of B columns with a = max|x| (the last block of a row padded with zeros):
+//   MX (B = 32): s = 2^(floor(log2 a) - 2), the power of two that brings a into [4, 8), as the
+//                OCP microscaling format defines it; values above 6 saturate.
+//   NV (B = 16): s = e4m3(a / (6 g)) * g with the matrix's fp32 scale g, so a maps to about 6.
+//   code = e2m1 nearest to x / s, ties to the even code, saturating at 6; s = 0 gives zeros.
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp4.cuh"
+
+namespace gptq {
+
+namespace {
+
+struct QParams {
+    const void* X;
+    int64_t rows, cols, ldx;
+    int64_t src_rows;        // rows of X
+    const int32_t* index;    // row r reads X row index[r] / per (negative: zeros); null: row r
+    int per;
+    const float* g;          // NV: the matrix's scale
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t pitch, tiles_k;
+    int* status;
+};
+
+constexpr int Q_THREADS = 128;
+constexpr int Q_COLS = 16;   // columns per thread: one NV block, half an MX block
+
+__device__ __forceinline__ float load_elem(const float* p) { return *p; }
+__device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// 16 consecutive values of one row as fp32, zeros past `n`
+template <typename T, bool VEC>
+__device__ __forceinline__ void load16(const T* x, int64_t n, float (&v)[Q_COLS]) {
+    if (VEC && n >= Q_COLS) {
+        constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+        for (int q = 0; q < Q_COLS / PER; ++q) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(x) + q);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            if (sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(u[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[8 * q + 2 * e] = __uint_as_float(u[e] << 16);
+                    v[8 * q + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < Q_COLS; ++e) v[e] = e < n ? load_elem(x + e) : 0.0f;
+    }
+}
+
+// 8 values (already divided by their block's scale) to 8 codes: nearest, ties to even, saturating
+__device__ __forceinline__ uint32_t to_codes(const float* y) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return r;
+}
+
+// One thread takes 16 columns of a row; an MX block's two threads share its maximum by one
+// shuffle. Streams x once and writes 1/2 byte per value plus the scales: bound by memory.
+template <typename T, bool MX, bool VEC>
+__global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p) {
+    const int64_t chunk = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
+    const int64_t c0 = chunk * Q_COLS;
+    const float g = MX ? 1.0f : *p.g;
+    for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        int64_t sr = r;
+        if (p.index) {
+            const int i = p.index[r];
+            sr = i < 0 ? -1 : i / p.per;
+            if (sr >= p.src_rows) {
+                sr = -1;
+                set_status(p.status, GPTQ_ERR_INVALID_ARG);
+            }
+        }
+        const int64_t n = sr < 0 ? 0 : p.cols - c0;
+        float v[Q_COLS];
+        load16<T, VEC>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx) + c0, n, v);
+        // the maximum over the magnitudes' bits: exact, and a NaN or infinity stays visible
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < Q_COLS; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        if (MX) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const bool bad = m >= 0x7F800000u;
+        if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
+        uint32_t byte;
+        float y[Q_COLS];
+        if (MX) {
+            // floor(log2 a) is a's exponent field; below 2^-125 the scale stays at 2^-127
+            byte = bad ? 255u : (uint32_t)max((int)(m >> 23) - 2, 0);
+            const float inv = __uint_as_float(byte < 254u ? (254u - byte) << 23 : 0x00400000u);
+#pragma unroll
+            for (int e = 0; e < Q_COLS; ++e) y[e] = v[e] * inv;   // exact: a power of two
+        } else {
+            const float a = __uint_as_float(m);
+            byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(a / (6.0f * g), __NV_SATFINITE, __NV_E4M3);
+            const float d = e4m3_value(byte) * g;
+            if (byte == 0u) {
+#pragma unroll
+                for (int e = 0; e < Q_COLS; ++e) y[e] = 0.0f;
+            } else if (d > 0x1p-100f && d < 0x1p100f) {
+                // x / d correctly rounded (Markstein 1990: with inv = 1 / d correctly rounded, one
+                // residual step on x * inv rounds the quotient correctly), so a value on a
+                // midpoint of the grid is seen as one
+                const float inv = 1.0f / d;
+#pragma unroll
+                for (int e = 0; e < Q_COLS; ++e) {
+                    const float q = v[e] * inv;
+                    y[e] = fmaf(fmaf(-q, d, v[e]), inv, q);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < Q_COLS; ++e) y[e] = v[e] / d;
+            }
+        }
+        if (c0 < 2 * p.pitch)
+            *reinterpret_cast<uint2*>(p.codes + r * p.pitch + c0 / 2) = make_uint2(to_codes(y), to_codes(y + 8));
+        // scales up to the end of the last tile: blocks past the columns get a zero byte
+        const int64_t b = MX ? chunk >> 1 : chunk;
+        if (b < 4 * p.tiles_k && !(MX && (chunk & 1)))
+            p.scales[fp4_scale_at(r, b, p.tiles_k)] = b * (MX ? 32 : 16) < p.cols ? (uint8_t)byte : (uint8_t)0;
+    }
+}
+
+struct DqParams {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const float* g;
+    int64_t rows, cols, pitch, tiles_k;
+    void* Y;
+    int64_t ldy;
+};
+
+__device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, bool MX, bool VEC>
+__global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParams p) {
+    const int64_t chunk = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
+    const int64_t c0 = chunk * Q_COLS, n = p.cols - c0;
+    if (n <= 0) return;
+    const float g = MX ? 1.0f : *p.g;
+    for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p.codes + r * p.pitch + c0 / 2);
+        const uint32_t sb = p.scales[fp4_scale_at(r, MX ? chunk >> 1 : chunk, p.tiles_k)];
+        const float s = MX ? e8m0_value(sb) : e4m3_value(sb) * g;
+        float v[Q_COLS];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 f = e2m1_values(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xFFu);
+            v[2 * e] = f.x * s;
+            v[2 * e + 1] = f.y * s;
+        }
+        T* y = static_cast<T*>(p.Y) + r * p.ldy + c0;
+        if (VEC && n >= Q_COLS) {
+            if (sizeof(T) == 4) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    reinterpret_cast<float4*>(y)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    reinterpret_cast<uint4*>(y)[q] =
+                        make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                                   pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < Q_COLS; ++e)
+                if (e < n) store_elem(y + e, v[e]);
+        }
+    }
+}
+
+// max|x| of a matrix, as the bits of an fp32 (ordered like the numbers, so an integer atomic
+// maximum is exact and independent of order), into out[0], which starts at 0
+template <typename T>
+__global__ void __launch_bounds__(256) fp4_amax_kernel(const T* X, int64_t rows, int64_t cols, int64_t ldx,
+                                                       uint32_t* out, int* status) {
+    uint32_t m = 0;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < cols; c += (int64_t)gridDim.x * 256)
+            m = max(m, __float_as_uint(load_elem(X + r * ldx + c)) & 0x7FFFFFFFu);
+    m = __reduce_max_sync(0xffffffffu, m);
+    __shared__ uint32_t part[8];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i) m = max(m, part[i]);
+        if (m >= 0x7F800000u) set_status(status, GPTQ_ERR_NONFINITE);
+        atomicMax(out, m);
+    }
+}
+
+// the least power of two g with max|x| <= 448 * 6 * g, in place of the maximum (1 for all zeros)
+__global__ void fp4_tensor_scale_kernel(uint32_t* out) {
+    const float a = __uint_as_float(*out);
+    int e = 0;
+    if (a > 0.0f && a < __uint_as_float(0x7F800000u)) {
+        frexpf(a / 2688.0f, &e);
+        if (ldexpf(0.5f, e) * 2688.0f >= a) --e;   // a / 2688 is a power of two itself
+    }
+    *out = __float_as_uint(ldexpf(1.0f, max(e, -126)));
+}
+
+__global__ void __launch_bounds__(256) fp4_tile_scales_kernel(const uint8_t* src, int64_t rows, int64_t blocks,
+                                                              int64_t lds, int64_t tiles_k, uint8_t* dst, int64_t total) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t tile = i / kFp4Tile;
+        const int at = (int)(i % kFp4Tile);
+        const int64_t r = tile / tiles_k * 128 + (at >> 2 & 3) * 32 + (at >> 4), b = tile % tiles_k * 4 + (at & 3);
+        dst[i] = r < rows && b < blocks ? src[r * lds + b] : (uint8_t)0;
+    }
+}
+
+bool bad_format(int f) { return f != GPTQ_MXFP4 && f != GPTQ_NVFP4; }
+bool bad_dtype(int t) { return t != GPTQ_F32 && t != GPTQ_BF16; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+constexpr int64_t kMaxDim = (1ll << 31) - 256;
+
+}  // namespace
+}  // namespace gptq
+
+using namespace gptq;
+
+extern "C" int64_t gptq_fp4_code_pitch(int64_t cols) { return cols < 0 ? 0 : fp4_pitch(cols); }
+
+extern "C" int64_t gptq_fp4_scale_bytes(int64_t rows, int64_t cols, int format) {
+    if (rows < 0 || cols < 0 || bad_format(format)) return 0;
+    return ceil_div(rows, 128) * fp4_tiles(cols, format) * kFp4Tile;
+}
+
+extern "C" int gptq_fp4_tensor_scale(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ldx, float* g,
+                                     void* stream) {
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim || bad_dtype(dtype) || !g || ldx < cols ||
+        (!X && rows * cols > 0))
+        return GPTQ_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallStatus st;
+    GPTQ_CUDA_TRY(st.begin(s));
+    uint32_t* out = reinterpret_cast<uint32_t*>(g);
+    GPTQ_CUDA_TRY(cudaMemsetAsync(out, 0, 4, s));
+    if (rows > 0 && cols > 0) {
+        const dim3 grid((unsigned)std::min<int64_t>(ceil_div(cols, 1024), 64), (unsigned)std::min<int64_t>(rows, 2048));
+        if (dtype == GPTQ_BF16)
+            GPTQ_LAUNCH(K_FP4_AMAX, s, fp4_amax_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(X), rows, cols, ldx, out, st.word));
+        else
+            GPTQ_LAUNCH(K_FP4_AMAX, s, fp4_amax_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(X), rows, cols, ldx, out, st.word));
+        GPTQ_LAUNCH_CHECK();
+    }
+    GPTQ_LAUNCH(K_FP4_AMAX, s, fp4_tensor_scale_kernel<<<1, 1, 0, s>>>(out));
+    GPTQ_LAUNCH_CHECK();
+    return st.finish(s);
+}
+
+extern "C" int gptq_fp4_quantize(const void* X, int dtype, int64_t src_rows, int64_t cols, int64_t ldx,
+                                 const int32_t* index, int64_t per, int64_t rows, int format, const float* g,
+                                 uint8_t* codes, uint8_t* scales, void* stream) {
+    if (rows < 0 || src_rows < 0 || cols < 0 || rows > kMaxDim || src_rows > kMaxDim || cols > kMaxDim || bad_dtype(dtype) ||
+        bad_format(format))
+        return GPTQ_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return GPTQ_OK;
+    if ((!X && src_rows > 0) || !codes || !scales || ldx < cols || (index ? (per < 1 || per > kMaxDim) : rows != src_rows) ||
+        (format == GPTQ_NVFP4 && !g) || !aligned16(codes) || !aligned16(scales))
+        return GPTQ_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallStatus st;
+    GPTQ_CUDA_TRY(st.begin(s));
+    QParams p{X, rows, cols, ldx, src_rows, index, (int)per, g, codes, scales, fp4_pitch(cols), fp4_tiles(cols, format), st.word};
+    const int64_t chunks = ceil_div(p.tiles_k * 4 * fp4_block(format), Q_COLS);
+    const dim3 grid((unsigned)ceil_div(chunks, Q_THREADS), (unsigned)std::min<int64_t>(rows, 32768));
+    const int64_t esize = dtype == GPTQ_BF16 ? 2 : 4;
+    const bool vec = aligned16(X) && (ldx * esize) % 16 == 0, mx = format == GPTQ_MXFP4;
+    auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_QUANT, s, kern<<<grid, Q_THREADS, 0, s>>>(p)); };
+    if (dtype == GPTQ_BF16) {
+        if (mx) vec ? go(fp4_quantize_kernel<__nv_bfloat16, true, true>) : go(fp4_quantize_kernel<__nv_bfloat16, true, false>);
+        else vec ? go(fp4_quantize_kernel<__nv_bfloat16, false, true>) : go(fp4_quantize_kernel<__nv_bfloat16, false, false>);
+    } else {
+        if (mx) vec ? go(fp4_quantize_kernel<float, true, true>) : go(fp4_quantize_kernel<float, true, false>);
+        else vec ? go(fp4_quantize_kernel<float, false, true>) : go(fp4_quantize_kernel<float, false, false>);
+    }
+    GPTQ_LAUNCH_CHECK();
+    return st.finish(s);
+}
+
+extern "C" int gptq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t rows, int64_t cols,
+                                   int format, void* Y, int dtype, int64_t ldy, void* stream) {
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim || bad_dtype(dtype) || bad_format(format))
+        return GPTQ_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return GPTQ_OK;
+    if (!codes || !scales || !Y || ldy < cols || (format == GPTQ_NVFP4 && !g) || !aligned16(codes) || !aligned16(scales))
+        return GPTQ_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DqParams p{codes, scales, g, rows, cols, fp4_pitch(cols), fp4_tiles(cols, format), Y, ldy};
+    const dim3 grid((unsigned)ceil_div(ceil_div(cols, Q_COLS), Q_THREADS), (unsigned)std::min<int64_t>(rows, 32768));
+    const int64_t esize = dtype == GPTQ_BF16 ? 2 : 4;
+    const bool vec = aligned16(Y) && (ldy * esize) % 16 == 0, mx = format == GPTQ_MXFP4;
+    auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_DEQUANT, s, kern<<<grid, Q_THREADS, 0, s>>>(p)); };
+    if (dtype == GPTQ_BF16) {
+        if (mx) vec ? go(fp4_dequantize_kernel<__nv_bfloat16, true, true>) : go(fp4_dequantize_kernel<__nv_bfloat16, true, false>);
+        else vec ? go(fp4_dequantize_kernel<__nv_bfloat16, false, true>) : go(fp4_dequantize_kernel<__nv_bfloat16, false, false>);
+    } else {
+        if (mx) vec ? go(fp4_dequantize_kernel<float, true, true>) : go(fp4_dequantize_kernel<float, true, false>);
+        else vec ? go(fp4_dequantize_kernel<float, false, true>) : go(fp4_dequantize_kernel<float, false, false>);
+    }
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+extern "C" int gptq_fp4_tile_scales(const uint8_t* src, int64_t rows, int64_t cols, int64_t lds, int format,
+                                    uint8_t* scales, void* stream) {
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim || bad_format(format)) return GPTQ_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return GPTQ_OK;
+    const int64_t blocks = ceil_div(cols, fp4_block(format));
+    if (!src || !scales || lds < blocks) return GPTQ_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t total = gptq_fp4_scale_bytes(rows, cols, format);
+    GPTQ_LAUNCH(K_FP4_TILE, s, fp4_tile_scales_kernel<<<(unsigned)std::min<int64_t>(ceil_div(total, 256), 8 * 152), 256, 0, s>>>(
+        src, rows, blocks, lds, fp4_tiles(cols, format), scales, total));
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}

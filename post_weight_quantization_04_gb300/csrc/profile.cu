@@ -48,7 +48,9 @@ const char* kNames[K_COUNT] = {
     "gptq_block_kernel",   "sgemm_kernel[trailing]", "g_idx_kernel",
     "pack_kernel",         "rtn_kernel",          "split_kernel",      "tc_gemm_nt_kernel[prepare]",
     "tc_gemm_nt_kernel[trailing]", "dequant_matmul_kernel", "merge_status_kernel",
-    "tc_gemm_nt_kernel[chain]",
+    "tc_gemm_nt_kernel[chain]", "fp4_amax_kernel", "fp4_quantize_kernel", "fp4_dequantize_kernel",
+    "fp4_tile_scales_kernel", "fp4_matmul_kernel", "expert_sort_kernel", "expert_gather_kernel",
+    "expert_combine_kernel", "expert_combine_grad_kernel",
 };
 
 }  // namespace

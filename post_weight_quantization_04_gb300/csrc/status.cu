@@ -34,6 +34,7 @@ constexpr int kStatusWords = 256;
 __device__ int g_call_status[kStatusWords];
 std::atomic<unsigned> g_next_word{0};
 ContextPtrCache g_call_status_addr;
+ContextPtrCache g_sticky_status_addr;
 
 using PfnCtxGetCurrent = CUresult (*)(CUcontext*);
 using PfnCtxGetId = CUresult (*)(CUcontext, unsigned long long*);
@@ -74,6 +75,19 @@ cudaError_t call_status_word(cudaStream_t s, int** out) {
     int* w = static_cast<int*>(base) + (g_next_word.fetch_add(1, std::memory_order_relaxed) % kStatusWords);
     *out = w;
     return cudaMemsetAsync(w, 0, sizeof(int), s);
+}
+
+cudaError_t CallStatus::begin(cudaStream_t s) {
+    deferred = g_mode.load(std::memory_order_relaxed) == GPTQ_STATUS_DEFERRED;
+    if (!deferred) return call_status_word(s, &word);
+    void* base = g_sticky_status_addr.find(current_context_id());
+    if (!base) {
+        const cudaError_t e = cudaGetSymbolAddress(&base, g_sticky_status);
+        if (e != cudaSuccess) return e;
+        g_sticky_status_addr.put(current_context_id(), base);
+    }
+    word = static_cast<int*>(base);
+    return cudaSuccess;
 }
 
 int finish_call(const int* status, cudaStream_t s) {

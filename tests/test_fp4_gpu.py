@@ -1,0 +1,306 @@
+"""The microscaled 4-bit form on the GPU against its fp64 oracle.
+
+Quantising is a sequence of exactly specified roundings, so codes and scale bytes are compared for
+equality, and dequantised values with the one fp32 (or bf16) rounding of code * scale. The product's
+bound follows from its arithmetic: products of e2m1 values and block scales are exact in fp32 up to
+one rounding per block, sums take at most K additions of relative error 2^-23 (rounded or truncated),
+the tensor scales two more roundings, and the result is rounded once:
+    |Y - Y_ref| <= ((K + 4) 2^-23) sum_k |x w| (+ 2^-8 |Y_ref| for bf16).
+Where scales and codes are chosen so that every partial sum is an integer multiple of one small unit
+below 2^24 of it, no rounding happens at all and Y has to be equal: a wrong code, scale, row or tile
+shows there.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4_oracle as F
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def npy(t):
+    return t.detach().float().cpu().numpy() if t.dtype == torch.bfloat16 else t.detach().cpu().numpy()
+
+
+def _matrix(rows, cols, dtype, seed, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols + pad, generator=g) * torch.randn(1, cols + pad, generator=g).exp()
+    x[:, ::7] *= 0.01
+    x[rows // 2, : min(cols, 40)] = 0.0                 # a block of zeros
+    x[rows // 3] = torch.randint(-24, 25, (cols + pad,), generator=g) / 4   # midpoints of the grid
+    return x.to(dtype)
+
+
+SHAPES = [(1, 1), (1, 4096), (3, 31), (5, 33), (128, 128), (129, 65), (300, 1000), (7, 2051)]
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt,g", [("mx", None), ("nv", 2.0 ** -7), ("nv", 0.0123)])
+def test_quantize_is_exact(lib, rows, cols, dtype, fmt, g):
+    xh = _matrix(rows, cols, dtype, rows * 31 + cols)
+    X = xh.to(DEV)
+    gt = None if g is None else torch.tensor([g], device=DEV)
+    q = lib.gptq_fp4_quantize(X, fmt, gt)
+    gf = None if g is None else float(np.float32(g))
+    v, codes, byte = F.quantise(npy(xh), fmt, gf)
+    np.testing.assert_array_equal(F.untile_scales(npy(q.scales), rows, byte.shape[1]), byte)
+    got = npy(q.codes)
+    # every byte of the pitch is written; the sign of a zero is free
+    want = F.pack_codes(codes)
+    fix = lambda b: np.where((b & 15) == 8, b & 0xF0, b)  # noqa: E731
+    zero = lambda b: np.where((b >> 4) == 8, fix(b) & 0x0F, fix(b))  # noqa: E731
+    np.testing.assert_array_equal(zero(got), zero(want))
+    # blocks past the columns are zero in every row of the matrix
+    t = npy(q.scales)
+    np.testing.assert_array_equal(F.untile_scales(t, rows, t.shape[1] * 4)[:, byte.shape[1]:], 0)
+    d32 = lib.gptq_fp4_dequantize(q)
+    np.testing.assert_array_equal(npy(d32), v.astype(np.float32))
+    d16 = lib.gptq_fp4_dequantize(q, torch.bfloat16)
+    np.testing.assert_array_equal(npy(d16), npy(torch.tensor(v.astype(np.float32)).to(torch.bfloat16)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_strides_and_extremes(lib, dtype):
+    big = torch.finfo(torch.bfloat16).max
+    xh = _matrix(40, 100, torch.float32, 5, pad=29)
+    xh[1, :32] = torch.linspace(-1, 1, 32) * big
+    xh[2, :32] = 2.0 ** -126
+    xh[3, :32] = torch.linspace(0, 2.0 ** -140, 32)
+    xh = xh.to(dtype)
+    X = xh.to(DEV)
+    for view, ref in ((X[:, 3:103], xh[:, 3:103]), (X[::3, :100], xh[::3, :100]), (X[:, 8:108], xh[:, 8:108])):
+        q = lib.gptq_fp4_quantize(view, "mx")
+        v, codes, byte = F.quantise(npy(ref.contiguous()), "mx")
+        np.testing.assert_array_equal(F.untile_scales(npy(q.scales), *byte.shape), byte)
+        np.testing.assert_array_equal(npy(lib.gptq_fp4_dequantize(q)), v.astype(np.float32))
+    # a tensor scale far below and far above the values: scales saturate, and vanish
+    for g in (2.0 ** -20, 2.0 ** 20):
+        q = lib.gptq_fp4_quantize(X[4:, 3:103], "nv", torch.tensor([g], device=DEV))
+        v, _, byte = F.quantise(npy(xh[4:, 3:103].contiguous()), "nv", g)
+        np.testing.assert_array_equal(F.untile_scales(npy(q.scales), *byte.shape), byte)
+        np.testing.assert_array_equal(npy(lib.gptq_fp4_dequantize(q)), v.astype(np.float32))
+
+
+def test_quantize_gathers_rows(lib):
+    X = _matrix(50, 200, torch.bfloat16, 8).to(DEV)
+    idx = torch.tensor([0, 99, 41, -1, 40, 7, -1, 98] * 20, dtype=torch.int32, device=DEV)
+    q = lib.gptq_fp4_quantize(X, "mx", index=idx, per=2)
+    rows = torch.where((idx >= 0).unsqueeze(1), X[(idx.clamp(min=0) // 2).long()], 0)
+    ref = lib.gptq_fp4_quantize(rows.contiguous(), "mx")
+    assert torch.equal(lib.gptq_fp4_dequantize(q), lib.gptq_fp4_dequantize(ref))
+    with pytest.raises(lib.GptqError) as e:
+        lib.gptq_fp4_quantize(X, "mx", index=idx, per=1)      # 99 is past the 50 rows
+    assert e.value.status == 1
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_nonfinite_is_reported(lib, fmt, bad):
+    X = torch.randn(9, 70).to(DEV)
+    g = torch.tensor([0.01], device=DEV)
+    X[4, 69] = bad
+    with pytest.raises(lib.GptqError) as e:
+        lib.gptq_fp4_quantize(X, fmt, g)
+    assert e.value.status == 7
+    with lib.deferred_status():
+        q = lib.gptq_fp4_quantize(X, fmt, g)
+        with pytest.raises(lib.GptqError) as e:
+            lib.status_sync()
+        assert e.value.status == 7
+        lib.status_sync()
+    v = lib.gptq_fp4_dequantize(q)
+    assert torch.isnan(v[4, 64:]).all() and torch.isfinite(v[4, :64]).all() and torch.isfinite(v[5:]).all()
+    with pytest.raises(lib.GptqError) as e:
+        lib.gptq_fp4_tensor_scale(X)
+    assert e.value.status == 7
+
+
+def test_tensor_scale(lib):
+    for amax, dtype in ((2688.0, torch.float32), (2689.0, torch.float32), (1e-3, torch.bfloat16), (0.0, torch.float32)):
+        X = (torch.rand(33, 77) * 0.5 * amax).to(dtype).to(DEV)
+        X[32, 76] = -amax
+        a = X.abs().max().item()
+        g = lib.gptq_fp4_tensor_scale(X).item()
+        assert np.log2(g) == round(np.log2(g))
+        assert (a <= 2688 * g and a > 2688 * g / 2) if a else g == 1.0
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_tile_scales(lib, fmt):
+    byte = np.random.default_rng(1).integers(0, 120, (261, 7)).astype(np.uint8)
+    cols = 7 * F.BLOCK[fmt] - 3
+    t = lib.gptq_fp4_tile_scales(torch.tensor(byte, device=DEV), cols, fmt)
+    np.testing.assert_array_equal(npy(t), F.tile_scales(byte, cols, fmt))
+
+
+# ------------------------------------------------------------------------------------- product
+
+def _stored(rng, rows, cols, fmt, exact, g):
+    """Random codes and scales; `exact`: few enough bits that sums of products are exact in fp32."""
+    codes = rng.integers(0, 16, (rows, cols))
+    blocks = -(-cols // F.BLOCK[fmt])
+    if fmt == "mx":
+        byte = rng.integers(126, 128, (rows, blocks)) if exact else rng.integers(120, 130, (rows, blocks))
+    else:
+        byte = rng.choice([48, 56], (rows, blocks)) if exact else rng.integers(20, 100, (rows, blocks))   # 0.5, 1
+    byte = byte.astype(np.uint8)
+    return codes, byte, F.values(codes, byte, fmt, g)
+
+
+def _fp4(lib, codes, byte, cols, fmt, g):
+    return lib.Fp4(torch.tensor(F.pack_codes(codes), device=DEV), torch.tensor(F.tile_scales(byte, cols, fmt), device=DEV), cols,
+                   fmt, torch.tensor([g], dtype=torch.float32, device=DEV) if fmt == "nv" else None)
+
+
+def _check(Y, xv, wv, exact, bf16, K):
+    ref = xv @ wv.T
+    if exact and not bf16:
+        np.testing.assert_array_equal(Y, ref)
+        return
+    bound = (K + 4) * 2.0 ** -23 * (np.abs(xv) @ np.abs(wv).T) + (2.0 ** -8 * np.abs(ref) if bf16 else 0) + 1e-30
+    bad = np.abs(Y - ref) > bound
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:5], float(np.max(np.abs(Y - ref) / bound)))
+
+
+PRODUCTS = [
+    # T, N, K
+    (1, 1, 1), (1, 16, 32), (1, 4096, 512), (2, 129, 96), (7, 333, 1000), (16, 128, 1056), (31, 250, 257), (33, 256, 300),
+    (64, 512, 768), (77, 2310, 1000), (127, 129, 64), (128, 128, 256), (129, 257, 800), (200, 640, 1500), (300, 1000, 128),
+    (513, 300, 1024), (1030, 700, 448), (2100, 1300, 320),
+]
+
+
+@pytest.mark.parametrize("T,N,K", PRODUCTS)
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_matmul_exact_sums(lib, T, N, K, fmt):
+    rng = np.random.default_rng(T + 3 * N + 7 * K)
+    cx, bx, xv = _stored(rng, T, K, fmt, True, 2.0)
+    cw, bw, wv = _stored(rng, N, K, fmt, True, 0.25)
+    Y = lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, 2.0), _fp4(lib, cw, bw, K, fmt, 0.25))
+    _check(npy(Y), xv, wv, True, False, K)
+
+
+@pytest.mark.parametrize("T,N,K", PRODUCTS[::2] + [(5, 300, 5000), (150, 300, 5000)])
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("bf16,relu", [(False, True), (True, False)])
+def test_matmul_bound(lib, T, N, K, fmt, bf16, relu):
+    rng = np.random.default_rng(T + 5 * N + 11 * K)
+    gx, gw = float(np.float32(0.37)), float(np.float32(1.9))
+    cx, bx, xv = _stored(rng, T, K, fmt, False, gx)
+    cw, bw, wv = _stored(rng, N, K, fmt, False, gw)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    wide = torch.full((T, N + 5), -7.0, dtype=dtype_of(bf16), device=DEV)
+    Y = lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, gx), _fp4(lib, cw, bw, K, fmt, gw), relu=relu, out_dtype=dt, out=wide[:, :N])
+    got = npy(Y)
+    if relu:
+        assert (got >= 0).all()
+        plain = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, gx), _fp4(lib, cw, bw, K, fmt, gw)))
+        np.testing.assert_array_equal(got, np.maximum(plain, 0))
+    else:
+        _check(got, xv, wv, False, bf16, K)
+    assert (wide[:, N:] == -7).all()              # nothing is written past the columns
+
+
+def dtype_of(bf16):
+    return torch.bfloat16 if bf16 else torch.float32
+
+
+GROUPED = [
+    # rows per expert (0: none), rows past the last one, N, K
+    ([1, 0, 2, 0, 0, 1], 0, 200, 96),
+    ([0, 0, 0], 5, 64, 64),
+    ([5, 130, 0, 127, 1, 300], 9, 300, 320),
+    ([33] * 9, 0, 129, 1000),
+    ([0, 700, 0, 0, 650], 130, 400, 544),
+    ([128, 128, 128], 0, 256, 256),
+    ([3, 1, 4, 1, 5, 9, 2, 6, 5, 3, 5, 8, 9, 7, 9, 3], 2, 520, 2048),
+]
+
+
+@pytest.mark.parametrize("sizes,tail,N,K", GROUPED)
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("per_expert", [False, True])
+def test_matmul_grouped(lib, sizes, tail, N, K, fmt, per_expert):
+    rng = np.random.default_rng(sum(sizes) + N + K)
+    T, E = sum(sizes) + tail, len(sizes)
+    cx, bx, xv = _stored(rng, T, K, fmt, True, 2.0)
+    gw = [2.0 ** -(e % 3) if per_expert else 0.5 for e in range(E)]
+    ws = [_stored(rng, N, K, fmt, True, gw[e]) for e in range(E)]
+    W = lib.Fp4(torch.tensor(np.stack([F.pack_codes(w[0]) for w in ws]), device=DEV),
+                torch.tensor(np.stack([F.tile_scales(w[1], K, fmt) for w in ws]), device=DEV), K, fmt,
+                None if fmt == "mx" else torch.tensor(gw if per_expert else gw[:1], device=DEV))
+    off = np.concatenate(([0], np.cumsum(sizes))).astype(np.int32)
+    out = torch.full((T, N), 99.0, device=DEV)
+    Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, 2.0), W, offsets=torch.tensor(off, device=DEV), out=out))
+    for e in range(E):
+        _check(Y[off[e]:off[e + 1]], xv[off[e]:off[e + 1]], ws[e][2], True, False, K)
+    np.testing.assert_array_equal(Y[off[-1]:], 0)
+
+
+def test_matmul_reports_bad_offsets(lib):
+    rng = np.random.default_rng(2)
+    cx, bx, _ = _stored(rng, 40, 64, "mx", True, 1)
+    cw, bw, _ = _stored(rng, 60, 64, "mx", True, 1)
+    W = _fp4(lib, cw, bw, 64, "mx", 1)
+    W3 = lib.Fp4(torch.stack([W.codes] * 3), torch.stack([W.scales] * 3), 64, "mx")
+    X = _fp4(lib, cx, bx, 64, "mx", 1)
+    for off in ([0, 10, 5, 40], [0, 10, 20, 41], [-1, 10, 20, 40]):
+        with pytest.raises(lib.GptqError) as e:
+            lib.gptq_fp4_matmul(X, W3, offsets=torch.tensor(off, dtype=torch.int32, device=DEV))
+        assert e.value.status == 1
+
+
+def test_matmul_repeats_bit_for_bit_on_any_stream(lib):
+    rng = np.random.default_rng(4)
+    for T, N, K in ((1, 900, 4096), (300, 900, 1024)):
+        cx, bx, _ = _stored(rng, T, K, "nv", False, 1)
+        cw, bw, _ = _stored(rng, N, K, "nv", False, 1)
+        X, W = _fp4(lib, cx, bx, K, "nv", 1.0), _fp4(lib, cw, bw, K, "nv", 1.0)
+        ref = lib.gptq_fp4_matmul(X, W)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with lib.deferred_status():
+            for _ in range(3):
+                got = lib.gptq_fp4_matmul(X, W, stream=s, out=torch.empty_like(ref))
+                s.synchronize()
+                assert torch.equal(got, ref)
+            lib.status_sync(s)
+
+
+def test_in_a_cuda_graph(lib):
+    """In deferred status mode the calls only enqueue kernels: quantise and product replay as a graph."""
+    X = torch.randn(48, 640, device=DEV).to(torch.bfloat16)
+    W = lib.gptq_fp4_quantize(torch.randn(300, 640, device=DEV), "mx")
+    ref = lib.gptq_fp4_matmul(lib.gptq_fp4_quantize(X, "mx"), W)
+    with lib.deferred_status():
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            lib.gptq_fp4_matmul(lib.gptq_fp4_quantize(X, "mx"), W)
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = lib.gptq_fp4_matmul(lib.gptq_fp4_quantize(X, "mx"), W)
+        got.zero_()
+        g.replay()
+        lib.status_sync()
+    torch.cuda.synchronize()
+    assert torch.equal(got, ref)
+
+
+def test_binding_refusals(lib):
+    X = torch.randn(8, 64, device=DEV)
+    q = lib.gptq_fp4_quantize(X, "mx")
+    n = lib.gptq_fp4_quantize(X, "nv")
+    for call in (lambda: lib.gptq_fp4_quantize(X.cpu(), "mx"), lambda: lib.gptq_fp4_quantize(X, "fp4"),
+                 lambda: lib.gptq_fp4_quantize(X.t(), "mx"), lambda: lib.gptq_fp4_quantize(X.half(), "mx"),
+                 lambda: lib.gptq_fp4_quantize(X[0], "mx"), lambda: lib.gptq_fp4_matmul(q, n),
+                 lambda: lib.gptq_fp4_matmul(q, q._replace(cols=63)), lambda: lib.gptq_fp4_matmul(q, q, out_dtype=torch.float16),
+                 lambda: lib.gptq_fp4_matmul(n, n._replace(tensor_scale=None)),
+                 lambda: lib.gptq_fp4_matmul(q, q, offsets=torch.zeros(2, dtype=torch.int32, device=DEV)),
+                 lambda: lib.gptq_fp4_dequantize(q, torch.float16), lambda: lib.gptq_fp4_dequantize(q, out=X[:, :63])):
+        with pytest.raises(ValueError):
+            call()
