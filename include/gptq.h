@@ -324,7 +324,8 @@ int gptq_fp4_tile_scales(const uint8_t* src, int64_t rows, int64_t cols, int64_t
  *   Y        device, (T, N) row-major, row stride ldy elements
  * Sums are fp32; the result is rounded once. Allocates nothing. Synchronises `stream` and
  * returns the device status (in the deferred status mode neither).
- * Errors: INVALID_ARG, UNSUPPORTED (more than 65536 experts), TIMEOUT, CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 1024 experts, or 2^31 rows of
+ * weights), TIMEOUT, CUDA. */
 enum { GPTQ_FP4_EXPERT_G = 4 };
 int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_g, int64_t T,
                     const uint8_t* w_codes, const uint8_t* w_scales, const float* w_g, int64_t N,

@@ -105,6 +105,7 @@ struct CallStatus {
 cudaError_t hessian_set_wait_limit(unsigned long long ns);
 cudaError_t tc_gemm_set_wait_limit(unsigned long long ns);
 cudaError_t dequant_set_wait_limit(unsigned long long ns);
+cudaError_t fp4_set_wait_limit(unsigned long long ns);
 
 static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

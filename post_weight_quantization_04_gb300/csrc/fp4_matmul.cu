@@ -1,133 +1,438 @@
 // fp4_matmul.cu — Y = X W^T for two matrices in the microscaled 4-bit form (fp4.cuh), dense or
 // with one weight per expert over rows sorted by expert:
 //   Y[t][o] = act(gx gw sum_b sx[t][b] sw[e(t)][o][b] sum_{k in b} x[t][k] w[e(t)][o][k])
-// Products of two e2m1 values are exact; sums are fp32.
+//
+// The tensor core multiplies this form itself (tcgen05.mma kind::mxf4 / kind::mxf4nvf4 with block
+// scales, 64 columns per instruction, fp32 sums in TMEM). The weights are the M operand (128
+// features per tile) and the tokens the N operand, whose width is chosen per tile: an expert with
+// few rows pays for few.
+//
+// Roles (one persistent CTA per SM):
+//   warp 0       producer: per stage of 256 columns the 128 x 128-byte box of weight codes and the
+//                64-row boxes of token codes by TMA (128-byte swizzle), the scale tiles by bulk copies
+//   warp 1       one thread: scale tiles shared memory -> TMEM (tcgen05.cp), then the stage's MMAs
+//   warps 2..9   epilogue: TMEM -> registers -> Y; a lane holds one feature, a register one token
+//
+// TMEM: the sums of a 128 x 256 tile take 256 columns, so two whole buffers would leave none for
+// scales. Even tiles use columns [0, 256), odd tiles [128, 384): only [128, 256) is shared, it is
+// drained first (all of it into registers, then released), and the next tile's MMAs start while
+// the rest is still being stored. Columns 384.. hold two stages' scales in turn.
+// Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind).
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "fp4.cuh"
+#include "tc_gemm.cuh"
 
 namespace gptq {
 
 namespace {
 
+constexpr int M_F = 128;                 // features per tile
+constexpr int M_T = 256;                 // most tokens per tile
+constexpr int M_KB = 128;                // bytes of codes per row and stage (256 columns)
+constexpr int M_TBOX = 64;               // tokens per TMA box
+constexpr int M_STAGES = 4;
+constexpr int M_THREADS = 32 * 10;
+constexpr uint32_t M_TMEM = 512, M_SF0 = 384;
+constexpr int M_MAX_EXPERTS = 1024;
+
+template <bool MX>
+struct Stage {
+    static constexpr int KA = MX ? 2 : 4;              // scale tiles along a stage's columns
+    static constexpr int W = M_F * M_KB, X = M_T * M_KB;
+    static constexpr int SW = KA * kFp4Tile, SX = 2 * KA * kFp4Tile;
+    static constexpr int BYTES = W + X + SW + SX;      // a multiple of 1024
+    static constexpr uint32_t SF_COLS = KA * 12;       // TMEM columns of one stage's scales
+};
+
 struct MParams {
-    const uint8_t *xc, *xs, *wc, *ws;
+    const uint8_t *xs, *ws;
     const float *xg, *wg;
-    int64_t T, N, K, pitch, tiles_k;
-    int64_t w_codes_stride, w_scales_stride;   // bytes from one expert to the next
+    int T, N, K;
+    int64_t tiles_k;
+    int64_t w_scales_stride;   // bytes from one expert to the next
     int wg_stride;
-    const int32_t* offsets;   // null: one expert, all rows
+    const int32_t* offsets;    // null: one expert, all rows
     int experts;
+    int ftiles;                // feature tiles
     int relu, bf16_out;
     void* Y;
     int64_t ldy;
     int* status;
 };
 
-// rows [lo, hi) of expert e, made safe: non-decreasing and within the rows of X
-__device__ __forceinline__ void expert_rows(const MParams& p, int e, int64_t* lo, int64_t* hi) {
+// rows [lo, hi) of expert e, made safe: within the rows of X
+__device__ __forceinline__ void expert_rows(const MParams& p, int e, int* lo, int* hi) {
     if (!p.offsets) {
         *lo = 0;
         *hi = p.T;
         return;
     }
-    const int64_t a = p.offsets[e], b = p.offsets[e + 1];
-    const int64_t l = min(max(a, (int64_t)0), p.T), h = min(max(b, l), p.T);
+    const int a = p.offsets[e], b = p.offsets[e + 1];
+    const int l = min(max(a, 0), p.T), h = min(max(b, l), p.T);
     if (l != a || h != b) set_status(p.status, GPTQ_ERR_INVALID_ARG);
     *lo = l;
     *hi = h;
 }
 
-constexpr int B_T = 64, B_N = 64, B_K = 32;
+// Token tiles of rows [lo, hi): they start on a multiple of 64 (where the tokens' scales may start
+// in TMEM), the first one ends within two 128-row scale tiles, the others are whole.
+__device__ __forceinline__ int token_tiles(int lo, int hi) {
+    if (hi <= lo) return 0;
+    const int t0 = lo & ~63, first = M_T - (t0 & 127);
+    const int rest = hi - t0 - first;
+    return 1 + (rest > 0 ? (rest + M_T - 1) / M_T : 0);
+}
 
-// 64 x 64 outputs per CTA, 32 columns at a time expanded to fp32 in shared memory.
-template <bool MX>
-__global__ void __launch_bounds__(256) fp4_matmul_kernel(const MParams p) {
-    __shared__ float xs[B_K][B_T + 1], ws[B_K][B_N + 1];
-    // the CTA's expert and its first row: experts in order, ceil(rows / 64) tiles each
-    int64_t tile = blockIdx.x, lo = 0, hi = 0;
-    int e = 0;
-    for (; e < p.experts; ++e) {
-        expert_rows(p, e, &lo, &hi);
-        const int64_t n = (hi - lo + B_T - 1) / B_T;
-        if (tile < n) break;
-        tile -= n;
+struct Tile {
+    int e, f0;        // expert, first feature
+    int t0, n;        // first token (a multiple of 64), tokens (a multiple of 32)
+    int lo, hi;       // the tokens that belong to the expert
+};
+
+// tile index -> tile; start[e] = token tiles before expert e
+__device__ __forceinline__ Tile find_tile(const MParams& p, const int32_t* start, int64_t i) {
+    Tile t;
+    const int tt = (int)(i / p.ftiles);
+    t.f0 = (int)(i % p.ftiles) * M_F;
+    int a = 0, b = p.experts;   // start[a] <= tt < start[b]
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (start[m] <= tt) a = m;
+        else b = m;
     }
-    const int64_t n0 = (int64_t)blockIdx.y * B_N;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    float acc[4][4] = {};
-    int64_t t0;
-    if (e < p.experts) {
-        t0 = lo + tile * B_T;
-        const uint8_t* wc = p.wc + e * p.w_codes_stride;
-        const uint8_t* wsc = p.ws + e * p.w_scales_stride;
-        const int r = tid >> 2, q = tid & 3;   // row of the tile, 8 columns of the step
-        for (int64_t k0 = 0; k0 < p.K; k0 += B_K) {
-            const int64_t b = k0 / (MX ? 32 : 16) + (MX ? 0 : q >> 1);
-            uint32_t cx = 0, cw = 0;
-            float sx = 0.0f, sw = 0.0f;
-            if (t0 + r < hi) {
-                cx = *reinterpret_cast<const uint32_t*>(p.xc + (t0 + r) * p.pitch + k0 / 2 + 4 * q);
-                const uint32_t s = p.xs[fp4_scale_at(t0 + r, b, p.tiles_k)];
-                sx = MX ? e8m0_value(s) : e4m3_value(s);
-            }
-            if (n0 + r < p.N) {
-                cw = *reinterpret_cast<const uint32_t*>(wc + (n0 + r) * p.pitch + k0 / 2 + 4 * q);
-                const uint32_t s = wsc[fp4_scale_at(n0 + r, b, p.tiles_k)];
-                sw = MX ? e8m0_value(s) : e4m3_value(s);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 a = e2m1_values((cx >> (8 * i)) & 0xFFu), c = e2m1_values((cw >> (8 * i)) & 0xFFu);
-                xs[8 * q + 2 * i][r] = a.x * sx;
-                xs[8 * q + 2 * i + 1][r] = a.y * sx;
-                ws[8 * q + 2 * i][r] = c.x * sw;
-                ws[8 * q + 2 * i + 1][r] = c.y * sw;
-            }
-            __syncthreads();
-#pragma unroll 8
-            for (int k = 0; k < B_K; ++k) {
-                float a[4], c[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[i] = xs[k][ty * 4 + i];
-                    c[i] = ws[k][tx + 16 * i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], c[j], acc[i][j]);
-            }
-        }
+    t.e = a;
+    if (p.offsets) {
+        t.lo = min(max(p.offsets[a], 0), p.T);
+        t.hi = min(max(p.offsets[a + 1], t.lo), p.T);
     } else {
-        // past the experts' tiles: rows that belong to none are zero
-        t0 = hi + tile * B_T;
-        hi = p.T;
-        e = 0;
+        t.lo = 0;
+        t.hi = p.T;
     }
-    const float g = MX ? 1.0f : *p.xg * p.wg[e * p.wg_stride];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + ty * 4 + i;
-        if (t >= hi) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t o = n0 + tx + 16 * j;
-            if (o >= p.N) continue;
-            float v = acc[i][j] * g;
-            if (p.relu) v = fmaxf(v, 0.0f);
-            if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[t * p.ldy + o] = __float2bfloat16_rn(v);
-            else static_cast<float*>(p.Y)[t * p.ldy + o] = v;
+    const int first0 = t.lo & ~63, first = M_T - (first0 & 127), j = tt - start[a];
+    t.t0 = j == 0 ? first0 : first0 + first + (j - 1) * M_T;
+    t.n = min((t.hi - t.t0 + 31) & ~31, j == 0 ? first : M_T);
+    return t;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory to four TMEM columns, in each quarter of the lanes
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(smem_desc(saddr, 0, 128, 0)) : "memory");
+}
+
+template <bool MX>
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+    if (MX)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: [4,6) B's scale byte | [7,10) A type (1 = e2m1) |
+// [10,12) B type | [17,23) N >> 3 | [23] scale type (1 = e8m0, 0 = e4m3) | [24,29) M >> 4 |
+// [29,31) A's scale byte
+template <bool MX>
+__device__ __forceinline__ uint32_t fp4_idesc(int n, uint32_t sf) {
+    return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((MX ? 1u : 0u) << 23) |
+           ((uint32_t)(M_F >> 4) << 24) | (sf << 29);
+}
+
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            set_status(status, GPTQ_ERR_TIMEOUT);
+            return;
         }
     }
 }
 
+// 32 tokens of one feature to Y: the lanes of a warp hold consecutive features, so each token is
+// one store of 64 or 128 consecutive bytes
+template <typename T>
+__device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (&v)[32], float g, bool relu, int first, int last) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (j >= first && j < last) {
+            const float x = __uint_as_float(v[j]) * g, z = relu ? fmaxf(x, 0.0f) : x;
+            if constexpr (sizeof(T) == 2) *y = __float2bfloat16_rn(z);
+            else *y = z;
+        }
+        y += ldy;
+    }
+}
+
+__device__ __forceinline__ void store_tokens(const MParams& p, const uint32_t (&v)[32], float g, const Tile& t, int tok, int f) {
+    if (f >= p.N) return;
+    const int first = max(t.lo - tok, 0), last = min(t.hi - tok, 32);
+    const int64_t at = (int64_t)tok * p.ldy + f;
+    if (p.bf16_out) store_tokens(static_cast<__nv_bfloat16*>(p.Y) + at, p.ldy, v, g, p.relu != 0, first, last);
+    else store_tokens(static_cast<float*>(p.Y) + at, p.ldy, v, g, p.relu != 0, first, last);
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_constant__ CUtensorMap tW,
+                                                                 const __grid_constant__ CUtensorMap tX, const MParams p) {
+    using S = Stage<MX>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M_STAGES * S::BYTES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * M_STAGES + 6);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int32_t* start = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [experts + 1]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (M_STAGES + s); };
+    auto tfull = [&](int b) { return bar0 + 8u * (2 * M_STAGES + b); };          // a tile's sums are done
+    auto own_free = [&](int b) { return bar0 + 8u * (2 * M_STAGES + 2 + b); };   // columns of one parity only
+    const uint32_t shared_free = bar0 + 8u * (2 * M_STAGES + 4);                 // columns of both parities
+    const uint32_t drain_bar = bar0 + 8u * (2 * M_STAGES + 5);
+    const int stages = (p.K + 2 * M_KB - 1) / (2 * M_KB);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < M_STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(own_free(b), 8);
+        }
+        mbar_init(shared_free, 8);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tW);
+            tma_prefetch_desc(&tX);
+        }
+        // token tiles before each expert
+        int carry = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            int lo = 0, hi = 0;
+            if (e0 + lane < p.experts) expert_rows(p, e0 + lane, &lo, &hi);
+            const int n = token_tiles(lo, hi);
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (e0 + lane < p.experts) start[e0 + lane] = carry + inc - n;
+            carry += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) start[p.experts] = carry;
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), M_TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t ntiles = (int64_t)start[p.experts] * p.ftiles;
+
+    if (warp == 0) {
+        // ------------------------------- producer -----------------------------------
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_par = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+                const Tile t = find_tile(p, start, i);
+                const int boxes = (t.n + M_TBOX - 1) / M_TBOX;
+                const int atoms = ((t.t0 & 127) + t.n + 127) >> 7;   // 128-row scale tiles of the tokens
+                const uint8_t* ws = p.ws + t.e * p.w_scales_stride + (int64_t)(t.f0 >> 7) * p.tiles_k * kFp4Tile;
+                const uint8_t* xs = p.xs + (int64_t)(t.t0 >> 7) * p.tiles_k * kFp4Tile;
+                for (int kt = 0; kt < stages; ++kt) {
+                    if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sb = (uint32_t)min((int64_t)S::KA, p.tiles_k - (int64_t)kt * S::KA) * kFp4Tile;
+                    const uint32_t base = sbase + stage * S::BYTES;
+                    mbar_expect_tx(full(stage), S::W + boxes * M_TBOX * M_KB + (1 + atoms) * sb);
+                    tma_load_2d(base, &tW, full(stage), kt * M_KB, t.e * p.N + t.f0);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(base + S::W + b * M_TBOX * M_KB, &tX, full(stage), kt * M_KB, t.t0 + b * M_TBOX);
+                    bulk_load(base + S::W + S::X, ws + (int64_t)kt * S::SW, sb, full(stage));
+                    for (int a = 0; a < atoms; ++a)
+                        bulk_load(base + S::W + S::X + S::SW + a * S::SW, xs + (a * p.tiles_k + (int64_t)kt * S::KA) * kFp4Tile, sb,
+                                  full(stage));
+                    issued |= 1u << stage;
+                    issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == M_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < M_STAGES; ++s)
+                if (issued & (1u << s)) drain(full(s), (issued_par >> s) & 1u, p.status);
+        }
+    } else if (warp == 1) {
+        // ------------------------------- MMA issuer ---------------------------------
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, it = 0, tile = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x, ++tile) {
+                const Tile t = find_tile(p, start, i);
+                const int atoms = ((t.t0 & 127) + t.n + 127) >> 7;
+                const uint32_t b = tile & 1u;
+                if (!mbar_wait(own_free(b), ((tile >> 1) & 1u) ^ 1u, abort_flag, p.status) ||
+                    !mbar_wait(shared_free, (tile & 1u) ^ 1u, abort_flag, p.status))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem + b * 128u;
+                for (int kt = 0; kt < stages; ++kt, ++it) {
+                    // this parity's scale columns: read by the MMAs of two stages ago
+                    if (it >= 2) {
+                        const uint32_t w = it - 2;
+                        if (!mbar_wait(empty(w % M_STAGES), (w / M_STAGES) & 1u, abort_flag, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!mbar_wait(full(stage), phase, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t base = sbase + stage * S::BYTES;
+                    const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
+                    const int ka = (int)min((int64_t)S::KA, p.tiles_k - (int64_t)kt * S::KA);
+#pragma unroll
+                    for (int a = 0; a < S::KA; ++a) {
+                        if (a >= ka) break;
+                        copy_scales(sf + a * 4, base + S::W + S::X + a * kFp4Tile);
+                        copy_scales(sf + S::KA * 4 + a * 8, base + S::W + S::X + S::SW + a * kFp4Tile);
+                        if (atoms > 1) copy_scales(sf + S::KA * 4 + a * 8 + 4, base + S::W + S::X + 2 * S::SW + a * kFp4Tile);
+                    }
+                    const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
+                    const uint32_t tcol = (uint32_t)(t.t0 & 127) >> 5;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= ksteps) break;
+                        const uint64_t ad = smem_desc(base + k * 32, 16, 1024, kSwizzle128B);
+                        const uint64_t bd = smem_desc(base + S::W + k * 32, 16, 1024, kSwizzle128B);
+                        const int a = MX ? k >> 1 : k;
+                        umma_fp4<MX>(d, ad, bd, fp4_idesc<MX>(t.n, MX ? 2u * (k & 1) : 0u), sf + a * 4,
+                                     sf + S::KA * 4 + a * 8 + tcol, (kt > 0 || k > 0) ? 1u : 0u);
+                    }
+                    umma_commit(empty(stage));
+                    if (++stage == M_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(tfull(b));
+            }
+            umma_commit(drain_bar);
+            drain(drain_bar, 0, p.status);
+        }
+    } else {
+        // ------------------------------- epilogue -----------------------------------
+        const int q = warp & 3;
+        const int half = 64 * ((warp - 2) >> 2);   // its 64 columns of each 128
+        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        // rows that belong to no expert: the clamped ranges' gaps are an error, the tail is zero
+        if (p.offsets) {
+            const int live = min(max(p.offsets[p.experts], 0), p.T);
+            const int64_t n = (int64_t)(p.T - live) * p.N;
+            for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x - 64; i < n; i += (int64_t)gridDim.x * 256) {
+                const int64_t at = (live + i / p.N) * p.ldy + i % p.N;
+                if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(0.0f);
+                else static_cast<float*>(p.Y)[at] = 0.0f;
+            }
+        }
+        const float gx = MX ? 1.0f : *p.xg;
+        uint32_t tile = 0;
+        for (int64_t i = blockIdx.x; i < ntiles; i += gridDim.x, ++tile) {
+            const Tile t = find_tile(p, start, i);
+            const uint32_t b = tile & 1u;
+            if (!mbar_wait_warp(tfull(b), (tile >> 1) & 1u, abort_flag, p.status)) break;
+            tc_fence_after();
+            const float g = MX ? 1.0f : gx * p.wg[t.e * p.wg_stride];
+            const int f = t.f0 + 32 * q + lane;
+            // first the columns that the next tile also uses: tokens 128.. of an even tile, 0..127 of
+            // an odd one; all of them into registers, so they are free before anything is stored
+            uint32_t v[2][32];
+#pragma unroll
+            for (int own = 0; own < 2; ++own) {
+                const int c0 = half + ((own != 0) == (b != 0) ? 128 : 0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (c0 + 32 * c < t.n) tmem_ld_32x32b_x32(tmem + lanes + b * 128u + c0 + 32 * c, v[c]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(own ? own_free(b) : shared_free);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, M_TMEM);
+    }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-constexpr int64_t kMaxDim = (1ll << 31) - 256;
+constexpr int64_t kMaxDim = (1ll << 31) - 512;
+
+bool code_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t pitch, int box_rows) {
+    auto enc = tma_encoder();
+    cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {(cuuint32_t)M_KB, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool MX>
+int launch(const CUtensorMap& tw, const CUtensorMap& tx, const MParams& p, int64_t most_tiles, cudaStream_t s) {
+    const int smem = 1024 + M_STAGES * Stage<MX>::BYTES + 8 * (2 * M_STAGES + 6) + 8 + 4 * (p.experts + 1);
+    GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const unsigned grid = (unsigned)std::min<int64_t>(most_tiles, device_sm_count());
+    GPTQ_LAUNCH(K_FP4_MM, s, fp4_matmul_kernel<MX><<<grid, M_THREADS, smem, s>>>(tw, tx, p));
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
 
 }  // namespace
 }  // namespace gptq
@@ -142,39 +447,43 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
         (format != GPTQ_MXFP4 && format != GPTQ_NVFP4) || (flags & ~(GPTQ_DQ_RELU | GPTQ_DQ_BF16_OUT | GPTQ_FP4_EXPERT_G)) ||
         (!offsets && experts != 1))
         return GPTQ_ERR_INVALID_ARG;
-    if (experts > 65536) return GPTQ_ERR_UNSUPPORTED;
+    if (experts > M_MAX_EXPERTS || N > kMaxDim / experts) return GPTQ_ERR_UNSUPPORTED;
     if (T == 0 || N == 0) return GPTQ_OK;
     if (!Y || ldy < N || K < 1 || !x_codes || !x_scales || !w_codes || !w_scales || !aligned16(x_codes) || !aligned16(x_scales) ||
         !aligned16(w_codes) || !aligned16(w_scales) || (format == GPTQ_NVFP4 && (!x_g || !w_g)))
         return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t pitch = fp4_pitch(K);
+    CUtensorMap tw, tx;
+    if (!code_map(&tw, w_codes, experts * N, pitch, M_F) || !code_map(&tx, x_codes, T, pitch, M_TBOX)) return GPTQ_ERR_CUDA;
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
     MParams p{};
-    p.xc = x_codes;
     p.xs = x_scales;
-    p.wc = w_codes;
     p.ws = w_scales;
     p.xg = x_g;
     p.wg = w_g;
-    p.T = T;
-    p.N = N;
-    p.K = K;
-    p.pitch = fp4_pitch(K);
+    p.T = (int)T;
+    p.N = (int)N;
+    p.K = (int)K;
     p.tiles_k = fp4_tiles(K, format);
-    p.w_codes_stride = N * p.pitch;
     p.w_scales_stride = gptq_fp4_scale_bytes(N, K, format);
     p.wg_stride = (flags & GPTQ_FP4_EXPERT_G) ? 1 : 0;
     p.offsets = offsets;
     p.experts = (int)experts;
+    p.ftiles = (int)ceil_div(N, M_F);
     p.relu = (flags & GPTQ_DQ_RELU) ? 1 : 0;
     p.bf16_out = (flags & GPTQ_DQ_BF16_OUT) ? 1 : 0;
     p.Y = Y;
     p.ldy = ldy;
     p.status = st.word;
-    const dim3 grid((unsigned)(ceil_div(T, B_T) + (offsets ? experts : 0)), (unsigned)ceil_div(N, B_N));
-    if (format == GPTQ_MXFP4) GPTQ_LAUNCH(K_FP4_MM, s, fp4_matmul_kernel<true><<<grid, 256, 0, s>>>(p));
-    else GPTQ_LAUNCH(K_FP4_MM, s, fp4_matmul_kernel<false><<<grid, 256, 0, s>>>(p));
-    GPTQ_LAUNCH_CHECK();
-    return st.finish(s);
+    // at most one more token tile per expert than whole tiles, and one more for the first's shift
+    const int64_t most = (ceil_div(T, M_T) + (offsets ? 2 * std::min(experts, T) : 0)) * p.ftiles;
+    const int rc = format == GPTQ_MXFP4 ? launch<true>(tw, tx, p, most, s) : launch<false>(tw, tx, p, most, s);
+    return rc != GPTQ_OK ? rc : st.finish(s);
 }
+
+namespace gptq {
+// this file's copy of the pipeline-wait limit (the library's test hook sets every copy)
+cudaError_t fp4_set_wait_limit(unsigned long long ns) { return set_pipeline_wait_limit_this_unit(ns); }
+}  // namespace gptq

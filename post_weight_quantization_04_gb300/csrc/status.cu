@@ -136,5 +136,6 @@ extern "C" int gptq_test_set_wait_limit_ns(unsigned long long ns) {
     GPTQ_CUDA_TRY(hessian_set_wait_limit(ns));
     GPTQ_CUDA_TRY(tc_gemm_set_wait_limit(ns));
     GPTQ_CUDA_TRY(dequant_set_wait_limit(ns));
+    GPTQ_CUDA_TRY(fp4_set_wait_limit(ns));
     return GPTQ_OK;
 }

@@ -97,7 +97,7 @@ def test_dequantize_refusals(clib, change, status):
 
 @pytest.mark.parametrize("change,status", [
     (dict(T=-1), 1), (dict(K=0), 1), (dict(N=0), 0), (dict(T=0), 0), (dict(fmt=2), 1), (dict(experts=0), 1),
-    (dict(experts=2), 1), (dict(offsets=P, experts=65537), 2), (dict(flags=8), 1), (dict(ldy=31), 1), (dict(Y=Z), 1),
+    (dict(experts=2), 1), (dict(offsets=P, experts=1025), 2), (dict(flags=8), 1), (dict(ldy=31), 1), (dict(Y=Z), 1),
     (dict(xc=ODD), 1), (dict(ws=ODD), 1), (dict(fmt=1, xg=Z), 1), (dict(fmt=1, wg=Z), 1), (dict(wc=Z), 1)])
 def test_matmul_refusals(clib, change, status):
     a = dict(xc=P, xs=P, xg=P, T=4, wc=P, ws=P, wg=P, N=32, K=64, fmt=0, offsets=Z, experts=1, flags=0, Y=P, ldy=32) | change
