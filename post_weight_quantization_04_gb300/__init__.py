@@ -455,9 +455,10 @@ class Fp4(NamedTuple):
 
 
 def _fp4_format(format: str) -> int:
-    if format not in _FP4:
+    f = _FP4.get(format)
+    if f is None:
         raise ValueError(f"format must be 'mx' or 'nv', got {format!r}")
-    return _FP4[format]
+    return f
 
 
 def gptq_fp4_code_pitch(cols: int) -> int:
@@ -472,43 +473,73 @@ def gptq_fp4_scale_bytes(rows: int, cols: int, format: str) -> int:
     return int(load().gptq_fp4_scale_bytes(rows, cols, _fp4_format(format)))
 
 
-def _rows_of(t: torch.Tensor, name: str) -> int:
-    """The dtype code of a matrix whose rows are contiguous (any row stride)."""
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+# The calls of a serving step are short, so their argument checks are kept to a few attribute reads:
+# a matrix is described once, addresses go to ctypes as plain integers, and the current stream is
+# read without a Stream object.
+_DTYPES = {torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _raw_stream(stream) -> int:
+    return _current_raw_stream(_current_device()) if stream is None else stream.cuda_stream
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
+    """(dtype code, rows, columns, row stride) of a matrix whose rows are contiguous."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA bf16 or fp32 tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} rows must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        ld = max(cols, 1)
+    elif ld < cols:
         raise ValueError(f"{name} rows must not overlap")
-    return GPTQ_BF16 if t.dtype == torch.bfloat16 else GPTQ_F32
+    return dt, rows, cols, ld
 
 
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _matrix_like(t: torch.Tensor, name: str, dtype, rows: int, cols: int) -> int:
+    """The row stride of a matrix that has to have this type and shape."""
+    _, r, c, ld = _matrix(t, name)
+    if r != rows or c != cols or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {(rows, cols)}, got {t.dtype} {tuple(t.shape)}")
+    return ld
 
 
-def _check_fp4(q: Fp4, name: str, dims: int) -> int:
-    f = _fp4_format(q.format)
-    lead = tuple(q.codes.shape[:-2])
-    if q.codes.dim() != dims:
-        raise ValueError(f"{name}.codes must have {dims} dimensions")
-    _dev(q.codes, torch.uint8, name + ".codes", (*lead, q.rows, gptq_fp4_code_pitch(q.cols)))
-    _dev(q.scales, torch.uint8, name + ".scales", (*lead, *_fp4_scale_shape(q.rows, q.cols, q.format)))
+def _check_fp4(q: Fp4, name: str, experts: Optional[int] = None) -> int:
+    """The format code of a stored matrix whose buffers fit its columns (experts: one per expert)."""
+    codes, scales, cols, format, g = q
+    f = _fp4_format(format)
+    tiles = _fp4_scale_shape(codes.shape[-2], cols, format)
+    lead = () if experts is None else (experts,)
+    if codes.shape != (*lead, codes.shape[-2], (cols + 31) // 32 * 16) or scales.shape != (*lead, *tiles):
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not those of "
+                         f"{'one matrix' if experts is None else f'{experts} matrices'} of {cols} columns in format {format!r}")
+    if not (codes.is_cuda and scales.is_cuda and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
+            and codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous CUDA uint8 tensors")
     if f == NVFP4:
-        if q.tensor_scale is None:
+        if g is None:
             raise ValueError(f"{name}: format 'nv' needs a tensor scale")
-        _dev(q.tensor_scale, torch.float32, name + ".tensor_scale")
-        if q.tensor_scale.numel() not in (1, lead[0] if lead else 1):
+        _dev(g, torch.float32, name + ".tensor_scale")
+        if g.numel() not in (1, experts):
             raise ValueError(f"{name}.tensor_scale must hold one number, or one per expert")
     return f
 
 
 def gptq_fp4_tensor_scale(X: torch.Tensor, stream=None) -> torch.Tensor:
     """The "nv" tensor scale of X: the least power of two for which no block scale saturates."""
-    dt = _rows_of(X, "X")
+    dt, rows, cols, ld = _matrix(X, "X")
     g = torch.empty(1, dtype=torch.float32, device=X.device)
-    _check("gptq_fp4_tensor_scale", load().gptq_fp4_tensor_scale(_ptr(X), dt, X.shape[0], X.shape[1], _ld(X), _ptr(g),
-                                                                 _stream(stream)))
+    _check("gptq_fp4_tensor_scale", load().gptq_fp4_tensor_scale(X.data_ptr(), dt, rows, cols, ld, g.data_ptr(),
+                                                                 _raw_stream(stream)))
     return g
 
 
@@ -518,8 +549,8 @@ def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optiona
     """X (bf16 or fp32, any row stride) in the microscaled 4-bit form. index (int32): row r is X row
     index[r] // per, zeros where index[r] < 0 (a Route's src with per = top gathers the experts' rows
     in the same pass). "nv" without a tensor scale takes gptq_fp4_tensor_scale(X)."""
-    f, dt = _fp4_format(format), _rows_of(X, "X")
-    n, cols = X.shape
+    f = _fp4_format(format)
+    dt, n, cols, ld = _matrix(X, "X")
     rows = n
     if index is not None:
         _dev(index, torch.int32, "index")
@@ -527,35 +558,38 @@ def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optiona
     if f == NVFP4:
         if tensor_scale is None:
             tensor_scale = gptq_fp4_tensor_scale(X, stream)
-        _dev(tensor_scale, torch.float32, "tensor_scale", (1,))
+        _dev(tensor_scale, torch.float32, "tensor_scale")
+        if tensor_scale.numel() != 1:
+            raise ValueError("tensor_scale must hold one number")
     else:
         tensor_scale = None
     if out is None:
-        out = Fp4(torch.empty(rows, gptq_fp4_code_pitch(cols), dtype=torch.uint8, device=X.device),
-                  torch.empty(_fp4_scale_shape(rows, cols, format), dtype=torch.uint8, device=X.device), cols, format,
-                  tensor_scale)
+        dev = X.device
+        out = Fp4(torch.empty((rows, (cols + 31) // 32 * 16), dtype=torch.uint8, device=dev),
+                  torch.empty(_fp4_scale_shape(rows, cols, format), dtype=torch.uint8, device=dev), cols, format, tensor_scale)
     else:
-        if out.cols != cols or out.format != format or out.codes.shape[-2] != rows:
+        if out.cols != cols or out.format != format or out.rows != rows:
             raise ValueError("out has another shape or format")
         out = out._replace(tensor_scale=tensor_scale)
-        _check_fp4(out, "out", 2)
+        _check_fp4(out, "out")
     _check("gptq_fp4_quantize", load().gptq_fp4_quantize(
-        _ptr(X), dt, n, cols, _ld(X), _ptr(index), per, rows, f, _ptr(tensor_scale), _ptr(out.codes), _ptr(out.scales),
-        _stream(stream)))
+        X.data_ptr(), dt, n, cols, ld, _addr(index), per, rows, f, _addr(tensor_scale), out.codes.data_ptr(),
+        out.scales.data_ptr(), _raw_stream(stream)))
     return out
 
 
 def gptq_fp4_dequantize(q: Fp4, dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values that q's codes and scales stand for."""
-    f = _check_fp4(q, "q", 2)
-    if dtype not in (torch.float32, torch.bfloat16):
+    f = _check_fp4(q, "q")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise ValueError("dtype must be float32 or bfloat16")
-    Y = out if out is not None else torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
-    dt = _rows_of(Y, "out")
-    if Y.dtype != dtype or tuple(Y.shape) != (q.rows, q.cols):
-        raise ValueError(f"out must be {dtype} of shape {(q.rows, q.cols)}")
+    rows, cols = q.rows, q.cols
+    Y = out if out is not None else torch.empty((rows, cols), dtype=dtype, device=q.codes.device)
+    ld = cols if out is None else _matrix_like(Y, "out", dtype, rows, cols)
     _check("gptq_fp4_dequantize", load().gptq_fp4_dequantize(
-        _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale), q.rows, q.cols, f, _ptr(Y), dt, _ld(Y), _stream(stream)))
+        q.codes.data_ptr(), q.scales.data_ptr(), _addr(q.tensor_scale), rows, cols, f, Y.data_ptr(), dt, ld,
+        _raw_stream(stream)))
     return Y
 
 
@@ -565,8 +599,8 @@ def gptq_fp4_tile_scales(scales: torch.Tensor, cols: int, format: str, stream=No
     rows = scales.shape[0]
     _dev(scales, torch.uint8, "scales", (rows, -(-cols // (32 if f == MXFP4 else 16))))
     out = torch.empty(_fp4_scale_shape(rows, cols, format), dtype=torch.uint8, device=scales.device)
-    _check("gptq_fp4_tile_scales", load().gptq_fp4_tile_scales(_ptr(scales), rows, cols, scales.shape[1], f, _ptr(out),
-                                                               _stream(stream)))
+    _check("gptq_fp4_tile_scales", load().gptq_fp4_tile_scales(scales.data_ptr(), rows, cols, scales.shape[1], f,
+                                                               out.data_ptr(), _raw_stream(stream)))
     return out
 
 
@@ -575,28 +609,27 @@ def gptq_fp4_matmul(X: Fp4, W: Fp4, offsets: Optional[torch.Tensor] = None, relu
     """Y = X W^T (optionally max(., 0)) of two matrices in the microscaled 4-bit form. With offsets
     (int32, experts + 1, a Route's) W holds one weight per expert and rows offsets[e]..offsets[e+1]
     of X use weight e; rows in no expert's range give zeros."""
-    f = _check_fp4(X, "X", 2)
-    _check_fp4(W, "W", 2 if offsets is None else 3)
+    f = _check_fp4(X, "X")
+    experts = 1
+    if offsets is None:
+        _check_fp4(W, "W")
+    else:
+        experts = W.codes.shape[0]
+        _check_fp4(W, "W", experts)
+        _dev(offsets, torch.int32, "offsets", (experts + 1,))
     if X.format != W.format or X.cols != W.cols:
         raise ValueError("X and W must have the same format and columns")
-    experts = 1 if offsets is None else W.codes.shape[0]
-    if offsets is not None:
-        _dev(offsets, torch.int32, "offsets", (experts + 1,))
-    if out_dtype not in (torch.float32, torch.bfloat16):
+    if out_dtype not in _DTYPES:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    T, N = X.rows, W.rows
-    Y = out if out is not None else torch.empty(T, N, dtype=out_dtype, device=X.codes.device)
-    _rows_of(Y, "out")
-    if Y.dtype != out_dtype or tuple(Y.shape) != (T, N):
-        raise ValueError(f"out must be {out_dtype} of shape {(T, N)}")
-    if X.tensor_scale is not None and X.tensor_scale.numel() != 1:
-        raise ValueError("X.tensor_scale must hold one number")
-    flags = (DQ_RELU if relu else 0) | (DQ_BF16_OUT if out_dtype == torch.bfloat16 else 0)
+    T, N = X.codes.shape[0], W.codes.shape[-2]
+    Y = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=X.codes.device)
+    ld = N if out is None else _matrix_like(Y, "out", out_dtype, T, N)
+    flags = (DQ_RELU if relu else 0) | (DQ_BF16_OUT if out_dtype is torch.bfloat16 else 0)
     if f == NVFP4 and experts > 1 and W.tensor_scale.numel() == experts:
         flags |= FP4_EXPERT_G
     _check("gptq_fp4_matmul", load().gptq_fp4_matmul(
-        _ptr(X.codes), _ptr(X.scales), _ptr(X.tensor_scale), T, _ptr(W.codes), _ptr(W.scales), _ptr(W.tensor_scale), N,
-        X.cols, f, _ptr(offsets), experts, flags, _ptr(Y), _ld(Y), _stream(stream)))
+        X.codes.data_ptr(), X.scales.data_ptr(), _addr(X.tensor_scale), T, W.codes.data_ptr(), W.scales.data_ptr(),
+        _addr(W.tensor_scale), N, X.cols, f, _addr(offsets), experts, flags, Y.data_ptr(), ld, _raw_stream(stream)))
     return Y
 
 
@@ -621,46 +654,44 @@ def gptq_expert_sort_workspace_bytes(tokens: int, top: int, experts: int) -> int
 def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor] = None, stream=None) -> Route:
     """ids (tokens, top) int32, each slot's expert (negative: dropped) -> the slots' places, stably
     sorted by expert."""
+    _dev(ids, torch.int32, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, top)")
-    _dev(ids, torch.int32, "ids")
     tokens, top = ids.shape
-    route = Route(torch.empty(experts + 1, dtype=torch.int32, device=ids.device),
-                  torch.empty(tokens * top, dtype=torch.int32, device=ids.device), torch.empty_like(ids))
-    if ws is None:
-        nb = gptq_expert_sort_workspace_bytes(tokens, top, experts)
-        ws = torch.empty(nb, dtype=torch.uint8, device=ids.device) if nb else None
-    _check("gptq_expert_sort", load().gptq_expert_sort(
-        _ptr(ids), tokens, top, experts, _ptr(route.offsets), _ptr(route.src), _ptr(route.pos), _ptr(ws),
-        ws.numel() if ws is not None else 0, _stream(stream)))
+    dev = ids.device
+    route = Route(torch.empty(experts + 1, dtype=torch.int32, device=dev),
+                  torch.empty(tokens * top, dtype=torch.int32, device=dev), torch.empty_like(ids))
+    lib = load()
+    nb = ws.numel() if ws is not None else int(lib.gptq_expert_sort_workspace_bytes(tokens, top, experts))
+    if ws is None and nb:
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _check("gptq_expert_sort", lib.gptq_expert_sort(
+        ids.data_ptr(), tokens, top, experts, route.offsets.data_ptr(), route.src.data_ptr(), route.pos.data_ptr(),
+        _addr(ws), nb, _raw_stream(stream)))
     return route
 
 
 def _check_route(route: Route) -> Tuple[int, int]:
-    tokens, top = route.pos.shape
-    _dev(route.pos, torch.int32, "route.pos")
-    _dev(route.src, torch.int32, "route.src", (tokens * top,))
-    _dev(route.offsets, torch.int32, "route.offsets")
+    offsets, src, pos = route
+    tokens, top = pos.shape
+    if (pos.dtype is not torch.int32 or src.dtype is not torch.int32 or offsets.dtype is not torch.int32 or not pos.is_cuda
+            or not src.is_cuda or not offsets.is_cuda or not pos.is_contiguous() or not src.is_contiguous()
+            or not offsets.is_contiguous() or src.shape != (tokens * top,) or offsets.dim() != 1):
+        raise ValueError("route must hold contiguous CUDA int32 tensors: offsets (experts + 1), src (tokens * top), pos (tokens, top)")
     return tokens, top
-
-
-def _like(t: torch.Tensor, name: str, dtype, shape) -> int:
-    dt = _rows_of(t, name)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return dt
 
 
 def gptq_expert_gather(X: torch.Tensor, route: Route, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The tokens' rows in the order of their experts (tokens * top rows, zeros past the live ones)."""
     tokens, top = _check_route(route)
-    d = X.shape[1]
-    dt = _like(X, "X", X.dtype, (tokens, d))
-    Xs = out if out is not None else torch.empty(tokens * top, d, dtype=X.dtype, device=X.device)
-    _like(Xs, "out", X.dtype, (tokens * top, d))
+    dt, rows, d, ld = _matrix(X, "X")
+    if rows != tokens:
+        raise ValueError(f"X has {rows} rows for {tokens} tokens")
+    Xs = out if out is not None else torch.empty((tokens * top, d), dtype=X.dtype, device=X.device)
+    lds = d if out is None else _matrix_like(Xs, "out", X.dtype, tokens * top, d)
     _check("gptq_expert_gather", load().gptq_expert_gather(
-        _ptr(X), dt, tokens, d, _ld(X), _ptr(route.pos), top, _ptr(route.offsets), route.experts, _ptr(Xs), _ld(Xs),
-        _stream(stream)))
+        X.data_ptr(), dt, tokens, d, ld, route.pos.data_ptr(), top, route.offsets.data_ptr(), route.experts, Xs.data_ptr(),
+        lds, _raw_stream(stream)))
     return Xs
 
 
@@ -668,14 +699,15 @@ def gptq_expert_combine(Ys: torch.Tensor, route: Route, weights: Optional[torch.
                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t][j] * the row of slot (t, j), in fp32, rounded once; weights None: 1."""
     tokens, top = _check_route(route)
-    d = Ys.shape[1]
-    dt = _like(Ys, "Ys", Ys.dtype, (tokens * top, d))
+    dt, rows, d, ld = _matrix(Ys, "Ys")
+    if rows != tokens * top:
+        raise ValueError(f"Ys has {rows} rows for {tokens} x {top} slots")
     if weights is not None:
         _dev(weights, torch.float32, "weights", (tokens, top))
-    Y = out if out is not None else torch.empty(tokens, d, dtype=Ys.dtype, device=Ys.device)
-    _like(Y, "out", Ys.dtype, (tokens, d))
+    Y = out if out is not None else torch.empty((tokens, d), dtype=Ys.dtype, device=Ys.device)
+    ldy = d if out is None else _matrix_like(Y, "out", Ys.dtype, tokens, d)
     _check("gptq_expert_combine", load().gptq_expert_combine(
-        _ptr(Ys), dt, tokens, d, _ld(Ys), _ptr(route.pos), top, _ptr(weights), _ptr(Y), _ld(Y), _stream(stream)))
+        Ys.data_ptr(), dt, tokens, d, ld, route.pos.data_ptr(), top, _addr(weights), Y.data_ptr(), ldy, _raw_stream(stream)))
     return Y
 
 
@@ -690,17 +722,18 @@ def gptq_expert_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, route: Route, w
                              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The gradients of gptq_expert_combine: (dYs, dweights)."""
     tokens, top = _check_route(route)
-    d = Ys.shape[1]
-    dt = _like(Ys, "Ys", Ys.dtype, (tokens * top, d))
-    _like(dY, "dY", Ys.dtype, (tokens, d))
+    dt, rows, d, ld = _matrix(Ys, "Ys")
+    if rows != tokens * top:
+        raise ValueError(f"Ys has {rows} rows for {tokens} x {top} slots")
+    lddy = _matrix_like(dY, "dY", Ys.dtype, tokens, d)
     _dev(weights, torch.float32, "weights", (tokens, top))
-    dYs, dW = out if out is not None else (torch.empty(tokens * top, d, dtype=Ys.dtype, device=Ys.device),
-                                           torch.empty_like(weights))
-    _like(dYs, "out[0]", Ys.dtype, (tokens * top, d))
-    _dev(dW, torch.float32, "out[1]", (tokens, top))
+    dYs, dW = out if out is not None else (torch.empty((rows, d), dtype=Ys.dtype, device=Ys.device), torch.empty_like(weights))
+    lds = d if out is None else _matrix_like(dYs, "out[0]", Ys.dtype, rows, d)
+    if out is not None:
+        _dev(dW, torch.float32, "out[1]", (tokens, top))
     _check("gptq_expert_combine_grad", load().gptq_expert_combine_grad(
-        _ptr(dY), _ld(dY), _ptr(Ys), _ld(Ys), dt, tokens, d, _ptr(route.pos), top, _ptr(route.offsets), route.experts,
-        _ptr(weights), _ptr(dYs), _ld(dYs), _ptr(dW), _stream(stream)))
+        dY.data_ptr(), lddy, Ys.data_ptr(), ld, dt, tokens, d, route.pos.data_ptr(), top, route.offsets.data_ptr(),
+        route.experts, weights.data_ptr(), dYs.data_ptr(), lds, dW.data_ptr(), _raw_stream(stream)))
     return dYs, dW
 
 
