@@ -94,10 +94,10 @@ struct Tile {
 };
 
 // tile index -> tile; start[e] = token tiles before expert e
-__device__ __forceinline__ Tile find_tile(const MParams& p, const int32_t* start, int64_t i) {
+__device__ __forceinline__ Tile find_tile(const MParams& p, const int32_t* start, uint32_t i) {
     Tile t;
-    const int tt = (int)(i / p.ftiles);
-    t.f0 = (int)(i % p.ftiles) * M_F;
+    const int tt = (int)(i / (uint32_t)p.ftiles);
+    t.f0 = (int)(i % (uint32_t)p.ftiles) * M_F;
     int a = 0, b = p.experts;   // start[a] <= tt < start[b]
     while (b - a > 1) {
         const int m = (a + b) >> 1;
@@ -122,6 +122,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// One lane of a converged warp: unlike a test of the lane number, the branch on it leaves the values
+// it uses warp-uniform, so the tensor instructions take their operands from uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// the bounded wait by a whole converged warp
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // 32 rows x 16 bytes of shared memory to four TMEM columns, in each quarter of the lanes
@@ -255,7 +269,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int64_t ntiles = (int64_t)start[p.experts] * p.ftiles;
+    const uint32_t ntiles = (uint32_t)start[p.experts] * (uint32_t)p.ftiles;
 
     if (warp == 0) {
         // ------------------------------- producer -----------------------------------
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_par = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+            for (uint32_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
                 const Tile t = find_tile(p, start, i);
                 const int boxes = (t.n + M_TBOX - 1) / M_TBOX;
                 const int atoms = ((t.t0 & 127) + t.n + 127) >> 7;   // 128-row scale tiles of the tokens
@@ -297,66 +311,72 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         }
     } else if (warp == 1) {
         // ------------------------------- MMA issuer ---------------------------------
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, it = 0, tile = 0;
-            bool ok = true;
-            for (int64_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x, ++tile) {
-                const Tile t = find_tile(p, start, i);
-                const int atoms = ((t.t0 & 127) + t.n + 127) >> 7;
-                const uint32_t b = tile & 1u;
-                if (!mbar_wait(own_free(b), ((tile >> 1) & 1u) ^ 1u, abort_flag, p.status) ||
-                    !mbar_wait(shared_free, (tile & 1u) ^ 1u, abort_flag, p.status))
-                    break;
-                tc_fence_after();
-                const uint32_t d = tmem + b * 128u;
-                for (int kt = 0; kt < stages; ++kt, ++it) {
-                    // this parity's scale columns: read by the MMAs of two stages ago
-                    if (it >= 2) {
-                        const uint32_t w = it - 2;
-                        if (!mbar_wait(empty(w % M_STAGES), (w / M_STAGES) & 1u, abort_flag, p.status)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    if (!mbar_wait(full(stage), phase, abort_flag, p.status)) {
+        const bool leader = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, it = 0, tile = 0;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x, ++tile) {
+            const Tile t = find_tile(p, start, i);
+            const bool two = (t.t0 & 127) + t.n > 128;   // the tokens' scales are in two row blocks
+            const uint32_t b = tile & 1u;
+            if (!wait_all(own_free(b), ((tile >> 1) & 1u) ^ 1u, abort_flag, p.status) ||
+                !wait_all(shared_free, (tile & 1u) ^ 1u, abort_flag, p.status))
+                break;
+            tc_fence_after();
+            const uint32_t d = tmem + b * 128u;
+            const uint32_t tcol = (uint32_t)(t.t0 & 127) >> 5;
+            const uint32_t idesc = fp4_idesc<MX>(t.n, 0), idesc2 = fp4_idesc<MX>(t.n, 2);
+            for (int kt = 0; kt < stages; ++kt, ++it) {
+                // this parity's scale columns: read by the MMAs of two stages ago
+                if (it >= 2) {
+                    const uint32_t w = it - 2;
+                    if (!wait_all(empty(w % M_STAGES), (w / M_STAGES) & 1u, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t base = sbase + stage * S::BYTES;
-                    const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
-                    const int ka = (int)min((int64_t)S::KA, p.tiles_k - (int64_t)kt * S::KA);
+                }
+                if (!wait_all(full(stage), phase, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = sbase + stage * S::BYTES;
+                const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
+                const int ka = min(S::KA, (int)p.tiles_k - kt * S::KA);
+                const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
+                if (leader) {
 #pragma unroll
                     for (int a = 0; a < S::KA; ++a) {
-                        if (a >= ka) break;
-                        copy_scales(sf + a * 4, base + S::W + S::X + a * kFp4Tile);
-                        copy_scales(sf + S::KA * 4 + a * 8, base + S::W + S::X + S::SW + a * kFp4Tile);
-                        if (atoms > 1) copy_scales(sf + S::KA * 4 + a * 8 + 4, base + S::W + S::X + 2 * S::SW + a * kFp4Tile);
+                        if (a < ka) {
+                            copy_scales(sf + a * 4, base + S::W + S::X + a * kFp4Tile);
+                            copy_scales(sf + S::KA * 4 + a * 8, base + S::W + S::X + S::SW + a * kFp4Tile);
+                            if (two) copy_scales(sf + S::KA * 4 + a * 8 + 4, base + S::W + S::X + 2 * S::SW + a * kFp4Tile);
+                        }
                     }
-                    const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
-                    const uint32_t tcol = (uint32_t)(t.t0 & 127) >> 5;
+                    const uint64_t ad = smem_desc(base, 16, 1024, kSwizzle128B), bd = smem_desc(base + S::W, 16, 1024, kSwizzle128B);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (k >= ksteps) break;
-                        const uint64_t ad = smem_desc(base + k * 32, 16, 1024, kSwizzle128B);
-                        const uint64_t bd = smem_desc(base + S::W + k * 32, 16, 1024, kSwizzle128B);
-                        const int a = MX ? k >> 1 : k;
-                        umma_fp4<MX>(d, ad, bd, fp4_idesc<MX>(t.n, MX ? 2u * (k & 1) : 0u), sf + a * 4,
-                                     sf + S::KA * 4 + a * 8 + tcol, (kt > 0 || k > 0) ? 1u : 0u);
+                        if (k < ksteps) {
+                            const int a = MX ? k >> 1 : k;
+                            umma_fp4<MX>(d, ad + 2 * k, bd + 2 * k, MX && (k & 1) ? idesc2 : idesc, sf + a * 4,
+                                         sf + S::KA * 4 + a * 8 + tcol, (kt > 0 || k > 0) ? 1u : 0u);
+                        }
                     }
                     umma_commit(empty(stage));
-                    if (++stage == M_STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    if (kt == stages - 1) umma_commit(tfull(b));
                 }
-                if (!ok) break;
-                umma_commit(tfull(b));
+                __syncwarp();
+                if (++stage == M_STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
+        }
+        if (leader) {
             umma_commit(drain_bar);
             drain(drain_bar, 0, p.status);
         }
+        __syncwarp();
     } else {
         // ------------------------------- epilogue -----------------------------------
         const int q = warp & 3;
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         }
         const float gx = MX ? 1.0f : *p.xg;
         uint32_t tile = 0;
-        for (int64_t i = blockIdx.x; i < ntiles; i += gridDim.x, ++tile) {
+        for (uint32_t i = blockIdx.x; i < ntiles; i += gridDim.x, ++tile) {
             const Tile t = find_tile(p, start, i);
             const uint32_t b = tile & 1u;
             if (!mbar_wait_warp(tfull(b), (tile >> 1) & 1u, abort_flag, p.status)) break;
@@ -448,6 +468,8 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
         (!offsets && experts != 1))
         return GPTQ_ERR_INVALID_ARG;
     if (experts > M_MAX_EXPERTS || N > kMaxDim / experts) return GPTQ_ERR_UNSUPPORTED;
+    // tile numbers have 31 bits (a Y beyond that is larger than the device)
+    if ((ceil_div(T, M_T) + 2 * experts) * ceil_div(N, M_F) > kMaxDim) return GPTQ_ERR_UNSUPPORTED;
     if (T == 0 || N == 0) return GPTQ_OK;
     if (!Y || ldy < N || K < 1 || !x_codes || !x_scales || !w_codes || !w_scales || !aligned16(x_codes) || !aligned16(x_scales) ||
         !aligned16(w_codes) || !aligned16(w_scales) || (format == GPTQ_NVFP4 && (!x_g || !w_g)))
