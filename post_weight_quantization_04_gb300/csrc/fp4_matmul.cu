@@ -3,21 +3,25 @@
 //   Y[t][o] = act(gx gw sum_b sx[t][b] sw[e(t)][o][b] sum_{k in b} x[t][k] w[e(t)][o][k])
 //
 // The tensor core multiplies this form itself (tcgen05.mma kind::mxf4 / kind::mxf4nvf4 with block
-// scales, 64 columns per instruction, fp32 sums in TMEM). The weights are the M operand (128
-// features per tile) and the tokens the N operand, whose width is chosen per tile: an expert with
-// few rows pays for few.
+// scales, 64 columns per instruction, fp32 sums in TMEM). The weights are the M operand and the
+// tokens the N operand, whose width is chosen per tile: an expert with few rows pays for few.
 //
-// Roles (one persistent CTA per SM):
-//   warp 0       producer: per stage of 256 columns the 128 x 128-byte box of weight codes and the
-//                64-row boxes of token codes by TMA (128-byte swizzle), the scale tiles by bulk copies
-//   warp 1       one thread: scale tiles shared memory -> TMEM (tcgen05.cp), then the stage's MMAs
+// Two CTAs on neighbouring SMs (a cluster) work on one tile of 256 features x up to 256 tokens with
+// cta_group::2 MMAs: each holds its own 128 features, half of the tokens and all the tile's scales,
+// so a stage brings 32 KB of codes into each SM where a 128 x 256 tile of its own would take 48 (the
+// kernel was bound by those loads). Roles in each CTA (persistent, one per SM):
+//   warp 0       producer: per stage of 256 columns four TMA copies, the 128 x 128-byte box of weight
+//                codes, that of token codes (128-byte swizzle), and the scale tiles of both
+//   warp 1       in the even CTA: scale tiles shared memory -> TMEM (tcgen05.cp, both CTAs) and the
+//                MMAs; in the odd CTA: tells the even one which stages have landed
 //   warps 2..9   epilogue: TMEM -> registers -> Y; a lane holds one feature, a register one token
 //
 // TMEM: the sums of a 128 x 256 tile take 256 columns, so two whole buffers would leave none for
 // scales. Even tiles use columns [0, 256), odd tiles [128, 384): only [128, 256) is shared, it is
 // drained first (all of it into registers, then released), and the next tile's MMAs start while
 // the rest is still being stored. Columns 384.. hold two stages' scales in turn.
-// Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind).
+// Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits
+// for its own copies, the even one for the MMAs, and both meet before either leaves).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -30,11 +34,11 @@ namespace gptq {
 
 namespace {
 
-constexpr int M_F = 128;                 // features per tile
+constexpr int M_F = 128;                 // features per CTA
+constexpr int M_PF = 2 * M_F;            // features per tile
 constexpr int M_T = 256;                 // most tokens per tile
 constexpr int M_KB = 128;                // bytes of codes per row and stage (256 columns)
-constexpr int M_TBOX = 64;               // tokens per TMA box
-constexpr int M_STAGES = 4;
+constexpr int M_TBOX = 32;               // tokens per TMA box where a CTA's half of a tile has at most this
 constexpr int M_THREADS = 32 * 10;
 constexpr uint32_t M_TMEM = 512, M_SF0 = 384;
 constexpr int M_MAX_EXPERTS = 1024;
@@ -42,18 +46,23 @@ constexpr int M_MAX_EXPERTS = 1024;
 template <bool MX>
 struct Stage {
     static constexpr int KA = MX ? 2 : 4;              // scale tiles along a stage's columns
-    static constexpr int W = M_F * M_KB, X = M_T * M_KB;
+    static constexpr int W = M_F * M_KB, X = M_T / 2 * M_KB;
     static constexpr int SW = KA * kFp4Tile, SX = 2 * KA * kFp4Tile;
     static constexpr int BYTES = W + X + SW + SX;      // a multiple of 1024
     static constexpr uint32_t SF_COLS = KA * 12;       // TMEM columns of one stage's scales
+    static constexpr int N = MX ? 6 : 5;               // stages: what fits in 227 KB
+};
+
+struct Maps {
+    CUtensorMap w, x, xsmall;   // codes: 128-row boxes, and one of M_TBOX rows for narrow tiles
+    CUtensorMap ws, xs;         // scales: tile bytes x tiles along the columns x row blocks
 };
 
 struct MParams {
-    const uint8_t *xs, *ws;
     const float *xg, *wg;
     int T, N, K;
-    int64_t tiles_k;
-    int64_t w_scales_stride;   // bytes from one expert to the next
+    int tiles_k;
+    int row_blocks;            // 128-row blocks of one expert's weights
     int wg_stride;
     const int32_t* offsets;    // null: one expert, all rows
     int experts;
@@ -97,7 +106,7 @@ struct Tile {
 __device__ __forceinline__ Tile find_tile(const MParams& p, const int32_t* start, uint32_t i) {
     Tile t;
     const int tt = (int)(i / (uint32_t)p.ftiles);
-    t.f0 = (int)(i % (uint32_t)p.ftiles) * M_F;
+    t.f0 = (int)(i % (uint32_t)p.ftiles) * M_PF;
     int a = 0, b = p.experts;   // start[a] <= tt < start[b]
     while (b - a > 1) {
         const int m = (a + b) >> 1;
@@ -118,11 +127,15 @@ __device__ __forceinline__ Tile find_tile(const MParams& p, const int32_t* start
     return t;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // One lane of a converged warp: unlike a test of the lane number, the branch on it leaves the values
 // it uses warp-uniform, so the tensor instructions take their operands from uniform registers.
@@ -132,15 +145,60 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// the bounded wait by a whole converged warp
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+// The bounded wait, polling some times before mbar_wait takes over: that one begins by reading the
+// time and its limit from memory, which takes longer than most waits here last (with it alone the
+// 16384 x 4096 x 14336 MX product took 568 us, WAITTIME with the polls first).
+constexpr int M_POLLS = 20;
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    for (int i = 0; i < M_POLLS; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, abort_flag, status);
 }
 
-// 32 rows x 16 bytes of shared memory to four TMEM columns, in each quarter of the lanes
+// The same by a whole converged warp, one lane polling: each lane's try_wait is an operation of its own
+// on the barrier's word, and 32 of them at a time slow the copies that count on it down.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    bool ok = true;
+    if (elect_one()) ok = wait_one(bar, parity, abort_flag, status);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// ------------------------------------ the pair of CTAs ------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// the even CTA's copy of a shared-memory address
+__device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+
+// What these arrivals order is TMEM and copies by TMA, neither written by this thread, so the default
+// (CTA) scope of the release is enough; .release.cluster would wait for the thread's own earlier
+// stores of Y to be acknowledged (measured: WHAT).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// arrive once on `bar` of both CTAs when the MMAs and scale copies issued before have completed
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// 32 rows x 16 bytes of each CTA's shared memory to four of its TMEM columns, in each quarter of the lanes
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(smem_desc(saddr, 0, 128, 0)) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(smem_desc(saddr, 0, 128, 0)) : "memory");
 }
 
 template <bool MX>
@@ -150,14 +208,14 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
             : "memory");
     else
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
             : "memory");
 }
@@ -168,7 +226,7 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
 template <bool MX>
 __device__ __forceinline__ uint32_t fp4_idesc(int n, uint32_t sf) {
     return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((MX ? 1u : 0u) << 23) |
-           ((uint32_t)(M_F >> 4) << 24) | (sf << 29);
+           ((uint32_t)(M_PF >> 4) << 24) | (sf << 29);
 }
 
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int* status) {
@@ -205,44 +263,50 @@ __device__ __forceinline__ void store_tokens(const MParams& p, const uint32_t (&
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_constant__ CUtensorMap tW,
-                                                                 const __grid_constant__ CUtensorMap tX, const MParams p) {
+__global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_constant__ Maps m, const MParams p) {
     using S = Stage<MX>;
+    constexpr int NS = S::N;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M_STAGES * S::BYTES);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * M_STAGES + 6);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NS * S::BYTES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 6);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* start = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [experts + 1]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // what steers a warp is made warp-uniform by a shuffle, so the branches and the operands of the
+    // tensor instructions stay in uniform registers
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t rank = uniform(cluster_rank());
     const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
-    auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (M_STAGES + s); };
-    auto tfull = [&](int b) { return bar0 + 8u * (2 * M_STAGES + b); };          // a tile's sums are done
-    auto own_free = [&](int b) { return bar0 + 8u * (2 * M_STAGES + 2 + b); };   // columns of one parity only
-    const uint32_t shared_free = bar0 + 8u * (2 * M_STAGES + 4);                 // columns of both parities
-    const uint32_t drain_bar = bar0 + 8u * (2 * M_STAGES + 5);
+    auto full = [&](int s) { return bar0 + 8u * s; };   // this CTA's copies landed (even CTA: the odd one's too)
+    auto empty = [&](int s) { return bar0 + 8u * (NS + s); };           // the stage's MMAs are done
+    auto tfull = [&](int b) { return bar0 + 8u * (2 * NS + b); };       // a tile's sums are done
+    auto own_free = [&](int b) { return bar0 + 8u * (2 * NS + 2 + b); };   // even CTA: columns of one parity only
+    const uint32_t shared_free = bar0 + 8u * (2 * NS + 4);                 // even CTA: columns of both parities
+    const uint32_t drain_bar = bar0 + 8u * (2 * NS + 5);
     const int stages = (p.K + 2 * M_KB - 1) / (2 * M_KB);
+    const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < M_STAGES; ++s) {
-            mbar_init(full(s), 1);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full(s), rank == 0 ? 2 : 1);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(own_free(b), 8);
+            mbar_init(own_free(b), 16);
         }
-        mbar_init(shared_free, 8);
+        mbar_init(shared_free, 16);
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&tW);
-            tma_prefetch_desc(&tX);
+            tma_prefetch_desc(&m.w);
+            tma_prefetch_desc(&m.x);
+            tma_prefetch_desc(&m.ws);
+            tma_prefetch_desc(&m.xs);
         }
         // token tiles before each expert
         int carry = 0;
@@ -262,79 +326,78 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         if (lane == 0) start[p.experts] = carry;
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), M_TMEM);
-        tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(M_TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();   // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t ntiles = (uint32_t)start[p.experts] * (uint32_t)p.ftiles;
+    const uint32_t tmem = uniform(*tmem_slot);
+    const uint32_t ntiles = uniform((uint32_t)start[p.experts] * (uint32_t)p.ftiles);
 
     if (warp == 0) {
         // ------------------------------- producer -----------------------------------
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, issued_par = 0;
-            bool ok = true;
-            for (uint32_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
-                const Tile t = find_tile(p, start, i);
-                const int boxes = (t.n + M_TBOX - 1) / M_TBOX;
-                const int atoms = ((t.t0 & 127) + t.n + 127) >> 7;   // 128-row scale tiles of the tokens
-                const uint8_t* ws = p.ws + t.e * p.w_scales_stride + (int64_t)(t.f0 >> 7) * p.tiles_k * kFp4Tile;
-                const uint8_t* xs = p.xs + (int64_t)(t.t0 >> 7) * p.tiles_k * kFp4Tile;
-                for (int kt = 0; kt < stages; ++kt) {
-                    if (!mbar_wait(empty(stage), phase ^ 1u, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sb = (uint32_t)min((int64_t)S::KA, p.tiles_k - (int64_t)kt * S::KA) * kFp4Tile;
-                    const uint32_t base = sbase + stage * S::BYTES;
-                    mbar_expect_tx(full(stage), S::W + boxes * M_TBOX * M_KB + (1 + atoms) * sb);
-                    tma_load_2d(base, &tW, full(stage), kt * M_KB, t.e * p.N + t.f0);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(base + S::W + b * M_TBOX * M_KB, &tX, full(stage), kt * M_KB, t.t0 + b * M_TBOX);
-                    bulk_load(base + S::W + S::X, ws + (int64_t)kt * S::SW, sb, full(stage));
-                    for (int a = 0; a < atoms; ++a)
-                        bulk_load(base + S::W + S::X + S::SW + a * S::SW, xs + (a * p.tiles_k + (int64_t)kt * S::KA) * kFp4Tile, sb,
-                                  full(stage));
-                    issued |= 1u << stage;
-                    issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == M_STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+        const bool leader = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, issued_par = 0;
+        bool ok = true;
+        for (uint32_t i = first; i < ntiles && ok; i += step) {
+            const Tile t = find_tile(p, start, i);
+            const int n = (int)uniform(t.n), t0 = (int)uniform(t.t0), e = (int)uniform(t.e);
+            const int f = (int)uniform(t.f0) + (int)rank * M_F;
+            const bool small = n <= 2 * M_TBOX;
+            const CUtensorMap* tx = small ? &m.xsmall : &m.x;
+            const uint32_t bytes = S::BYTES - (small ? (M_T / 2 - M_TBOX) * M_KB : 0);
+            const int wrow = e * p.N + f, xrow = t0 + (int)rank * (n >> 1);
+            // (features past the last one: their sums are not stored, so any scales will do)
+            const int wblock = e * p.row_blocks + min(f >> 7, p.row_blocks - 1), xblock = t0 >> 7;
+            for (int kt = 0; kt < stages; ++kt) {
+                if (!wait_all(empty(stage), phase ^ 1u, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    const uint32_t base = sbase + stage * S::BYTES, bar = full(stage);
+                    mbar_expect_tx(bar, bytes);
+                    tma_load_2d(base, &m.w, bar, kt * M_KB, wrow);
+                    tma_load_2d(base + S::W, tx, bar, kt * M_KB, xrow);
+                    tma_load_3d(base + S::W + S::X, &m.ws, bar, 0, kt * S::KA, wblock);
+                    tma_load_3d(base + S::W + S::X + S::SW, &m.xs, bar, 0, kt * S::KA, xblock);
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            for (int s = 0; s < M_STAGES; ++s)
-                if (issued & (1u << s)) drain(full(s), (issued_par >> s) & 1u, p.status);
         }
-    } else if (warp == 1) {
+        if (leader)
+            for (int s = 0; s < NS; ++s)
+                if (issued & (1u << s)) drain(full(s), (issued_par >> s) & 1u, p.status);
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
         // ------------------------------- MMA issuer ---------------------------------
         const bool leader = elect_one();
         int stage = 0;
         uint32_t phase = 0, it = 0, tile = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; i < ntiles && ok; i += gridDim.x, ++tile) {
-            const Tile t = find_tile(p, start, i);
+        for (uint32_t i = first; i < ntiles && ok; i += step, ++tile) {
+            Tile t = find_tile(p, start, i);
+            t.t0 = (int)uniform(t.t0);
+            t.n = (int)uniform(t.n);
             const bool two = (t.t0 & 127) + t.n > 128;   // the tokens' scales are in two row blocks
             const uint32_t b = tile & 1u;
-            if (!wait_all(own_free(b), ((tile >> 1) & 1u) ^ 1u, abort_flag, p.status) ||
-                !wait_all(shared_free, (tile & 1u) ^ 1u, abort_flag, p.status))
-                break;
+            const uint32_t op = ((tile >> 1) & 1u) ^ 1u, sp = (tile & 1u) ^ 1u;
+            if (!wait_all(own_free(b), op, abort_flag, p.status) || !wait_all(shared_free, sp, abort_flag, p.status)) break;
             tc_fence_after();
             const uint32_t d = tmem + b * 128u;
             const uint32_t tcol = (uint32_t)(t.t0 & 127) >> 5;
             const uint32_t idesc = fp4_idesc<MX>(t.n, 0), idesc2 = fp4_idesc<MX>(t.n, 2);
             for (int kt = 0; kt < stages; ++kt, ++it) {
-                // this parity's scale columns: read by the MMAs of two stages ago
-                if (it >= 2) {
-                    const uint32_t w = it - 2;
-                    if (!wait_all(empty(w % M_STAGES), (w / M_STAGES) & 1u, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                }
                 if (!wait_all(full(stage), phase, abort_flag, p.status)) {
                     ok = false;
                     break;
@@ -342,7 +405,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                 tc_fence_after();
                 const uint32_t base = sbase + stage * S::BYTES;
                 const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
-                const int ka = min(S::KA, (int)p.tiles_k - kt * S::KA);
+                const int ka = min(S::KA, p.tiles_k - kt * S::KA);
                 const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
                 if (leader) {
 #pragma unroll
@@ -362,27 +425,47 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                                          sf + S::KA * 4 + a * 8 + tcol, (kt > 0 || k > 0) ? 1u : 0u);
                         }
                     }
-                    umma_commit(empty(stage));
-                    if (kt == stages - 1) umma_commit(tfull(b));
+                    commit_pair(empty(stage));
+                    if (kt == stages - 1) commit_pair(tfull(b));
                 }
                 __syncwarp();
-                if (++stage == M_STAGES) {
+                if (++stage == NS) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
         }
         if (leader) {
-            umma_commit(drain_bar);
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_bar) : "memory");
             drain(drain_bar, 0, p.status);
         }
         __syncwarp();
+    } else if (warp == 1) {
+        // ------------------- odd CTA: passes on which stages have landed ------------
+        const bool leader = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (uint32_t i = first; i < ntiles && ok; i += step) {
+            for (int kt = 0; kt < stages; ++kt) {
+                if (!wait_all(full(stage), phase, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (leader) arrive_cluster(in_even_cta(full(stage)));
+                __syncwarp();
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
     } else {
         // ------------------------------- epilogue -----------------------------------
         const int q = warp & 3;
         const int half = 64 * ((warp - 2) >> 2);   // its 64 columns of each 128
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
-        // rows that belong to no expert: the clamped ranges' gaps are an error, the tail is zero
+        // rows that belong to no expert are zero (ranges that were clamped are an error)
         if (p.offsets) {
             const int live = min(max(p.offsets[p.experts], 0), p.T);
             const int64_t n = (int64_t)(p.T - live) * p.N;
@@ -394,13 +477,13 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         }
         const float gx = MX ? 1.0f : *p.xg;
         uint32_t tile = 0;
-        for (uint32_t i = blockIdx.x; i < ntiles; i += gridDim.x, ++tile) {
+        for (uint32_t i = first; i < ntiles; i += step, ++tile) {
             const Tile t = find_tile(p, start, i);
             const uint32_t b = tile & 1u;
-            if (!mbar_wait_warp(tfull(b), (tile >> 1) & 1u, abort_flag, p.status)) break;
+            if (!wait_all(tfull(b), (tile >> 1) & 1u, abort_flag, p.status)) break;
             tc_fence_after();
             const float g = MX ? 1.0f : gx * p.wg[t.e * p.wg_stride];
-            const int f = t.f0 + 32 * q + lane;
+            const int f = t.f0 + (int)rank * M_F + 32 * q + lane;
             // first the columns that the next tile also uses: tokens 128.. of an even tile, 0..127 of
             // an odd one; all of them into registers, so they are free before anything is stored
             uint32_t v[2][32];
@@ -413,7 +496,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(own ? own_free(b) : shared_free);
+                if (lane == 0) arrive_cluster(in_even_cta(own ? own_free(b) : shared_free));
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f);
@@ -423,10 +506,11 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync();   // neither CTA leaves, or frees TMEM, while the other may still use it
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, M_TMEM);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(M_TMEM) : "memory");
     }
 }
 
@@ -444,13 +528,37 @@ bool code_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t pitch,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// a scale tile is 128 32-bit elements; tiles past the columns or rows read as zero
+bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t tiles_k, int64_t blocks, int ka, int box_blocks) {
+    auto enc = tma_encoder();
+    cuuint64_t dims[3] = {kFp4Tile / 4, (cuuint64_t)tiles_k, (cuuint64_t)blocks};
+    cuuint64_t strides[2] = {kFp4Tile, (cuuint64_t)(tiles_k * kFp4Tile)};
+    cuuint32_t box[3] = {kFp4Tile / 4, (cuuint32_t)ka, (cuuint32_t)box_blocks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 3, const_cast<uint8_t*>(scales), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool MX>
-int launch(const CUtensorMap& tw, const CUtensorMap& tx, const MParams& p, int64_t most_tiles, cudaStream_t s) {
-    const int smem = 1024 + M_STAGES * Stage<MX>::BYTES + 8 * (2 * M_STAGES + 6) + 8 + 4 * (p.experts + 1);
+int launch(const Maps& m, const MParams& p, int64_t most_tiles, cudaStream_t s) {
+    const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * (2 * Stage<MX>::N + 6) + 8 + 4 * (p.experts + 1);
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    const unsigned grid = (unsigned)std::min<int64_t>(most_tiles, device_sm_count());
-    GPTQ_LAUNCH(K_FP4_MM, s, fp4_matmul_kernel<MX><<<grid, M_THREADS, smem, s>>>(tw, tx, p));
-    GPTQ_LAUNCH_CHECK();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2));
+    cfg.blockDim = dim3(M_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaSuccess;
+    GPTQ_LAUNCH(K_FP4_MM, s, e = cudaLaunchKernelEx(&cfg, fp4_matmul_kernel<MX>, m, p));
+    GPTQ_CUDA_TRY(e);
     return GPTQ_OK;
 }
 
@@ -475,25 +583,27 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
         !aligned16(w_codes) || !aligned16(w_scales) || (format == GPTQ_NVFP4 && (!x_g || !w_g)))
         return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t pitch = fp4_pitch(K);
-    CUtensorMap tw, tx;
-    if (!code_map(&tw, w_codes, experts * N, pitch, M_F) || !code_map(&tx, x_codes, T, pitch, M_TBOX)) return GPTQ_ERR_CUDA;
+    const int64_t pitch = fp4_pitch(K), tiles_k = fp4_tiles(K, format), row_blocks = ceil_div(N, 128);
+    const int ka = format == GPTQ_MXFP4 ? Stage<true>::KA : Stage<false>::KA;
+    Maps m;
+    if (!code_map(&m.w, w_codes, experts * N, pitch, M_F) || !code_map(&m.x, x_codes, T, pitch, M_T / 2) ||
+        !code_map(&m.xsmall, x_codes, T, pitch, M_TBOX) || !scale_map(&m.ws, w_scales, tiles_k, experts * row_blocks, ka, 1) ||
+        !scale_map(&m.xs, x_scales, tiles_k, ceil_div(T, 128), ka, 2))
+        return GPTQ_ERR_CUDA;
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
     MParams p{};
-    p.xs = x_scales;
-    p.ws = w_scales;
     p.xg = x_g;
     p.wg = w_g;
     p.T = (int)T;
     p.N = (int)N;
     p.K = (int)K;
-    p.tiles_k = fp4_tiles(K, format);
-    p.w_scales_stride = gptq_fp4_scale_bytes(N, K, format);
+    p.tiles_k = (int)tiles_k;
+    p.row_blocks = (int)row_blocks;
     p.wg_stride = (flags & GPTQ_FP4_EXPERT_G) ? 1 : 0;
     p.offsets = offsets;
     p.experts = (int)experts;
-    p.ftiles = (int)ceil_div(N, M_F);
+    p.ftiles = (int)ceil_div(N, M_PF);
     p.relu = (flags & GPTQ_DQ_RELU) ? 1 : 0;
     p.bf16_out = (flags & GPTQ_DQ_BF16_OUT) ? 1 : 0;
     p.Y = Y;
@@ -501,7 +611,7 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
     p.status = st.word;
     // at most one more token tile per expert than whole tiles, and one more for the first's shift
     const int64_t most = (ceil_div(T, M_T) + (offsets ? 2 * std::min(experts, T) : 0)) * p.ftiles;
-    const int rc = format == GPTQ_MXFP4 ? launch<true>(tw, tx, p, most, s) : launch<false>(tw, tx, p, most, s);
+    const int rc = format == GPTQ_MXFP4 ? launch<true>(m, p, most, s) : launch<false>(m, p, most, s);
     return rc != GPTQ_OK ? rc : st.finish(s);
 }
 
