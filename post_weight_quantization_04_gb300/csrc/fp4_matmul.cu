@@ -6,20 +6,18 @@
 // scales, 64 columns per instruction, fp32 sums in TMEM). The weights are the M operand and the
 // tokens the N operand, whose width is chosen per tile: an expert with few rows pays for few.
 //
-// Two CTAs on neighbouring SMs (a cluster) work on one tile of 256 features x up to 256 tokens with
+// Two CTAs on neighbouring SMs (a cluster) work on one tile of 256 features x up to 192 tokens with
 // cta_group::2 MMAs: each holds its own 128 features, half of the tokens and all the tile's scales,
-// so a stage brings 32 KB of codes into each SM where a 128 x 256 tile of its own would take 48 (the
-// kernel was bound by those loads). Roles in each CTA (persistent, one per SM):
+// so a stage brings 28 KB of codes into each SM where a 128 x 192 tile of its own would take 40. Roles in each CTA (persistent, one per SM):
 //   warp 0       producer: per stage of 256 columns four TMA copies, the 128 x 128-byte box of weight
 //                codes, that of token codes (128-byte swizzle), and the scale tiles of both
 //   warp 1       in the even CTA: scale tiles shared memory -> TMEM (tcgen05.cp, both CTAs) and the
 //                MMAs; in the odd CTA: tells the even one which stages have landed
 //   warps 2..9   epilogue: TMEM -> registers -> Y; a lane holds one feature, a register one token
 //
-// TMEM: the sums of a 128 x 256 tile take 256 columns, so two whole buffers would leave none for
-// scales. Even tiles use columns [0, 256), odd tiles [128, 384): only [128, 256) is shared, it is
-// drained first (all of it into registers, then released), and the next tile's MMAs start while
-// the rest is still being stored. Columns 384.. hold two stages' scales in turn.
+// TMEM: two buffers of sums, 192 columns (tokens) each, so one tile's sums are stored while the next
+// tile's MMAs run, and two stages' scales in turn in the columns from 384. (Tiles of 256 tokens leave
+// room for scales only if the two buffers overlap; waiting for the shared columns cost 1.2 us a tile.)
 // Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits
 // for its own copies, the even one for the MMAs, and both meet before either leaves).
 #include <cuda_bf16.h>
@@ -36,7 +34,7 @@ namespace {
 
 constexpr int M_F = 128;                 // features per CTA
 constexpr int M_PF = 2 * M_F;            // features per tile
-constexpr int M_T = 256;                 // most tokens per tile
+constexpr int M_T = 192;                 // most tokens per tile
 constexpr int M_KB = 128;                // bytes of codes per row and stage (256 columns)
 constexpr int M_TBOX = 32;               // tokens per TMA box where a CTA's half of a tile has at most this
 constexpr int M_THREADS = 32 * 10;
@@ -50,7 +48,7 @@ struct Stage {
     static constexpr int SW = KA * kFp4Tile, SX = 2 * KA * kFp4Tile;
     static constexpr int BYTES = W + X + SW + SX;      // a multiple of 1024
     static constexpr uint32_t SF_COLS = KA * 12;       // TMEM columns of one stage's scales
-    static constexpr int N = MX ? 6 : 5;               // stages: what fits in 227 KB
+    static constexpr int N = 6;                        // stages: what fits in 227 KB
 };
 
 struct Maps {
@@ -87,13 +85,10 @@ __device__ __forceinline__ void expert_rows(const MParams& p, int e, int* lo, in
     *hi = h;
 }
 
-// Token tiles of rows [lo, hi): they start on a multiple of 64 (where the tokens' scales may start
-// in TMEM), the first one ends within two 128-row scale tiles, the others are whole.
+// Token tiles of rows [lo, hi). They start on multiples of 64, where the tokens' scales may start in
+// TMEM, so a tile of up to 192 tokens has its scales in two 128-row blocks.
 __device__ __forceinline__ int token_tiles(int lo, int hi) {
-    if (hi <= lo) return 0;
-    const int t0 = lo & ~63, first = M_T - (t0 & 127);
-    const int rest = hi - t0 - first;
-    return 1 + (rest > 0 ? (rest + M_T - 1) / M_T : 0);
+    return hi <= lo ? 0 : (hi - (lo & ~63) + M_T - 1) / M_T;
 }
 
 struct Tile {
@@ -121,9 +116,8 @@ __device__ __forceinline__ Tile find_tile(const MParams& p, const int32_t* start
         t.lo = 0;
         t.hi = p.T;
     }
-    const int first0 = t.lo & ~63, first = M_T - (first0 & 127), j = tt - start[a];
-    t.t0 = j == 0 ? first0 : first0 + first + (j - 1) * M_T;
-    t.n = min((t.hi - t.t0 + 31) & ~31, j == 0 ? first : M_T);
+    t.t0 = (t.lo & ~63) + (tt - start[a]) * M_T;
+    t.n = min((t.hi - t.t0 + 31) & ~31, M_T);
     return t;
 }
 
@@ -145,22 +139,17 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// The bounded wait, polling some times before mbar_wait takes over: that one begins by reading the
-// time and its limit from memory, which takes longer than most waits here last (with it alone the
-// 16384 x 4096 x 14336 MX product took 568 us, WAITTIME with the polls first).
-constexpr int M_POLLS = 20;
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    for (int i = 0; i < M_POLLS; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, abort_flag, status);
-}
-
-// The same by a whole converged warp, one lane polling: each lane's try_wait is an operation of its own
-// on the barrier's word, and 32 of them at a time slow the copies that count on it down.
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    bool ok = true;
-    if (elect_one()) ok = wait_one(bar, parity, abort_flag, status);
-    return __all_sync(0xffffffffu, ok);
+// The bounded wait, by a whole converged warp. Only the time is looked at while it waits: what a wait
+// that gave up has to record is done after the loops, because a global atomic (or the load of its
+// limit) in them cost the warps that feed the tensor core more than the waiting itself
+// (8192 x 8192 x 8192 MX: 225 us with mbar_wait, 155 us with this).
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, uint64_t limit) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 >= limit)) return false;
+    }
 }
 
 // ------------------------------------ the pair of CTAs ------------------------------------
@@ -269,9 +258,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NS * S::BYTES);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 6);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int32_t* start = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [experts + 1]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 5);
+    int32_t* start = reinterpret_cast<int32_t*>(tmem_slot + 1);   // [experts + 1]
 
     // what steers a warp is made warp-uniform by a shuffle, so the branches and the operands of the
     // tensor instructions stay in uniform registers
@@ -281,9 +269,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     auto full = [&](int s) { return bar0 + 8u * s; };   // this CTA's copies landed (even CTA: the odd one's too)
     auto empty = [&](int s) { return bar0 + 8u * (NS + s); };           // the stage's MMAs are done
     auto tfull = [&](int b) { return bar0 + 8u * (2 * NS + b); };       // a tile's sums are done
-    auto own_free = [&](int b) { return bar0 + 8u * (2 * NS + 2 + b); };   // even CTA: columns of one parity only
-    const uint32_t shared_free = bar0 + 8u * (2 * NS + 4);                 // even CTA: columns of both parities
-    const uint32_t drain_bar = bar0 + 8u * (2 * NS + 5);
+    auto tfree = [&](int b) { return bar0 + 8u * (2 * NS + 2 + b); };   // even CTA: both have read a tile's sums
+    const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
     const int stages = (p.K + 2 * M_KB - 1) / (2 * M_KB);
     const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -294,11 +281,9 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull(b), 1);
-            mbar_init(own_free(b), 16);
+            mbar_init(tfree(b), 16);
         }
-        mbar_init(shared_free, 16);
         mbar_init(drain_bar, 1);
-        *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 0) {
@@ -335,6 +320,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     cluster_sync();   // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
+    const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_pipeline_wait_limit_ns);
+    bool ok = true;   // false: a wait gave up
     const uint32_t ntiles = uniform((uint32_t)start[p.experts] * (uint32_t)p.ftiles);
 
     if (warp == 0) {
@@ -342,7 +329,6 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         const bool leader = elect_one();
         int stage = 0;
         uint32_t phase = 0, issued = 0, issued_par = 0;
-        bool ok = true;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
             const Tile t = find_tile(p, start, i);
             const int n = (int)uniform(t.n), t0 = (int)uniform(t.t0), e = (int)uniform(t.e);
@@ -354,10 +340,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
             // (features past the last one: their sums are not stored, so any scales will do)
             const int wblock = e * p.row_blocks + min(f >> 7, p.row_blocks - 1), xblock = t0 >> 7;
             for (int kt = 0; kt < stages; ++kt) {
-                if (!wait_all(empty(stage), phase ^ 1u, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_all(empty(stage), phase ^ 1u, limit);
+                if (!ok) break;
                 if (leader) {
                     const uint32_t base = sbase + stage * S::BYTES, bar = full(stage);
                     mbar_expect_tx(bar, bytes);
@@ -381,33 +365,29 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         // ------------------------------- MMA issuer ---------------------------------
-        const bool leader = elect_one();
         int stage = 0;
         uint32_t phase = 0, it = 0, tile = 0;
-        bool ok = true;
         for (uint32_t i = first; i < ntiles && ok; i += step, ++tile) {
             Tile t = find_tile(p, start, i);
             t.t0 = (int)uniform(t.t0);
             t.n = (int)uniform(t.n);
             const bool two = (t.t0 & 127) + t.n > 128;   // the tokens' scales are in two row blocks
             const uint32_t b = tile & 1u;
-            const uint32_t op = ((tile >> 1) & 1u) ^ 1u, sp = (tile & 1u) ^ 1u;
-            if (!wait_all(own_free(b), op, abort_flag, p.status) || !wait_all(shared_free, sp, abort_flag, p.status)) break;
+            ok = wait_all(tfree(b), ((tile >> 1) & 1u) ^ 1u, limit);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t d = tmem + b * 128u;
+            const uint32_t d = tmem + b * (uint32_t)M_T;
             const uint32_t tcol = (uint32_t)(t.t0 & 127) >> 5;
             const uint32_t idesc = fp4_idesc<MX>(t.n, 0), idesc2 = fp4_idesc<MX>(t.n, 2);
             for (int kt = 0; kt < stages; ++kt, ++it) {
-                if (!wait_all(full(stage), phase, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_all(full(stage), phase, limit);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = sbase + stage * S::BYTES;
                 const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
                 const int ka = min(S::KA, p.tiles_k - kt * S::KA);
                 const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
-                if (leader) {
+                if (elect_one()) {
 #pragma unroll
                     for (int a = 0; a < S::KA; ++a) {
                         if (a < ka) {
@@ -435,7 +415,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                 }
             }
         }
-        if (leader) {
+        if (elect_one()) {
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_bar) : "memory");
             drain(drain_bar, 0, p.status);
         }
@@ -445,13 +425,10 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         const bool leader = elect_one();
         int stage = 0;
         uint32_t phase = 0;
-        bool ok = true;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
             for (int kt = 0; kt < stages; ++kt) {
-                if (!wait_all(full(stage), phase, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_all(full(stage), phase, limit);
+                if (!ok) break;
                 if (leader) arrive_cluster(in_even_cta(full(stage)));
                 __syncwarp();
                 if (++stage == NS) {
@@ -463,7 +440,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     } else {
         // ------------------------------- epilogue -----------------------------------
         const int q = warp & 3;
-        const int half = 64 * ((warp - 2) >> 2);   // its 64 columns of each 128
+        const int c0 = M_T / 2 * ((warp - 2) >> 2);   // its half of the columns
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         // rows that belong to no expert are zero (ranges that were clamped are an error)
         if (p.offsets) {
@@ -480,30 +457,27 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         for (uint32_t i = first; i < ntiles; i += step, ++tile) {
             const Tile t = find_tile(p, start, i);
             const uint32_t b = tile & 1u;
-            if (!wait_all(tfull(b), (tile >> 1) & 1u, abort_flag, p.status)) break;
+            ok = wait_all(tfull(b), (tile >> 1) & 1u, limit);
+            if (!ok) break;
             tc_fence_after();
             const float g = MX ? 1.0f : gx * p.wg[t.e * p.wg_stride];
             const int f = t.f0 + (int)rank * M_F + 32 * q + lane;
-            // first the columns that the next tile also uses: tokens 128.. of an even tile, 0..127 of
-            // an odd one; all of them into registers, so they are free before anything is stored
-            uint32_t v[2][32];
+            // all of its columns into registers, so the buffer is free before anything is stored
+            uint32_t v[M_T / 64][32];
 #pragma unroll
-            for (int own = 0; own < 2; ++own) {
-                const int c0 = half + ((own != 0) == (b != 0) ? 128 : 0);
+            for (int c = 0; c < M_T / 64; ++c)
+                if (c0 + 32 * c < t.n) tmem_ld_32x32b_x32(tmem + lanes + b * (uint32_t)M_T + c0 + 32 * c, v[c]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(in_even_cta(tfree(b)));
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (c0 + 32 * c < t.n) tmem_ld_32x32b_x32(tmem + lanes + b * 128u + c0 + 32 * c, v[c]);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_cluster(in_even_cta(own ? own_free(b) : shared_free));
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f);
-            }
+            for (int c = 0; c < M_T / 64; ++c)
+                if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f);
         }
     }
 
+    if (!ok && lane == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // neither CTA leaves, or frees TMEM, while the other may still use it
@@ -542,7 +516,7 @@ bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t tiles_k, int64_t b
 
 template <bool MX>
 int launch(const Maps& m, const MParams& p, int64_t most_tiles, cudaStream_t s) {
-    const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * (2 * Stage<MX>::N + 6) + 8 + 4 * (p.experts + 1);
+    const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * (2 * Stage<MX>::N + 5) + 8 + 4 * (p.experts + 1);
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2));
@@ -609,7 +583,7 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
     p.Y = Y;
     p.ldy = ldy;
     p.status = st.word;
-    // at most one more token tile per expert than whole tiles, and one more for the first's shift
+    // an expert's first tile may start up to 63 rows early and its last one be partial
     const int64_t most = (ceil_div(T, M_T) + (offsets ? 2 * std::min(experts, T) : 0)) * p.ftiles;
     const int rc = format == GPTQ_MXFP4 ? launch<true>(m, p, most, s) : launch<false>(m, p, most, s);
     return rc != GPTQ_OK ? rc : st.finish(s);
