@@ -13,7 +13,9 @@
 //                codes, that of token codes (128-byte swizzle), and the scale tiles of both
 //   warp 1       in the even CTA: scale tiles shared memory -> TMEM (tcgen05.cp, both CTAs) and the
 //                MMAs; in the odd CTA: tells the even one which stages have landed
-//   warps 2..9   epilogue: TMEM -> registers -> Y; a lane holds one feature, a register one token
+//   warps 2..9   epilogue: TMEM -> registers -> Y. bf16 rows are turned in shared memory (stmatrix), so
+//                that a token's features leave in 16-byte pieces; fp32, or a Y that is not aligned for
+//                that, is stored straight from the registers, where a lane holds one feature
 //
 // TMEM: two buffers of sums, 192 columns (tokens) each, so one tile's sums are stored while the next
 // tile's MMAs run, and two stages' scales in turn in the columns from 384. (Tiles of 256 tokens leave
@@ -40,6 +42,7 @@ constexpr int M_TBOX = 32;               // tokens per TMA box where a CTA's hal
 constexpr int M_THREADS = 32 * 10;
 constexpr uint32_t M_TMEM = 512, M_SF0 = 384;
 constexpr int M_MAX_EXPERTS = 1024;
+constexpr int M_TURN = 32 * 64;          // bytes of a warp's buffer: 32 tokens x 32 features of bf16
 
 template <bool MX>
 struct Stage {
@@ -65,7 +68,7 @@ struct MParams {
     const int32_t* offsets;    // null: one expert, all rows
     int experts;
     int ftiles;                // feature tiles
-    int relu, bf16_out;
+    int relu, bf16_out, vec;   // vec: bf16 rows that 16-byte stores can take
     void* Y;
     int64_t ldy;
     int* status;
@@ -251,13 +254,63 @@ __device__ __forceinline__ void store_tokens(const MParams& p, const uint32_t (&
     else store_tokens(static_cast<float*>(p.Y) + at, p.ldy, v, g, p.relu != 0, first, last);
 }
 
+// 16 lanes x 32 columns of TMEM: of each 8 columns thread i gets lane i / 4, columns 2 (i % 4) and the
+// next, then the same of lane 8 + i / 4 (the layout that stmatrix takes)
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ uint32_t two_bf16(uint32_t a, uint32_t b, float g, bool relu) {
+    float x = __uint_as_float(a) * g, y = __uint_as_float(b) * g;
+    if (relu) {
+        x = fmaxf(x, 0.0f);
+        y = fmaxf(y, 0.0f);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 tokens x 32 features (v[h]: features 16 h ..) to Y through the warp's 2 KB of shared memory: rows
+// of 64 bytes, one per token, whose 16-byte pieces are permuted so that neither side has conflicts
+__device__ __forceinline__ void turn_tokens(const MParams& p, const uint32_t (&v)[2][16], float g, const Tile& t, int tok, int f0,
+                                            uint32_t buf) {
+    const int lane = threadIdx.x & 31;
+    const bool relu = p.relu != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 8 * j + (lane & 7);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         buf + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4)),
+                     "r"(two_bf16(v[0][4 * j], v[0][4 * j + 1], g, relu)), "r"(two_bf16(v[0][4 * j + 2], v[0][4 * j + 3], g, relu)),
+                     "r"(two_bf16(v[1][4 * j], v[1][4 * j + 1], g, relu)), "r"(two_bf16(v[1][4 * j + 2], v[1][4 * j + 3], g, relu))
+                     : "memory");
+    }
+    __syncwarp();
+    const int f = f0 + 8 * (lane & 3);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y) + f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 8 * j + (lane >> 2), r = tok + row;
+        uint4 w;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)));
+        if (f < p.N && r >= t.lo && r < t.hi) *reinterpret_cast<uint4*>(y + (int64_t)r * p.ldy) = w;
+    }
+    __syncwarp();
+}
+
 template <bool MX>
 __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_constant__ Maps m, const MParams p) {
     using S = Stage<MX>;
     constexpr int NS = S::N;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NS * S::BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NS * S::BYTES + 8 * M_TURN);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NS + 5);
     int32_t* start = reinterpret_cast<int32_t*>(tmem_slot + 1);   // [experts + 1]
 
@@ -442,6 +495,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         const int q = warp & 3;
         const int c0 = M_T / 2 * ((warp - 2) >> 2);   // its half of the columns
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        const uint32_t turn = sbase + NS * S::BYTES + (warp - 2) * M_TURN;
         // rows that belong to no expert are zero (ranges that were clamped are an error)
         if (p.offsets) {
             const int live = min(max(p.offsets[p.experts], 0), p.T);
@@ -461,19 +515,36 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
             if (!ok) break;
             tc_fence_after();
             const float g = MX ? 1.0f : gx * p.wg[t.e * p.wg_stride];
-            const int f = t.f0 + (int)rank * M_F + 32 * q + lane;
-            // all of its columns into registers, so the buffer is free before anything is stored
-            uint32_t v[M_T / 64][32];
+            const int f0 = t.f0 + (int)rank * M_F + 32 * q;
+            const uint32_t sums = tmem + lanes + b * (uint32_t)M_T + c0;
+            // all of its columns into registers (those past the tile's tokens too: the buffer has them), so
+            // the buffer is free before anything is stored
+            if (p.vec) {
+                uint32_t v[M_T / 64][2][16];
 #pragma unroll
-            for (int c = 0; c < M_T / 64; ++c)
-                if (c0 + 32 * c < t.n) tmem_ld_32x32b_x32(tmem + lanes + b * (uint32_t)M_T + c0 + 32 * c, v[c]);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(in_even_cta(tfree(b)));
+                for (int c = 0; c < M_T / 64; ++c) {
+                    tmem_ld_16x256b_x4(sums + 32 * c, v[c][0]);
+                    tmem_ld_16x256b_x4(sums + (16u << 16) + 32 * c, v[c][1]);
+                }
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_even_cta(tfree(b)));
 #pragma unroll
-            for (int c = 0; c < M_T / 64; ++c)
-                if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f);
+                for (int c = 0; c < M_T / 64; ++c)
+                    if (c0 + 32 * c < t.n) turn_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f0, turn);
+            } else {
+                uint32_t v[M_T / 64][32];
+#pragma unroll
+                for (int c = 0; c < M_T / 64; ++c) tmem_ld_32x32b_x32(sums + 32 * c, v[c]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_even_cta(tfree(b)));
+#pragma unroll
+                for (int c = 0; c < M_T / 64; ++c)
+                    if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f0 + lane);
+            }
         }
     }
 
@@ -516,7 +587,7 @@ bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t tiles_k, int64_t b
 
 template <bool MX>
 int launch(const Maps& m, const MParams& p, int64_t most_tiles, cudaStream_t s) {
-    const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * (2 * Stage<MX>::N + 5) + 8 + 4 * (p.experts + 1);
+    const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * M_TURN + 8 * (2 * Stage<MX>::N + 5) + 8 + 4 * (p.experts + 1);
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2));
@@ -580,6 +651,7 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
     p.ftiles = (int)ceil_div(N, M_PF);
     p.relu = (flags & GPTQ_DQ_RELU) ? 1 : 0;
     p.bf16_out = (flags & GPTQ_DQ_BF16_OUT) ? 1 : 0;
+    p.vec = p.bf16_out && N % 8 == 0 && ldy % 8 == 0 && aligned16(Y) ? 1 : 0;
     p.Y = Y;
     p.ldy = ldy;
     p.status = st.word;
