@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -20,10 +21,16 @@ namespace gptq {
 namespace {
 
 // ------------------------------------------------------------------------------------ sort
-constexpr int S_WARPS = 8, S_THREADS = 32 * S_WARPS;
-constexpr int S_CHUNK = 2048;          // least slots per CTA: below that one CTA does it all
-constexpr int S_MAX_EXPERTS = 1024;    // S_WARPS counters per expert in shared memory
+// Up to S_ALONE slots are sorted by one CTA of 32 warps in one launch; more by CTAs of 8 warps, which
+// count their slots in a first launch and place them in a second. Either way a warp owns a
+// contiguous share of the slots and counts equal experts among 32 slots at a time, so places are
+// stable without atomics. Equal experts are found by one ballot per bit of the expert's number
+// (match.any took several times as long).
+constexpr int S_ALONE = 4096;
+constexpr int S_CHUNK = 512;           // otherwise the least slots per CTA
+constexpr int S_MAX_EXPERTS = 1024;    // one counter per warp and expert in shared memory
 constexpr int S_MAX_CTAS = 152;        // every CTA reads every CTA's counts
+constexpr int S_AHEAD = 8;             // loads of 32 slots in flight per warp
 
 struct SParams {
     const int32_t* ids;
@@ -34,61 +41,92 @@ struct SParams {
     int* status;
 };
 
-__device__ __forceinline__ int slot_expert(const SParams& p, int64_t i, int64_t end) {
-    if (i >= end) return -1;
-    const int e = p.ids[i];
-    if (e >= p.experts) set_status(p.status, GPTQ_ERR_INVALID_ARG);
-    return e >= 0 && e < p.experts ? e : -1;
-}
-
-// counts[w][e] += the slots of expert e that warp w of this CTA owns (its share is contiguous)
-__device__ __forceinline__ void count_slots(const SParams& p, int64_t begin, int64_t end, int32_t* mine) {
+// the experts of up to 32 S_AHEAD slots from i0 on, -1 where there is none
+__device__ __forceinline__ void load_experts(const SParams& p, int64_t i0, int64_t end, int (&e)[S_AHEAD]) {
     const int lane = threadIdx.x & 31;
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-        const int e = slot_expert(p, i0 + lane, end);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (same & ((1u << lane) - 1u)) == 0) mine[e] += __popc(same);
-        __syncwarp();
+#pragma unroll
+    for (int u = 0; u < S_AHEAD; ++u) e[u] = i0 + 32 * u + lane < end ? p.ids[i0 + 32 * u + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < S_AHEAD; ++u) {
+        if (e[u] >= p.experts) {
+            set_status(p.status, GPTQ_ERR_INVALID_ARG);
+            e[u] = -1;
+        }
+        e[u] = max(e[u], -1);
     }
 }
 
-__device__ __forceinline__ void warp_share(const SParams& p, int64_t* begin, int64_t* end) {
-    const int64_t share = p.chunk / S_WARPS;
-    *begin = (int64_t)blockIdx.x * p.chunk + (threadIdx.x >> 5) * share;
-    *end = min(*begin + share, p.slots);
+// the lanes with the same expert (bits: of the largest expert's number)
+__device__ __forceinline__ uint32_t same_expert(int e, int bits) {
+    uint32_t same = __ballot_sync(0xffffffffu, e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = e >> b & 1;
+        const uint32_t m = __ballot_sync(0xffffffffu, one);
+        same &= one ? m : ~m;
+    }
+    return same;   // only looked at by lanes with an expert
 }
 
-__global__ void __launch_bounds__(S_THREADS) expert_count_kernel(const SParams p) {
-    extern __shared__ int32_t cnt[];   // [S_WARPS][experts]
-    for (int i = threadIdx.x; i < S_WARPS * p.experts; i += S_THREADS) cnt[i] = 0;
+// mine[e] += the slots of expert e in this warp's share
+__device__ __forceinline__ void count_slots(const SParams& p, int64_t begin, int64_t end, int32_t* mine) {
+    const int lane = threadIdx.x & 31, bits = 32 - __clz(p.experts - 1);
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * S_AHEAD) {
+        int e[S_AHEAD];
+        load_experts(p, i0, end, e);
+#pragma unroll
+        for (int u = 0; u < S_AHEAD; ++u) {
+            if (i0 + 32 * u >= end) break;
+            const uint32_t same = same_expert(e[u], bits);
+            if (e[u] >= 0 && (same & ((1u << lane) - 1u)) == 0) mine[e[u]] += __popc(same);
+            __syncwarp();
+        }
+    }
+}
+
+template <int WARPS>
+__device__ __forceinline__ void warp_share(const SParams& p, int64_t* begin, int64_t* end) {
+    // whole groups of 32 slots per warp
+    const int64_t cta = (int64_t)blockIdx.x * p.chunk, last = min(cta + p.chunk, p.slots);
+    const int64_t share = ((last - cta + 32 * WARPS - 1) / (32 * WARPS)) * 32;
+    *begin = min(cta + (threadIdx.x >> 5) * share, last);
+    *end = min(*begin + share, last);
+}
+
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) expert_count_kernel(const SParams p) {
+    extern __shared__ int32_t cnt[];   // [WARPS][experts]
+    pdl_trigger();
+    for (int i = threadIdx.x; i < WARPS * p.experts; i += 32 * WARPS) cnt[i] = 0;
     __syncthreads();
     int64_t b, e;
-    warp_share(p, &b, &e);
+    warp_share<WARPS>(p, &b, &e);
     count_slots(p, b, e, cnt + (threadIdx.x >> 5) * p.experts);
     __syncthreads();
-    for (int i = threadIdx.x; i < p.experts; i += S_THREADS) {
+    for (int i = threadIdx.x; i < p.experts; i += 32 * WARPS) {
         int32_t n = 0;
-        for (int w = 0; w < S_WARPS; ++w) n += cnt[w * p.experts + i];
+        for (int w = 0; w < WARPS; ++w) n += cnt[w * p.experts + i];
         p.counts[(int64_t)blockIdx.x * p.experts + i] = n;
     }
 }
 
 // Places every slot. With one CTA the counts are its own; with more, each CTA sums the counts of
 // all CTAs (totals, for the offsets) and of those before it.
-__global__ void __launch_bounds__(S_THREADS) expert_place_kernel(const SParams p) {
-    extern __shared__ int32_t cnt[];       // [S_WARPS][experts], then totals [experts]
-    int32_t* total = cnt + S_WARPS * p.experts;
-    __shared__ int32_t warp_sum[S_WARPS], carry;
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) expert_place_kernel(const SParams p) {
+    constexpr int THREADS = 32 * WARPS;
+    extern __shared__ int32_t cnt[];       // [WARPS][experts]
+    __shared__ int32_t warp_sum[WARPS], carry;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < S_WARPS * p.experts; i += S_THREADS) cnt[i] = 0;
+    for (int i = threadIdx.x; i < WARPS * p.experts; i += THREADS) cnt[i] = 0;
     if (threadIdx.x == 0) carry = 0;
     __syncthreads();
     int64_t b, e;
-    warp_share(p, &b, &e);
+    warp_share<WARPS>(p, &b, &e);
     count_slots(p, b, e, cnt + warp * p.experts);
     __syncthreads();
-    // exclusive prefix over the experts, S_THREADS at a time
-    for (int e0 = 0; e0 < p.experts; e0 += S_THREADS) {
+    pdl_wait();   // the counts of the other CTAs (everything before is this kernel's own input)
+    // exclusive prefix over the experts, THREADS at a time
+    for (int e0 = 0; e0 < p.experts; e0 += THREADS) {
         const int x = e0 + threadIdx.x;
         int32_t all = 0, before = 0;
         if (x < p.experts) {
@@ -99,7 +137,7 @@ __global__ void __launch_bounds__(S_THREADS) expert_place_kernel(const SParams p
                     if (c < (int)blockIdx.x) before += n;
                 }
             } else {
-                for (int w = 0; w < S_WARPS; ++w) all += cnt[w * p.experts + x];
+                for (int w = 0; w < WARPS; ++w) all += cnt[w * p.experts + x];
             }
         }
         int32_t inc = all;
@@ -113,45 +151,61 @@ __global__ void __launch_bounds__(S_THREADS) expert_place_kernel(const SParams p
         int32_t first = carry + inc - all;
         for (int w = 0; w < warp; ++w) first += warp_sum[w];
         if (x < p.experts) {
-            total[x] = first + all;
             if (blockIdx.x == 0) p.offsets[x] = first;
             // where each warp's slots of this expert start
             int32_t at = first + before;
-            for (int w = 0; w < S_WARPS; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const int32_t n = cnt[w * p.experts + x];
                 cnt[w * p.experts + x] = at;
                 at += n;
             }
         }
         __syncthreads();
-        if (threadIdx.x == S_THREADS - 1) carry = first + all;
+        if (threadIdx.x == THREADS - 1) carry = first + all;
         __syncthreads();
     }
-    const int32_t live = total[p.experts - 1];
+    const int32_t live = carry;
     if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.experts] = live;
     int32_t* mine = cnt + warp * p.experts;
-    for (int64_t i0 = b; i0 < e; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int x = slot_expert(p, i, e);
-        const uint32_t same = __match_any_sync(0xffffffffu, x);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        int32_t at = -1;
-        if (x >= 0) at = mine[x] + rank;
-        __syncwarp();
-        if (x >= 0 && rank == 0) mine[x] += __popc(same);
-        __syncwarp();
-        if (i < e) {
-            p.pos[i] = at;
-            if (at >= 0) p.src[at] = (int32_t)i;
+    const int bits = 32 - __clz(p.experts - 1);
+    for (int64_t i0 = b; i0 < e; i0 += 32 * S_AHEAD) {
+        int x[S_AHEAD];
+        load_experts(p, i0, e, x);
+#pragma unroll
+        for (int u = 0; u < S_AHEAD; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            if (i0 + 32 * u >= e) break;
+            const uint32_t same = same_expert(x[u], bits);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            int32_t at = -1;
+            if (x[u] >= 0) at = mine[x[u]] + rank;
+            __syncwarp();
+            if (x[u] >= 0 && rank == 0) mine[x[u]] += __popc(same);
+            __syncwarp();
+            if (i < e) {
+                p.pos[i] = at;
+                if (at >= 0) p.src[at] = (int32_t)i;
+            }
         }
     }
-    for (int64_t i = live + (int64_t)blockIdx.x * S_THREADS + threadIdx.x; i < p.slots; i += (int64_t)gridDim.x * S_THREADS)
+    for (int64_t i = live + (int64_t)blockIdx.x * THREADS + threadIdx.x; i < p.slots; i += (int64_t)gridDim.x * THREADS)
         p.src[i] = -1;
 }
 
 int64_t sort_chunk(int64_t slots) {
-    const int64_t c = std::max<int64_t>(S_CHUNK, ceil_div(slots, S_MAX_CTAS));
-    return ceil_div(c, 32 * S_WARPS) * (32 * S_WARPS);
+    if (slots <= S_ALONE) return S_ALONE;
+    return ceil_div(std::max<int64_t>(S_CHUNK, ceil_div(slots, S_MAX_CTAS)), 256) * 256;
+}
+
+template <int WARPS>
+cudaError_t launch_place(const SParams& p, unsigned grid, cudaStream_t s) {
+    const size_t smem = sizeof(int32_t) * WARPS * p.experts;
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(expert_place_kernel<WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (grid > 1) GPTQ_LAUNCH(K_EXPERT_SORT, s, e = launch_pdl(expert_place_kernel<WARPS>, dim3(grid), dim3(32 * WARPS), smem, s, p));
+    else GPTQ_LAUNCH(K_EXPERT_SORT, s, expert_place_kernel<WARPS><<<grid, 32 * WARPS, smem, s>>>(p));
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------- rows there and back
@@ -253,29 +307,49 @@ __device__ __forceinline__ void store_row(T* y, const float (&v)[N]) {
     }
 }
 
-template <typename T, int N>
+// The places of SLOTS of a token's slots from j0 on, 0 where there is none (a row that may be read, and
+// is, so that all the rows' loads are in flight together), and which of them count.
+template <int SLOTS>
+__device__ __forceinline__ uint32_t places(const RParams& p, int64_t t, int j0, int64_t (&at)[SLOTS]) {
+    uint32_t live = 0;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+        const int64_t a = SLOTS == 1 || j0 + j < p.top ? place(p, t * p.top + j0 + j) : -1;
+        live |= (a >= 0 ? 1u : 0u) << j;
+        at[j] = max(a, (int64_t)0);
+    }
+    return live;
+}
+
+// A thread sums N columns of a token over its slots, SLOTS rows in flight.
+template <typename T, int N, int SLOTS>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_kernel(const RParams p, int chunks) {
     const int64_t t = blockIdx.x / chunks;
     const int64_t c = ((int64_t)(blockIdx.x % chunks) * R_THREADS + threadIdx.x) * N;
     if (c >= p.d) return;
-    const T* X = static_cast<const T*>(p.X);
+    const T* X = static_cast<const T*>(p.X) + c;
     float acc[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-    for (int j = 0; j < p.top; ++j) {
-        const int64_t at = place(p, t * p.top + j);
-        if (at < 0) continue;
-        const float w = p.w ? p.w[t * p.top + j] : 1.0f;
-        float v[N];
-        load_row<T, N>(X + at * p.ldx + c, v);
+    for (int j0 = 0; j0 < p.top; j0 += SLOTS) {
+        int64_t at[SLOTS];
+        float v[SLOTS][N];
+        const uint32_t live = places<SLOTS>(p, t, j0, at);
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int j = 0; j < SLOTS; ++j) load_row<T, N>(X + at[j] * p.ldx, v[j]);
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const float w = p.w ? (live >> j & 1 ? p.w[t * p.top + j0 + j] : 0.0f) : 1.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] = live >> j & 1 ? fmaf(w, v[j][e], acc[e]) : acc[e];
+        }
     }
     store_row<T, N>(static_cast<T*>(p.Y) + t * p.ldy + c, acc);
 }
 
-// One CTA per token: dy is read once per slot from L1, ys once, dys written once.
-template <typename T, int N>
+// One CTA per token, SLOTS slots at a time: dy and the slots' rows are read once (dy again for each
+// further group), the products of a group are summed across the CTA together.
+template <typename T, int N, int SLOTS>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_grad_kernel(const RParams p) {
     const T* X = static_cast<const T*>(p.X);
     T* Y = static_cast<T*>(p.Y);
@@ -286,36 +360,64 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_grad_kernel(const RP
             for (int64_t c = threadIdx.x * N; c < p.d; c += R_THREADS * N) store_row<T, N>(Y + r * p.ldy + c, zero);
         return;
     }
-    __shared__ float part[R_THREADS / 32];
+    __shared__ float part[R_THREADS / 32][SLOTS];
     const int64_t t = blockIdx.x;
     const T* dy = static_cast<const T*>(p.dY) + t * p.lddy;
-    for (int j = 0; j < p.top; ++j) {
-        const int64_t at = place(p, t * p.top + j);   // the same for the whole CTA
-        float dot = 0.0f;
-        if (at >= 0) {
-            const float w = p.w[t * p.top + j];
-            for (int64_t c = threadIdx.x * N; c < p.d; c += R_THREADS * N) {
-                float a[N], b[N];
-                load_row<T, N>(dy + c, a);
-                load_row<T, N>(X + at * p.ldx + c, b);
+    for (int j0 = 0; j0 < p.top; j0 += SLOTS) {
+        int64_t at[SLOTS];
+        const uint32_t live = places<SLOTS>(p, t, j0, at);   // the same for the whole CTA
+        float w[SLOTS], dot[SLOTS];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            w[j] = live >> j & 1 ? p.w[t * p.top + j0 + j] : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int64_t c = threadIdx.x * N; c < p.d; c += R_THREADS * N) {
+            float a[N], b[SLOTS][N];
+            load_row<T, N>(dy + c, a);
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) load_row<T, N>(X + at[j] * p.ldx + c, b[j]);
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    dot = fmaf(a[e], b[e], dot);
-                    a[e] *= w;
+                    dot[j] = fmaf(a[e], b[j][e], dot[j]);
+                    b[j][e] = a[e] * w[j];
                 }
-                store_row<T, N>(Y + at * p.ldy + c, a);
+                if (live >> j & 1) store_row<T, N>(Y + at[j] * p.ldy + c, b[j]);
             }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float sum = 0.0f;
-            for (int i = 0; i < R_THREADS / 32; ++i) sum += part[i];
-            p.dw[t * p.top + j] = sum;
+        for (int j = 0; j < SLOTS; ++j) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
         }
         __syncthreads();
+        if (threadIdx.x < SLOTS && j0 + (int)threadIdx.x < p.top) {
+            float sum = 0.0f;
+            for (int i = 0; i < R_THREADS / 32; ++i) sum += part[i][threadIdx.x];
+            p.dw[t * p.top + j0 + threadIdx.x] = live >> threadIdx.x & 1 ? sum : 0.0f;
+        }
+        __syncthreads();
+    }
+}
+
+// Calls f(T(), units per access, slots per group): 16-byte accesses where pointers and strides allow,
+// one element otherwise; the rows of 1, 2 or 4 slots in flight, whichever the token has.
+template <typename F>
+void with_row_types(int dtype, bool vec, int64_t top, F f) {
+    auto slots = [&](auto t, auto n) {
+        if (top == 1) f(t, n, std::integral_constant<int, 1>());
+        else if (top == 2) f(t, n, std::integral_constant<int, 2>());
+        else f(t, n, std::integral_constant<int, 4>());
+    };
+    if (dtype == GPTQ_BF16) {
+        if (vec) slots(__nv_bfloat16(), std::integral_constant<int, 8>());
+        else slots(__nv_bfloat16(), std::integral_constant<int, 1>());
+    } else {
+        if (vec) slots(float(), std::integral_constant<int, 4>());
+        else slots(float(), std::integral_constant<int, 1>());
     }
 }
 
@@ -351,13 +453,15 @@ extern "C" int gptq_expert_sort(const int32_t* ids, int64_t tokens, int64_t top,
     GPTQ_CUDA_TRY(st.begin(s));
     SParams p{ids, tokens * top, sort_chunk(tokens * top), (int)experts, offsets, src, pos, static_cast<int32_t*>(ws), st.word};
     const unsigned grid = (unsigned)std::max<int64_t>(1, ceil_div(p.slots, p.chunk));
-    const size_t smem = sizeof(int32_t) * S_WARPS * experts;
     if (grid > 1) {
-        GPTQ_LAUNCH(K_EXPERT_SORT, s, expert_count_kernel<<<grid, S_THREADS, smem, s>>>(p));
+        GPTQ_LAUNCH(K_EXPERT_SORT, s, expert_count_kernel<8><<<grid, 256, sizeof(int32_t) * 8 * experts, s>>>(p));
         GPTQ_LAUNCH_CHECK();
+        GPTQ_CUDA_TRY(launch_place<8>(p, grid, s));
+    } else if (p.slots <= 1024) {
+        GPTQ_CUDA_TRY(launch_place<8>(p, grid, s));
+    } else {
+        GPTQ_CUDA_TRY(launch_place<32>(p, grid, s));
     }
-    GPTQ_LAUNCH(K_EXPERT_SORT, s, expert_place_kernel<<<grid, S_THREADS, smem + sizeof(int32_t) * experts, s>>>(p));
-    GPTQ_LAUNCH_CHECK();
     return st.finish(s);
 }
 
@@ -397,9 +501,10 @@ extern "C" int gptq_expert_combine(const void* Ys, int dtype, int64_t tokens, in
     RParams p{Ys, ldys, nullptr, 0, Y, ldy, tokens, tokens * top, (int)top, d, pos, nullptr, weights, nullptr, st.word};
     const int64_t chunks = ceil_div(d, R_THREADS * (vec ? 16 / es : 1));
     if (tokens * chunks > kMaxSlots) return GPTQ_ERR_UNSUPPORTED;
-    auto go = [&](auto kern) { GPTQ_LAUNCH(K_EXPERT_COMBINE, s, kern<<<(unsigned)(tokens * chunks), R_THREADS, 0, s>>>(p, (int)chunks)); };
-    if (dtype == GPTQ_BF16) vec ? go(expert_combine_kernel<__nv_bfloat16, 8>) : go(expert_combine_kernel<__nv_bfloat16, 1>);
-    else vec ? go(expert_combine_kernel<float, 4>) : go(expert_combine_kernel<float, 1>);
+    with_row_types(dtype, vec, top, [&](auto t, auto n, auto k) {
+        auto kern = expert_combine_kernel<decltype(t), decltype(n)::value, decltype(k)::value>;
+        GPTQ_LAUNCH(K_EXPERT_COMBINE, s, kern<<<(unsigned)(tokens * chunks), R_THREADS, 0, s>>>(p, (int)chunks));
+    });
     GPTQ_LAUNCH_CHECK();
     return st.finish(s);
 }
@@ -417,9 +522,10 @@ extern "C" int gptq_expert_combine_grad(const void* dY, int64_t lddy, const void
     const bool vec = vec16(dY, lddy, es) && vec16(Ys, ldys, es) && vec16(dYs, lddys, es) && (d * es) % 16 == 0;
     RParams p{Ys, ldys, dY, lddy, dYs, lddys, tokens, tokens * top, (int)top, d, pos, offsets + experts, weights, dW, st.word};
     const unsigned grid = (unsigned)(tokens + tail_ctas(p.slots));
-    auto go = [&](auto kern) { GPTQ_LAUNCH(K_EXPERT_GRAD, s, kern<<<grid, R_THREADS, 0, s>>>(p)); };
-    if (dtype == GPTQ_BF16) vec ? go(expert_combine_grad_kernel<__nv_bfloat16, 8>) : go(expert_combine_grad_kernel<__nv_bfloat16, 1>);
-    else vec ? go(expert_combine_grad_kernel<float, 4>) : go(expert_combine_grad_kernel<float, 1>);
+    with_row_types(dtype, vec, top, [&](auto t, auto n, auto k) {
+        auto kern = expert_combine_grad_kernel<decltype(t), decltype(n)::value, decltype(k)::value>;
+        GPTQ_LAUNCH(K_EXPERT_GRAD, s, kern<<<grid, R_THREADS, 0, s>>>(p));
+    });
     GPTQ_LAUNCH_CHECK();
     return st.finish(s);
 }

@@ -73,8 +73,10 @@ __device__ __forceinline__ uint32_t to_codes(const float* y) {
     return r;
 }
 
-// One thread takes 16 columns of a row; an MX block's two threads share its maximum by one
-// shuffle. Streams x once and writes 1/2 byte per value plus the scales: bound by memory.
+// One thread takes 16 columns of a row; an MX block's two threads share its maximum by one shuffle, and
+// the scales of four blocks (one word of a scale tile) are stored together. Streams x once and writes
+// 1/2 byte per value plus the scales: bound by memory. Two rows per thread in flight were slower
+// (16384 x 4096 bf16 MX: 35 us against 29; fewer CTAs fit).
 template <typename T, bool MX, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p) {
     const int64_t chunk = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
@@ -83,31 +85,29 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
     for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
         int64_t sr = r;
         if (p.index) {
-            const int i = p.index[r];
-            sr = i < 0 ? -1 : i / p.per;
+            const int k = p.index[r];
+            sr = k < 0 ? -1 : k / p.per;
             if (sr >= p.src_rows) {
                 sr = -1;
                 set_status(p.status, GPTQ_ERR_INVALID_ARG);
             }
         }
-        const int64_t n = sr < 0 ? 0 : p.cols - c0;
-        float v[Q_COLS];
-        load16<T, VEC>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx) + c0, n, v);
+        float y[Q_COLS];
+        load16<T, VEC>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + c0), sr < 0 ? 0 : p.cols - c0, y);
         // the maximum over the magnitudes' bits: exact, and a NaN or infinity stays visible
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < Q_COLS; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < Q_COLS; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
         if (MX) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const bool bad = m >= 0x7F800000u;
         if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
         uint32_t byte;
-        float y[Q_COLS];
         if (MX) {
             // floor(log2 a) is a's exponent field; below 2^-125 the scale stays at 2^-127
             byte = bad ? 255u : (uint32_t)max((int)(m >> 23) - 2, 0);
             const float inv = __uint_as_float(byte < 254u ? (254u - byte) << 23 : 0x00400000u);
 #pragma unroll
-            for (int e = 0; e < Q_COLS; ++e) y[e] = v[e] * inv;   // exact: a power of two
+            for (int e = 0; e < Q_COLS; ++e) y[e] *= inv;   // exact: a power of two
         } else {
             const float a = __uint_as_float(m);
             byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(a / (6.0f * g), __NV_SATFINITE, __NV_E4M3);
@@ -122,20 +122,24 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
                 const float inv = 1.0f / d;
 #pragma unroll
                 for (int e = 0; e < Q_COLS; ++e) {
-                    const float q = v[e] * inv;
-                    y[e] = fmaf(fmaf(-q, d, v[e]), inv, q);
+                    const float q = y[e] * inv;
+                    y[e] = fmaf(fmaf(-q, d, y[e]), inv, q);
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < Q_COLS; ++e) y[e] = v[e] / d;
+                for (int e = 0; e < Q_COLS; ++e) y[e] = y[e] / d;
             }
         }
         if (c0 < 2 * p.pitch)
             *reinterpret_cast<uint2*>(p.codes + r * p.pitch + c0 / 2) = make_uint2(to_codes(y), to_codes(y + 8));
         // scales up to the end of the last tile: blocks past the columns get a zero byte
-        const int64_t b = MX ? chunk >> 1 : chunk;
-        if (b < 4 * p.tiles_k && !(MX && (chunk & 1)))
-            p.scales[fp4_scale_at(r, b, p.tiles_k)] = b * (MX ? 32 : 16) < p.cols ? (uint8_t)byte : (uint8_t)0;
+        constexpr int LANES = MX ? 2 : 1;   // threads per block
+        const int64_t b = chunk / LANES;
+        uint32_t word = b * (MX ? 32 : 16) < p.cols ? byte : 0u;
+        word |= __shfl_down_sync(0xffffffffu, word, LANES) << 8;
+        word |= __shfl_down_sync(0xffffffffu, word, 2 * LANES) << 16;
+        if (chunk % (4 * LANES) == 0 && b < 4 * p.tiles_k)
+            *reinterpret_cast<uint32_t*>(p.scales + fp4_scale_at(r, b, p.tiles_k)) = word;
     }
 }
 
@@ -156,40 +160,48 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// One thread writes 16 consecutive bytes (4 fp32 or 8 bf16 columns), so a warp's store is one run of
+// whole sectors; DQ_ROWS rows in flight. Bound by the bytes written.
+constexpr int DQ_ROWS = 4;
 template <typename T, bool MX, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParams p) {
-    const int64_t chunk = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
-    const int64_t c0 = chunk * Q_COLS, n = p.cols - c0;
+    constexpr int C = 16 / sizeof(T);
+    const int64_t c0 = ((int64_t)blockIdx.x * Q_THREADS + threadIdx.x) * C, n = p.cols - c0;
     if (n <= 0) return;
     const float g = MX ? 1.0f : *p.g;
-    for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p.codes + r * p.pitch + c0 / 2);
-        const uint32_t sb = p.scales[fp4_scale_at(r, MX ? chunk >> 1 : chunk, p.tiles_k)];
-        const float s = MX ? e8m0_value(sb) : e4m3_value(sb) * g;
-        float v[Q_COLS];
+    const int64_t b = c0 / (MX ? 32 : 16);
+    for (int64_t r0 = (int64_t)blockIdx.y * DQ_ROWS; r0 < p.rows; r0 += (int64_t)gridDim.y * DQ_ROWS) {
+        uint32_t w[DQ_ROWS], sb[DQ_ROWS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 f = e2m1_values(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xFFu);
-            v[2 * e] = f.x * s;
-            v[2 * e + 1] = f.y * s;
+        for (int i = 0; i < DQ_ROWS; ++i) {
+            const int64_t r = min(r0 + i, p.rows - 1);
+            const uint8_t* src = p.codes + r * p.pitch + c0 / 2;
+            w[i] = C == 8 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
+            sb[i] = p.scales[fp4_scale_at(r, b, p.tiles_k)];
         }
-        T* y = static_cast<T*>(p.Y) + r * p.ldy + c0;
-        if (VEC && n >= Q_COLS) {
-            if (sizeof(T) == 4) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    reinterpret_cast<float4*>(y)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        for (int i = 0; i < DQ_ROWS; ++i) {
+            if (r0 + i >= p.rows) break;
+            const float s = MX ? e8m0_value(sb[i]) : e4m3_value(sb[i]) * g;
+            float v[C];
+#pragma unroll
+            for (int e = 0; e < C / 2; ++e) {
+                const float2 f = e2m1_values((w[i] >> (8 * e)) & 0xFFu);
+                v[2 * e] = f.x * s;
+                v[2 * e + 1] = f.y * s;
+            }
+            T* y = static_cast<T*>(p.Y) + (r0 + i) * p.ldy + c0;
+            if (VEC && n >= C) {
+                if constexpr (C == 4)
+                    *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+                else
+                    *reinterpret_cast<uint4*>(y) =
+                        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
             } else {
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    reinterpret_cast<uint4*>(y)[q] =
-                        make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                                   pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+                for (int e = 0; e < C; ++e)
+                    if (e < n) store_elem(y + e, v[e]);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < Q_COLS; ++e)
-                if (e < n) store_elem(y + e, v[e]);
         }
     }
 }
@@ -239,6 +251,13 @@ bool bad_format(int f) { return f != GPTQ_MXFP4 && f != GPTQ_NVFP4; }
 bool bad_dtype(int t) { return t != GPTQ_F32 && t != GPTQ_BF16; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int64_t kMaxDim = (1ll << 31) - 256;
+
+// CTAs along the rows: enough to fill the device, each looping over the rest (a CTA per few rows spends
+// as long starting as copying)
+unsigned rows_grid(int64_t groups, int64_t ctas_x, int per_sm) {
+    const int64_t want = std::max<int64_t>(1, ceil_div((int64_t)device_sm_count() * per_sm, ctas_x));
+    return (unsigned)std::min<int64_t>(groups, std::min<int64_t>(want, 65535));
+}
 
 }  // namespace
 }  // namespace gptq
@@ -290,7 +309,7 @@ extern "C" int gptq_fp4_quantize(const void* X, int dtype, int64_t src_rows, int
     GPTQ_CUDA_TRY(st.begin(s));
     QParams p{X, rows, cols, ldx, src_rows, index, (int)per, g, codes, scales, fp4_pitch(cols), fp4_tiles(cols, format), st.word};
     const int64_t chunks = ceil_div(p.tiles_k * 4 * fp4_block(format), Q_COLS);
-    const dim3 grid((unsigned)ceil_div(chunks, Q_THREADS), (unsigned)std::min<int64_t>(rows, 32768));
+    const dim3 grid((unsigned)ceil_div(chunks, Q_THREADS), rows_grid(rows, ceil_div(chunks, Q_THREADS), 64));
     const int64_t esize = dtype == GPTQ_BF16 ? 2 : 4;
     const bool vec = aligned16(X) && (ldx * esize) % 16 == 0, mx = format == GPTQ_MXFP4;
     auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_QUANT, s, kern<<<grid, Q_THREADS, 0, s>>>(p)); };
@@ -314,8 +333,8 @@ extern "C" int gptq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
         return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DqParams p{codes, scales, g, rows, cols, fp4_pitch(cols), fp4_tiles(cols, format), Y, ldy};
-    const dim3 grid((unsigned)ceil_div(ceil_div(cols, Q_COLS), Q_THREADS), (unsigned)std::min<int64_t>(rows, 32768));
     const int64_t esize = dtype == GPTQ_BF16 ? 2 : 4;
+    const dim3 grid((unsigned)ceil_div(cols * esize, 16 * Q_THREADS), rows_grid(ceil_div(rows, DQ_ROWS), ceil_div(cols * esize, 16 * Q_THREADS), 32));
     const bool vec = aligned16(Y) && (ldy * esize) % 16 == 0, mx = format == GPTQ_MXFP4;
     auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_DEQUANT, s, kern<<<grid, Q_THREADS, 0, s>>>(p)); };
     if (dtype == GPTQ_BF16) {
