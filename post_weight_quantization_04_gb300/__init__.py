@@ -119,8 +119,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             raise RuntimeError(f"libgptq.so not built ({path}); run post_weight_quantization_04_gb300.build")
         lib = ctypes.CDLL(path)
         _declare(lib)
+        _setup_call(lib)
         _lib = lib
     return _lib
+
+
+def _setup_call(lib: ctypes.CDLL) -> None:
+    """Hands the C module of the serving calls what it needs: torch's types and the library's entry points."""
+    from . import _call
+    names = ("gptq_fp4_quantize", "gptq_fp4_dequantize", "gptq_fp4_matmul", "gptq_expert_sort_workspace_bytes",
+             "gptq_expert_sort", "gptq_expert_gather", "gptq_expert_combine", "gptq_expert_combine_grad")
+    _call.setup({"float32": torch.float32, "bfloat16": torch.bfloat16, "uint8": torch.uint8, "int32": torch.int32,
+                 "empty": torch.empty, "raw_stream": _current_raw_stream, "current_device": _current_device,
+                 "Fp4": Fp4, "Route": Route, "check": _check},
+                {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names})
+    globals()["_fast"] = _call
 
 
 def _str(status: int) -> str:
@@ -473,9 +486,17 @@ def gptq_fp4_scale_bytes(rows: int, cols: int, format: str) -> int:
     return int(load().gptq_fp4_scale_bytes(rows, cols, _fp4_format(format)))
 
 
-# The calls of a serving step are short, so their argument checks are kept to a few attribute reads:
-# a matrix is described once, addresses go to ctypes as plain integers, and the current stream is
-# read without a Stream object.
+# The calls of a serving step are short. Their common form (results allocated here, on the current
+# stream) goes through the C module _call, which returns NotImplemented for what it does not
+# recognise; the functions below then check in Python, and raise.
+_fast = None
+
+
+def _load_fast():
+    load()
+    return _fast
+
+
 _DTYPES = {torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -549,6 +570,10 @@ def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optiona
     """X (bf16 or fp32, any row stride) in the microscaled 4-bit form. index (int32): row r is X row
     index[r] // per, zeros where index[r] < 0 (a Route's src with per = top gathers the experts' rows
     in the same pass). "nv" without a tensor scale takes gptq_fp4_tensor_scale(X)."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).quantize(X, format, tensor_scale, index, per)
+        if r is not NotImplemented:
+            return r
     f = _fp4_format(format)
     dt, n, cols, ld = _matrix(X, "X")
     rows = n
@@ -580,6 +605,10 @@ def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optiona
 
 def gptq_fp4_dequantize(q: Fp4, dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values that q's codes and scales stand for."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).dequantize(q, dtype)
+        if r is not NotImplemented:
+            return r
     f = _check_fp4(q, "q")
     dt = _DTYPES.get(dtype)
     if dt is None:
@@ -609,6 +638,10 @@ def gptq_fp4_matmul(X: Fp4, W: Fp4, offsets: Optional[torch.Tensor] = None, relu
     """Y = X W^T (optionally max(., 0)) of two matrices in the microscaled 4-bit form. With offsets
     (int32, experts + 1, a Route's) W holds one weight per expert and rows offsets[e]..offsets[e+1]
     of X use weight e; rows in no expert's range give zeros."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).matmul(X, W, offsets, relu, out_dtype)
+        if r is not NotImplemented:
+            return r
     f = _check_fp4(X, "X")
     experts = 1
     if offsets is None:
@@ -654,6 +687,10 @@ def gptq_expert_sort_workspace_bytes(tokens: int, top: int, experts: int) -> int
 def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor] = None, stream=None) -> Route:
     """ids (tokens, top) int32, each slot's expert (negative: dropped) -> the slots' places, stably
     sorted by expert."""
+    if ws is None and stream is None:
+        r = (_fast or _load_fast()).sort(ids, experts)
+        if r is not NotImplemented:
+            return r
     _dev(ids, torch.int32, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, top)")
@@ -683,6 +720,10 @@ def _check_route(route: Route) -> Tuple[int, int]:
 
 def gptq_expert_gather(X: torch.Tensor, route: Route, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The tokens' rows in the order of their experts (tokens * top rows, zeros past the live ones)."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).gather(X, route)
+        if r is not NotImplemented:
+            return r
     tokens, top = _check_route(route)
     dt, rows, d, ld = _matrix(X, "X")
     if rows != tokens:
@@ -698,6 +739,10 @@ def gptq_expert_gather(X: torch.Tensor, route: Route, out: Optional[torch.Tensor
 def gptq_expert_combine(Ys: torch.Tensor, route: Route, weights: Optional[torch.Tensor],
                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t][j] * the row of slot (t, j), in fp32, rounded once; weights None: 1."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).combine(Ys, route, weights)
+        if r is not NotImplemented:
+            return r
     tokens, top = _check_route(route)
     dt, rows, d, ld = _matrix(Ys, "Ys")
     if rows != tokens * top:
@@ -721,6 +766,10 @@ def gptq_expert_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, route: Route, w
                              out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
                              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The gradients of gptq_expert_combine: (dYs, dweights)."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).combine_grad(dY, Ys, route, weights)
+        if r is not NotImplemented:
+            return r
     tokens, top = _check_route(route)
     dt, rows, d, ld = _matrix(Ys, "Ys")
     if rows != tokens * top:

@@ -1,7 +1,7 @@
-"""Build libgptq.so in-tree with nvcc for sm_103a (GB300).
+"""Build libgptq.so in-tree with nvcc for sm_103a (GB300), and the binding's C module.
 
 Each CUDA translation unit is compiled in parallel, then linked into one shared
-library next to this file. Run as a module (``python -m
+library next to this file; csrc/call.c becomes the extension module _call. Run as a module (``python -m
 post_weight_quantization_04_gb300.build``) or call :func:`build`.
 """
 from __future__ import annotations
@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgptq.so")
+CALL = os.path.join(HERE, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["hessian.cu", "prepare.cu", "quantize.cu", "sgemm.cu", "tc_gemm.cu", "dequant_matmul.cu", "profile.cu",
            "status.cu", "fp4.cu", "fp4_matmul.cu", "expert.cu"]
@@ -40,7 +42,7 @@ def _newer(src_paths, out) -> bool:
 
 
 def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = False) -> str:
-    """Compile every .cu under csrc/ and link libgptq.so; returns the library path."""
+    """Compile every .cu under csrc/ and link libgptq.so, and compile _call; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
@@ -56,6 +58,11 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
             if ptxas_verbose:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
+
+    call_src = os.path.join(CSRC, "call.c")
+    if force or _newer([call_src, os.path.join(INCLUDE, "gptq.h"), __file__], CALL):
+        jobs.append([shutil.which("gcc") or "cc", "-O2", "-std=c11", "-fPIC", "-shared", "-I", INCLUDE, "-I",
+                     sysconfig.get_paths()["include"], call_src, "-o", CALL])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
