@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(32 * WARPS) expert_place_kernel(const SParams 
     for (int i = threadIdx.x; i < WARPS * p.experts; i += THREADS) cnt[i] = 0;
     if (threadIdx.x == 0) carry = 0;
     __syncthreads();
+    pdl_trigger();   // the gather's launch
     int64_t b, e;
     warp_share<WARPS>(p, &b, &e);
     count_slots(p, b, e, cnt + warp * p.experts);
@@ -249,6 +250,7 @@ template <typename U>
 __global__ void __launch_bounds__(R_THREADS) expert_gather_kernel(const RParams p, int64_t units, int chunks, int64_t main_ctas) {
     const U* X = static_cast<const U*>(p.X);
     U* Y = static_cast<U*>(p.Y);
+    pdl_wait();
     if (blockIdx.x >= main_ctas) {   // the rows past the last live one
         const int64_t n = gridDim.x - main_ctas;
         const U zero = {};
@@ -480,11 +482,14 @@ extern "C" int gptq_expert_gather(const void* X, int dtype, int64_t tokens, int6
     const int64_t chunks = ceil_div(units, R_THREADS), main_ctas = tokens * chunks;
     if (main_ctas > kMaxSlots) return GPTQ_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)(main_ctas + tail_ctas(p.slots));
-    auto go = [&](auto kern) { GPTQ_LAUNCH(K_EXPERT_GATHER, s, kern<<<grid, R_THREADS, 0, s>>>(p, units, (int)chunks, main_ctas)); };
+    cudaError_t e = cudaSuccess;
+    auto go = [&](auto kern) {
+        GPTQ_LAUNCH(K_EXPERT_GATHER, s, e = launch_pdl(kern, dim3(grid), dim3(R_THREADS), 0, s, p, units, (int)chunks, main_ctas));
+    };
     if (vec) go(expert_gather_kernel<uint4>);
     else if (es == 2) go(expert_gather_kernel<uint16_t>);
     else go(expert_gather_kernel<uint32_t>);
-    GPTQ_LAUNCH_CHECK();
+    GPTQ_CUDA_TRY(e);
     return st.finish(s);
 }
 

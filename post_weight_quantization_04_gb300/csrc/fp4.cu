@@ -81,6 +81,7 @@ template <typename T, bool MX, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p) {
     const int64_t chunk = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
     const int64_t c0 = chunk * Q_COLS;
+    pdl_trigger();   // the product's or the inverse's prologue may begin
     const float g = MX ? 1.0f : *p.g;
     for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
         int64_t sr = r;
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParam
     constexpr int C = 16 / sizeof(T);
     const int64_t c0 = ((int64_t)blockIdx.x * Q_THREADS + threadIdx.x) * C, n = p.cols - c0;
     if (n <= 0) return;
+    pdl_wait();
     const float g = MX ? 1.0f : *p.g;
     const int64_t b = c0 / (MX ? 32 : 16);
     for (int64_t r0 = (int64_t)blockIdx.y * DQ_ROWS; r0 < p.rows; r0 += (int64_t)gridDim.y * DQ_ROWS) {
@@ -336,7 +338,8 @@ extern "C" int gptq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
     const int64_t esize = dtype == GPTQ_BF16 ? 2 : 4;
     const dim3 grid((unsigned)ceil_div(cols * esize, 16 * Q_THREADS), rows_grid(ceil_div(rows, DQ_ROWS), ceil_div(cols * esize, 16 * Q_THREADS), 32));
     const bool vec = aligned16(Y) && (ldy * esize) % 16 == 0, mx = format == GPTQ_MXFP4;
-    auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_DEQUANT, s, kern<<<grid, Q_THREADS, 0, s>>>(p)); };
+    cudaError_t e = cudaSuccess;
+    auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_DEQUANT, s, e = launch_pdl(kern, grid, dim3(Q_THREADS), 0, s, p)); };
     if (dtype == GPTQ_BF16) {
         if (mx) vec ? go(fp4_dequantize_kernel<__nv_bfloat16, true, true>) : go(fp4_dequantize_kernel<__nv_bfloat16, true, false>);
         else vec ? go(fp4_dequantize_kernel<__nv_bfloat16, false, true>) : go(fp4_dequantize_kernel<__nv_bfloat16, false, false>);
@@ -344,7 +347,7 @@ extern "C" int gptq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, 
         if (mx) vec ? go(fp4_dequantize_kernel<float, true, true>) : go(fp4_dequantize_kernel<float, true, false>);
         else vec ? go(fp4_dequantize_kernel<float, false, true>) : go(fp4_dequantize_kernel<float, false, false>);
     }
-    GPTQ_LAUNCH_CHECK();
+    GPTQ_CUDA_TRY(e);
     return GPTQ_OK;
 }
 

@@ -60,6 +60,7 @@ struct Maps {
 };
 
 struct MParams {
+    const uint8_t *xc, *xs, *wc, *ws;
     const float *xg, *wg;
     int T, N, K;
     int tiles_k;
@@ -86,6 +87,17 @@ __device__ __forceinline__ void expert_rows(const MParams& p, int e, int* lo, in
     if (l != a || h != b) set_status(p.status, GPTQ_ERR_INVALID_ARG);
     *lo = l;
     *hi = h;
+}
+
+// rows that belong to no expert are zero (ranges that were clamped are an error)
+__device__ __forceinline__ void zero_tail(const MParams& p, int64_t i, int64_t step) {
+    const int live = min(max(p.offsets[p.experts], 0), p.T);
+    const int64_t n = (int64_t)(p.T - live) * p.N;
+    for (; i < n; i += step) {
+        const int64_t at = (live + i / p.N) * p.ldy + i % p.N;
+        if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(0.0f);
+        else static_cast<float*>(p.Y)[at] = 0.0f;
+    }
 }
 
 // Token tiles of rows [lo, hi). They start on multiples of 64, where the tokens' scales may start in
@@ -339,13 +351,19 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         mbar_init(drain_bar, 1);
         fence_barrier_init();
     }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&m.w);
+        tma_prefetch_desc(&m.x);
+        tma_prefetch_desc(&m.ws);
+        tma_prefetch_desc(&m.xs);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(M_TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();   // from here on memory that the kernel before writes or reads is touched
     if (warp == 0) {
-        if (lane == 0) {
-            tma_prefetch_desc(&m.w);
-            tma_prefetch_desc(&m.x);
-            tma_prefetch_desc(&m.ws);
-            tma_prefetch_desc(&m.xs);
-        }
         // token tiles before each expert
         int carry = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
@@ -362,11 +380,6 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
             carry += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) start[p.experts] = carry;
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(M_TMEM)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -496,16 +509,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         const int c0 = M_T / 2 * ((warp - 2) >> 2);   // its half of the columns
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         const uint32_t turn = sbase + NS * S::BYTES + (warp - 2) * M_TURN;
-        // rows that belong to no expert are zero (ranges that were clamped are an error)
-        if (p.offsets) {
-            const int live = min(max(p.offsets[p.experts], 0), p.T);
-            const int64_t n = (int64_t)(p.T - live) * p.N;
-            for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x - 64; i < n; i += (int64_t)gridDim.x * 256) {
-                const int64_t at = (live + i / p.N) * p.ldy + i % p.N;
-                if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(0.0f);
-                else static_cast<float*>(p.Y)[at] = 0.0f;
-            }
-        }
+        if (p.offsets) zero_tail(p, (int64_t)blockIdx.x * 256 + threadIdx.x - 64, (int64_t)gridDim.x * 256);
         const float gx = MX ? 1.0f : *p.xg;
         uint32_t tile = 0;
         for (uint32_t i = first; i < ntiles; i += step, ++tile) {
@@ -559,8 +563,153 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     }
 }
 
+// ------------------------------------------------------------------------------- few rows
+// With a handful of tokens the product is the stream of the weights, and what counts is to have all of
+// it in flight at once. A CTA of 128 threads computes 8 features: a thread takes 32 columns (16 bytes of
+// codes) of each feature and of up to 4 tokens, every 128th such piece. Codes become half2 (one
+// conversion per byte), and the products of 16 columns are summed in half2: each is a multiple of
+// 1/4 up to 36, so 8 of them per half stay below 512 in steps of 1/4, which 11 bits hold exactly. Those
+// sums go to fp32 with the product of both scales (at most 8 bits), and are added over the columns
+// and, in a fixed order, over the CTA.
+// The 8 features are two neighbours of each 32-row quarter of a scale tile, whose scales share sectors.
+constexpr int F_THREADS = 128, F_FEATURES = 8, F_TOKENS = 4;
+
+__device__ __forceinline__ void to_half2(const uint4& c, __half2 (&h)[16]) {
+    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        h[i] = __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((u[i >> 2] >> (8 * (i & 3))) & 0xFFu), __NV_E2M1));
+}
+
+// the scales of 32 columns from a word of a scale tile: one (MX) or two (NV); c: index of the 32 columns
+template <bool MX>
+__device__ __forceinline__ float2 two_scales(uint32_t word, int c) {
+    if (MX) {
+        const float s = e8m0_value((word >> (8 * (c & 3))) & 0xFFu);
+        return make_float2(s, s);
+    }
+    const uint32_t b = word >> (16 * (c & 1));
+    return make_float2(e4m3_value(b & 0xFFu), e4m3_value((b >> 8) & 0xFFu));
+}
+
+// byte of the 16-byte row (4 quarters x 4 blocks) of scale tiles for row r and 32 columns c
+template <bool MX>
+__device__ __forceinline__ int64_t scale_row(int64_t r, int c, int tiles_k) {
+    return ((r >> 7) * tiles_k + c / (MX ? 4 : 2)) * kFp4Tile + (r & 31) * 16;
+}
+
+// tokens t0 .. t0 + n - 1 (n <= NT) of expert e times features fb + (i & 1) + 32 (i >> 1), i < 8
+template <bool MX, int NT>
+__device__ __forceinline__ void few_rows(const MParams& p, int e, int t0, int n, int fb, float (*part)[F_FEATURES * F_TOKENS]) {
+    const int64_t pitch = fp4_pitch(p.K);
+    const uint8_t* wc = p.wc + (int64_t)e * p.N * pitch;
+    const uint8_t* ws = p.ws + (int64_t)e * p.row_blocks * p.tiles_k * kFp4Tile;
+    float acc[F_FEATURES][NT] = {};
+    for (int c = threadIdx.x; c < (int)(pitch >> 4); c += F_THREADS) {
+        uint4 w[F_FEATURES], x[NT], sw[2];
+        uint32_t sx[NT];
+#pragma unroll
+        for (int i = 0; i < F_FEATURES; ++i) {
+            const int f = min(fb + (i & 1) + 32 * (i >> 1), p.N - 1);
+            w[i] = __ldg(reinterpret_cast<const uint4*>(wc + f * pitch) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sw[i] = __ldg(reinterpret_cast<const uint4*>(ws + scale_row<MX>(fb + i, c, p.tiles_k)));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = t0 + min(t, n - 1);
+            x[t] = __ldg(reinterpret_cast<const uint4*>(p.xc + r * pitch) + c);
+            sx[t] = __ldg(reinterpret_cast<const uint32_t*>(p.xs + scale_row<MX>(r, c, p.tiles_k)) + ((r >> 5) & 3));
+        }
+        __half2 xh[NT][16];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) to_half2(x[t], xh[t]);
+#pragma unroll
+        for (int i = 0; i < F_FEATURES; ++i) {
+            __half2 wh[16];
+            to_half2(w[i], wh);
+            const uint4& s4 = sw[i & 1];
+            const float2 sc = two_scales<MX>(i < 2 ? s4.x : i < 4 ? s4.y : i < 6 ? s4.z : s4.w, c);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                __half2 h0 = __hmul2(wh[0], xh[t][0]), h1 = __hmul2(wh[8], xh[t][8]);
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                    h0 = __hfma2(wh[k], xh[t][k], h0);
+                    h1 = __hfma2(wh[8 + k], xh[t][8 + k], h1);
+                }
+                const float2 f0 = __half22float2(h0), f1 = __half22float2(h1), st = two_scales<MX>(sx[t], c);
+                if (MX) acc[i][t] = fmaf((f0.x + f0.y) + (f1.x + f1.y), sc.x * st.x, acc[i][t]);
+                else acc[i][t] = fmaf(f1.x + f1.y, sc.y * st.y, fmaf(f0.x + f0.y, sc.x * st.x, acc[i][t]));
+            }
+        }
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < F_FEATURES; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float v = acc[i][t];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) part[warp][i * NT + t] = v;
+        }
+    __syncthreads();
+    if (threadIdx.x < F_FEATURES * NT) {
+        const int i = threadIdx.x / NT, t = threadIdx.x % NT, f = fb + (i & 1) + 32 * (i >> 1);
+        float v = 0.0f;
+        for (int k = 0; k < F_THREADS / 32; ++k) v += part[k][threadIdx.x];
+        if (!MX) v *= *p.xg * p.wg[e * p.wg_stride];
+        if (p.relu) v = fmaxf(v, 0.0f);
+        if (f < p.N && t < n) {
+            const int64_t at = (int64_t)(t0 + t) * p.ldy + f;
+            if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(v);
+            else static_cast<float*>(p.Y)[at] = v;
+        }
+    }
+    __syncthreads();
+}
+
+// MOST: the most tokens at a time; a kernel that cannot take four has the registers of one that is not
+// made to, so more of its CTAs fit
+template <bool MX, int MOST>
+__global__ void __launch_bounds__(F_THREADS) fp4_few_rows_kernel(const MParams p) {
+    __shared__ float part[F_THREADS / 32][F_FEATURES * F_TOKENS];
+    const int e = blockIdx.y;
+    pdl_wait();
+    if (e == p.experts) {   // (only with offsets)
+        zero_tail(p, (int64_t)blockIdx.x * F_THREADS + threadIdx.x, (int64_t)gridDim.x * F_THREADS);
+        return;
+    }
+    int lo, hi;
+    expert_rows(p, e, &lo, &hi);
+    const int fb = (int)(blockIdx.x >> 4) * 128 + (int)(blockIdx.x & 15) * 2;
+    for (int t = lo; t < hi;) {
+        const int n = hi - t;
+        if (MOST >= 4 && n >= 3) {
+            few_rows<MX, 4>(p, e, t, min(n, 4), fb, part);
+            t += 4;
+        } else if (MOST >= 2 && n >= 2) {
+            few_rows<MX, 2>(p, e, t, 2, fb, part);
+            t += 2;
+        } else {
+            few_rows<MX, 1>(p, e, t, 1, fb, part);
+            t += 1;
+        }
+    }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int64_t kMaxDim = (1ll << 31) - 512;
+
+// Whether the kernel for few rows is the faster one. Its time grows with the weights it reads and,
+// token by token, expands and multiplies; the other one's with the columns alone while its tiles
+// fit the device. Measured (us, few rows / pairs; MX):
+//   4096 x 4096   1 token 4.1 / 7.3   2 tokens 5.9 / 7.2   4 tokens 9.3 / 7.3
+//   14336 x 4096  1 token 11.6 / 9.8      1024 x 4096  4 tokens 5.1 / 7.3   8 tokens 8.5 / 7.3
+bool few_rows_pay(int64_t T, int64_t N, int64_t K, int64_t experts) {
+    return T <= 4 && (std::min(experts, T) + T) * N * K <= 60000000;
+}
 
 bool code_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t pitch, int box_rows) {
     auto enc = tma_encoder();
@@ -586,6 +735,19 @@ bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t tiles_k, int64_t b
 }
 
 template <bool MX>
+int launch_few(const MParams& p, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    const dim3 grid((unsigned)(16 * p.row_blocks), (unsigned)(p.experts + (p.offsets ? 1 : 0)));
+    // (with experts the rows of each are not known here: mostly one or two)
+    auto go = [&](auto kern) { GPTQ_LAUNCH(K_FP4_MM, s, e = launch_pdl(kern, grid, dim3(F_THREADS), 0, s, p)); };
+    if (p.T == 1) go(fp4_few_rows_kernel<MX, 1>);
+    else if (p.T == 2 || p.offsets) go(fp4_few_rows_kernel<MX, 2>);
+    else go(fp4_few_rows_kernel<MX, 4>);
+    GPTQ_CUDA_TRY(e);
+    return GPTQ_OK;
+}
+
+template <bool MX>
 int launch(const Maps& m, const MParams& p, int64_t most_tiles, cudaStream_t s) {
     const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * M_TURN + 8 * (2 * Stage<MX>::N + 5) + 8 + 4 * (p.experts + 1);
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -594,13 +756,15 @@ int launch(const Maps& m, const MParams& p, int64_t most_tiles, cudaStream_t s) 
     cfg.blockDim = dim3(M_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t e = cudaSuccess;
     GPTQ_LAUNCH(K_FP4_MM, s, e = cudaLaunchKernelEx(&cfg, fp4_matmul_kernel<MX>, m, p));
     GPTQ_CUDA_TRY(e);
@@ -629,15 +793,20 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
         return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t pitch = fp4_pitch(K), tiles_k = fp4_tiles(K, format), row_blocks = ceil_div(N, 128);
+    const bool few = few_rows_pay(T, N, K, experts);
     const int ka = format == GPTQ_MXFP4 ? Stage<true>::KA : Stage<false>::KA;
     Maps m;
-    if (!code_map(&m.w, w_codes, experts * N, pitch, M_F) || !code_map(&m.x, x_codes, T, pitch, M_T / 2) ||
+    if (!few && (!code_map(&m.w, w_codes, experts * N, pitch, M_F) || !code_map(&m.x, x_codes, T, pitch, M_T / 2) ||
         !code_map(&m.xsmall, x_codes, T, pitch, M_TBOX) || !scale_map(&m.ws, w_scales, tiles_k, experts * row_blocks, ka, 1) ||
-        !scale_map(&m.xs, x_scales, tiles_k, ceil_div(T, 128), ka, 2))
+        !scale_map(&m.xs, x_scales, tiles_k, ceil_div(T, 128), ka, 2)))
         return GPTQ_ERR_CUDA;
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
     MParams p{};
+    p.xc = x_codes;
+    p.xs = x_scales;
+    p.wc = w_codes;
+    p.ws = w_scales;
     p.xg = x_g;
     p.wg = w_g;
     p.T = (int)T;
@@ -655,6 +824,10 @@ extern "C" int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, 
     p.Y = Y;
     p.ldy = ldy;
     p.status = st.word;
+    if (few) {
+        const int rc = format == GPTQ_MXFP4 ? launch_few<true>(p, s) : launch_few<false>(p, s);
+        return rc != GPTQ_OK ? rc : st.finish(s);
+    }
     // an expert's first tile may start up to 63 rows early and its last one be partial
     const int64_t most = (ceil_div(T, M_T) + (offsets ? 2 * std::min(experts, T) : 0)) * p.ftiles;
     const int rc = format == GPTQ_MXFP4 ? launch<true>(m, p, most, s) : launch<false>(m, p, most, s);
