@@ -786,6 +786,26 @@ def gptq_expert_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, route: Route, w
     return dYs, dW
 
 
+def gptq_expert_mlp(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W_up: Fp4, W_down: Fp4,
+                    up_scale: Optional[torch.Tensor] = None, down_scale: Optional[torch.Tensor] = None):
+    """A layer of experts on microscaled 4-bit weights: y[t] = sum_j weights[t][j] *
+    W_down[e] relu(W_up[e] x[t]) with e = ids[t][j] (negative: dropped), activations quantised
+    to the weights' format before each product. X (tokens, d) bf16 or fp32; W_up, W_down: one
+    matrix per expert; up_scale, down_scale: the activations' "nv" tensor scales (None: taken
+    from the activations). Returns (y bf16, route, the experts' rows ys bf16), what
+    gptq_expert_combine_grad needs for the gradients of the router's weights. Host
+    orchestration only: every step runs in the library, on the current stream."""
+    route = gptq_expert_sort(ids, W_up.codes.shape[0])
+    top = ids.shape[1]
+    if W_up.format == "nv" and up_scale is None:
+        up_scale = gptq_fp4_tensor_scale(X)
+    xs = gptq_fp4_quantize(X, W_up.format, up_scale, index=route.src, per=top)
+    h = gptq_fp4_matmul(xs, W_up, offsets=route.offsets, relu=True, out_dtype=torch.bfloat16)
+    hs = gptq_fp4_quantize(h, W_down.format, down_scale)
+    ys = gptq_fp4_matmul(hs, W_down, offsets=route.offsets, out_dtype=torch.bfloat16)
+    return gptq_expert_combine(ys, route, weights), route, ys
+
+
 def gptq_status_string(status: int) -> str:
     return _str(status)
 
@@ -818,7 +838,7 @@ __all__ = [
     "Fp4", "MXFP4", "NVFP4", "gptq_fp4_code_pitch", "gptq_fp4_scale_bytes", "gptq_fp4_tensor_scale", "gptq_fp4_quantize",
     "gptq_fp4_dequantize", "gptq_fp4_tile_scales", "gptq_fp4_matmul", "Route", "gptq_expert_sort",
     "gptq_expert_sort_workspace_bytes", "gptq_expert_gather", "gptq_expert_gather_grad", "gptq_expert_combine",
-    "gptq_expert_combine_grad",
+    "gptq_expert_combine_grad", "gptq_expert_mlp",
     "set_status_mode", "status_sync", "deferred_status", "STATUS_SYNC", "STATUS_DEFERRED",
     "EXPORTS", "LIB_PATH",
 ]

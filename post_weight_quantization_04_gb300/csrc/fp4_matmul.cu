@@ -158,12 +158,24 @@ __device__ __forceinline__ bool elect_one() {
 // that gave up has to record is done after the loops, because a global atomic (or the load of its
 // limit) in them cost the warps that feed the tensor core more than the waiting itself
 // (8192 x 8192 x 8192 MX: 225 us with mbar_wait, 155 us with this).
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, uint64_t limit) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if (__any_sync(0xffffffffu, globaltimer_ns() - t0 >= limit)) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     }
 }
 
@@ -183,7 +195,7 @@ __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
 
 // What these arrivals order is TMEM and copies by TMA, neither written by this thread, so the default
 // (CTA) scope of the release is enough; .release.cluster would wait for the thread's own earlier
-// stores of Y to be acknowledged (measured: WHAT).
+// stores of Y to be acknowledged (8192 x 8192 x 8192 MX took 408 us with it and 269 without).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -233,13 +245,13 @@ __device__ __forceinline__ uint32_t fp4_idesc(int n, uint32_t sf) {
            ((uint32_t)(M_PF >> 4) << 24) | (sf << 29);
 }
 
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, int* status) {
+// Waits for the phase of a barrier that counts copies or MMAs in flight, before the CTA leaves. They land
+// within microseconds; the limit is for an unwinding pair, whose even CTA's stages may also be
+// waiting for a word from the odd one that is not coming.
+constexpr uint64_t M_DRAIN_NS = 20000000ull;
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            set_status(status, GPTQ_ERR_TIMEOUT);
-            return;
-        }
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < M_DRAIN_NS) {
     }
 }
 
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         }
         if (leader)
             for (int s = 0; s < NS; ++s)
-                if (issued & (1u << s)) drain(full(s), (issued_par >> s) & 1u, p.status);
+                if (issued & (1u << s)) drain(full(s), (issued_par >> s) & 1u);
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         // ------------------------------- MMA issuer ---------------------------------
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         }
         if (elect_one()) {
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_bar) : "memory");
-            drain(drain_bar, 0, p.status);
+            drain(drain_bar, 0);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -169,7 +169,7 @@ PRODUCTS = [
     # T, N, K
     (1, 1, 1), (1, 16, 32), (1, 4096, 512), (2, 129, 96), (7, 333, 1000), (16, 128, 1056), (31, 250, 257), (33, 256, 300),
     (64, 512, 768), (77, 2310, 1000), (127, 129, 64), (128, 128, 256), (129, 257, 800), (200, 640, 1500), (300, 1000, 128),
-    (513, 300, 1024), (1030, 700, 448), (2100, 1300, 320),
+    (513, 300, 1024), (1030, 700, 448), (2100, 1300, 320), (3, 100, 2048), (4, 130, 1500), (2, 2310, 999), (5, 130, 1500),
 ]
 
 
@@ -238,6 +238,26 @@ def test_matmul_grouped(lib, sizes, tail, N, K, fmt, per_expert):
     for e in range(E):
         _check(Y[off[e]:off[e + 1]], xv[off[e]:off[e + 1]], ws[e][2], True, False, K)
     np.testing.assert_array_equal(Y[off[-1]:], 0)
+
+
+def test_matmul_bounded_waits_time_out_and_unwind(lib):
+    """With the library's test hook the waits of the pairs' pipeline give up at once: the product reports
+    GPTQ_ERR_TIMEOUT after unwinding, and the next call is as right as the one before."""
+    clib = lib.load()
+    rng = np.random.default_rng(9)
+    T, N, K = 300, 700, 2000
+    cx, bx, xv = _stored(rng, T, K, "mx", False, 1)
+    cw, bw, wv = _stored(rng, N, K, "mx", False, 1)
+    X, W = _fp4(lib, cx, bx, K, "mx", 1.0), _fp4(lib, cw, bw, K, "mx", 1.0)
+    ref = lib.gptq_fp4_matmul(X, W)
+    try:
+        assert clib.gptq_test_set_wait_limit_ns(0) == 0
+        with pytest.raises(lib.GptqError) as e:
+            lib.gptq_fp4_matmul(X, W)
+        assert e.value.status == 5
+    finally:
+        assert clib.gptq_test_set_wait_limit_ns(2_000_000_000) == 0
+    assert torch.equal(lib.gptq_fp4_matmul(X, W), ref)
 
 
 def test_matmul_reports_bad_offsets(lib):
