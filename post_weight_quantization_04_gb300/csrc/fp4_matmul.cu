@@ -8,7 +8,8 @@
 //
 // Two CTAs on neighbouring SMs (a cluster) work on one tile of 256 features x up to 192 tokens with
 // cta_group::2 MMAs: each holds its own 128 features, half of the tokens and all the tile's scales,
-// so a stage brings 28 KB of codes into each SM where a 128 x 192 tile of its own would take 40. Roles in each CTA (persistent, one per SM):
+// so a stage brings 28 KB of codes into each SM where a 128 x 192 tile of its own would take 40.
+// Roles in each CTA (persistent, one per SM):
 //   warp 0       producer: per stage of 256 columns four TMA copies, the 128 x 128-byte box of weight
 //                codes, that of token codes (128-byte swizzle), and the scale tiles of both
 //   warp 1       in the even CTA: scale tiles shared memory -> TMEM (tcgen05.cp, both CTAs) and the
@@ -20,6 +21,14 @@
 // TMEM: two buffers of sums, 192 columns (tokens) each, so one tile's sums are stored while the next
 // tile's MMAs run, and two stages' scales in turn in the columns from 384. (Tiles of 256 tokens leave
 // room for scales only if the two buffers overlap; waiting for the shared columns cost 1.2 us a tile.)
+//
+// What bounds it (8192 x 8192 x 8192): MX 152 us, 7.3 PFLOP/s; the tensor pipe needs 128 cycles for 64
+// columns of a 256 x 256 tile, 130 us here, the scale copies that run in the same pipe 10, the stores
+// of Y 10. NV 184 us, with twice the scale copies. Both are past the power limit when they
+// run for long (1.67 GHz at 1370 W: 16384 x 4096 x 14336 MX 283 us in short runs, 310 in long ones).
+// Taken back: 256-token tiles with overlapping buffers, 128 and 64 tokens (slower at every size from 256
+// tokens up), other tile orders, a cluster of 2 or 4 pairs sharing a tile's columns (slower but for
+// K = 14336).
 // Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits
 // for its own copies, the even one for the MMAs, and both meet before either leaves).
 #include <cuda_bf16.h>
@@ -462,6 +471,10 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = sbase + stage * S::BYTES;
+                // The scale copies need no wait of their own: the tensor pipe runs one thread's copies and MMAs
+                // in the order they were issued, and with two slots in turn a whole stage's MMAs lie
+                // between a slot's last reader and the copy that overwrites it. (Waiting for that
+                // reader all the same cost NV 16 % and MX 17 % at 8192 x 8192 x 8192, with the same results.)
                 const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
                 const int ka = min(S::KA, p.tiles_k - kt * S::KA);
                 const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
