@@ -112,23 +112,20 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
         } else {
             const float a = __uint_as_float(m);
             byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(a / (6.0f * g), __NV_SATFINITE, __NV_E4M3);
-            const float d = e4m3_value(byte) * g;
-            if (byte == 0u) {
+            // x / d correctly rounded (Markstein 1990: with inv = 1 / d correctly rounded, one residual
+            // step on x * inv rounds the quotient correctly), so a value on a midpoint of the grid is
+            // seen as one. x is first cut to 8 d, beyond which every quotient saturates, and both are
+            // brought near 1 by a power of two where d is far from it, so nothing overflows or
+            // vanishes on the way. A scale of zero (or past fp32) has zeros.
+            float d = e4m3_value(byte) * g;
+            const float f = d < 0x1p-60f ? 0x1p64f : d > 0x1p60f ? 0x1p-64f : 1.0f;
+            const bool none = d == 0.0f || d > 0x1.fffffep127f;
+            d *= f;
+            const float inv = 1.0f / d, most = 8.0f * d;
 #pragma unroll
-                for (int e = 0; e < Q_COLS; ++e) y[e] = 0.0f;
-            } else if (d > 0x1p-100f && d < 0x1p100f) {
-                // x / d correctly rounded (Markstein 1990: with inv = 1 / d correctly rounded, one
-                // residual step on x * inv rounds the quotient correctly), so a value on a
-                // midpoint of the grid is seen as one
-                const float inv = 1.0f / d;
-#pragma unroll
-                for (int e = 0; e < Q_COLS; ++e) {
-                    const float q = y[e] * inv;
-                    y[e] = fmaf(fmaf(-q, d, y[e]), inv, q);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < Q_COLS; ++e) y[e] = y[e] / d;
+            for (int e = 0; e < Q_COLS; ++e) {
+                const float x = fminf(fmaxf(y[e] * f, -most), most), q = x * inv;
+                y[e] = none ? 0.0f : fmaf(fmaf(-q, d, x), inv, q);
             }
         }
         if (c0 < 2 * p.pitch)
@@ -210,19 +207,23 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParam
 
 // max|x| of a matrix, as the bits of an fp32 (ordered like the numbers, so an integer atomic
 // maximum is exact and independent of order), into out[0], which starts at 0
-template <typename T>
-__global__ void __launch_bounds__(256) fp4_amax_kernel(const T* X, int64_t rows, int64_t cols, int64_t ldx,
-                                                       uint32_t* out, int* status) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(Q_THREADS) fp4_amax_kernel(const T* X, int64_t rows, int64_t cols, int64_t ldx,
+                                                             uint32_t* out, int* status) {
+    const int64_t c0 = ((int64_t)blockIdx.x * Q_THREADS + threadIdx.x) * Q_COLS;
     uint32_t m = 0;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < cols; c += (int64_t)gridDim.x * 256)
-            m = max(m, __float_as_uint(load_elem(X + r * ldx + c)) & 0x7FFFFFFFu);
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        float v[Q_COLS];
+        load16<T, VEC>(X + r * ldx + c0, cols - c0, v);
+#pragma unroll
+        for (int e = 0; e < Q_COLS; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    }
     m = __reduce_max_sync(0xffffffffu, m);
-    __shared__ uint32_t part[8];
+    __shared__ uint32_t part[Q_THREADS / 32];
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < 8; ++i) m = max(m, part[i]);
+        for (int i = 1; i < Q_THREADS / 32; ++i) m = max(m, part[i]);
         if (m >= 0x7F800000u) set_status(status, GPTQ_ERR_NONFINITE);
         atomicMax(out, m);
     }
@@ -284,11 +285,17 @@ extern "C" int gptq_fp4_tensor_scale(const void* X, int dtype, int64_t rows, int
     uint32_t* out = reinterpret_cast<uint32_t*>(g);
     GPTQ_CUDA_TRY(cudaMemsetAsync(out, 0, 4, s));
     if (rows > 0 && cols > 0) {
-        const dim3 grid((unsigned)std::min<int64_t>(ceil_div(cols, 1024), 64), (unsigned)std::min<int64_t>(rows, 2048));
-        if (dtype == GPTQ_BF16)
-            GPTQ_LAUNCH(K_FP4_AMAX, s, fp4_amax_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(X), rows, cols, ldx, out, st.word));
-        else
-            GPTQ_LAUNCH(K_FP4_AMAX, s, fp4_amax_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(X), rows, cols, ldx, out, st.word));
+        const int64_t ctas_x = ceil_div(cols, Q_COLS * Q_THREADS);
+        const dim3 grid((unsigned)ctas_x, rows_grid(rows, ctas_x, 16));
+        const bool vec = aligned16(X) && (ldx * (dtype == GPTQ_BF16 ? 2 : 4)) % 16 == 0;
+        auto go = [&](auto kern, auto* x) { GPTQ_LAUNCH(K_FP4_AMAX, s, kern<<<grid, Q_THREADS, 0, s>>>(x, rows, cols, ldx, out, st.word)); };
+        if (dtype == GPTQ_BF16) {
+            auto* x = static_cast<const __nv_bfloat16*>(X);
+            vec ? go(fp4_amax_kernel<__nv_bfloat16, true>, x) : go(fp4_amax_kernel<__nv_bfloat16, false>, x);
+        } else {
+            auto* x = static_cast<const float*>(X);
+            vec ? go(fp4_amax_kernel<float, true>, x) : go(fp4_amax_kernel<float, false>, x);
+        }
         GPTQ_LAUNCH_CHECK();
     }
     GPTQ_LAUNCH(K_FP4_AMAX, s, fp4_tensor_scale_kernel<<<1, 1, 0, s>>>(out));

@@ -139,6 +139,26 @@ def test_places_past_the_rows_are_reported(lib):
         assert e.value.status == 1
 
 
+@pytest.mark.parametrize("T", [40, 3000])
+def test_results_given_and_on_a_stream(lib, T):
+    """The forms with `out`, `ws` and `stream` give what the common form gives."""
+    _, r, x, ys, dy, w = _setup(lib, T, 3, 6, 96, "bf16")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ids = torch.tensor(_ids(T, 3, 6, T + 96), device=DEV)
+    nb = lib.gptq_expert_sort_workspace_bytes(T, 3, 6)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV) if nb else None
+    r2 = lib.gptq_expert_sort(ids, 6, ws=ws, stream=s)
+    xs = lib.gptq_expert_gather(x, r2, out=torch.empty_like(ys), stream=s)
+    y = lib.gptq_expert_combine(ys, r2, w, out=torch.empty_like(x), stream=s)
+    dys, dw = lib.gptq_expert_combine_grad(dy, ys, r2, w, out=(torch.empty_like(ys), torch.empty_like(w)), stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(r, r2))
+    ref = lib.gptq_expert_combine_grad(dy, ys, r, w)
+    assert torch.equal(xs, lib.gptq_expert_gather(x, r)) and torch.equal(y, lib.gptq_expert_combine(ys, r, w))
+    assert torch.equal(dys, ref[0]) and torch.equal(dw, ref[1])
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits(lib):
     """More than 2^31 elements of gathered rows: the last rows are as right as the first."""

@@ -84,6 +84,34 @@ def test_quantize_strides_and_extremes(lib, dtype):
         np.testing.assert_array_equal(npy(lib.gptq_fp4_dequantize(q)), v.astype(np.float32))
 
 
+@pytest.mark.parametrize("g", [1e-38, 2.0 ** -126, 3e-30, 1e-20, 1e20, 2.0 ** 110, 1e36, 3e38])
+def test_quantize_with_tensor_scales_at_the_ends(lib, g):
+    """Scales near the ends of fp32, with values that fit them and values that do not: still the nearest
+    codes, saturating with their sign; a scale past fp32 has zeros."""
+    rng = np.random.default_rng(3)
+    big = np.float32(3.3e38)
+    g = np.float32(g)
+    with np.errstate(over="ignore", under="ignore"):
+        rows = [np.clip(rng.normal(size=64) * np.float64(g) * m, -big, big) for m in (1e-3, 1.0, 100.0, 3000.0, 1e5)]
+    rows += [np.linspace(-1, 1, 64) * big, np.full(64, 1e-44), np.zeros(64)]
+    x = np.stack(rows).astype(np.float32)
+    q = lib.gptq_fp4_quantize(torch.tensor(x, device=DEV), "nv", torch.tensor([g], device=DEV))
+    with np.errstate(over="ignore", under="ignore", invalid="ignore", divide="ignore"):
+        _, codes, byte = F.quantise(x, "nv", float(g))
+        s = np.repeat(np.float32(byte_value(byte)) * g, 16, axis=1)
+    codes = np.where(np.isinf(s), 0, codes)
+    np.testing.assert_array_equal(F.untile_scales(npy(q.scales), *byte.shape), byte)
+    got = npy(q.codes)
+    got = np.stack([got & 15, got >> 4], -1).reshape(len(x), -1)[:, :64]
+    flat = lambda c: np.where(c == 8, 0, c)  # noqa: E731  (the sign of a zero is free)
+    np.testing.assert_array_equal(flat(got), flat(codes))
+
+
+def byte_value(byte):
+    e, f = byte.astype(int) >> 3, byte.astype(int) & 7
+    return np.where(e > 0, np.ldexp(1 + f / 8, e - 7), f / 512)
+
+
 def test_quantize_gathers_rows(lib):
     X = _matrix(50, 200, torch.bfloat16, 8).to(DEV)
     idx = torch.tensor([0, 99, 41, -1, 40, 7, -1, 98] * 20, dtype=torch.int32, device=DEV)
@@ -288,6 +316,43 @@ def test_matmul_repeats_bit_for_bit_on_any_stream(lib):
                 s.synchronize()
                 assert torch.equal(got, ref)
             lib.status_sync(s)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("T", [2, 70, 400])
+def test_a_nan_scale_stays_in_its_row(lib, fmt, T):
+    """A NaN scale (what quantising a NaN leaves) makes its row, or its feature, NaN and nothing else."""
+    rng = np.random.default_rng(T)
+    N, K = 300, 700
+    cx, bx, xv = _stored(rng, T, K, fmt, True, 1)
+    cw, bw, wv = _stored(rng, N, K, fmt, True, 1)
+    bx[1, 3] = bw[130, 5] = 255 if fmt == "mx" else 127
+    Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, 1.0), _fp4(lib, cw, bw, K, fmt, 1.0)))
+    nan = np.zeros((T, N), bool)
+    nan[1] = nan[:, 130] = True
+    np.testing.assert_array_equal(np.isnan(Y), nan)
+    np.testing.assert_array_equal(Y[~nan], (xv @ wv.T)[~nan])
+
+
+def test_results_given_and_on_the_current_stream(lib):
+    """The forms with `out` and `stream`, and the common form on a stream of the caller's, agree."""
+    X = torch.randn(150, 300, device=DEV).to(torch.bfloat16)
+    W = lib.gptq_fp4_quantize(torch.randn(200, 300, device=DEV), "nv")
+    g = lib.gptq_fp4_tensor_scale(X)
+    q = lib.gptq_fp4_quantize(X, "nv", g)
+    Y, V = lib.gptq_fp4_matmul(q, W), lib.gptq_fp4_dequantize(q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        q2 = lib.gptq_fp4_quantize(X, "nv", g)
+        Y2 = lib.gptq_fp4_matmul(q2, W)
+    q3 = lib.Fp4(torch.empty_like(q.codes), torch.zeros_like(q.scales), 300, "nv")
+    q3 = lib.gptq_fp4_quantize(X, "nv", g, out=q3, stream=s)
+    Y3 = lib.gptq_fp4_matmul(q3, W, out=torch.empty_like(Y), stream=s)
+    V3 = lib.gptq_fp4_dequantize(q3, out=torch.empty_like(V), stream=s)
+    s.synchronize()
+    assert torch.equal(q2.codes, q.codes) and torch.equal(q3.codes, q.codes)
+    assert torch.equal(Y2, Y) and torch.equal(Y3, Y) and torch.equal(V3, V)
 
 
 def test_in_a_cuda_graph(lib):
