@@ -33,30 +33,37 @@ constexpr int Q_COLS = 16;   // columns per thread: one NV block, half an MX blo
 __device__ __forceinline__ float load_elem(const float* p) { return *p; }
 __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// 16 consecutive values of one row as fp32, zeros past `n`
+// 16 consecutive values of one row as fp32, zeros past `n`. Returns the greatest magnitude's bits: exact,
+// and a NaN or infinity stays visible (bf16 pairs are compared two at a time).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const T* x, int64_t n, float (&v)[Q_COLS]) {
+__device__ __forceinline__ uint32_t load16(const T* x, int64_t n, float (&v)[Q_COLS]) {
+    uint32_t m = 0;
     if (VEC && n >= Q_COLS) {
         constexpr int PER = 16 / sizeof(T);
 #pragma unroll
         for (int q = 0; q < Q_COLS / PER; ++q) {
             const uint4 w = __ldg(reinterpret_cast<const uint4*>(x) + q);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            if (sizeof(T) == 4) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(u[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(T) == 4) {
+                    v[4 * q + e] = __uint_as_float(u[e]);
+                    m = max(m, u[e] & 0x7FFFFFFFu);
+                } else {
                     v[8 * q + 2 * e] = __uint_as_float(u[e] << 16);
                     v[8 * q + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                    m = __vmaxu2(m, u[e] & 0x7FFF7FFFu);
                 }
             }
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < Q_COLS; ++e) v[e] = e < n ? load_elem(x + e) : 0.0f;
+        return sizeof(T) == 4 ? m : max(m << 16, m & 0xFFFF0000u);
     }
+#pragma unroll
+    for (int e = 0; e < Q_COLS; ++e) {
+        v[e] = e < n ? load_elem(x + e) : 0.0f;
+        m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    }
+    return m;
 }
 
 // 8 values (already divided by their block's scale) to 8 codes: nearest, ties to even, saturating
@@ -82,7 +89,8 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
     const int64_t chunk = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x;
     const int64_t c0 = chunk * Q_COLS;
     pdl_trigger();   // the product's or the inverse's prologue may begin
-    const float g = MX ? 1.0f : *p.g;
+    const float g = MX ? 1.0f : *p.g, inv6g = MX ? 1.0f : 1.0f / (6.0f * g);
+    const bool easy = (__float_as_uint(g) & 0x007FFFFFu) == 0 && g > 0x1p-40f && g < 0x1p40f;
     for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
         int64_t sr = r;
         if (p.index) {
@@ -94,11 +102,7 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
             }
         }
         float y[Q_COLS];
-        load16<T, VEC>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + c0), sr < 0 ? 0 : p.cols - c0, y);
-        // the maximum over the magnitudes' bits: exact, and a NaN or infinity stays visible
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < Q_COLS; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+        uint32_t m = load16<T, VEC>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + c0), sr < 0 ? 0 : p.cols - c0, y);
         if (MX) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const bool bad = m >= 0x7F800000u;
         if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
@@ -111,21 +115,36 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
             for (int e = 0; e < Q_COLS; ++e) y[e] *= inv;   // exact: a power of two
         } else {
             const float a = __uint_as_float(m);
-            byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(a / (6.0f * g), __NV_SATFINITE, __NV_E4M3);
-            // x / d correctly rounded (Markstein 1990: with inv = 1 / d correctly rounded, one residual
-            // step on x * inv rounds the quotient correctly), so a value on a midpoint of the grid is
-            // seen as one. x is first cut to 8 d, beyond which every quotient saturates, and both are
-            // brought near 1 by a power of two where d is far from it, so nothing overflows or
-            // vanishes on the way. A scale of zero (or past fp32) has zeros.
+            // a / (6 g) and x / d correctly rounded (Markstein 1990: with the divisor's reciprocal correctly
+            // rounded, one residual step on the product rounds the quotient correctly), so a value on
+            // a midpoint of the grid is seen as one. x is first cut to 8 d, beyond which every
+            // quotient saturates, and both are brought near 1 by a power of two where d is far from
+            // it, so nothing overflows or vanishes on the way. A scale of zero (or past fp32) has zeros.
+            const float aq = a * inv6g;
+            const float ratio = aq > 0x1p-100f && aq < 0x1p100f && inv6g > 0x1p-60f && inv6g < 0x1p60f
+                                    ? fmaf(fmaf(-aq, 6.0f * g, a), inv6g, aq) : a / (6.0f * g);
+            byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
             float d = e4m3_value(byte) * g;
-            const float f = d < 0x1p-60f ? 0x1p64f : d > 0x1p60f ? 0x1p-64f : 1.0f;
-            const bool none = d == 0.0f || d > 0x1.fffffep127f;
-            d *= f;
-            const float inv = 1.0f / d, most = 8.0f * d;
+            if (!(d >= 0x1p-60f && d <= 0x1p60f)) {
+                const float f = d < 1.0f ? 0x1p64f : 0x1p-64f;
 #pragma unroll
-            for (int e = 0; e < Q_COLS; ++e) {
-                const float x = fminf(fmaxf(y[e] * f, -most), most), q = x * inv;
-                y[e] = none ? 0.0f : fmaf(fmaf(-q, d, x), inv, q);
+                for (int e = 0; e < Q_COLS; ++e) y[e] *= f;
+                d = d < 0x1.fffffep127f ? d * f : d > 0.0f ? 0.0f : d;   // past fp32: none (a NaN stays)
+            }
+            const float inv = d != 0.0f ? 1.0f / d : 0.0f;
+            if (sizeof(T) == 2 && easy) {
+                // x has 8 significant bits and d 4 (g is a power of two): a quotient that is not a midpoint
+                // is 2^-8 away from it, and for the eight d the reciprocals are exact or up to
+                // 2^-24 too large, so the product cut towards zero is the midpoint where x / d is one
+#pragma unroll
+                for (int e = 0; e < Q_COLS; ++e) y[e] = __fmul_rz(y[e], inv);
+            } else {
+                const float most = 8.0f * d;
+#pragma unroll
+                for (int e = 0; e < Q_COLS; ++e) {
+                    const float x = fminf(fmaxf(y[e], -most), most), q = x * inv;
+                    y[e] = fmaf(fmaf(-q, d, x), inv, q);
+                }
             }
         }
         if (c0 < 2 * p.pitch)
@@ -214,9 +233,7 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_amax_kernel(const T* X, int64_t
     uint32_t m = 0;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
         float v[Q_COLS];
-        load16<T, VEC>(X + r * ldx + c0, cols - c0, v);
-#pragma unroll
-        for (int e = 0; e < Q_COLS; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        m = max(m, load16<T, VEC>(X + r * ldx + c0, cols - c0, v));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     __shared__ uint32_t part[Q_THREADS / 32];

@@ -107,6 +107,27 @@ def test_quantize_with_tensor_scales_at_the_ends(lib, g):
     np.testing.assert_array_equal(flat(got), flat(codes))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("g", [1.0, 2.0 ** -9, 2.0 ** -70, 2.0 ** 50])
+def test_quantize_midpoints_of_every_scale(lib, dtype, g):
+    """All midpoints of the grid under each of e4m3's scales (8 bits hold them), both signs, and the bf16
+    numbers next to them."""
+    mid = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    rows = []
+    for e in (-2, 0, 5):
+        for j in range(8):
+            s = (1 + j / 8) * 2.0 ** e
+            for k in (-1, 0, 1):
+                v = np.concatenate((mid, -mid)) * s
+                v = np.nextafter(v.astype(np.float32), np.float32(np.inf * k)) if k and dtype == torch.float32 else v * (1 + k * 2.0 ** -7)
+                rows.append(np.concatenate(([6 * s], v, [0.0])) * g)
+    x = torch.tensor(np.array(rows, dtype=np.float32)).to(dtype)
+    q = lib.gptq_fp4_quantize(x.to(DEV), "nv", torch.tensor([g], device=DEV))
+    v, _, byte = F.quantise(npy(x), "nv", g)
+    np.testing.assert_array_equal(F.untile_scales(npy(q.scales), *byte.shape), byte)
+    np.testing.assert_array_equal(npy(lib.gptq_fp4_dequantize(q)), v.astype(np.float32))
+
+
 def byte_value(byte):
     e, f = byte.astype(int) >> 3, byte.astype(int) & 7
     return np.where(e > 0, np.ldexp(1 + f / 8, e - 7), f / 512)
