@@ -488,7 +488,8 @@ def gptq_fp4_scale_bytes(rows: int, cols: int, format: str) -> int:
 
 # The calls of a serving step are short. Their common form (results allocated here, on the current
 # stream) goes through the C module _call, which returns NotImplemented for what it does not
-# recognise; the functions below then check in Python, and raise.
+# recognise; the functions below then check in Python, and raise. With `stream`, results are still
+# allocated on the current stream: a caller keeps them and the inputs until that stream is done.
 _fast = None
 
 
@@ -702,6 +703,8 @@ def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor]
     nb = ws.numel() if ws is not None else int(lib.gptq_expert_sort_workspace_bytes(tokens, top, experts))
     if ws is None and nb:
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)
     _check("gptq_expert_sort", lib.gptq_expert_sort(
         ids.data_ptr(), tokens, top, experts, route.offsets.data_ptr(), route.src.data_ptr(), route.pos.data_ptr(),
         _addr(ws), nb, _raw_stream(stream)))

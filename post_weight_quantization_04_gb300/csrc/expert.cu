@@ -25,7 +25,9 @@ namespace {
 // count their slots in a first launch and place them in a second. Either way a warp owns a
 // contiguous share of the slots and counts equal experts among 32 slots at a time, so places are
 // stable without atomics. Equal experts are found by one ballot per bit of the expert's number
-// (match.any took several times as long).
+// (match.any took several times as long). Bound by latency: 10 slots 2.4 us, 32768 slots and 8 experts
+// 8 us in two launches, of which the second starts while the first runs; one CTA for all of them
+// took 22.
 constexpr int S_ALONE = 4096;
 constexpr int S_CHUNK = 512;           // otherwise the least slots per CTA
 constexpr int S_MAX_EXPERTS = 1024;    // one counter per warp and expert in shared memory
@@ -245,7 +247,8 @@ __device__ __forceinline__ int64_t live_rows(const RParams& p) {
 }
 
 // Rows are moved in units of U (16 bytes where pointers and strides allow, one element
-// otherwise), `units` per row. Each row of x is read once and written `top` times.
+// otherwise), `units` per row. Each row of x is read once and written `top` times, so the traffic is
+// the least there is: 16384 x 2 x 4096 bf16, 403 MB, in 55 us (7.3 TB/s).
 template <typename U>
 __global__ void __launch_bounds__(R_THREADS) expert_gather_kernel(const RParams p, int64_t units, int chunks, int64_t main_ctas) {
     const U* X = static_cast<const U*>(p.X);
@@ -323,7 +326,9 @@ __device__ __forceinline__ uint32_t places(const RParams& p, int64_t t, int j0, 
     return live;
 }
 
-// A thread sums N columns of a token over its slots, SLOTS rows in flight.
+// A thread sums N columns of a token over its slots, SLOTS rows in flight. Bound by memory: 16384 x 2 x
+// 4096 bf16, 403 MB, in 66 us (6.1 TB/s); with the rows one after another 76, with loads behind
+// the test of their slot 128.
 template <typename T, int N, int SLOTS>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_kernel(const RParams p, int chunks) {
     const int64_t t = blockIdx.x / chunks;
@@ -350,7 +355,8 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_kernel(const RParams
 }
 
 // One CTA per token, SLOTS slots at a time: dy and the slots' rows are read once (dy again for each
-// further group), the products of a group are summed across the CTA together.
+// further group), the products of a group are summed across the CTA together. Bound by memory: 16384 x
+// 2 x 4096 bf16, 671 MB, in 99 us (6.8 TB/s); slot by slot, with a sum across the CTA for each, 108.
 template <typename T, int N, int SLOTS>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_grad_kernel(const RParams p) {
     const T* X = static_cast<const T*>(p.X);

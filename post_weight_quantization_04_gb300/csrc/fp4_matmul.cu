@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
 // sums go to fp32 with the product of both scales (at most 8 bits), and are added over the columns
 // and, in a fixed order, over the CTA.
 // The 8 features are two neighbours of each 32-row quarter of a scale tile, whose scales share sectors.
+// One token x 4096 x 4096 MX: 4.1 us with its launch (9 MB); what bounds it there is latency, and with
+// more weights the conversions (14336 x 4096: 11.6 us, 2.7 TB/s), where the other kernel takes over.
 constexpr int F_THREADS = 128, F_FEATURES = 8, F_TOKENS = 4;
 
 __device__ __forceinline__ void to_half2(const uint4& c, __half2 (&h)[16]) {
