@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.cuh"
@@ -212,6 +213,10 @@ cudaError_t launch_place(const SParams& p, unsigned grid, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------- rows there and back
+// Rows move in units of 16 bytes where pointers, strides and lengths allow, of 4 bytes or of one
+// element otherwise; neighbouring threads take neighbouring units, and of the short ones several
+// each, so that as many bytes are in flight (rows of 4095 bf16 took four times as long as rows of 4096
+// with one element per thread). A CTA has as many threads as a row has work for, up to 256.
 constexpr int R_THREADS = 256;
 
 struct RParams {
@@ -246,10 +251,9 @@ __device__ __forceinline__ int64_t live_rows(const RParams& p) {
     return n < 0 ? 0 : n < p.slots ? n : p.slots;
 }
 
-// Rows are moved in units of U (16 bytes where pointers and strides allow, one element
-// otherwise), `units` per row. Each row of x is read once and written `top` times, so the traffic is
-// the least there is: 16384 x 2 x 4096 bf16, 403 MB, in 55 us (7.3 TB/s).
-template <typename U>
+// Each row of x is read once and written `top` times, so the traffic is the least there is: 16384 x 2 x
+// 4096 bf16, 403 MB, in 55 us (7.3 TB/s).
+template <typename U, int UNITS>
 __global__ void __launch_bounds__(R_THREADS) expert_gather_kernel(const RParams p, int64_t units, int chunks, int64_t main_ctas) {
     const U* X = static_cast<const U*>(p.X);
     U* Y = static_cast<U*>(p.Y);
@@ -258,30 +262,40 @@ __global__ void __launch_bounds__(R_THREADS) expert_gather_kernel(const RParams 
         const int64_t n = gridDim.x - main_ctas;
         const U zero = {};
         for (int64_t r = live_rows(p) + (blockIdx.x - main_ctas); r < p.slots; r += n)
-            for (int64_t u = threadIdx.x; u < units; u += R_THREADS) Y[r * p.ldy + u] = zero;
+            for (int64_t u = threadIdx.x; u < units; u += blockDim.x) Y[r * p.ldy + u] = zero;
         return;
     }
     const int64_t t = blockIdx.x / chunks;
-    const int64_t u = (int64_t)(blockIdx.x % chunks) * R_THREADS + threadIdx.x;
-    if (u >= units) return;
-    const U v = X[t * p.ldx + u];
+    const int64_t u0 = (int64_t)(blockIdx.x % chunks) * (blockDim.x * UNITS) + threadIdx.x;
+    U v[UNITS];
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i)
+        if (u0 + i * blockDim.x < units) v[i] = X[t * p.ldx + u0 + i * blockDim.x];
     for (int j = 0; j < p.top; ++j) {
         const int64_t at = place(p, t * p.top + j);
-        if (at >= 0) Y[at * p.ldy + u] = v;
+        if (at < 0) continue;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+            if (u0 + i * blockDim.x < units) Y[at * p.ldy + u0 + i * blockDim.x] = v[i];
     }
 }
 
-// N consecutive elements as fp32
+// a unit of N consecutive elements as fp32
 template <typename T, int N>
 __device__ __forceinline__ void load_row(const T* x, float (&v)[N]) {
     if constexpr (N == 1) {
         if constexpr (sizeof(T) == 2) v[0] = __bfloat162float(*x);
         else v[0] = *x;
     } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(x);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t u[N * sizeof(T) / 4];
+        if constexpr (N * sizeof(T) == 4) {
+            u[0] = *reinterpret_cast<const uint32_t*>(x);
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(x);
+            u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < (int)(N * sizeof(T) / 4); ++e) {
             if constexpr (sizeof(T) == 2) {
                 v[2 * e] = __uint_as_float(u[e] << 16);
                 v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
@@ -298,9 +312,9 @@ __device__ __forceinline__ void store_row(T* y, const float (&v)[N]) {
         if constexpr (sizeof(T) == 2) *y = __float2bfloat16_rn(v[0]);
         else *y = v[0];
     } else {
-        uint32_t u[4];
+        uint32_t u[N * sizeof(T) / 4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < (int)(N * sizeof(T) / 4); ++e) {
             if constexpr (sizeof(T) == 2) {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
                 u[e] = *reinterpret_cast<const uint32_t*>(&h);
@@ -308,7 +322,8 @@ __device__ __forceinline__ void store_row(T* y, const float (&v)[N]) {
                 u[e] = __float_as_uint(v[e]);
             }
         }
-        *reinterpret_cast<uint4*>(y) = make_uint4(u[0], u[1], u[2], u[3]);
+        if constexpr (N * sizeof(T) == 4) *reinterpret_cast<uint32_t*>(y) = u[0];
+        else *reinterpret_cast<uint4*>(y) = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
 
@@ -326,46 +341,53 @@ __device__ __forceinline__ uint32_t places(const RParams& p, int64_t t, int j0, 
     return live;
 }
 
-// A thread sums N columns of a token over its slots, SLOTS rows in flight. Bound by memory: 16384 x 2 x
-// 4096 bf16, 403 MB, in 66 us (6.1 TB/s); with the rows one after another 76, with loads behind
-// the test of their slot 128.
-template <typename T, int N, int SLOTS>
+// A thread sums UNITS units of N columns of a token over its slots, SLOTS rows in flight. Bound by memory:
+// 16384 x 2 x 4096 bf16, 403 MB, in 66 us (6.1 TB/s); with the rows one after another 76, with loads
+// behind the test of their slot 128.
+template <typename T, int N, int UNITS, int SLOTS>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_kernel(const RParams p, int chunks) {
     const int64_t t = blockIdx.x / chunks;
-    const int64_t c = ((int64_t)(blockIdx.x % chunks) * R_THREADS + threadIdx.x) * N;
+    const int64_t step = (int64_t)blockDim.x * N;
+    const int64_t c = (int64_t)(blockIdx.x % chunks) * step * UNITS + threadIdx.x * N;
     if (c >= p.d) return;
     const T* X = static_cast<const T*>(p.X) + c;
-    float acc[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+    float acc[UNITS][N] = {};
     for (int j0 = 0; j0 < p.top; j0 += SLOTS) {
         int64_t at[SLOTS];
-        float v[SLOTS][N];
+        float v[SLOTS][UNITS][N];
         const uint32_t live = places<SLOTS>(p, t, j0, at);
 #pragma unroll
-        for (int j = 0; j < SLOTS; ++j) load_row<T, N>(X + at[j] * p.ldx, v[j]);
+        for (int j = 0; j < SLOTS; ++j)
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i)
+                if (UNITS == 1 || c + i * step < p.d) load_row<T, N>(X + at[j] * p.ldx + i * step, v[j][i]);
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const float w = p.w ? (live >> j & 1 ? p.w[t * p.top + j0 + j] : 0.0f) : 1.0f;
 #pragma unroll
-            for (int e = 0; e < N; ++e) acc[e] = live >> j & 1 ? fmaf(w, v[j][e], acc[e]) : acc[e];
+            for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+                for (int e = 0; e < N; ++e) acc[i][e] = live >> j & 1 ? fmaf(w, v[j][i][e], acc[i][e]) : acc[i][e];
         }
     }
-    store_row<T, N>(static_cast<T*>(p.Y) + t * p.ldy + c, acc);
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i)
+        if (UNITS == 1 || c + i * step < p.d) store_row<T, N>(static_cast<T*>(p.Y) + t * p.ldy + c + i * step, acc[i]);
 }
 
 // One CTA per token, SLOTS slots at a time: dy and the slots' rows are read once (dy again for each
 // further group), the products of a group are summed across the CTA together. Bound by memory: 16384 x
 // 2 x 4096 bf16, 671 MB, in 99 us (6.8 TB/s); slot by slot, with a sum across the CTA for each, 108.
-template <typename T, int N, int SLOTS>
+template <typename T, int N, int UNITS, int SLOTS>
 __global__ void __launch_bounds__(R_THREADS) expert_combine_grad_kernel(const RParams p) {
     const T* X = static_cast<const T*>(p.X);
     T* Y = static_cast<T*>(p.Y);
+    const int64_t step = (int64_t)blockDim.x * N;
     if (blockIdx.x >= p.tokens) {
         const int64_t n = gridDim.x - p.tokens;
         float zero[N] = {};
         for (int64_t r = live_rows(p) + (blockIdx.x - p.tokens); r < p.slots; r += n)
-            for (int64_t c = threadIdx.x * N; c < p.d; c += R_THREADS * N) store_row<T, N>(Y + r * p.ldy + c, zero);
+            for (int64_t c = threadIdx.x * N; c < p.d; c += step) store_row<T, N>(Y + r * p.ldy + c, zero);
         return;
     }
     __shared__ float part[R_THREADS / 32][SLOTS];
@@ -380,20 +402,28 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_grad_kernel(const RP
             w[j] = live >> j & 1 ? p.w[t * p.top + j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int64_t c = threadIdx.x * N; c < p.d; c += R_THREADS * N) {
-            float a[N], b[SLOTS][N];
-            load_row<T, N>(dy + c, a);
+        for (int64_t c = threadIdx.x * N; c < p.d; c += step * UNITS) {
+            float a[UNITS][N], b[SLOTS][UNITS][N];
 #pragma unroll
-            for (int j = 0; j < SLOTS; ++j) load_row<T, N>(X + at[j] * p.ldx + c, b[j]);
+            for (int i = 0; i < UNITS; ++i)
+                if (UNITS == 1 || c + i * step < p.d) load_row<T, N>(dy + c + i * step, a[i]);
 #pragma unroll
-            for (int j = 0; j < SLOTS; ++j) {
+            for (int j = 0; j < SLOTS; ++j)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    dot[j] = fmaf(a[e], b[j][e], dot[j]);
-                    b[j][e] = a[e] * w[j];
+                for (int i = 0; i < UNITS; ++i)
+                    if (UNITS == 1 || c + i * step < p.d) load_row<T, N>(X + at[j] * p.ldx + c + i * step, b[j][i]);
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j)
+#pragma unroll
+                for (int i = 0; i < UNITS; ++i) {
+                    if (UNITS > 1 && c + i * step >= p.d) continue;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        dot[j] = fmaf(a[i][e], b[j][i][e], dot[j]);
+                        b[j][i][e] = a[i][e] * w[j];
+                    }
+                    if (live >> j & 1) store_row<T, N>(Y + at[j] * p.ldy + c + i * step, b[j][i]);
                 }
-                if (live >> j & 1) store_row<T, N>(Y + at[j] * p.ldy + c, b[j]);
-            }
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
@@ -404,33 +434,50 @@ __global__ void __launch_bounds__(R_THREADS) expert_combine_grad_kernel(const RP
         __syncthreads();
         if (threadIdx.x < SLOTS && j0 + (int)threadIdx.x < p.top) {
             float sum = 0.0f;
-            for (int i = 0; i < R_THREADS / 32; ++i) sum += part[i][threadIdx.x];
+            for (int i = 0; i < (int)blockDim.x / 32; ++i) sum += part[i][threadIdx.x];
             p.dw[t * p.top + j0 + threadIdx.x] = live >> threadIdx.x & 1 ? sum : 0.0f;
         }
         __syncthreads();
     }
 }
 
-// Calls f(T(), units per access, slots per group): 16-byte accesses where pointers and strides allow,
-// one element otherwise; the rows of 1, 2 or 4 slots in flight, whichever the token has.
+// Calls f(T(), columns per unit, units per thread, slots per group), the last three as constants
 template <typename F>
-void with_row_types(int dtype, bool vec, int64_t top, F f) {
-    auto slots = [&](auto t, auto n) {
-        if (top == 1) f(t, n, std::integral_constant<int, 1>());
-        else if (top == 2) f(t, n, std::integral_constant<int, 2>());
-        else f(t, n, std::integral_constant<int, 4>());
+void with_row_types(int dtype, int unit_bytes, int64_t top, F f) {
+    auto slots = [&](auto t, auto n, auto u) {
+        if (top == 1) f(t, n, u, std::integral_constant<int, 1>());
+        else if (top == 2) f(t, n, u, std::integral_constant<int, 2>());
+        else f(t, n, u, std::integral_constant<int, 4>());
     };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 4> four;
     if (dtype == GPTQ_BF16) {
-        if (vec) slots(__nv_bfloat16(), std::integral_constant<int, 8>());
-        else slots(__nv_bfloat16(), std::integral_constant<int, 1>());
+        if (unit_bytes == 16) slots(__nv_bfloat16(), std::integral_constant<int, 8>(), one);
+        else if (unit_bytes == 4) slots(__nv_bfloat16(), std::integral_constant<int, 2>(), four);
+        else slots(__nv_bfloat16(), one, four);
     } else {
-        if (vec) slots(float(), std::integral_constant<int, 4>());
-        else slots(float(), std::integral_constant<int, 1>());
+        if (unit_bytes == 16) slots(float(), four, one);
+        else slots(float(), one, four);
     }
 }
 
+// threads for rows of `units` units, several per thread
+unsigned row_threads(int64_t units, int per) {
+    const int64_t n = ceil_div(ceil_div(units, per), 32) * 32;
+    return (unsigned)std::min<int64_t>(std::max<int64_t>(n, 32), R_THREADS);
+}
+
 bool bad_dtype(int t) { return t != GPTQ_F32 && t != GPTQ_BF16; }
-bool vec16(const void* p, int64_t ld, int64_t esize) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esize) % 16 == 0; }
+// bytes of the units that all these rows of d elements can move in
+struct Rows {
+    const void* p;
+    int64_t ld;
+};
+int unit_of(int64_t es, int64_t d, std::initializer_list<Rows> rows) {
+    uint64_t all = (uint64_t)(d * es);
+    for (const Rows& r : rows) all |= reinterpret_cast<uintptr_t>(r.p) | (uint64_t)(r.ld * es);
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)es;
+}
 constexpr int64_t kMaxSlots = (1ll << 31) - 4096;
 bool bad_shape(int64_t tokens, int64_t top, int64_t d) {
     return tokens < 0 || top < 1 || top > 65535 || d < 0 || d > kMaxSlots || tokens > kMaxSlots / top;
@@ -482,19 +529,20 @@ extern "C" int gptq_expert_gather(const void* X, int dtype, int64_t tokens, int6
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
     const int64_t es = dtype == GPTQ_BF16 ? 2 : 4;
-    const bool vec = vec16(X, ldx, es) && vec16(Xs, lds, es) && (d * es) % 16 == 0;
-    const int64_t unit = vec ? 16 / es : 1, units = d / unit;
+    const int bytes = unit_of(es, d, {{X, ldx}, {Xs, lds}}), per = bytes == 16 ? 1 : bytes == 4 ? 4 : 8;
+    const int64_t unit = bytes / es, units = d / unit;
     RParams p{X, ldx / unit, nullptr, 0, Xs, lds / unit, tokens, tokens * top, (int)top, d, pos, offsets + experts, nullptr, nullptr, st.word};
-    const int64_t chunks = ceil_div(units, R_THREADS), main_ctas = tokens * chunks;
+    const unsigned threads = row_threads(units, per);
+    const int64_t chunks = ceil_div(units, threads * per), main_ctas = tokens * chunks;
     if (main_ctas > kMaxSlots) return GPTQ_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)(main_ctas + tail_ctas(p.slots));
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kern) {
-        GPTQ_LAUNCH(K_EXPERT_GATHER, s, e = launch_pdl(kern, dim3(grid), dim3(R_THREADS), 0, s, p, units, (int)chunks, main_ctas));
+        GPTQ_LAUNCH(K_EXPERT_GATHER, s, e = launch_pdl(kern, dim3(grid), dim3(threads), 0, s, p, units, (int)chunks, main_ctas));
     };
-    if (vec) go(expert_gather_kernel<uint4>);
-    else if (es == 2) go(expert_gather_kernel<uint16_t>);
-    else go(expert_gather_kernel<uint32_t>);
+    if (bytes == 16) go(expert_gather_kernel<uint4, 1>);
+    else if (bytes == 4) go(expert_gather_kernel<uint32_t, 4>);
+    else go(expert_gather_kernel<uint16_t, 8>);
     GPTQ_CUDA_TRY(e);
     return st.finish(s);
 }
@@ -508,13 +556,15 @@ extern "C" int gptq_expert_combine(const void* Ys, int dtype, int64_t tokens, in
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
     const int64_t es = dtype == GPTQ_BF16 ? 2 : 4;
-    const bool vec = vec16(Ys, ldys, es) && vec16(Y, ldy, es) && (d * es) % 16 == 0;
+    const int bytes = unit_of(es, d, {{Ys, ldys}, {Y, ldy}}), per = bytes == 16 ? 1 : 4;
     RParams p{Ys, ldys, nullptr, 0, Y, ldy, tokens, tokens * top, (int)top, d, pos, nullptr, weights, nullptr, st.word};
-    const int64_t chunks = ceil_div(d, R_THREADS * (vec ? 16 / es : 1));
+    const int64_t units = d / (bytes / es);
+    const unsigned threads = row_threads(units, per);
+    const int64_t chunks = ceil_div(units, threads * per);
     if (tokens * chunks > kMaxSlots) return GPTQ_ERR_UNSUPPORTED;
-    with_row_types(dtype, vec, top, [&](auto t, auto n, auto k) {
-        auto kern = expert_combine_kernel<decltype(t), decltype(n)::value, decltype(k)::value>;
-        GPTQ_LAUNCH(K_EXPERT_COMBINE, s, kern<<<(unsigned)(tokens * chunks), R_THREADS, 0, s>>>(p, (int)chunks));
+    with_row_types(dtype, bytes, top, [&](auto t, auto n, auto u, auto k) {
+        auto kern = expert_combine_kernel<decltype(t), decltype(n)::value, decltype(u)::value, decltype(k)::value>;
+        GPTQ_LAUNCH(K_EXPERT_COMBINE, s, kern<<<(unsigned)(tokens * chunks), threads, 0, s>>>(p, (int)chunks));
     });
     GPTQ_LAUNCH_CHECK();
     return st.finish(s);
@@ -530,12 +580,12 @@ extern "C" int gptq_expert_combine_grad(const void* dY, int64_t lddy, const void
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
     const int64_t es = dtype == GPTQ_BF16 ? 2 : 4;
-    const bool vec = vec16(dY, lddy, es) && vec16(Ys, ldys, es) && vec16(dYs, lddys, es) && (d * es) % 16 == 0;
+    const int bytes = unit_of(es, d, {{dY, lddy}, {Ys, ldys}, {dYs, lddys}});
     RParams p{Ys, ldys, dY, lddy, dYs, lddys, tokens, tokens * top, (int)top, d, pos, offsets + experts, weights, dW, st.word};
-    const unsigned grid = (unsigned)(tokens + tail_ctas(p.slots));
-    with_row_types(dtype, vec, top, [&](auto t, auto n, auto k) {
-        auto kern = expert_combine_grad_kernel<decltype(t), decltype(n)::value, decltype(k)::value>;
-        GPTQ_LAUNCH(K_EXPERT_GRAD, s, kern<<<grid, R_THREADS, 0, s>>>(p));
+    const unsigned grid = (unsigned)(tokens + tail_ctas(p.slots)), threads = row_threads(d / (bytes / es), bytes == 16 ? 1 : 4);
+    with_row_types(dtype, bytes, top, [&](auto t, auto n, auto u, auto k) {
+        auto kern = expert_combine_grad_kernel<decltype(t), decltype(n)::value, decltype(u)::value, decltype(k)::value>;
+        GPTQ_LAUNCH(K_EXPERT_GRAD, s, kern<<<grid, threads, 0, s>>>(p));
     });
     GPTQ_LAUNCH_CHECK();
     return st.finish(s);

@@ -66,6 +66,33 @@ __device__ __forceinline__ uint32_t load16(const T* x, int64_t n, float (&v)[Q_C
     return m;
 }
 
+// The same for a row that 16-byte loads cannot take: the warp reads its 512 columns (x, n: those of its
+// lane 0) in order and hands each lane its 16 through shared memory, one word in 17 left out so that
+// neither side has conflicts. Loading 16 neighbours per lane took twice as long.
+template <typename T>
+__device__ __forceinline__ uint32_t load16_turned(const T* x, int64_t n, float (&v)[Q_COLS], float* buf) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < Q_COLS; ++e) {
+        const int c = lane + 32 * e;
+        v[e] = c < n ? load_elem(x + c) : 0.0f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < Q_COLS; ++e) {
+        const int c = lane + 32 * e;
+        buf[c + (c >> 4)] = v[e];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < Q_COLS; ++e) {
+        v[e] = buf[17 * lane + e];
+        m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    }
+    return m;
+}
+
 // 8 values (already divided by their block's scale) to 8 codes: nearest, ties to even, saturating
 __device__ __forceinline__ uint32_t to_codes(const float* y) {
     uint32_t r;
@@ -103,7 +130,15 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
             }
         }
         float y[Q_COLS];
-        uint32_t m = load16<T, VEC>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + c0), sr < 0 ? 0 : p.cols - c0, y);
+        uint32_t m;
+        if constexpr (VEC) {
+            m = load16<T, true>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + c0), sr < 0 ? 0 : p.cols - c0, y);
+        } else {
+            __shared__ float buf[Q_THREADS / 32][17 * 32];
+            const int64_t cw = c0 - (int64_t)(threadIdx.x & 31) * Q_COLS;
+            m = load16_turned(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + cw), sr < 0 ? 0 : p.cols - cw, y,
+                              buf[threadIdx.x >> 5]);
+        }
         if (MX) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const bool bad = m >= 0x7F800000u;
         if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
@@ -186,7 +221,9 @@ template <typename T, bool MX, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParams p) {
     constexpr int C = 16 / sizeof(T);
     const int64_t c0 = ((int64_t)blockIdx.x * Q_THREADS + threadIdx.x) * C, n = p.cols - c0;
-    if (n <= 0) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t cw = c0 - lane * C;   // the warp's first column
+    if (cw >= p.cols) return;
     pdl_wait();
     const float g = MX ? 1.0f : *p.g;
     const int64_t b = c0 / (MX ? 32 : 16);
@@ -195,9 +232,9 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParam
 #pragma unroll
         for (int i = 0; i < DQ_ROWS; ++i) {
             const int64_t r = min(r0 + i, p.rows - 1);
-            const uint8_t* src = p.codes + r * p.pitch + c0 / 2;
+            const uint8_t* src = p.codes + r * p.pitch + min(c0 / 2, p.pitch - C / 2);   // (lanes past the row: any)
             w[i] = C == 8 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
-            sb[i] = p.scales[fp4_scale_at(r, b, p.tiles_k)];
+            sb[i] = p.scales[fp4_scale_at(r, min(b, 4 * p.tiles_k - 1), p.tiles_k)];
         }
 #pragma unroll
         for (int i = 0; i < DQ_ROWS; ++i) {
@@ -210,17 +247,32 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_dequantize_kernel(const DqParam
                 v[2 * e] = f.x * s;
                 v[2 * e + 1] = f.y * s;
             }
-            T* y = static_cast<T*>(p.Y) + (r0 + i) * p.ldy + c0;
-            if (VEC && n >= C) {
-                if constexpr (C == 4)
-                    *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
-                else
-                    *reinterpret_cast<uint4*>(y) =
-                        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-            } else {
+            T* y = static_cast<T*>(p.Y) + (r0 + i) * p.ldy;
+            if constexpr (VEC) {
+                if (n >= C) {
+                    if constexpr (C == 4)
+                        *reinterpret_cast<float4*>(y + c0) = make_float4(v[0], v[1], v[2], v[3]);
+                    else
+                        *reinterpret_cast<uint4*>(y + c0) =
+                            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                } else {
 #pragma unroll
-                for (int e = 0; e < C; ++e)
-                    if (e < n) store_elem(y + e, v[e]);
+                    for (int e = 0; e < C; ++e)
+                        if (e < n) store_elem(y + c0 + e, v[e]);
+                }
+            } else {
+                // in order through shared memory (a word left out after every 32, so no conflicts)
+                __shared__ float buf[Q_THREADS / 32][33 * C];
+                float* mine = buf[threadIdx.x >> 5];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < C; ++e) mine[C * lane + e + ((C * lane + e) >> 5)] = v[e];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < C; ++e) {
+                    const int c = lane + 32 * e;
+                    if (cw + c < p.cols) store_elem(y + cw + c, mine[c + (c >> 5)]);
+                }
             }
         }
     }
