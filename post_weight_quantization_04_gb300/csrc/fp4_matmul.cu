@@ -22,13 +22,16 @@
 // tile's MMAs run, and two stages' scales in turn in the columns from 384. (Tiles of 256 tokens leave
 // room for scales only if the two buffers overlap; waiting for the shared columns cost 1.2 us a tile.)
 //
-// What bounds it (8192 x 8192 x 8192): MX 152 us, 7.3 PFLOP/s; the tensor pipe needs 128 cycles for 64
-// columns of a 256 x 256 tile, 130 us here, the scale copies that run in the same pipe 10, the stores
-// of Y 10. NV 184 us, with twice the scale copies. Both are past the power limit when they
-// run for long (1.67 GHz at 1370 W: 16384 x 4096 x 14336 MX 283 us in short runs, 310 in long ones).
+// What bounds it: the tensor pipe, which needs 96 cycles for 64 columns of a 256 x 192 tile. A stage of MX
+// takes its 0.197 us (4 x 96 cycles at 1.95 GHz) while few pairs run, the scale copies hidden behind
+// the MMAs; 0.22 with all of them (the clock falls under the load) and 0.235 with their copies and stores
+// in full flow; a tile's end costs another 0.3. NV, with twice the scale copies in the same pipe, 0.27
+// and 0.28. Below 192 tokens the copies' latency over six stages keeps a stage at 0.2 us.
+// 8192 x 8192 x 8192: MX 152 us, 7.3 PFLOP/s, NV 184 us, 6.0. When run for long both meet the power limit
+// (1.67 GHz at 1370 W: 16384 x 4096 x 14336 MX 283 us in short runs, 310 in long ones).
 // Taken back: 256-token tiles with overlapping buffers, 128 and 64 tokens (slower at every size from 256
-// tokens up), other tile orders, a cluster of 2 or 4 pairs sharing a tile's columns (slower but for
-// K = 14336).
+// tokens up), a cluster of 2 or 4 pairs sharing a tile's columns (slower but for K = 14336), the odd
+// CTA's copies counted on the even one's barriers directly (no faster).
 // Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits
 // for its own copies, the even one for the MMAs, and both meet before either leaves).
 #include <cuda_bf16.h>
