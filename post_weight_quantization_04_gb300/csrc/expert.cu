@@ -129,20 +129,35 @@ __global__ void __launch_bounds__(32 * WARPS) expert_place_kernel(const SParams 
     count_slots(p, b, e, cnt + warp * p.experts);
     __syncthreads();
     pdl_wait();   // the counts of the other CTAs (everything before is this kernel's own input)
-    // exclusive prefix over the experts, THREADS at a time
+    // exclusive prefix over the experts, THREADS at a time; where there are fewer, several threads share
+    // the CTAs' counts of one (with one thread each the sum over 64 CTAs took 4 us)
+    int wide = 32;
+    while (wide < p.experts && wide < THREADS) wide <<= 1;
+    const int groups = THREADS / wide, mine_of = (int)threadIdx.x % wide, group = (int)threadIdx.x / wide;
     for (int e0 = 0; e0 < p.experts; e0 += THREADS) {
         const int x = e0 + threadIdx.x;
         int32_t all = 0, before = 0;
-        if (x < p.experts) {
-            if (gridDim.x > 1) {
-                for (int c = 0; c < (int)gridDim.x; ++c) {
-                    const int32_t n = p.counts[(int64_t)c * p.experts + x];
+        if (gridDim.x > 1) {
+            __shared__ int32_t sum_all[THREADS], sum_before[THREADS];
+            if (e0 + mine_of < p.experts) {
+#pragma unroll 4
+                for (int c = group; c < (int)gridDim.x; c += groups) {
+                    const int32_t n = p.counts[(int64_t)c * p.experts + e0 + mine_of];
                     all += n;
                     if (c < (int)blockIdx.x) before += n;
                 }
-            } else {
-                for (int w = 0; w < WARPS; ++w) all += cnt[w * p.experts + x];
             }
+            sum_all[threadIdx.x] = all;
+            sum_before[threadIdx.x] = before;
+            __syncthreads();
+            all = before = 0;
+            if (x < p.experts && group == 0)
+                for (int k = 0; k < groups; ++k) {
+                    all += sum_all[k * wide + mine_of];
+                    before += sum_before[k * wide + mine_of];
+                }
+        } else if (x < p.experts) {
+            for (int w = 0; w < WARPS; ++w) all += cnt[w * p.experts + x];
         }
         int32_t inc = all;
 #pragma unroll
