@@ -67,30 +67,68 @@ __device__ __forceinline__ uint32_t load16(const T* x, int64_t n, float (&v)[Q_C
 }
 
 // The same for a row that 16-byte loads cannot take: the warp reads its 512 columns (x, n: those of its
-// lane 0) in order and hands each lane its 16 through shared memory, one word in 17 left out so that
+// lane 0, which is column `col` of the row) in order, 4 bytes at a time, and hands each lane its 16
+// through shared memory, one word left out after every 16 (fp32) or 8 (pairs of bf16) so that
 // neither side has conflicts. Loading 16 neighbours per lane took twice as long.
-template <typename T>
-__device__ __forceinline__ uint32_t load16_turned(const T* x, int64_t n, float (&v)[Q_COLS], float* buf) {
+constexpr int Q_BUF = 17 * 32;   // words per warp
+__device__ __forceinline__ uint32_t load16_turned(const float* x, int64_t, int64_t n, float (&v)[Q_COLS], uint32_t* buf) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < Q_COLS; ++e) {
         const int c = lane + 32 * e;
-        v[e] = c < n ? load_elem(x + c) : 0.0f;
+        v[e] = c < n ? x[c] : 0.0f;
     }
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < Q_COLS; ++e) {
         const int c = lane + 32 * e;
-        buf[c + (c >> 4)] = v[e];
+        buf[c + (c >> 4)] = __float_as_uint(v[e]);
     }
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < Q_COLS; ++e) {
-        v[e] = buf[17 * lane + e];
+        v[e] = __uint_as_float(buf[17 * lane + e]);
         m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
     }
     return m;
+}
+
+// bf16: whole aligned words, which for a row on an odd element hold its columns shifted by one; the
+// words at the row's ends that are not all its own are put together from single elements
+__device__ __forceinline__ uint32_t load16_turned(const __nv_bfloat16* x, int64_t col, int64_t n, float (&v)[Q_COLS], uint32_t* buf) {
+    const int lane = threadIdx.x & 31;
+    const int odd = (int)(reinterpret_cast<uintptr_t>(x) >> 1) & 1;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(x) & ~uintptr_t(3));
+    const uint16_t* halves = reinterpret_cast<const uint16_t*>(x);
+    auto word = [&](int i) -> uint32_t {   // columns c and c + 1
+        const int c = 2 * i - odd;
+        if (c + 1 < n && (c >= 0 || col > 0)) return words[i];
+        return (c >= 0 && c < n ? (uint32_t)halves[c] : 0u) | (c + 1 < n ? (uint32_t)halves[c + 1] << 16 : 0u);
+    };
+    __syncwarp();
+    uint32_t u[9];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = word(lane + 32 * e);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int i = lane + 32 * e;
+        buf[i + (i >> 3)] = u[e];
+    }
+    if (odd && lane == 0) buf[256 + 32] = word(256);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = buf[9 * lane + k];
+    u[8] = odd ? buf[9 * lane + 9] : 0u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t pair = odd ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
+        v[2 * k] = __uint_as_float(pair << 16);
+        v[2 * k + 1] = __uint_as_float(pair & 0xFFFF0000u);
+        m = __vmaxu2(m, pair & 0x7FFF7FFFu);
+    }
+    return max(m << 16, m & 0xFFFF0000u);
 }
 
 // 8 values (already divided by their block's scale) to 8 codes: nearest, ties to even, saturating
@@ -134,9 +172,9 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
         if constexpr (VEC) {
             m = load16<T, true>(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + c0), sr < 0 ? 0 : p.cols - c0, y);
         } else {
-            __shared__ float buf[Q_THREADS / 32][17 * 32];
+            __shared__ uint32_t buf[Q_THREADS / 32][Q_BUF];
             const int64_t cw = c0 - (int64_t)(threadIdx.x & 31) * Q_COLS;
-            m = load16_turned(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + cw), sr < 0 ? 0 : p.cols - cw, y,
+            m = load16_turned(static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx + cw), cw, sr < 0 ? 0 : p.cols - cw, y,
                               buf[threadIdx.x >> 5]);
         }
         if (MX) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
