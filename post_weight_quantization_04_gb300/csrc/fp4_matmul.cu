@@ -10,7 +10,7 @@
 // cta_group::2 MMAs: each holds its own 128 features, half of the tokens and all the tile's scales,
 // so a stage brings 28 KB of codes into each SM where a 128 x 192 tile of its own would take 40.
 // Roles in each CTA (persistent, one per SM):
-//   warp 0       producer: per stage of 256 columns four TMA copies, the 128 x 128-byte box of weight
+//   warp 0       producer: per stage (256 columns) four TMA copies, the 128 x 128-byte box of weight
 //                codes, that of token codes (128-byte swizzle), and the scale tiles of both
 //   warp 1       in the even CTA: scale tiles shared memory -> TMEM (tcgen05.cp, both CTAs) and the
 //                MMAs; in the odd CTA: tells the even one which stages have landed
@@ -22,13 +22,16 @@
 // tile's MMAs run, and two stages' scales in turn in the columns from 384. (Tiles of 256 tokens leave
 // room for scales only if the two buffers overlap; waiting for the shared columns cost 1.2 us a tile.)
 //
-// What bounds it: the tensor pipe, which needs 96 cycles for 64 columns of a 256 x 192 tile. A stage of MX
-// takes its 0.197 us (4 x 96 cycles at 1.95 GHz) while few pairs run, the scale copies hidden behind
-// the MMAs; 0.22 with all of them (the clock falls under the load) and 0.235 with their copies and stores
-// in full flow; a tile's end costs another 0.3. NV, with twice the scale copies in the same pipe, 0.27
-// and 0.28. Below 192 tokens the copies' latency over six stages keeps a stage at 0.2 us.
-// 8192 x 8192 x 8192: MX 152 us, 7.3 PFLOP/s, NV 184 us, 6.0. When run for long both meet the power limit
-// (1.67 GHz at 1370 W: 16384 x 4096 x 14336 MX 283 us in short runs, 310 in long ones).
+// The MMA warp's own loop takes about 200 cycles for each wait, whether or not it has to wait, so stages
+// are filled and released one by one but waited for in pairs (8192 x 8192 x 8192: MX 151 -> 147 us, NV
+// 184 -> 163; stages of twice the size instead left the copies too little room, 152 and 169).
+//
+// What bounds it: the tensor pipe, which needs 96 cycles for 64 columns of a 256 x 192 tile, 0.19 us a stage,
+// and that is what a stage of MX takes while few pairs run (NV 0.21, with twice the scale copies in the
+// same pipe); 0.21 and 0.24 when all of them do and the clock falls. Below 160 tokens a stage stays at
+// 0.14 (NV 0.19). 8192 x 8192 x 8192: MX 147 us, 7.5 PFLOP/s, NV 163 us, 6.7. When run for long both
+// meet the power limit (1.67 GHz at 1370 W: 16384 x 4096 x 14336 MX 283 us in short runs, 310 in long
+// ones).
 // Taken back: 256-token tiles with overlapping buffers, 128 and 64 tokens (slower at every size from 256
 // tokens up), a cluster of 2 or 4 pairs sharing a tile's columns (slower but for K = 14336), the odd
 // CTA's copies counted on the even one's barriers directly (no faster).
@@ -63,7 +66,7 @@ struct Stage {
     static constexpr int SW = KA * kFp4Tile, SX = 2 * KA * kFp4Tile;
     static constexpr int BYTES = W + X + SW + SX;      // a multiple of 1024
     static constexpr uint32_t SF_COLS = KA * 12;       // TMEM columns of one stage's scales
-    static constexpr int N = 6;                        // stages: what fits in 227 KB
+    static constexpr int N = 6;                        // stages: what fits in 227 KB; an even number
 };
 
 struct Maps {
@@ -357,17 +360,17 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = uniform(cluster_rank());
     const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
-    auto full = [&](int s) { return bar0 + 8u * s; };   // this CTA's copies landed (even CTA: the odd one's too)
+    auto full = [&](int s) { return bar0 + 8u * (s >> 1); };   // a pair of stages: copies landed (even CTA: the odd one's too)
     auto empty = [&](int s) { return bar0 + 8u * (NS + s); };           // the stage's MMAs are done
     auto tfull = [&](int b) { return bar0 + 8u * (2 * NS + b); };       // a tile's sums are done
     auto tfree = [&](int b) { return bar0 + 8u * (2 * NS + 2 + b); };   // even CTA: both have read a tile's sums
     const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
-    const int stages = (p.K + 2 * M_KB - 1) / (2 * M_KB);
+    const int stages = (p.K + 4 * M_KB - 1) / (4 * M_KB) * 2;   // (a last one past the columns brings zeros)
     const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(full(s), rank == 0 ? 2 : 1);
+            if (!(s & 1)) mbar_init(full(s), rank == 0 ? 3 : 2);
             mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
     } else if (warp == 1 && rank == 0) {
         // ------------------------------- MMA issuer ---------------------------------
         int stage = 0;
-        uint32_t phase = 0, it = 0, tile = 0;
+        uint32_t phase = 0, tile = 0;
         for (uint32_t i = first; i < ntiles && ok; i += step, ++tile) {
             Tile t = find_tile(p, start, i);
             t.t0 = (int)uniform(t.t0);
@@ -471,41 +474,44 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
             const uint32_t d = tmem + b * (uint32_t)M_T;
             const uint32_t tcol = (uint32_t)(t.t0 & 127) >> 5;
             const uint32_t idesc = fp4_idesc<MX>(t.n, 0), idesc2 = fp4_idesc<MX>(t.n, 2);
-            for (int kt = 0; kt < stages; ++kt, ++it) {
+            for (int kt = 0; kt < stages; kt += 2) {
                 ok = wait_all(full(stage), phase, limit);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t base = sbase + stage * S::BYTES;
                 // The scale copies need no wait of their own: the tensor pipe runs one thread's copies and MMAs
                 // in the order they were issued, and with two slots in turn a whole stage's MMAs lie
                 // between a slot's last reader and the copy that overwrites it. (Waiting for that
-                // reader all the same cost NV 16 % and MX 17 % at 8192 x 8192 x 8192, with the same results.)
-                const uint32_t sf = tmem + M_SF0 + (it & 1u) * S::SF_COLS;
-                const int ka = min(S::KA, p.tiles_k - kt * S::KA);
-                const int ksteps = min(4, (p.K - kt * 2 * M_KB + 63) / 64);
+                // reader all the same cost 16 % at 8192 x 8192 x 8192, with the same results.)
                 if (elect_one()) {
 #pragma unroll
-                    for (int a = 0; a < S::KA; ++a) {
-                        if (a < ka) {
-                            copy_scales(sf + a * 4, base + S::W + S::X + a * kFp4Tile);
-                            copy_scales(sf + S::KA * 4 + a * 8, base + S::W + S::X + S::SW + a * kFp4Tile);
-                            if (two) copy_scales(sf + S::KA * 4 + a * 8 + 4, base + S::W + S::X + 2 * S::SW + a * kFp4Tile);
-                        }
-                    }
-                    const uint64_t ad = smem_desc(base, 16, 1024, kSwizzle128B), bd = smem_desc(base + S::W, 16, 1024, kSwizzle128B);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t base = sbase + (stage + u) * S::BYTES;
+                        const uint32_t sf = tmem + M_SF0 + u * S::SF_COLS;
+                        const int ka = p.tiles_k - (kt + u) * S::KA;
+                        const int ksteps = (p.K - (kt + u) * 2 * M_KB + 63) / 64;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k < ksteps) {
-                            const int a = MX ? k >> 1 : k;
-                            umma_fp4<MX>(d, ad + 2 * k, bd + 2 * k, MX && (k & 1) ? idesc2 : idesc, sf + a * 4,
-                                         sf + S::KA * 4 + a * 8 + tcol, (kt > 0 || k > 0) ? 1u : 0u);
+                        for (int a = 0; a < S::KA; ++a) {
+                            if (a < ka) {
+                                copy_scales(sf + a * 4, base + S::W + S::X + a * kFp4Tile);
+                                copy_scales(sf + S::KA * 4 + a * 8, base + S::W + S::X + S::SW + a * kFp4Tile);
+                                if (two) copy_scales(sf + S::KA * 4 + a * 8 + 4, base + S::W + S::X + 2 * S::SW + a * kFp4Tile);
+                            }
                         }
+                        const uint64_t ad = smem_desc(base, 16, 1024, kSwizzle128B), bd = smem_desc(base + S::W, 16, 1024, kSwizzle128B);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k < ksteps) {
+                                const int a = MX ? k >> 1 : k;
+                                umma_fp4<MX>(d, ad + 2 * k, bd + 2 * k, MX && (k & 1) ? idesc2 : idesc, sf + a * 4,
+                                             sf + S::KA * 4 + a * 8 + tcol, (kt > 0 || u > 0 || k > 0) ? 1u : 0u);
+                            }
+                        }
+                        commit_pair(empty(stage + u));
                     }
-                    commit_pair(empty(stage));
-                    if (kt == stages - 1) commit_pair(tfull(b));
+                    if (kt == stages - 2) commit_pair(tfull(b));
                 }
                 __syncwarp();
-                if (++stage == NS) {
+                if ((stage += 2) == NS) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -522,12 +528,12 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         int stage = 0;
         uint32_t phase = 0;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
-            for (int kt = 0; kt < stages; ++kt) {
+            for (int kt = 0; kt < stages; kt += 2) {
                 ok = wait_all(full(stage), phase, limit);
                 if (!ok) break;
                 if (leader) arrive_cluster(in_even_cta(full(stage)));
                 __syncwarp();
-                if (++stage == NS) {
+                if ((stage += 2) == NS) {
                     stage = 0;
                     phase ^= 1u;
                 }
