@@ -105,12 +105,13 @@ __device__ __forceinline__ void expert_rows(const MParams& p, int e, int* lo, in
     *hi = h;
 }
 
-// rows that belong to no expert are zero (ranges that were clamped are an error)
-__device__ __forceinline__ void zero_tail(const MParams& p, int64_t i, int64_t step) {
-    const int live = min(max(p.offsets[p.experts], 0), p.T);
-    const int64_t n = (int64_t)(p.T - live) * p.N;
+// rows that belong to no expert, before the first range and after the last one, are zero (ranges that
+// were clamped are an error)
+__device__ __forceinline__ void zero_rest(const MParams& p, int64_t i, int64_t step) {
+    const int first = min(max(p.offsets[0], 0), p.T), last = max(min(p.offsets[p.experts], p.T), first);
+    const int64_t n = (int64_t)(p.T - (last - first)) * p.N;
     for (; i < n; i += step) {
-        const int64_t at = (live + i / p.N) * p.ldy + i % p.N;
+        const int64_t r = i / p.N, at = (r < first ? r : r + (last - first)) * p.ldy + i % p.N;
         if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(0.0f);
         else static_cast<float*>(p.Y)[at] = 0.0f;
     }
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
         const int c0 = M_T / 2 * ((warp - 2) >> 2);   // its half of the columns
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         const uint32_t turn = sbase + NS * S::BYTES + (warp - 2) * M_TURN;
-        if (p.offsets) zero_tail(p, (int64_t)blockIdx.x * 256 + threadIdx.x - 64, (int64_t)gridDim.x * 256);
+        if (p.offsets) zero_rest(p, (int64_t)blockIdx.x * 256 + threadIdx.x - 64, (int64_t)gridDim.x * 256);
         const float gx = MX ? 1.0f : *p.xg;
         uint32_t tile = 0;
         for (uint32_t i = first; i < ntiles; i += step, ++tile) {
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(F_THREADS) fp4_few_rows_kernel(const MParams p
     const int e = blockIdx.y;
     pdl_wait();
     if (e == p.experts) {   // (only with offsets)
-        zero_tail(p, (int64_t)blockIdx.x * F_THREADS + threadIdx.x, (int64_t)gridDim.x * F_THREADS);
+        zero_rest(p, (int64_t)blockIdx.x * F_THREADS + threadIdx.x, (int64_t)gridDim.x * F_THREADS);
         return;
     }
     int lo, hi;

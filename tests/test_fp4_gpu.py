@@ -355,6 +355,26 @@ def test_a_nan_scale_stays_in_its_row(lib, fmt, T):
     np.testing.assert_array_equal(Y[~nan], (xv @ wv.T)[~nan])
 
 
+@pytest.mark.parametrize("T,first,last", [(3, 1, 2), (4, 4, 4), (70, 9, 61), (400, 130, 399)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_rows_in_no_range_are_zero(lib, T, first, last, bf16):
+    """Rows before the first range and after the last one, with a Y that held something else."""
+    rng = np.random.default_rng(T + first)
+    N, K = 136, 320
+    cx, bx, xv = _stored(rng, T, K, "mx", True, 1)
+    cw, bw, wv = _stored(rng, 2 * N, K, "mx", True, 1)
+    one = [_fp4(lib, cw[e * N:(e + 1) * N], bw[e * N:(e + 1) * N], K, "mx", 1.0) for e in range(2)]
+    W = one[0]._replace(codes=torch.stack([q.codes for q in one]), scales=torch.stack([q.scales for q in one]))
+    mid = (first + last) // 2
+    offsets = torch.tensor([first, mid, last], dtype=torch.int32, device=DEV)
+    out = torch.full((T, N), 7.0, dtype=dtype_of(bf16), device=DEV)
+    lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, "mx", 1.0), W, offsets=offsets, out_dtype=dtype_of(bf16), out=out)
+    want = np.zeros((T, N))
+    want[first:mid] = xv[first:mid] @ wv[:N].T
+    want[mid:last] = xv[mid:last] @ wv[N:].T
+    np.testing.assert_array_equal(npy(out), npy(torch.tensor(want).to(dtype_of(bf16))))
+
+
 def test_results_given_and_on_the_current_stream(lib):
     """The forms with `out` and `stream`, and the common form on a stream of the caller's, agree."""
     X = torch.randn(150, 300, device=DEV).to(torch.bfloat16)
