@@ -320,7 +320,7 @@ int gptq_fp4_tile_scales(const uint8_t* src, int64_t rows, int64_t cols, int64_t
  *   w_codes, w_scales  the experts' stored matrices one after another
  *   x_g, w_g device fp32, NVFP4 only: x_g one number, w_g one, or `experts` numbers with
  *            GPTQ_FP4_EXPERT_G
- *   flags    GPTQ_DQ_RELU, GPTQ_DQ_BF16_OUT (else fp32), GPTQ_FP4_EXPERT_G
+ *   flags    GPTQ_DQ_RELU (a NaN stays one), GPTQ_DQ_BF16_OUT (else fp32), GPTQ_FP4_EXPERT_G
  *   Y        device, (T, N) row-major, row stride ldy elements
  * Sums are fp32; the result is rounded once. Allocates nothing. Synchronises `stream` and
  * returns the device status (in the deferred status mode neither).

@@ -273,6 +273,13 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     }
 }
 
+// max(x, 0) that keeps a NaN
+__device__ __forceinline__ float relu_of(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 32 tokens of one feature to Y: the lanes of a warp hold consecutive features, so each token is
 // one store of 64 or 128 consecutive bytes
 template <typename T>
@@ -280,7 +287,7 @@ __device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
         if (j >= first && j < last) {
-            const float x = __uint_as_float(v[j]) * g, z = relu ? fmaxf(x, 0.0f) : x;
+            const float x = __uint_as_float(v[j]) * g, z = relu ? relu_of(x) : x;
             if constexpr (sizeof(T) == 2) *y = __float2bfloat16_rn(z);
             else *y = z;
         }
@@ -309,8 +316,8 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 __device__ __forceinline__ uint32_t two_bf16(uint32_t a, uint32_t b, float g, bool relu) {
     float x = __uint_as_float(a) * g, y = __uint_as_float(b) * g;
     if (relu) {
-        x = fmaxf(x, 0.0f);
-        y = fmaxf(y, 0.0f);
+        x = relu_of(x);
+        y = relu_of(y);
     }
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -699,7 +706,7 @@ __device__ __forceinline__ void few_rows(const MParams& p, int e, int t0, int n,
         float v = 0.0f;
         for (int k = 0; k < F_THREADS / 32; ++k) v += part[k][threadIdx.x];
         if (!MX) v *= *p.xg * p.wg[e * p.wg_stride];
-        if (p.relu) v = fmaxf(v, 0.0f);
+        if (p.relu) v = relu_of(v);
         if (f < p.N && t < n) {
             const int64_t at = (int64_t)(t0 + t) * p.ldy + f;
             if (p.bf16_out) static_cast<__nv_bfloat16*>(p.Y)[at] = __float2bfloat16_rn(v);

@@ -355,6 +355,23 @@ def test_a_nan_scale_stays_in_its_row(lib, fmt, T):
     np.testing.assert_array_equal(Y[~nan], (xv @ wv.T)[~nan])
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("T,N,bf16", [(2, 300, False), (70, 300, False), (70, 304, True), (400, 304, True)])
+def test_relu_keeps_a_nan(lib, fmt, T, N, bf16):
+    rng = np.random.default_rng(T)
+    K = 700
+    cx, bx, xv = _stored(rng, T, K, fmt, True, 1)
+    cw, bw, wv = _stored(rng, N, K, fmt, True, 1)
+    bx[1, 3] = bw[130, 5] = 255 if fmt == "mx" else 127
+    Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, 1.0), _fp4(lib, cw, bw, K, fmt, 1.0), relu=True,
+                                out_dtype=dtype_of(bf16)))
+    nan = np.zeros((T, N), bool)
+    nan[1] = nan[:, 130] = True
+    np.testing.assert_array_equal(np.isnan(Y), nan)
+    want = npy(torch.tensor(np.maximum(xv @ wv.T, 0)).to(dtype_of(bf16)))
+    np.testing.assert_array_equal(Y[~nan], want[~nan])
+
+
 @pytest.mark.parametrize("T,first,last", [(3, 1, 2), (4, 4, 4), (70, 9, 61), (400, 130, 399)])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_rows_in_no_range_are_zero(lib, T, first, last, bf16):
