@@ -289,7 +289,8 @@ int gptq_fp4_tensor_scale(const void* X, int dtype, int64_t rows, int64_t cols, 
  * index[r] < 0 (gptq_expert_sort's src with per = its top gathers and quantises the experts'
  * rows in one pass); NULL: rows == src_rows, in order. Per block, with a = max|x|:
  *   MXFP4  c = max(floor(log2 a) - 2 + 127, 0), s = 2^(c - 127) (c = 0 where a = 0)
- *   NVFP4  c = e4m3(min(a / (6 g), 448)) to nearest even, s = c * g (g: device, 1 fp32)
+ *   NVFP4  c = e4m3(min(a / (6 g), 448)) to nearest even, 0 where a = 0; s = c * g (g: device,
+ *          1 fp32)
  * and code = the e2m1 number nearest to x / s (the fp32 quotient), ties to even, saturating
  * at 6; zeros where s = 0. Synchronises `stream` to report a NaN or infinity in X as
  * NONFINITE (its block's scale is then NaN) or an index past X's rows as INVALID_ARG (read as

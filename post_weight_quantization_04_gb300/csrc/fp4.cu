@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_quantize_kernel(const QParams p
             const float aq = a * inv6g;
             const float ratio = aq > 0x1p-100f && aq < 0x1p100f && inv6g > 0x1p-60f && inv6g < 0x1p60f
                                     ? fmaf(fmaf(-aq, 6.0f * g, a), inv6g, aq) : a / (6.0f * g);
-            byte = bad ? 127u : (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
+            // (a block of zeros has a scale of zero under any g: g = max|x| / 2688 of a matrix of zeros is 0)
+            byte = bad ? 127u : a > 0.0f ? (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3) : 0u;
             float d = e4m3_value(byte) * g;
             if (!(d >= 0x1p-60f && d <= 0x1p60f)) {
                 const float f = d < 1.0f ? 0x1p64f : 0x1p-64f;

@@ -392,6 +392,16 @@ def test_rows_in_no_range_are_zero(lib, T, first, last, bf16):
     np.testing.assert_array_equal(npy(out), npy(torch.tensor(want).to(dtype_of(bf16))))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [64, 65])
+def test_zeros_under_a_scale_of_zero(lib, dtype, cols):
+    """A tensor scale of max|x| / 2688 is zero for a matrix of zeros, and its blocks are zeros all the same."""
+    q = lib.gptq_fp4_quantize(torch.zeros(5, cols, dtype=dtype, device=DEV), "nv", torch.zeros(1, device=DEV))
+    assert (lib.gptq_fp4_dequantize(q) == 0).all()
+    w = lib.gptq_fp4_quantize(torch.ones(40, cols, device=DEV), "nv")
+    assert (lib.gptq_fp4_matmul(q, w) == 0).all()
+
+
 def test_results_given_and_on_the_current_stream(lib):
     """The forms with `out` and `stream`, and the common form on a stream of the caller's, agree."""
     X = torch.randn(150, 300, device=DEV).to(torch.bfloat16)
