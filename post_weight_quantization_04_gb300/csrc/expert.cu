@@ -590,7 +590,8 @@ extern "C" int gptq_expert_combine_grad(const void* dY, int64_t lddy, const void
                                         const float* weights, void* dYs, int64_t lddys, float* dW, void* stream) {
     if (bad_shape(tokens, top, d) || bad_dtype(dtype) || experts < 1) return GPTQ_ERR_INVALID_ARG;
     if (tokens == 0) return GPTQ_OK;
-    if (!dY || !Ys || !pos || !offsets || !weights || !dYs || !dW || lddy < d || ldys < d || lddys < d) return GPTQ_ERR_INVALID_ARG;
+    if ((d > 0 && (!dY || !Ys || !dYs)) || !pos || !offsets || !weights || !dW || lddy < d || ldys < d || lddys < d)
+        return GPTQ_ERR_INVALID_ARG;   // (rows of no columns are no memory; dW is 0)
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));

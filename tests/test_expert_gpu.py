@@ -128,6 +128,14 @@ def test_nonfinite_rows_that_no_slot_reads_stay_out(lib):
     assert torch.isfinite(dys).all() and torch.isfinite(dw).all()
 
 
+def test_rows_of_no_columns(lib):
+    r = lib.gptq_expert_sort(torch.tensor([[0, 1], [1, -1]], dtype=torch.int32, device=DEV), 2)
+    x, ys, w = torch.empty(2, 0, device=DEV), torch.empty(4, 0, device=DEV), torch.ones(2, 2, device=DEV)
+    assert lib.gptq_expert_gather(x, r).shape == (4, 0) and lib.gptq_expert_combine(ys, r, w).shape == (2, 0)
+    dys, dw = lib.gptq_expert_combine_grad(x, ys, r, w)
+    assert dys.shape == (4, 0) and (dw == 0).all()
+
+
 def test_places_past_the_rows_are_reported(lib):
     _, r, x, ys, dy, w = _setup(lib, 8, 2, 4, 64, "f32", drop=0.0)
     r = r._replace(pos=r.pos.clone())
