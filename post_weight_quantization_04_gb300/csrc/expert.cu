@@ -220,7 +220,13 @@ template <int WARPS>
 cudaError_t launch_place(const SParams& p, unsigned grid, cudaStream_t s) {
     const size_t smem = sizeof(int32_t) * WARPS * p.experts;
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(expert_place_kernel<WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // 48 KB, static and dynamic together, is what a launch may have by default. The limit is the kernel's and not the
+    // call's, so it is raised to what the most experts need: another thread's call sets the same. (8 warps
+    // stay below 48 KB.)
+    constexpr size_t kStatic = sizeof(int32_t) * (2 * 32 * WARPS + WARPS + 1) + 64, kMost = sizeof(int32_t) * WARPS * S_MAX_EXPERTS;
+    static_assert(kStatic + kMost <= 227 * 1024, "an SM's shared memory");
+    if (smem + kStatic > 48 * 1024)
+        e = cudaFuncSetAttribute(expert_place_kernel<WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
     if (grid > 1) GPTQ_LAUNCH(K_EXPERT_SORT, s, e = launch_pdl(expert_place_kernel<WARPS>, dim3(grid), dim3(32 * WARPS), smem, s, p));
     else GPTQ_LAUNCH(K_EXPERT_SORT, s, expert_place_kernel<WARPS><<<grid, 32 * WARPS, smem, s>>>(p));

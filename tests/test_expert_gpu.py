@@ -197,3 +197,44 @@ def test_binding_refusals(lib):
                  lambda: lib.gptq_expert_combine_grad(dy.bfloat16(), ys, r, w), lambda: lib.gptq_expert_combine_grad(dy, ys, r, w[:2])):
         with pytest.raises(ValueError):
             call()
+
+
+# 1025 to 4096 slots are sorted by one CTA of 32 warps, whose counters (128 bytes per expert) need more shared
+# memory than a launch has by default from 319 experts on; those run before larger numbers
+@pytest.mark.parametrize("T,k", [(1025, 1), (256, 8), (2048, 2)])
+@pytest.mark.parametrize("E", [318, 319, 384, 383, 385, 1024])
+def test_sort_in_one_block_with_many_experts(lib, T, k, E):
+    ids = _ids(T, k, E, T + k + E, 0.1)
+    r = lib.gptq_expert_sort(torch.tensor(ids, device=DEV), E)
+    o, s, p = F.route(ids, E)
+    np.testing.assert_array_equal(r.offsets.cpu().numpy(), o)
+    np.testing.assert_array_equal(r.pos.cpu().numpy(), p)
+    np.testing.assert_array_equal(r.src.cpu().numpy(), s)
+
+
+def test_sorts_of_two_threads(lib):
+    """Two host threads that sort for other numbers of experts on streams of their own: what a launch needs
+    of the kernel is not what the other thread set for its own."""
+    import threading
+    failed = []
+
+    def work(E):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                ids = _ids(500, 4, E, E)
+                want = torch.tensor(F.route(ids, E)[2].astype(np.int32), device=DEV)
+                t = torch.tensor(ids, device=DEV)
+                for _ in range(3000):
+                    r = lib.gptq_expert_sort(t, E)
+                assert torch.equal(r.pos, want)
+        except Exception as e:  # noqa: BLE001
+            failed.append((E, repr(e)))
+
+    with lib.deferred_status():
+        threads = [threading.Thread(target=work, args=(E,)) for E in (400, 1024)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        lib.status_sync()
+    assert not failed, failed
