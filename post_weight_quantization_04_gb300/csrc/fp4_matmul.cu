@@ -795,8 +795,12 @@ int launch_few(const MParams& p, cudaStream_t s) {
 
 template <bool MX>
 int launch(const Maps& m, const MParams& p, int64_t most_tiles, cudaStream_t s) {
-    const int smem = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * M_TURN + 8 * (2 * Stage<MX>::N + 5) + 8 + 4 * (p.experts + 1);
-    GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    constexpr int kFixed = 1024 + Stage<MX>::N * Stage<MX>::BYTES + 8 * M_TURN + 8 * (2 * Stage<MX>::N + 5) + 8;
+    constexpr int kMost = kFixed + 4 * (M_MAX_EXPERTS + 1);
+    static_assert(kMost <= 227 * 1024, "an SM's shared memory");
+    const int smem = kFixed + 4 * (p.experts + 1);
+    // the limit is the kernel's and not the call's: every thread's calls set it to the same number
+    GPTQ_CUDA_TRY(cudaFuncSetAttribute(fp4_matmul_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2));
     cfg.blockDim = dim3(M_THREADS);

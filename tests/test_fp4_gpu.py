@@ -457,3 +457,38 @@ def test_binding_refusals(lib):
                  lambda: lib.gptq_fp4_dequantize(q, torch.float16), lambda: lib.gptq_fp4_dequantize(q, out=X[:, :63])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_products_of_two_threads(lib):
+    """Two host threads on streams of their own, one with a dense product, one with many experts: what a
+    launch needs of the kernel is not what the other thread set for its own."""
+    import threading
+    rng = np.random.default_rng(6)
+    T, N, K, E = 70, 64, 64, 600
+    cx, bx, xv = _stored(rng, T, K, "nv", True, 1)
+    X = _fp4(lib, cx, bx, K, "nv", 1.0)
+    cw, bw, wv = _stored(rng, E * N, K, "nv", True, 1)
+    ones = [_fp4(lib, cw[e * N:(e + 1) * N], bw[e * N:(e + 1) * N], K, "nv", 1.0) for e in range(E)]
+    W = ones[0]._replace(codes=torch.stack([q.codes for q in ones]), scales=torch.stack([q.scales for q in ones]))
+    offsets = torch.tensor([0] * E + [T], dtype=torch.int32, device=DEV)       # all rows to the last one
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(w, off, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(3000):
+                    Y = lib.gptq_fp4_matmul(X, w, offsets=off)
+                np.testing.assert_array_equal(npy(Y), want)
+        except Exception as e:  # noqa: BLE001
+            failed.append((off is None, repr(e)))
+
+    with lib.deferred_status():
+        threads = [threading.Thread(target=work, args=a)
+                   for a in ((ones[0], None, xv @ wv[:N].T), (W, offsets, xv @ wv[-N:].T))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        lib.status_sync()
+    assert not failed, failed
