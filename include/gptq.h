@@ -323,6 +323,7 @@ int gptq_fp4_tile_scales(const uint8_t* src, int64_t rows, int64_t cols, int64_t
  *            GPTQ_FP4_EXPERT_G
  *   flags    GPTQ_DQ_RELU (a NaN stays one), GPTQ_DQ_BF16_OUT (else fp32), GPTQ_FP4_EXPERT_G
  *   Y        device, (T, N) row-major, row stride ldy elements
+ * K >= 1 (the Python binding gives the zeros of K = 0 itself).
  * Sums are fp32; the result is rounded once. Allocates nothing. Synchronises `stream` and
  * returns the device status (in the deferred status mode neither).
  * Errors: INVALID_ARG, UNSUPPORTED (more than 1024 experts, or 2^31 rows of

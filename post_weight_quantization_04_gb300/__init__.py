@@ -658,6 +658,9 @@ def gptq_fp4_matmul(X: Fp4, W: Fp4, offsets: Optional[torch.Tensor] = None, relu
     T, N = X.codes.shape[0], W.codes.shape[-2]
     Y = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=X.codes.device)
     ld = N if out is None else _matrix_like(Y, "out", out_dtype, T, N)
+    if X.cols == 0:   # a sum of nothing; the library's products have a column or more
+        with torch.cuda.stream(stream):
+            return Y.zero_()
     flags = (DQ_RELU if relu else 0) | (DQ_BF16_OUT if out_dtype is torch.bfloat16 else 0)
     if f == NVFP4 and experts > 1 and W.tensor_scale.numel() == experts:
         flags |= FP4_EXPERT_G

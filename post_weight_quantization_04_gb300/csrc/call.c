@@ -254,7 +254,7 @@ static PyObject* matmul(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Tensor offsets = {0};
     const int grouped = n == 5 && a[2] != Py_None;
     if (n != 5 || dtype_code(a[4]) < 0 || !read_fp4(a[0], 0, &x) || !read_fp4(a[1], grouped, &w) || x.format != w.format ||
-        x.cols != w.cols || (grouped && (!read_typed(a[2], o_i32, 1, &offsets) || offsets.shape[0] != w.experts + 1)))
+        x.cols != w.cols || x.cols == 0 || (grouped && (!read_typed(a[2], o_i32, 1, &offsets) || offsets.shape[0] != w.experts + 1)))
         Py_RETURN_NOTIMPLEMENTED;
     const int relu = PyObject_IsTrue(a[3]);
     if (relu < 0) return NULL;

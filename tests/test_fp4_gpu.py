@@ -492,3 +492,23 @@ def test_products_of_two_threads(lib):
             t.join()
         lib.status_sync()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("T", [0, 3, 200])
+def test_product_of_no_columns(lib, fmt, T):
+    """A sum over no columns is 0, dense and by expert, into a result that held something else."""
+    x, w = torch.empty(T, 0, device=DEV), torch.empty(72, 0, device=DEV, dtype=torch.bfloat16)
+    X, W = lib.gptq_fp4_quantize(x, fmt), lib.gptq_fp4_quantize(w, fmt)
+    Y = lib.gptq_fp4_matmul(X, W, relu=True)
+    assert Y.shape == (T, 72) and (Y == 0).all()
+    wide = torch.full((T, 80), 7.0, dtype=torch.bfloat16, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    lib.gptq_fp4_matmul(X, W, out_dtype=torch.bfloat16, out=wide[:, :72], stream=s)
+    s.synchronize()
+    assert (wide[:, :72] == 0).all() and (wide[:, 72:] == 7).all()
+    E = lib.Fp4(torch.stack([W.codes] * 2), torch.stack([W.scales] * 2), 0, fmt, W.tensor_scale)
+    offsets = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    Y = lib.gptq_fp4_matmul(X, E, offsets=offsets)
+    assert Y.shape == (T, 72) and (Y == 0).all()
