@@ -273,6 +273,25 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     }
 }
 
+// The product of both tensor scales as g * back * back. back is 1 unless the product is subnormal or past
+// fp32, where it would lose bits, or all of them, although the scales and the results are ordinary numbers
+// (1e-22 * 1e-22 has 3 bits, while sums of codes and block scales reach 1e9).
+struct TensorScale {
+    float g, back;
+};
+__device__ __forceinline__ TensorScale tensor_scale(float a, float b) {
+    const float m = fabsf(a * b);
+    const float s = m < 0x1p-126f ? 0x1p32f : m > 0x1.fffffep127f ? 0x1p-64f : 1.0f;
+    return {(a * s) * (b * s), 1.0f / s};
+}
+
+// sums times the tensor scale where that is not one number, which is left as 1
+template <int N>
+__device__ __forceinline__ void apply_unusual(uint32_t (&v)[N], const TensorScale& t) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * t.g * t.back * t.back);
+}
+
 // max(x, 0) that keeps a NaN
 __device__ __forceinline__ float relu_of(float x) {
     float y;
@@ -562,7 +581,9 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
             ok = wait_all(tfull(b), (tile >> 1) & 1u, limit);
             if (!ok) break;
             tc_fence_after();
-            const float g = MX ? 1.0f : gx * p.wg[t.e * p.wg_stride];
+            TensorScale g = {1.0f, 1.0f};
+            if (!MX) g = tensor_scale(gx, p.wg[t.e * p.wg_stride]);
+            const bool unusual = !MX && g.back != 1.0f;
             const int f0 = t.f0 + (int)rank * M_F + 32 * q;
             const uint32_t sums = tmem + lanes + b * (uint32_t)M_T + c0;
             // all of its columns into registers (those past the tile's tokens too: the buffer has them), so
@@ -578,9 +599,14 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_even_cta(tfree(b)));
+                if (unusual) {
+#pragma unroll
+                    for (int c = 0; c < M_T / 32; ++c) apply_unusual(v[c >> 1][c & 1], g);
+                    g.g = 1.0f;
+                }
 #pragma unroll
                 for (int c = 0; c < M_T / 64; ++c)
-                    if (c0 + 32 * c < t.n) turn_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f0, turn);
+                    if (c0 + 32 * c < t.n) turn_tokens(p, v[c], g.g, t, t.t0 + c0 + 32 * c, f0, turn);
             } else {
                 uint32_t v[M_T / 64][32];
 #pragma unroll
@@ -589,9 +615,14 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_even_cta(tfree(b)));
+                if (unusual) {
+#pragma unroll
+                    for (int c = 0; c < M_T / 64; ++c) apply_unusual(v[c], g);
+                    g.g = 1.0f;
+                }
 #pragma unroll
                 for (int c = 0; c < M_T / 64; ++c)
-                    if (c0 + 32 * c < t.n) store_tokens(p, v[c], g, t, t.t0 + c0 + 32 * c, f0 + lane);
+                    if (c0 + 32 * c < t.n) store_tokens(p, v[c], g.g, t, t.t0 + c0 + 32 * c, f0 + lane);
             }
         }
     }
@@ -705,7 +736,10 @@ __device__ __forceinline__ void few_rows(const MParams& p, int e, int t0, int n,
         const int i = threadIdx.x / NT, t = threadIdx.x % NT, f = fb + (i & 1) + 32 * (i >> 1);
         float v = 0.0f;
         for (int k = 0; k < F_THREADS / 32; ++k) v += part[k][threadIdx.x];
-        if (!MX) v *= *p.xg * p.wg[e * p.wg_stride];
+        if (!MX) {
+            const TensorScale g = tensor_scale(*p.xg, p.wg[e * p.wg_stride]);
+            v = v * g.g * g.back * g.back;
+        }
         if (p.relu) v = relu_of(v);
         if (f < p.N && t < n) {
             const int64_t at = (int64_t)(t0 + t) * p.ldy + f;

@@ -512,3 +512,45 @@ def test_product_of_no_columns(lib, fmt, T):
     offsets = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
     Y = lib.gptq_fp4_matmul(X, E, offsets=offsets)
     assert Y.shape == (T, 72) and (Y == 0).all()
+
+
+
+def _close(Y, xv, wv, bf16, K):
+    """The bound of the module for results near the ends of fp32 (plus one unit of its, or bf16's, subnormal numbers)."""
+    ref = xv @ wv.T
+    bound = (K + 4) * 2.0 ** -23 * (np.abs(xv) @ np.abs(wv).T) + (2.0 ** -8 * np.abs(ref) + 2.0 ** -133 if bf16 else 2.0 ** -148)
+    assert np.isfinite(Y).all() and (np.abs(Y - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("gx,gw", [(1e-22, 1e-22), (3e-30, 7e-12), (1e-8, 2e-37), (1e22, 1e17), (5e37, 20.0)])
+@pytest.mark.parametrize("T,N,bf16", [(1, 300, False), (3, 300, True), (70, 300, False), (70, 304, True), (400, 300, True)])
+def test_matmul_with_a_product_of_tensor_scales_outside_fp32(lib, gx, gw, T, N, bf16):
+    """Both tensor scales and every result are ordinary numbers, their product is subnormal or past fp32.
+    The bound of the module, with the product of the tensor scales rounded once as ever."""
+    rng = np.random.default_rng(T + N)
+    K = 200
+    gx, gw = float(np.float32(gx)), float(np.float32(gw))
+    cx, cw = rng.integers(0, 16, (T, K)), rng.integers(0, 16, (N, K))
+    lo, hi = (100, 126) if gx < 1 else (1, 3)             # large or small block scales: every result fits fp32
+    bx, bw = (rng.integers(lo, hi, (r, -(-K // 16))).astype(np.uint8) for r in (T, N))
+    cx[0] = 0                                             # a row of zeros
+    xv, wv = F.values(cx, bx, "nv", gx), F.values(cw, bw, "nv", gw)
+    Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, "nv", gx), _fp4(lib, cw, bw, K, "nv", gw), out_dtype=dtype_of(bf16)))
+    _close(Y, xv, wv, bf16, K)
+    assert (Y[0] == 0).all()
+
+
+def test_grouped_matmul_with_products_of_tensor_scales_outside_fp32(lib):
+    rng = np.random.default_rng(12)
+    T, N, K, gx, gw = 150, 136, 160, float(np.float32(1e-22)), [1.0, float(np.float32(2e-21)), 0.5]
+    cx, bx = rng.integers(0, 16, (T, K)), rng.integers(100, 126, (T, K // 16)).astype(np.uint8)
+    cw, bw = rng.integers(0, 16, (3, N, K)), rng.integers(100, 126, (3, N, K // 16)).astype(np.uint8)
+    off = [0, 50, 101, 150]
+    for t in (T, 3):                                      # (3 rows: the kernel for few rows)
+        o = off if t == T else [0, 1, 2, 3]
+        W = lib.Fp4(torch.tensor(np.stack([F.pack_codes(c) for c in cw]), device=DEV),
+                    torch.tensor(np.stack([F.tile_scales(b, K, "nv") for b in bw]), device=DEV), K, "nv", torch.tensor(gw, device=DEV))
+        Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx[:t], bx[:t], K, "nv", gx), W, offsets=torch.tensor(o, dtype=torch.int32, device=DEV)))
+        for e in range(3):
+            r = slice(o[e], o[e + 1])
+            _close(Y[r], F.values(cx[r], bx[r], "nv", gx), F.values(cw[e], bw[e], "nv", gw[e]), False, K)
