@@ -277,7 +277,8 @@ int64_t gptq_fp4_code_pitch(int64_t cols);
 int64_t gptq_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
 
 /* *g (device) = the least power of two for which no NVFP4 block scale of X saturates:
- * max|x| <= 448 * 6 * g; 1 where X is all zeros. A power of two keeps block scale * g exact.
+ * max|x| <= 448 * 6 * g, 2^-126 at least; 1 where X is all zeros. A power of two keeps block
+ * scale * g exact.
  * X (rows, cols) bf16 or fp32, row stride ldx. Synchronises `stream` to report a NaN or
  * infinity in X as NONFINITE (not in the deferred status mode). Errors: INVALID_ARG,
  * NONFINITE, CUDA. */

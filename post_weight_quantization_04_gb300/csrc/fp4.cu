@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(Q_THREADS) fp4_amax_kernel(const T* X, int64_t
     }
 }
 
-// the least power of two g with max|x| <= 448 * 6 * g, in place of the maximum (1 for all zeros)
+// the least normal power of two g with max|x| <= 448 * 6 * g, in place of the maximum (1 for all zeros)
 __global__ void fp4_tensor_scale_kernel(uint32_t* out) {
     const float a = __uint_as_float(*out);
     int e = 0;
     if (a > 0.0f && a < __uint_as_float(0x7F800000u)) {
-        frexpf(a / 2688.0f, &e);
+        frexpf(fmaxf(a / 2688.0f, 0x1p-126f), &e);   // (below that the quotient has few bits or is 0)
         if (ldexpf(0.5f, e) * 2688.0f >= a) --e;   // a / 2688 is a power of two itself
     }
     *out = __float_as_uint(ldexpf(1.0f, max(e, -126)));

@@ -554,3 +554,11 @@ def test_grouped_matmul_with_products_of_tensor_scales_outside_fp32(lib):
         for e in range(3):
             r = slice(o[e], o[e + 1])
             _close(Y[r], F.values(cx[r], bx[r], "nv", gx), F.values(cw[e], bw[e], "nv", gw[e]), False, K)
+
+
+@pytest.mark.parametrize("amax", [2.0 ** -149, 1e-42, 2.0 ** -138, 2688 * 2.0 ** -149, 1e-38, 2688 * 2.0 ** -126])
+def test_tensor_scale_of_subnormal_numbers(lib, amax):
+    """The least power of two that fp32 holds as a normal number, also where max|x| / 2688 vanishes."""
+    X = torch.zeros(3, 20, device=DEV)
+    X[1, 7] = -amax
+    assert lib.gptq_fp4_tensor_scale(X).item() == 2.0 ** -126
