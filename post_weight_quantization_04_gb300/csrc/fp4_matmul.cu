@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
 // codes) of each feature and of up to 4 tokens, every 128th such piece. Codes become half2 (one
 // conversion per byte), and the products of 16 columns are summed in half2: each is a multiple of
 // 1/4 up to 36, so 8 of them per half stay below 512 in steps of 1/4, which 11 bits hold exactly. Those
-// sums go to fp32 with the product of both scales (at most 8 bits), and are added over the columns
+// sums go to fp32 with both scales (whose product has at most 8 bits), and are added over the columns
 // and, in a fixed order, over the CTA.
 // The 8 features are two neighbours of each 32-row quarter of a scale tile, whose scales share sectors.
 // One token x 4096 x 4096 MX: 4.1 us with its launch (9 MB); what bounds it there is latency, and with
@@ -667,6 +667,16 @@ __device__ __forceinline__ float2 two_scales(uint32_t word, int c) {
     }
     const uint32_t b = word >> (16 * (c & 1));
     return make_float2(e4m3_value(b & 0xFFu), e4m3_value((b >> 8) & 0xFFu));
+}
+
+// acc + v a b for a sum v of 32 products and two e8m0 scales. The product of the scales may be past fp32
+// where v is 0 or v a b is not; v times the smaller scale is exact (at most 13 bits from 2^-129 up) and
+// overflows only if v a b does. A NaN scale makes it NaN.
+__device__ __forceinline__ float add_scaled(float v, float a, float b, float acc) {
+    float lo, hi;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(a), "f"(b));
+    return fmaf(v * lo, hi, acc);
 }
 
 // byte of the 16-byte row (4 quarters x 4 blocks) of scale tiles for row r and 32 columns c
@@ -716,7 +726,7 @@ __device__ __forceinline__ void few_rows(const MParams& p, int e, int t0, int n,
                     h1 = __hfma2(wh[8 + k], xh[t][8 + k], h1);
                 }
                 const float2 f0 = __half22float2(h0), f1 = __half22float2(h1), st = two_scales<MX>(sx[t], c);
-                if (MX) acc[i][t] = fmaf((f0.x + f0.y) + (f1.x + f1.y), sc.x * st.x, acc[i][t]);
+                if (MX) acc[i][t] = add_scaled((f0.x + f0.y) + (f1.x + f1.y), sc.x, st.x, acc[i][t]);
                 else acc[i][t] = fmaf(f1.x + f1.y, sc.y * st.y, fmaf(f0.x + f0.y, sc.x * st.x, acc[i][t]));
             }
         }

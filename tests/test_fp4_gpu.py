@@ -562,3 +562,37 @@ def test_tensor_scale_of_subnormal_numbers(lib, amax):
     X = torch.zeros(3, 20, device=DEV)
     X[1, 7] = -amax
     assert lib.gptq_fp4_tensor_scale(X).item() == 2.0 ** -126
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 70])
+def test_mx_scales_whose_product_is_past_fp32(lib, T):
+    """Blocks whose sum is 0, or small enough, count for what they are under any two scales: exactly with a few
+    rows, whose blocks are summed one by one, and within the module's bound, which is wide next to products that
+    cancel, on the tensor cores. A NaN scale still makes its row NaN."""
+    import math
+    N, K = 40, 128
+    cx, bx = np.zeros((T, K), int), np.full((T, 4), 127, np.uint8)
+    cw, bw = np.zeros((N, K), int), np.full((N, 4), 127, np.uint8)
+
+    def check():
+        terms = (F.values(cx, bx, "mx") * F.values(cw[:1], bw[:1], "mx"))[0]
+        want = math.fsum(terms)                                # (all rows and features are alike)
+        Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, "mx", 1.0), _fp4(lib, cw, bw, K, "mx", 1.0)))
+        if T <= 4:
+            np.testing.assert_array_equal(Y, np.float32(want))
+        else:
+            assert np.isfinite(Y).all() and (np.abs(Y - want) <= (K + 4) * 2.0 ** -23 * np.abs(terms).sum()).all()
+
+    cx[:, 0], cw[:, 0] = 2, 4                                  # 1 * 2 in the first block
+    cx[:, 32:64], cw[:, 32:64:2], cw[:, 33:64:2] = 2, 2, 10    # 1 and -1 in turn: 0
+    for sx, sw in ((227, 157), (157, 227), (252, 252), (10, 252), (252, 10)):
+        bx[:, 1], bw[:, 1] = sx, sw
+        check()
+    cx[:, 32:64], cw[:, 32:64] = 0, 0
+    cx[:, 40], cw[:, 40] = 1, 9                                # 0.5 * -0.5
+    for sx, sw in ((191, 191), (222, 160), (160, 222), (252, 2), (64, 64)):
+        bx[:, 1], bw[:, 1] = sx, sw
+        check()
+    bx[0, 1], bw[:, 1] = 255, 252
+    Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, "mx", 1.0), _fp4(lib, cw, bw, K, "mx", 1.0)))
+    assert np.isnan(Y[0]).all()
