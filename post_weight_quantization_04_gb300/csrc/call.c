@@ -113,6 +113,10 @@ static int read_fp4(PyObject* q, int experts, Fp4* f) {
         !read_typed(PyTuple_GET_ITEM(q, 1), o_u8, 3 + lead, &f->scales))
         return 0;
     f->cols = PyLong_AsLongLong(cols);
+    if (PyErr_Occurred()) {   /* past 64 bits */
+        PyErr_Clear();
+        return 0;
+    }
     const int64_t *c = f->codes.shape + lead, *s = f->scales.shape + lead, span = f->format == GPTQ_MXFP4 ? 128 : 64;
     f->rows = c[0];
     f->experts = lead ? f->codes.shape[0] : 1;

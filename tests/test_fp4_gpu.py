@@ -596,3 +596,11 @@ def test_mx_scales_whose_product_is_past_fp32(lib, T):
     bx[0, 1], bw[:, 1] = 255, 252
     Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, "mx", 1.0), _fp4(lib, cw, bw, K, "mx", 1.0)))
     assert np.isnan(Y[0]).all()
+
+
+def test_a_number_of_columns_past_64_bits_is_refused(lib):
+    q = lib.gptq_fp4_quantize(torch.randn(8, 64, device=DEV), "mx")
+    wrong = q._replace(cols=2 ** 70)
+    for call in (lambda: lib.gptq_fp4_dequantize(wrong), lambda: lib.gptq_fp4_matmul(wrong, q), lambda: lib.gptq_fp4_matmul(q, wrong)):
+        with pytest.raises(ValueError):
+            call()
