@@ -345,7 +345,8 @@ int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, const float
  *   pos      tokens * top int32: each slot's place, -1 where dropped; slots of one expert
  *            keep their order
  *   src      tokens * top int32: the slot in each place, -1 past the last live place
- * ws: device, gptq_expert_sort_workspace_bytes(tokens, top, experts) bytes (may be 0).
+ * ws: device, 4-byte aligned, gptq_expert_sort_workspace_bytes(tokens, top, experts) bytes (may
+ * be 0).
  * Synchronises `stream` to report an id >= experts as INVALID_ARG (it counts as dropped);
  * not in the deferred status mode. Errors: INVALID_ARG, UNSUPPORTED (experts > 1024),
  * WORKSPACE, CUDA. */

@@ -703,7 +703,9 @@ def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor]
     route = Route(torch.empty(experts + 1, dtype=torch.int32, device=dev),
                   torch.empty(tokens * top, dtype=torch.int32, device=dev), torch.empty_like(ids))
     lib = load()
-    nb = ws.numel() if ws is not None else int(lib.gptq_expert_sort_workspace_bytes(tokens, top, experts))
+    if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
+        raise ValueError("ws must be a contiguous CUDA tensor")
+    nb = ws.numel() * ws.element_size() if ws is not None else int(lib.gptq_expert_sort_workspace_bytes(tokens, top, experts))
     if ws is None and nb:
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         if stream is not None:

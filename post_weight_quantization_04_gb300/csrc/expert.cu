@@ -524,6 +524,7 @@ extern "C" int gptq_expert_sort(const int32_t* ids, int64_t tokens, int64_t top,
     if (!offsets || (tokens > 0 && (!ids || !src || !pos))) return GPTQ_ERR_INVALID_ARG;
     const size_t need = gptq_expert_sort_workspace_bytes(tokens, top, experts);
     if (need > 0 && (!ws || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
+    if (need > 0 && reinterpret_cast<uintptr_t>(ws) % sizeof(int32_t) != 0) return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));

@@ -238,3 +238,22 @@ def test_sorts_of_two_threads(lib):
             t.join()
         lib.status_sync()
     assert not failed, failed
+
+
+def test_sort_workspaces(lib):
+    """A workspace of the caller's on any word; one that is off a word, on the host, or repeats its memory is refused."""
+    ids = torch.tensor(_ids(5000, 2, 9, 1), device=DEV)
+    want, nb = lib.gptq_expert_sort(ids, 9), lib.gptq_expert_sort_workspace_bytes(5000, 2, 9)
+    ws = torch.empty(nb + 4, dtype=torch.uint8, device=DEV)
+    for good in (ws[4:], torch.empty(nb // 4, dtype=torch.int32, device=DEV)):
+        got = lib.gptq_expert_sort(ids, 9, ws=good)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for bad in (ws.cpu(), ws[:1].expand(nb), ws[::2]):
+        with pytest.raises(ValueError):
+            lib.gptq_expert_sort(ids, 9, ws=bad)
+    with pytest.raises(lib.GptqError) as e:
+        lib.gptq_expert_sort(ids, 9, ws=ws[1:nb + 1])
+    assert e.value.status == 1
+    with pytest.raises(lib.GptqError) as e:
+        lib.gptq_expert_sort(ids, 9, ws=ws[:nb - 4])
+    assert e.value.status == 6

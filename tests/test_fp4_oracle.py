@@ -120,3 +120,8 @@ def test_other_refusals(clib):
     grad = lambda **c: clib.gptq_expert_combine_grad(*(dict(dY=P, l0=64, Y=P, l1=64, dt=1, T=4, d=64, p=P, k=2, o=P, E=8, w=P, dX=P,  # noqa: E731
                                                             l2=64, dw=P) | c).values(), Z)
     assert grad(w=Z) == 1 and grad(dw=Z) == 1 and grad(l0=3) == 1 and grad(T=0) == 0 and grad(E=0) == 1
+
+
+def test_a_sort_workspace_has_to_be_aligned(clib):
+    for at, status in ((66, 1), (65, 1)):
+        assert clib.gptq_expert_sort(P, 1 << 20, 2, 8, P, P, P, ctypes.c_void_p(at), 1 << 30, Z) == status
