@@ -511,11 +511,23 @@ def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _here(t: torch.Tensor, name: str) -> None:
+    """The library launches on the current device, and only reaches the tensors there."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _dev_here(t: torch.Tensor, dtype, name: str, shape=None) -> None:
+    _dev(t, dtype, name, shape)
+    _here(t, name)
+
+
 def _matrix(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
     """(dtype code, rows, columns, row stride) of a matrix whose rows are contiguous."""
     dt = _DTYPES.get(t.dtype)
     if dt is None or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA bf16 or fp32 tensor")
+    _here(t, name)
     rows, cols = t.shape
     ld, one = t.stride()
     if one != 1 and cols > 1:
@@ -547,10 +559,12 @@ def _check_fp4(q: Fp4, name: str, experts: Optional[int] = None) -> int:
     if not (codes.is_cuda and scales.is_cuda and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
             and codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous CUDA uint8 tensors")
+    _here(codes, name + ".codes")
+    _here(scales, name + ".scales")
     if f == NVFP4:
         if g is None:
             raise ValueError(f"{name}: format 'nv' needs a tensor scale")
-        _dev(g, torch.float32, name + ".tensor_scale")
+        _dev_here(g, torch.float32, name + ".tensor_scale")
         if g.numel() not in (1, experts):
             raise ValueError(f"{name}.tensor_scale must hold one number, or one per expert")
     return f
@@ -579,12 +593,12 @@ def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optiona
     dt, n, cols, ld = _matrix(X, "X")
     rows = n
     if index is not None:
-        _dev(index, torch.int32, "index")
+        _dev_here(index, torch.int32, "index")
         rows = index.numel()
     if f == NVFP4:
         if tensor_scale is None:
             tensor_scale = gptq_fp4_tensor_scale(X, stream)
-        _dev(tensor_scale, torch.float32, "tensor_scale")
+        _dev_here(tensor_scale, torch.float32, "tensor_scale")
         if tensor_scale.numel() != 1:
             raise ValueError("tensor_scale must hold one number")
     else:
@@ -627,7 +641,7 @@ def gptq_fp4_tile_scales(scales: torch.Tensor, cols: int, format: str, stream=No
     """Row-major scale bytes (rows, blocks) of a checkpoint, in the tiled order of Fp4.scales."""
     f = _fp4_format(format)
     rows = scales.shape[0]
-    _dev(scales, torch.uint8, "scales", (rows, -(-cols // (32 if f == MXFP4 else 16))))
+    _dev_here(scales, torch.uint8, "scales", (rows, -(-cols // (32 if f == MXFP4 else 16))))
     out = torch.empty(_fp4_scale_shape(rows, cols, format), dtype=torch.uint8, device=scales.device)
     _check("gptq_fp4_tile_scales", load().gptq_fp4_tile_scales(scales.data_ptr(), rows, cols, scales.shape[1], f,
                                                                out.data_ptr(), _raw_stream(stream)))
@@ -650,7 +664,7 @@ def gptq_fp4_matmul(X: Fp4, W: Fp4, offsets: Optional[torch.Tensor] = None, relu
     else:
         experts = W.codes.shape[0]
         _check_fp4(W, "W", experts)
-        _dev(offsets, torch.int32, "offsets", (experts + 1,))
+        _dev_here(offsets, torch.int32, "offsets", (experts + 1,))
     if X.format != W.format or X.cols != W.cols:
         raise ValueError("X and W must have the same format and columns")
     if out_dtype not in _DTYPES:
@@ -695,7 +709,7 @@ def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor]
         r = (_fast or _load_fast()).sort(ids, experts)
         if r is not NotImplemented:
             return r
-    _dev(ids, torch.int32, "ids")
+    _dev_here(ids, torch.int32, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, top)")
     tokens, top = ids.shape
@@ -705,6 +719,8 @@ def gptq_expert_sort(ids: torch.Tensor, experts: int, ws: Optional[torch.Tensor]
     lib = load()
     if ws is not None and not (ws.is_cuda and ws.is_contiguous()):
         raise ValueError("ws must be a contiguous CUDA tensor")
+    if ws is not None:
+        _here(ws, "ws")
     nb = ws.numel() * ws.element_size() if ws is not None else int(lib.gptq_expert_sort_workspace_bytes(tokens, top, experts))
     if ws is None and nb:
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
@@ -723,6 +739,8 @@ def _check_route(route: Route) -> Tuple[int, int]:
             or not src.is_cuda or not offsets.is_cuda or not pos.is_contiguous() or not src.is_contiguous()
             or not offsets.is_contiguous() or src.shape != (tokens * top,) or offsets.dim() != 1):
         raise ValueError("route must hold contiguous CUDA int32 tensors: offsets (experts + 1), src (tokens * top), pos (tokens, top)")
+    for t in route:
+        _here(t, "route")
     return tokens, top
 
 
@@ -756,7 +774,7 @@ def gptq_expert_combine(Ys: torch.Tensor, route: Route, weights: Optional[torch.
     if rows != tokens * top:
         raise ValueError(f"Ys has {rows} rows for {tokens} x {top} slots")
     if weights is not None:
-        _dev(weights, torch.float32, "weights", (tokens, top))
+        _dev_here(weights, torch.float32, "weights", (tokens, top))
     Y = out if out is not None else torch.empty((tokens, d), dtype=Ys.dtype, device=Ys.device)
     ldy = d if out is None else _matrix_like(Y, "out", Ys.dtype, tokens, d)
     _check("gptq_expert_combine", load().gptq_expert_combine(
@@ -783,11 +801,11 @@ def gptq_expert_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, route: Route, w
     if rows != tokens * top:
         raise ValueError(f"Ys has {rows} rows for {tokens} x {top} slots")
     lddy = _matrix_like(dY, "dY", Ys.dtype, tokens, d)
-    _dev(weights, torch.float32, "weights", (tokens, top))
+    _dev_here(weights, torch.float32, "weights", (tokens, top))
     dYs, dW = out if out is not None else (torch.empty((rows, d), dtype=Ys.dtype, device=Ys.device), torch.empty_like(weights))
     lds = d if out is None else _matrix_like(dYs, "out[0]", Ys.dtype, rows, d)
     if out is not None:
-        _dev(dW, torch.float32, "out[1]", (tokens, top))
+        _dev_here(dW, torch.float32, "out[1]", (tokens, top))
     _check("gptq_expert_combine_grad", load().gptq_expert_combine_grad(
         dY.data_ptr(), lddy, Ys.data_ptr(), ld, dt, tokens, d, route.pos.data_ptr(), top, route.offsets.data_ptr(),
         route.experts, weights.data_ptr(), dYs.data_ptr(), lds, dW.data_ptr(), _raw_stream(stream)))

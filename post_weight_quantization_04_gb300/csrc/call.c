@@ -14,7 +14,7 @@
 
 #include "gptq.h"
 
-static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_data_ptr, *s_device, *s_is_contiguous, *s_mx, *s_nv;
+static PyObject *s_dtype, *s_get_device, *s_shape, *s_stride, *s_data_ptr, *s_device, *s_is_contiguous, *s_mx, *s_nv;
 static PyObject *o_f32, *o_bf16, *o_u8, *o_i32, *f_empty, *f_raw_stream, *f_current_device, *t_fp4, *t_route, *f_check;
 static PyObject* k_empty; /* ("dtype", "device") */
 
@@ -31,6 +31,19 @@ static int (*p_combine)(const void*, int, int64_t, int64_t, int64_t, const int32
 static int (*p_combine_grad)(const void*, int64_t, const void*, int64_t, int, int64_t, int64_t, const int32_t*, int64_t,
                              const int32_t*, int64_t, const float*, void*, int64_t, float*, void*);
 
+/* The device that a call of this thread launches on; its tensors have to be there. */
+static _Thread_local long here;
+
+static void find_device(void) {
+    PyObject* d = PyObject_CallNoArgs(f_current_device);
+    here = d ? PyLong_AsLong(d) : -2;   /* -1 is the host */
+    Py_XDECREF(d);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        here = -2;
+    }
+}
+
 /* ------------------------------------------------------------------------------ what a tensor is */
 
 typedef struct {
@@ -42,11 +55,11 @@ typedef struct {
 } Tensor;
 
 /* Reads t; `rows`: two dimensions whose rows are contiguous (any row stride), otherwise contiguous as a
- * whole. 0: not that, or not a CUDA tensor. */
+ * whole. 0: not that, or not on the device of the call. */
 static int read_tensor(PyObject* t, int rows, Tensor* out) {
     int ok = 0;
-    PyObject *cuda = PyObject_GetAttr(t, s_is_cuda), *dtype = NULL, *shape = NULL, *stride = NULL, *ptr = NULL;
-    if (cuda != Py_True) goto done;
+    PyObject *device = PyObject_CallMethodNoArgs(t, s_get_device), *dtype = NULL, *shape = NULL, *stride = NULL, *ptr = NULL;
+    if (!device || PyLong_AsLong(device) != here) goto done;
     dtype = PyObject_GetAttr(t, s_dtype);
     shape = PyObject_GetAttr(t, s_shape);
     if (!dtype || !shape || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) > 4) goto done;
@@ -69,7 +82,7 @@ static int read_tensor(PyObject* t, int rows, Tensor* out) {
     out->ptr = PyLong_AsVoidPtr(ptr);
     ok = 1;
 done:
-    Py_XDECREF(cuda);
+    Py_XDECREF(device);
     Py_XDECREF(dtype);
     Py_XDECREF(shape);
     Py_XDECREF(stride);
@@ -171,7 +184,7 @@ static PyObject* empty(int dims, const int64_t* shape, PyObject* dtype, PyObject
 }
 
 static int current_stream(void** s) {
-    PyObject *d = PyObject_CallNoArgs(f_current_device), *v = d ? PyObject_CallOneArg(f_raw_stream, d) : NULL;
+    PyObject *d = PyLong_FromLong(here), *v = d ? PyObject_CallOneArg(f_raw_stream, d) : NULL;
     if (v) *s = PyLong_AsVoidPtr(v);
     Py_XDECREF(d);
     Py_XDECREF(v);
@@ -207,6 +220,7 @@ static PyObject* named(PyObject* type, int n, PyObject** items) {
 
 /* quantize(X, format, tensor_scale, index, per) */
 static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Tensor x, g = {0}, index = {0};
     if (n != 5) Py_RETURN_NOTIMPLEMENTED;
     const int f = format_code(a[1]);
@@ -238,6 +252,7 @@ fail:
 
 /* dequantize(q, dtype) */
 static PyObject* dequantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Fp4 q;
     if (n != 2 || dtype_code(a[1]) < 0 || !read_fp4(a[0], 0, &q)) Py_RETURN_NOTIMPLEMENTED;
     const int64_t shape[2] = {q.rows, q.cols};
@@ -254,6 +269,7 @@ fail:
 
 /* matmul(X, W, offsets, relu, out_dtype) */
 static PyObject* matmul(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Fp4 x, w;
     Tensor offsets = {0};
     const int grouped = n == 5 && a[2] != Py_None;
@@ -278,6 +294,7 @@ fail:
 
 /* sort(ids, experts) */
 static PyObject* sort(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Tensor ids;
     if (n != 2 || !PyLong_Check(a[1]) || !read_typed(a[0], o_i32, 2, &ids)) Py_RETURN_NOTIMPLEMENTED;
     const int64_t tokens = ids.shape[0], top = ids.shape[1], experts = PyLong_AsLongLong(a[1]);
@@ -306,6 +323,7 @@ fail:
 
 /* gather(X, route) */
 static PyObject* gather(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Tensor x;
     Route r;
     if (n != 2 || !read_matrix(a[0], &x) || !read_route(a[1], &r) || x.shape[0] != r.tokens) Py_RETURN_NOTIMPLEMENTED;
@@ -323,6 +341,7 @@ fail:
 
 /* combine(Ys, route, weights) */
 static PyObject* combine(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Tensor ys, w = {0};
     Route r;
     if (n != 3 || !read_matrix(a[0], &ys) || !read_route(a[1], &r) || ys.shape[0] != r.tokens * r.top ||
@@ -342,6 +361,7 @@ fail:
 
 /* combine_grad(dY, Ys, route, weights) */
 static PyObject* combine_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    find_device();
     Tensor dy, ys, w;
     Route r;
     if (n != 4 || !read_matrix(a[0], &dy) || !read_matrix(a[1], &ys) || !read_route(a[2], &r) || !read_typed(a[3], o_f32, 2, &w) ||
@@ -409,7 +429,7 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", "The serving
 
 PyMODINIT_FUNC PyInit__call(void) {
     s_dtype = PyUnicode_InternFromString("dtype");
-    s_is_cuda = PyUnicode_InternFromString("is_cuda");
+    s_get_device = PyUnicode_InternFromString("get_device");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");

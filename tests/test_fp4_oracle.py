@@ -125,3 +125,75 @@ def test_other_refusals(clib):
 def test_a_sort_workspace_has_to_be_aligned(clib):
     for at, status in ((66, 1), (65, 1)):
         assert clib.gptq_expert_sort(P, 1 << 20, 2, 8, P, P, P, ctypes.c_void_p(at), 1 << 30, Z) == status
+
+
+class _OnDevice:
+    """What the binding asks a CUDA tensor, which this is not."""
+    is_cuda = True
+
+    def __init__(self, device, dtype, *shape):
+        import torch
+        self.index, self.dtype, self.shape, self.device = device, dtype, torch.Size(shape), torch.device("cuda", device)
+
+    def get_device(self):
+        return self.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def stride(self):
+        return tuple(self.shape[i + 1:].numel() for i in range(len(self.shape)))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_tensors_of_another_device_are_refused(clib, monkeypatch):
+    """Each tensor of each call in turn on device 1 while device 0 is the current one."""
+    import torch
+    import post_weight_quantization_04_gb300 as g
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    tensors = dict(x=(f32, 4, 64), w=(f32, 4, 2), ids=(i32, 4, 2), rows=(f32, 8, 64), offsets=(i32, 3), src=(i32, 8), pos=(i32, 4, 2),
+                   xc=(u8, 4, 32), xs=(u8, 1, 1, 512), xg=(f32, 1), wc=(u8, 2, 8, 32), ws=(u8, 2, 1, 1, 512), wg=(f32, 2),
+                   index=(i32, 4), bytes=(u8, 4, 4), work=(u8, 4096), y=(f32, 4, 8))
+    route = lambda t: g.Route(t["offsets"], t["src"], t["pos"])                                     # noqa: E731
+    X = lambda t: g.Fp4(t["xc"], t["xs"], 64, "nv", t["xg"])                                        # noqa: E731
+    W = lambda t: g.Fp4(t["wc"], t["ws"], 64, "nv", t["wg"])                                        # noqa: E731
+    calls = [
+        ("x", lambda t: g.gptq_fp4_tensor_scale(t["x"])),
+        ("x xg index", lambda t: g.gptq_fp4_quantize(t["x"], "nv", t["xg"], index=t["index"])),
+        ("x xc xs", lambda t: g.gptq_fp4_quantize(t["x"], "nv", t["xg"], out=X(t))),
+        ("xc xs xg", lambda t: g.gptq_fp4_dequantize(X(t))),
+        ("y", lambda t: g.gptq_fp4_dequantize(X(t), out=t["x"] if t["y"].index == 0 else _OnDevice(1, f32, 4, 64))),
+        ("bytes", lambda t: g.gptq_fp4_tile_scales(t["bytes"], 64, "nv")),
+        ("xc xs xg wc ws wg offsets", lambda t: g.gptq_fp4_matmul(X(t), W(t), offsets=t["offsets"])),
+        ("y", lambda t: g.gptq_fp4_matmul(X(t), W(t), offsets=t["offsets"], out=t["y"])),
+        ("ids", lambda t: g.gptq_expert_sort(t["ids"], 2)),
+        ("work", lambda t: g.gptq_expert_sort(t["ids"], 2, ws=t["work"])),
+        ("x offsets src pos", lambda t: g.gptq_expert_gather(t["x"], route(t))),
+        ("rows offsets src pos w", lambda t: g.gptq_expert_combine(t["rows"], route(t), t["w"])),
+        ("x rows offsets src pos w", lambda t: g.gptq_expert_combine_grad(t["x"], t["rows"], route(t), t["w"])),
+    ]
+    real = torch.empty
+    monkeypatch.setattr(g, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: real(*a, **k))      # (results that are never used)
+    monkeypatch.setattr(torch, "empty_like", lambda t, **k: real(1))
+    g._setup_call(clib)
+    try:
+        for names, call in calls:
+            for n in names.split():
+                t = {k: _OnDevice(int(k == n), *v) for k, v in tensors.items()}
+                with pytest.raises(ValueError, match="device"):
+                    call(t)
+    finally:
+        monkeypatch.undo()
+        g._setup_call(clib)
