@@ -604,3 +604,57 @@ def test_a_number_of_columns_past_64_bits_is_refused(lib):
     for call in (lambda: lib.gptq_fp4_dequantize(wrong), lambda: lib.gptq_fp4_matmul(wrong, q), lambda: lib.gptq_fp4_matmul(q, wrong)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("T,N,K", PRODUCTS[::2] + [(5, 300, 5000), (150, 300, 5000)])
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_matmul_fp32_bound(lib, T, N, K, fmt):
+    """The bound of the module for an fp32 result, general block scales and tensor scales that are no powers of two."""
+    rng = np.random.default_rng(T + 5 * N + 13 * K)
+    gx, gw = float(np.float32(0.37)), float(np.float32(1.9))
+    cx, bx, xv = _stored(rng, T, K, fmt, False, gx)
+    cw, bw, wv = _stored(rng, N, K, fmt, False, gw)
+    Y = lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, gx), _fp4(lib, cw, bw, K, fmt, gw))
+    _check(npy(Y), xv, wv, False, False, K)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("sizes", [[1, 0, 2, 1], [70, 3, 0, 200]])
+def test_grouped_fp32_bound(lib, fmt, sizes):
+    rng = np.random.default_rng(sum(sizes))
+    T, E, N, K = sum(sizes) + 1, len(sizes), 200, 600
+    gx, gw = float(np.float32(0.37)), [float(np.float32(v)) for v in (1.9, 0.3, 0.011, 70.7)]
+    cx, bx, xv = _stored(rng, T, K, fmt, False, gx)
+    ws = [_stored(rng, N, K, fmt, False, gw[e]) for e in range(E)]
+    W = lib.Fp4(torch.tensor(np.stack([F.pack_codes(w[0]) for w in ws]), device=DEV),
+                torch.tensor(np.stack([F.tile_scales(w[1], K, fmt) for w in ws]), device=DEV), K, fmt,
+                None if fmt == "mx" else torch.tensor(gw, dtype=torch.float32, device=DEV))
+    off = np.concatenate(([0], np.cumsum(sizes))).astype(np.int32)
+    Y = npy(lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, fmt, gx), W, offsets=torch.tensor(off, device=DEV)))
+    for e in range(E):
+        _check(Y[off[e]:off[e + 1]], xv[off[e]:off[e + 1]], ws[e][2], False, False, K)
+    np.testing.assert_array_equal(Y[off[-1]:], 0)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("bf16,N", [(True, 14336), (True, 14333), (False, 14336)])
+def test_product_past_32_bits(lib, bf16, N):
+    """More than 2^31 elements of Y, a third of its rows in no expert's range: rows at both ends and on either side of
+    the ranges' ends."""
+    rng = np.random.default_rng(N)
+    T, K, E = 160001, 64, 3
+    off = [1000, 50003, 50003, 108002]
+    cx, bx, xv = _stored(rng, T, K, "mx", True, 1)
+    ws = [_stored(rng, N, K, "mx", True, 1) for _ in range(E)]
+    W = lib.Fp4(torch.tensor(np.stack([F.pack_codes(w[0]) for w in ws]), device=DEV),
+                torch.tensor(np.stack([F.tile_scales(w[1], K, "mx") for w in ws]), device=DEV), K, "mx")
+    out = torch.full((T, N), 7.0, dtype=dtype_of(bf16), device=DEV)
+    assert out.numel() > 1 << 31
+    lib.gptq_fp4_matmul(_fp4(lib, cx, bx, K, "mx", 1.0), W, offsets=torch.tensor(off, dtype=torch.int32, device=DEV),
+                        out_dtype=dtype_of(bf16), out=out)
+    for t in (0, 999, 1000, 50002, 50003, 108001, 108002, T - 1):
+        e = 0 if 1000 <= t < 50003 else 2 if 50003 <= t < 108002 else None
+        want = np.zeros(N) if e is None else xv[t] @ ws[e][2].T
+        np.testing.assert_array_equal(npy(out[t]), npy(torch.tensor(want).to(dtype_of(bf16))))
+    rows = torch.cat((out[:1000], out[108002:]))
+    assert not rows.any()
