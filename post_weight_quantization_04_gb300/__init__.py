@@ -490,6 +490,9 @@ def gptq_fp4_scale_bytes(rows: int, cols: int, format: str) -> int:
 # stream) goes through the C module _call, which returns NotImplemented for what it does not
 # recognise; the functions below then check in Python, and raise. With `stream`, results are still
 # allocated on the current stream: a caller keeps them and the inputs until that stream is done.
+# All tensors are on the current device. Results have no autograd graph, whether or not an input requires
+# a gradient; gptq_expert_gather_grad and gptq_expert_combine_grad are the gradients there are, and the
+# 4-bit product has none.
 _fast = None
 
 
@@ -582,7 +585,7 @@ def gptq_fp4_tensor_scale(X: torch.Tensor, stream=None) -> torch.Tensor:
 def gptq_fp4_quantize(X: torch.Tensor, format: str = "mx", tensor_scale: Optional[torch.Tensor] = None,
                       index: Optional[torch.Tensor] = None, per: int = 1, out: Optional[Fp4] = None,
                       stream=None) -> Fp4:
-    """X (bf16 or fp32, any row stride) in the microscaled 4-bit form. index (int32): row r is X row
+    """X (bf16 or fp32, any stride between rows that do not overlap) in the microscaled 4-bit form. index (int32): row r is X row
     index[r] // per, zeros where index[r] < 0 (a Route's src with per = top gathers the experts' rows
     in the same pass). "nv" without a tensor scale takes gptq_fp4_tensor_scale(X)."""
     if out is None and stream is None:

@@ -3,10 +3,13 @@
  *
  * Each function takes what the public function of the same name takes, in the form without `out`,
  * `ws` and `stream`: it checks the arguments, allocates the results with torch.empty and calls the
- * library on the current stream. Anything it does not recognise (another type, a layout that has to
- * be refused, a subclass) makes it return NotImplemented; the public function then goes through the
- * checks in Python, which has the messages. A one-token linear layer is two such calls; in Python they
- * took 27 us of host time, more than the kernels.
+ * library on the current stream. Anything it does not recognise (a layout, type or device that has to
+ * be refused, an Fp4 or Route that is a subclass) makes it return NotImplemented; the public function then
+ * goes through the checks in Python, which has the messages. Tensors are known by what they answer (device,
+ * type, shape, strides, address), so a subclass that answers as a tensor does is read as one.
+ * A one-token linear layer is two such calls; in Python they took 27 us of host time, more than the kernels.
+ * A combination takes 6.8 us here: 2.2 in the library, mostly the launch, 1.5 for the result's allocation,
+ * the rest for what five tensors are asked.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

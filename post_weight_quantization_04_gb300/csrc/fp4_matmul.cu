@@ -106,7 +106,9 @@ __device__ __forceinline__ void expert_rows(const MParams& p, int e, int* lo, in
 }
 
 // rows that belong to no expert, before the first range and after the last one, are zero (ranges that
-// were clamped are an error)
+// were clamped are an error). One element at a time, with a division each, and by the pairs before their first
+// tile, so it is dear where many rows are dropped: 8 experts of 4096 x 4096, 16384 rows to bf16, MX: 94 us with none
+// dropped, 95 with 1 %, 131 with 30 % and 175 with 60 %, where the live rows alone take 69 and 46.
 __device__ __forceinline__ void zero_rest(const MParams& p, int64_t i, int64_t step) {
     const int first = min(max(p.offsets[0], 0), p.T), last = max(min(p.offsets[p.experts], p.T), first);
     const int64_t n = (int64_t)(p.T - (last - first)) * p.N;
@@ -647,8 +649,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
 // sums go to fp32 with both scales (whose product has at most 8 bits), and are added over the columns
 // and, in a fixed order, over the CTA.
 // The 8 features are two neighbours of each 32-row quarter of a scale tile, whose scales share sectors.
-// One token x 4096 x 4096 MX: 4.1 us with its launch (9 MB); what bounds it there is latency, and with
-// more weights the conversions (14336 x 4096: 11.6 us, 2.7 TB/s), where the other kernel takes over.
+// One token x 4096 x 4096 MX: 5.5 us with its launch (9 MB; 4.3 where L2 has them); what bounds it there is
+// latency, and with more weights the conversions (14336 x 4096: 11.7 us, 2.7 TB/s), where the other kernel takes over.
 constexpr int F_THREADS = 128, F_FEATURES = 8, F_TOKENS = 4;
 
 __device__ __forceinline__ void to_half2(const uint4& c, __half2 (&h)[16]) {
@@ -794,9 +796,22 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 
 // Whether the kernel for few rows is the faster one. Its time grows with the weights it reads and,
 // token by token, expands and multiplies; the other one's with the columns alone while its tiles
-// fit the device. Measured (us, few rows / pairs; MX):
-//   4096 x 4096   1 token 4.1 / 7.3   2 tokens 5.9 / 7.2   4 tokens 9.3 / 7.3
-//   14336 x 4096  1 token 11.6 / 9.8      1024 x 4096  4 tokens 5.1 / 7.3   8 tokens 8.5 / 7.3
+// fit the device. Measured (us, few rows / pairs; weights from memory, features x columns; the bound was set on MX,
+// dense, with the weights in L2):
+//                        1 token      2 tokens     3 tokens     4 tokens
+//   MX   4096 x 4096    5.5 / 8.0    8.0 / 8.1   11.2 / 8.0   11.1 / 8.0
+//   NV   4096 x 4096    5.8 / 8.7    6.6 / 8.7   13.3 / 8.7   13.4 / 8.7
+//   MX  14336 x 4096   11.7 / 9.9   16.6 / 9.8
+//   NV  14336 x 4096   11.1 / 10.4  16.0 / 10.3
+//   MX   1024 x 4096    2.7 / 6.6    3.3 / 6.5    5.4 / 6.6    5.4 / 6.5
+//   NV   1024 x 4096    3.1 / 7.6    3.4 / 7.5    5.0 / 7.7    4.9 / 7.6
+//   8 experts of 4096 x 4096, each row its own expert:
+//   MX                  5.9 / 7.1    9.4 / 7.5   13.7 / 9.2   17.9 / 10.8
+//   NV                  5.0 / 8.2    7.9 / 8.9   11.1 / 9.9   14.3 / 11.6
+//   16 of 1024 x 4096: MX 3.3 / 7.1 to 6.8 / 8.1, NV 3.2 / 8.1 to 5.9 / 8.6 (all rows one expert's: 8.4 / 7.3 and 8.3 / 8.2)
+// It takes the slower side where many columns meet one token (4096 x 14336: MX 12.5 / 15.6, NV 14.2 / 17.0, pairs
+// taken), for 3 and 4 tokens on few columns (4096 x 1024: MX 8.7 / 4.8, NV 8.2 / 5.3, few rows taken), and for
+// very many experts, whose CTAs start for nothing (128 of 768 x 2048: MX 9.4 / 6.8 and up, few rows taken).
 bool few_rows_pay(int64_t T, int64_t N, int64_t K, int64_t experts) {
     return T <= 4 && (std::min(experts, T) + T) * N * K <= 60000000;
 }
