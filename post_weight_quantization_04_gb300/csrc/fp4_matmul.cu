@@ -687,6 +687,8 @@ __device__ __forceinline__ int64_t scale_row(int64_t r, int c, int tiles_k) {
     return ((r >> 7) * tiles_k + c / (MX ? 4 : 2)) * kFp4Tile + (r & 31) * 16;
 }
 
+// (Plain loads: this kernel starts while the one before may still be writing its operands, so they are not
+// read-only for as long as it runs, which is what the read-only path asks for.)
 // tokens t0 .. t0 + n - 1 (n <= NT) of expert e times features fb + (i & 1) + 32 (i >> 1), i < 8
 template <bool MX, int NT>
 __device__ __forceinline__ void few_rows(const MParams& p, int e, int t0, int n, int fb, float (*part)[F_FEATURES * F_TOKENS]) {
@@ -700,15 +702,15 @@ __device__ __forceinline__ void few_rows(const MParams& p, int e, int t0, int n,
 #pragma unroll
         for (int i = 0; i < F_FEATURES; ++i) {
             const int f = min(fb + (i & 1) + 32 * (i >> 1), p.N - 1);
-            w[i] = __ldg(reinterpret_cast<const uint4*>(wc + f * pitch) + c);
+            w[i] = *(reinterpret_cast<const uint4*>(wc + f * pitch) + c);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sw[i] = __ldg(reinterpret_cast<const uint4*>(ws + scale_row<MX>(fb + i, c, p.tiles_k)));
+        for (int i = 0; i < 2; ++i) sw[i] = *reinterpret_cast<const uint4*>(ws + scale_row<MX>(fb + i, c, p.tiles_k));
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = t0 + min(t, n - 1);
-            x[t] = __ldg(reinterpret_cast<const uint4*>(p.xc + r * pitch) + c);
-            sx[t] = __ldg(reinterpret_cast<const uint32_t*>(p.xs + scale_row<MX>(r, c, p.tiles_k)) + ((r >> 5) & 3));
+            x[t] = *(reinterpret_cast<const uint4*>(p.xc + r * pitch) + c);
+            sx[t] = *(reinterpret_cast<const uint32_t*>(p.xs + scale_row<MX>(r, c, p.tiles_k)) + ((r >> 5) & 3));
         }
         __half2 xh[NT][16];
 #pragma unroll

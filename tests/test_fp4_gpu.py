@@ -658,3 +658,30 @@ def test_product_past_32_bits(lib, bf16, N):
         np.testing.assert_array_equal(npy(out[t]), npy(torch.tensor(want).to(dtype_of(bf16))))
     rows = torch.cat((out[:1000], out[108002:]))
     assert not rows.any()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("T", [1, 3, 70])
+def test_product_right_behind_what_writes_its_operands(lib, fmt, T):
+    """Both operands written anew in the same buffers by the call before, many times without a pause: each product is
+    that of its own operands."""
+    N, K = 256, 512
+    rng = np.random.default_rng(T)
+    g = 2.0 ** -3 if fmt == "nv" else None
+    gt = None if g is None else torch.tensor([g], device=DEV)
+    xs = [torch.tensor(rng.normal(size=(T, K)), dtype=torch.bfloat16, device=DEV) for _ in range(8)]
+    ws = [torch.tensor(rng.normal(size=(N, K)), dtype=torch.bfloat16, device=DEV) for _ in range(8)]
+    want = [[lib.gptq_fp4_matmul(lib.gptq_fp4_quantize(x, fmt, gt), lib.gptq_fp4_quantize(w, fmt, gt)) for w in ws] for x in xs]
+    x, w = lib.gptq_fp4_quantize(xs[0], fmt, gt), lib.gptq_fp4_quantize(ws[0], fmt, gt)
+    got = []
+    with lib.deferred_status():
+        for i in range(200):
+            if i % 2:
+                lib.gptq_fp4_quantize(xs[i // 2 % 8], fmt, gt, out=x)
+                lib.gptq_fp4_quantize(ws[i // 3 % 8], fmt, gt, out=w)
+            else:
+                lib.gptq_fp4_quantize(ws[i // 3 % 8], fmt, gt, out=w)
+                lib.gptq_fp4_quantize(xs[i // 2 % 8], fmt, gt, out=x)
+            got.append(lib.gptq_fp4_matmul(x, w))
+        lib.status_sync()
+    assert all(torch.equal(y, want[i // 2 % 8][i // 3 % 8]) for i, y in enumerate(got))
