@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(M_THREADS, 1) fp4_matmul_kernel(const __grid_c
 // sums go to fp32 with both scales (whose product has at most 8 bits), and are added over the columns
 // and, in a fixed order, over the CTA.
 // The 8 features are two neighbours of each 32-row quarter of a scale tile, whose scales share sectors.
-// One token x 4096 x 4096 MX: 5.5 us with its launch (9 MB; 4.3 where L2 has them); what bounds it there is
-// latency, and with more weights the conversions (14336 x 4096: 11.7 us, 2.7 TB/s), where the other kernel takes over.
+// One token x 4096 x 4096 MX: 5.6 us with its launch (9 MB; 4.3 where L2 has them); what bounds it there is
+// latency, and with more weights the conversions (14336 x 4096: 11.8 us, 2.7 TB/s), where the other kernel takes over.
 constexpr int F_THREADS = 128, F_FEATURES = 8, F_TOKENS = 4;
 
 __device__ __forceinline__ void to_half2(const uint4& c, __half2 (&h)[16]) {
@@ -801,19 +801,19 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 // fit the device. Measured (us, few rows / pairs; weights from memory, features x columns; the bound was set on MX,
 // dense, with the weights in L2):
 //                        1 token      2 tokens     3 tokens     4 tokens
-//   MX   4096 x 4096    5.5 / 8.0    8.0 / 8.1   11.2 / 8.0   11.1 / 8.0
-//   NV   4096 x 4096    5.8 / 8.7    6.6 / 8.7   13.3 / 8.7   13.4 / 8.7
-//   MX  14336 x 4096   11.7 / 9.9   16.6 / 9.8
-//   NV  14336 x 4096   11.1 / 10.4  16.0 / 10.3
-//   MX   1024 x 4096    2.7 / 6.6    3.3 / 6.5    5.4 / 6.6    5.4 / 6.5
-//   NV   1024 x 4096    3.1 / 7.6    3.4 / 7.5    5.0 / 7.7    4.9 / 7.6
+//   MX   4096 x 4096    5.6 / 8.0    6.6 / 8.1   11.0 / 8.0   11.0 / 8.1
+//   NV   4096 x 4096    5.8 / 8.7    6.6 / 8.7   13.0 / 8.7   13.0 / 8.8
+//   MX  14336 x 4096   11.8 / 9.8   14.5 / 9.8
+//   NV  14336 x 4096   11.1 / 10.3  16.0 / 10.4
+//   MX   1024 x 4096    2.6 / 6.5    3.2 / 6.5    5.3 / 6.5    5.3 / 6.5
+//   NV   1024 x 4096    3.0 / 7.6    3.4 / 7.5    4.9 / 7.6    4.8 / 7.6
 //   8 experts of 4096 x 4096, each row its own expert:
-//   MX                  5.9 / 7.1    9.4 / 7.5   13.7 / 9.2   17.9 / 10.8
-//   NV                  5.0 / 8.2    7.9 / 8.9   11.1 / 9.9   14.3 / 11.6
-//   16 of 1024 x 4096: MX 3.3 / 7.1 to 6.8 / 8.1, NV 3.2 / 8.1 to 5.9 / 8.6 (all rows one expert's: 8.4 / 7.3 and 8.3 / 8.2)
-// It takes the slower side where many columns meet one token (4096 x 14336: MX 12.5 / 15.6, NV 14.2 / 17.0, pairs
-// taken), for 3 and 4 tokens on few columns (4096 x 1024: MX 8.7 / 4.8, NV 8.2 / 5.3, few rows taken), and for
-// very many experts, whose CTAs start for nothing (128 of 768 x 2048: MX 9.4 / 6.8 and up, few rows taken).
+//   MX                  6.0 / 7.1    8.2 / 7.6   11.8 / 9.1   15.0 / 10.8
+//   NV                  5.0 / 8.2    8.0 / 8.8   11.1 / 9.9   14.4 / 11.7
+//   16 of 1024 x 4096: MX 3.1 / 7.1 to 6.3 / 8.2, NV 3.3 / 8.2 to 6.0 / 8.7 (all rows one expert's: 8.7 / 7.0 and 8.4 / 8.1)
+// It takes the slower side where many columns meet one token (4096 x 14336: MX 12.8 / 15.6, NV 14.2 / 17.0, pairs
+// taken), for 3 and 4 tokens on few columns (4096 x 1024: MX 8.7 / 4.9, NV 7.8 / 5.3, few rows taken), and for
+// very many experts, whose CTAs start for nothing (128 of 768 x 2048: MX 9.5 / 6.7 and up, few rows taken).
 bool few_rows_pay(int64_t T, int64_t N, int64_t K, int64_t experts) {
     return T <= 4 && (std::min(experts, T) + T) * N * K <= 60000000;
 }
