@@ -336,6 +336,72 @@ int gptq_fp4_matmul(const uint8_t* x_codes, const uint8_t* x_scales, const float
                     void* Y, int64_t ldy, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * The 8-bit integer form (no counterpart on the pages): whole numbers -128 .. 127 with one fp32
+ * scale >= 0 per row, of activations a token's, of weights an output channel's. A stored matrix
+ * (rows, cols) is
+ *   codes   16-byte aligned, rows * gptq_int8_pitch(cols) bytes (pitch 16 * ceil(cols / 16)),
+ *           codes past cols zero
+ *   scales  rows fp32: value = code * scale
+ * ------------------------------------------------------------------------------------ */
+int64_t gptq_int8_pitch(int64_t cols);
+
+/* X (src_rows, cols) bf16 or fp32, row stride ldx -> codes, scales of `rows` rows; index, per as
+ * for gptq_fp4_quantize. Per row, with a = max|x|: s = a / 127 (fp32) and code = the whole
+ * number nearest to x / s (the fp32 quotient), ties to even, within +-127; zeros where s = 0.
+ * Synchronises `stream` to report a NaN or infinity in X as NONFINITE (its row's scale is then
+ * NaN, its codes are of no meaning) or an index past X's rows as INVALID_ARG (read as
+ * negative); not in the deferred status mode. Allocates nothing. Errors: INVALID_ARG,
+ * NONFINITE, CUDA. */
+int gptq_int8_quantize(const void* X, int dtype, int64_t src_rows, int64_t cols, int64_t ldx,
+                       const int32_t* index, int64_t per, int64_t rows, int8_t* codes,
+                       float* scales, void* stream);
+
+/* The inverse: Y (rows, cols) bf16 (rounded to nearest even) or fp32 = code * scale, row stride
+ * ldy. Asynchronous. Errors: INVALID_ARG, CUDA. */
+int gptq_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                         void* Y, int dtype, int64_t ldy, void* stream);
+
+/* The root-mean-square norm before a product in this form. Per row of X and residual (rows, cols;
+ * both bf16 or both fp32, row strides ldx and ldr; residual may be NULL), in fp32:
+ *   h = x + residual rounded to X's type (x itself where there is none), written to H (row
+ *       stride ldh) where there is a residual; H may be X or residual itself
+ *   rstd = 1 / sqrt(mean h^2 + eps) (fp32, rows; 0 < eps), y = (h * rstd) * gain (fp32, cols)
+ * and y -> codes, scales as gptq_int8_quantize does. Synchronises `stream` to report a NaN or
+ * infinity in y as NONFINITE (not in the deferred status mode). Allocates nothing.
+ * Errors: INVALID_ARG, NONFINITE, CUDA. */
+int gptq_int8_rms_norm(const void* X, int64_t ldx, const void* residual, int64_t ldr, int dtype,
+                       int64_t rows, int64_t cols, const float* gain, float eps, int8_t* codes,
+                       float* scales, void* H, int64_t ldh, float* rstd, void* stream);
+
+/* Its gradient, straight through the rounding: dY (rows, cols) is that of the values the codes
+ * stand for, dH (may be NULL: 0) the one that reaches h past the norm; dY, H (h), dH and dX of one
+ * type. With u = h * rstd and v = dY * gain:
+ *   dX = dH + rstd (v - u mean(u v))   (X's gradient and residual's; may be dY, H or dH itself)
+ *   dgain (fp32, cols) = the sum over the rows of dY * u, in a fixed order
+ * ws: device, 4-byte aligned, gptq_int8_rms_norm_grad_workspace_bytes(rows, cols) bytes.
+ * Asynchronous; a NaN or infinity goes into the results. Errors: INVALID_ARG, WORKSPACE, CUDA. */
+size_t gptq_int8_rms_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH,
+                            int64_t lddh, int dtype, int64_t rows, int64_t cols, const float* gain,
+                            const float* rstd, void* dX, int64_t lddx, float* dgain, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Y[t][o] = act(sx[t] sw_e[o] sum_k x[t][k] w_e[o][k]) for X (T, K) and W_e (N, K) in this form.
+ *   offsets  as for gptq_fp4_matmul: NULL (experts = 1), or the rows of each expert; rows in none
+ *            of the ranges get Y = 0
+ *   w_codes, w_scales  the experts' stored matrices one after another
+ *   flags    GPTQ_DQ_RELU (a NaN stays one), GPTQ_DQ_BF16_OUT (else fp32)
+ *   Y        device, (T, N) row-major, row stride ldy elements
+ * The sum is the exact whole number where its partial sums stay within 2^24 and is otherwise rounded in
+ * fp32; the result is rounded once more. Allocates nothing. Synchronises `stream` and returns the
+ * device status (in the deferred status mode neither).
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 1024 experts, 2^31 rows of weights, or K >= 2^17),
+ * TIMEOUT, CUDA. */
+int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, int64_t T, const int8_t* w_codes,
+                     const float* w_scales, int64_t N, int64_t K, const int32_t* offsets,
+                     int64_t experts, int flags, void* Y, int64_t ldy, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Tokens sorted by expert and back (no counterpart on the pages). Token t has `top` slots;
  * slot i = t * top + j goes to expert ids[i], or nowhere (negative: dropped). One Hessian per
  * expert is gptq_hessian_accumulate on its contiguous rows of the gathered matrix.
@@ -379,6 +445,32 @@ int gptq_expert_combine_grad(const void* dY, int64_t lddy, const void* Ys, int64
                              int64_t top, const int32_t* offsets, int64_t experts,
                              const float* weights, void* dYs, int64_t lddys, float* dW,
                              void* stream);
+
+/* The balance loss of a router (no counterpart on the pages). Z (tokens, experts) bf16 or fp32, row
+ * stride ldz: the router's logits; ids (device, int32, tokens * top): each slot's expert, or
+ * negative; mask (device, one byte per token, or NULL): tokens whose byte is 0 do not count, and
+ * their rows of Z are not looked at. With p[t] = softmax(Z[t]), n the tokens that count and
+ * c[e] their slots that go to expert e:
+ *   loss (device, one fp32) = experts / (top n^2) sum_e c[e] sum_t p[t][e]; 0 where n = 0
+ *   counts (device, int32, experts + 1) = c, then n
+ * Logits of -inf have p = 0; a row of nothing else adds nothing (it does count in n).
+ * ws: device, 4-byte aligned, gptq_expert_balance_workspace_bytes(tokens, experts) bytes.
+ * Sums are fp32 in a fixed order. Synchronises `stream` to report a NaN or +inf in a row that
+ * counts as NONFINITE (the loss is then NaN) or an id >= experts as INVALID_ARG (it counts as
+ * negative); not in the deferred status mode. Errors: INVALID_ARG, UNSUPPORTED (experts > 1024),
+ * WORKSPACE, NONFINITE, CUDA. */
+size_t gptq_expert_balance_workspace_bytes(int64_t tokens, int64_t experts);
+int gptq_expert_balance(const void* Z, int dtype, int64_t tokens, int64_t experts, int64_t ldz,
+                        const int32_t* ids, int64_t top, const uint8_t* mask, float* loss,
+                        int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient (the counts are constants): dZ[t][e] = dloss experts / (top n^2) p[t][e] (c[e] -
+ * sum_j p[t][j] c[j]), 0 in rows that do not count. dloss: device, one fp32, or NULL for 1; counts as
+ * gptq_expert_balance leaves them; dZ of Z's type (may be Z itself), row stride lddz. Status as
+ * above. Errors: INVALID_ARG, UNSUPPORTED (experts > 1024), NONFINITE, CUDA. */
+int gptq_expert_balance_grad(const float* dloss, const void* Z, int dtype, int64_t tokens,
+                             int64_t experts, int64_t ldz, const int32_t* counts, int64_t top,
+                             const uint8_t* mask, void* dZ, int64_t lddz, void* stream);
 
 /* Static text for a status code. */
 const char* gptq_status_string(int status);

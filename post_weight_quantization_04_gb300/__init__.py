@@ -35,6 +35,9 @@ EXPORTS = [
     "gptq_fp4_code_pitch", "gptq_fp4_scale_bytes", "gptq_fp4_tensor_scale", "gptq_fp4_quantize", "gptq_fp4_dequantize",
     "gptq_fp4_tile_scales", "gptq_fp4_matmul", "gptq_expert_sort_workspace_bytes", "gptq_expert_sort",
     "gptq_expert_gather", "gptq_expert_combine", "gptq_expert_combine_grad",
+    "gptq_int8_pitch", "gptq_int8_quantize", "gptq_int8_dequantize", "gptq_int8_rms_norm",
+    "gptq_int8_rms_norm_grad_workspace_bytes", "gptq_int8_rms_norm_grad", "gptq_int8_matmul",
+    "gptq_expert_balance_workspace_bytes", "gptq_expert_balance", "gptq_expert_balance_grad",
     "gptq_status_string", "gptq_set_status_mode", "gptq_status_mode", "gptq_status_sync",
     "gptq_launch_count", "gptq_profile_enable", "gptq_profile_read", "gptq_profile_kernel_count",
     "gptq_profile_kernel_name",
@@ -91,6 +94,16 @@ def _declare(lib: ctypes.CDLL) -> None:
         "gptq_expert_gather": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
         "gptq_expert_combine": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P]),
         "gptq_expert_combine_grad": (_I, [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P]),
+        "gptq_int8_pitch": (_I64, [_I64]),
+        "gptq_int8_quantize": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _P]),
+        "gptq_int8_dequantize": (_I, [_P, _P, _I64, _I64, _P, _I, _I64, _P]),
+        "gptq_int8_rms_norm": (_I, [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _F, _P, _P, _P, _I64, _P, _P]),
+        "gptq_int8_rms_norm_grad_workspace_bytes": (_SZ, [_I64, _I64]),
+        "gptq_int8_rms_norm_grad": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I64, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+        "gptq_int8_matmul": (_I, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _P, _I64, _P]),
+        "gptq_expert_balance_workspace_bytes": (_SZ, [_I64, _I64]),
+        "gptq_expert_balance": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+        "gptq_expert_balance_grad": (_I, [_P, _P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P]),
         "gptq_status_string": (ctypes.c_char_p, [_I]),
         "gptq_set_status_mode": (_I, [_I]),
         "gptq_status_mode": (_I, []),
@@ -687,6 +700,181 @@ def gptq_fp4_matmul(X: Fp4, W: Fp4, offsets: Optional[torch.Tensor] = None, relu
     return Y
 
 
+# ---------------------------------------------------------------------- the 8-bit integer form
+
+class Int8(NamedTuple):
+    """A matrix (rows, cols), or one per expert, as whole numbers with a scale per row: codes int8
+    ([experts,] rows, gptq_int8_pitch(cols)), zeros past cols, and scales fp32 ([experts,] rows), not
+    negative; value = code * scale."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+
+def gptq_int8_pitch(cols: int) -> int:
+    return (cols + 15) // 16 * 16
+
+
+def _check_int8(q: Int8, name: str, experts: Optional[int] = None) -> None:
+    """A stored matrix whose buffers fit its columns (experts: one per expert)."""
+    codes, scales, cols = q
+    rows = codes.shape[-2] if codes.dim() >= 2 else 0
+    lead = () if experts is None else (experts,)
+    if cols < 0 or codes.shape != (*lead, rows, gptq_int8_pitch(cols)) or scales.shape != (*lead, rows):
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not those of "
+                         f"{'one matrix' if experts is None else f'{experts} matrices'} of {cols} columns")
+    _dev_here(codes, torch.int8, name + ".codes")
+    _dev_here(scales, torch.float32, name + ".scales")
+
+
+def _new_int8(rows: int, cols: int, dev) -> Int8:
+    return Int8(torch.empty((rows, gptq_int8_pitch(cols)), dtype=torch.int8, device=dev),
+                torch.empty((rows,), dtype=torch.float32, device=dev), cols)
+
+
+def _int8_out(out: Optional[Int8], rows: int, cols: int, dev) -> Int8:
+    if out is None:
+        return _new_int8(rows, cols, dev)
+    _check_int8(out, "out")
+    if out.cols != cols or out.rows != rows:
+        raise ValueError("out has another shape")
+    return out
+
+
+def gptq_int8_quantize(X: torch.Tensor, index: Optional[torch.Tensor] = None, per: int = 1, out: Optional[Int8] = None,
+                       stream=None) -> Int8:
+    """X (bf16 or fp32, any stride between rows that do not overlap) in 8-bit integers, scale = max|x| / 127 of each
+    row. index (int32): row r is X row index[r] // per, zeros where index[r] < 0 (a Route's src with per = top
+    gathers the experts' rows in the same pass)."""
+    dt, n, cols, ld = _matrix(X, "X")
+    rows = n
+    if index is not None:
+        _dev_here(index, torch.int32, "index")
+        rows = index.numel()
+    out = _int8_out(out, rows, cols, X.device)
+    _check("gptq_int8_quantize", load().gptq_int8_quantize(
+        X.data_ptr(), dt, n, cols, ld, _addr(index), per, rows, out.codes.data_ptr(), out.scales.data_ptr(), _raw_stream(stream)))
+    return out
+
+
+def gptq_int8_dequantize(q: Int8, dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values that q's codes and scales stand for."""
+    _check_int8(q, "q")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("dtype must be float32 or bfloat16")
+    rows, cols = q.rows, q.cols
+    Y = out if out is not None else torch.empty((rows, cols), dtype=dtype, device=q.codes.device)
+    ld = cols if out is None else _matrix_like(Y, "out", dtype, rows, cols)
+    _check("gptq_int8_dequantize", load().gptq_int8_dequantize(
+        q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, Y.data_ptr(), dt, ld, _raw_stream(stream)))
+    return Y
+
+
+def gptq_int8_rms_norm(X: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                       out: Optional[Tuple[Int8, Optional[torch.Tensor], torch.Tensor]] = None,
+                       stream=None) -> Tuple[Int8, torch.Tensor, torch.Tensor]:
+    """(q, h, rstd): h = X + residual in X's type (X itself without a residual), rstd = 1 / sqrt(mean h^2 + eps) per
+    row, and q = (h rstd) gain in 8-bit integers. gain fp32 (cols). h and rstd are what gptq_int8_rms_norm_grad needs.
+    out: (q, h, rstd) to write to; its h may be X or residual itself."""
+    dt, rows, cols, ld = _matrix(X, "X")
+    _dev_here(gain, torch.float32, "gain", (cols,))
+    ldr = _matrix_like(residual, "residual", X.dtype, rows, cols) if residual is not None else 0
+    q, h, rstd = out if out is not None else (None, None, None)
+    q = _int8_out(q, rows, cols, X.device)
+    if residual is None:
+        if h is not None and h is not X:
+            raise ValueError("out[1] must be X or None without a residual: h is X")
+        h, ldh = X, ld
+    elif h is None:
+        h, ldh = torch.empty((rows, cols), dtype=X.dtype, device=X.device), cols
+    else:
+        ldh = _matrix_like(h, "out[1]", X.dtype, rows, cols)
+    if rstd is None:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=X.device)
+    else:
+        _dev_here(rstd, torch.float32, "out[2]", (rows,))
+    _check("gptq_int8_rms_norm", load().gptq_int8_rms_norm(
+        X.data_ptr(), ld, _addr(residual), ldr, dt, rows, cols, gain.data_ptr(), float(eps), q.codes.data_ptr(),
+        q.scales.data_ptr(), None if residual is None else h.data_ptr(), ldh, rstd.data_ptr(), _raw_stream(stream)))
+    return q, h, rstd
+
+
+def gptq_int8_rms_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load().gptq_int8_rms_norm_grad_workspace_bytes(rows, cols))
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, dev, stream) -> Tuple[Optional[torch.Tensor], int]:
+    """A workspace and its bytes: the caller's, or a new one."""
+    if ws is not None:
+        if not (ws.is_cuda and ws.is_contiguous()):
+            raise ValueError("ws must be a contiguous CUDA tensor")
+        _here(ws, "ws")
+        return ws, ws.numel() * ws.element_size()
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)
+    return ws, need
+
+
+def gptq_int8_rms_norm_grad(dY: torch.Tensor, h: torch.Tensor, gain: torch.Tensor, rstd: torch.Tensor,
+                            dh: Optional[torch.Tensor] = None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                            ws: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dX, dgain) of gptq_int8_rms_norm, straight through the rounding: dY is the gradient of q's values, dh (None: 0)
+    the one that reaches h past the norm. dX, of X's type, is residual's gradient too; it may be written to dY, h or dh
+    (out). dgain is fp32."""
+    dt, rows, cols, ldh = _matrix(h, "h")
+    lddy = _matrix_like(dY, "dY", h.dtype, rows, cols)
+    lddh = _matrix_like(dh, "dh", h.dtype, rows, cols) if dh is not None else 0
+    _dev_here(gain, torch.float32, "gain", (cols,))
+    _dev_here(rstd, torch.float32, "rstd", (rows,))
+    if out is None:
+        dX, dgain = torch.empty((rows, cols), dtype=h.dtype, device=h.device), torch.empty((cols,), dtype=torch.float32, device=h.device)
+        lddx = cols
+    else:
+        dX, dgain = out
+        lddx = _matrix_like(dX, "out[0]", h.dtype, rows, cols)
+        _dev_here(dgain, torch.float32, "out[1]", (cols,))
+    lib = load()
+    ws, nb = _workspace(ws, int(lib.gptq_int8_rms_norm_grad_workspace_bytes(rows, cols)), h.device, stream)
+    _check("gptq_int8_rms_norm_grad", lib.gptq_int8_rms_norm_grad(
+        dY.data_ptr(), lddy, h.data_ptr(), ldh, _addr(dh), lddh, dt, rows, cols, gain.data_ptr(), rstd.data_ptr(), dX.data_ptr(),
+        lddx, dgain.data_ptr(), _addr(ws), nb, _raw_stream(stream)))
+    return dX, dgain
+
+
+def gptq_int8_matmul(X: Int8, W: Int8, offsets: Optional[torch.Tensor] = None, relu: bool = False, out_dtype=torch.float32,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W^T (optionally max(., 0)) of two matrices in 8-bit integers, times the scales of X's row and of W's. With
+    offsets (int32, experts + 1, a Route's) W holds one weight per expert and rows offsets[e]..offsets[e+1] of X use
+    weight e; rows in no expert's range give zeros."""
+    _check_int8(X, "X")
+    experts = 1
+    if offsets is None:
+        _check_int8(W, "W")
+    else:
+        experts = W.codes.shape[0]
+        _check_int8(W, "W", experts)
+        _dev_here(offsets, torch.int32, "offsets", (experts + 1,))
+    if X.cols != W.cols:
+        raise ValueError("X and W must have the same columns")
+    if out_dtype not in _DTYPES:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    T, N = X.rows, W.rows
+    Y = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=X.codes.device)
+    ld = N if out is None else _matrix_like(Y, "out", out_dtype, T, N)
+    flags = (DQ_RELU if relu else 0) | (DQ_BF16_OUT if out_dtype is torch.bfloat16 else 0)
+    _check("gptq_int8_matmul", load().gptq_int8_matmul(
+        X.codes.data_ptr(), X.scales.data_ptr(), T, W.codes.data_ptr(), W.scales.data_ptr(), N, X.cols, _addr(offsets), experts,
+        flags, Y.data_ptr(), ld, _raw_stream(stream)))
+    return Y
+
+
 # ------------------------------------------------------- tokens sorted by expert, and back
 
 class Route(NamedTuple):
@@ -815,17 +1003,87 @@ def gptq_expert_combine_grad(dY: torch.Tensor, Ys: torch.Tensor, route: Route, w
     return dYs, dW
 
 
-def gptq_expert_mlp(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W_up: Fp4, W_down: Fp4,
+class Balance(NamedTuple):
+    """What gptq_expert_balance leaves: loss fp32 (1), counts int32 (experts + 1: each expert's slots, then the
+    tokens that count) and the slots per token."""
+    loss: torch.Tensor
+    counts: torch.Tensor
+    top: int
+
+
+def gptq_expert_balance_workspace_bytes(tokens: int, experts: int) -> int:
+    return int(load().gptq_expert_balance_workspace_bytes(tokens, experts))
+
+
+def _check_mask(mask: Optional[torch.Tensor], tokens: int) -> None:
+    if mask is not None:
+        _dev_here(mask, torch.uint8 if mask.dtype is torch.uint8 else torch.bool, "mask", (tokens,))
+
+
+def gptq_expert_balance(logits: torch.Tensor, ids: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                        out: Optional[Balance] = None, ws: Optional[torch.Tensor] = None, stream=None) -> Balance:
+    """The balance loss experts / (top n^2) sum_e c[e] sum_t softmax(logits[t])[e] of a router's logits (tokens,
+    experts; bf16 or fp32) and choice ids (tokens, top; int32, negative: dropped), with c[e] the slots of expert e
+    and n the tokens that count; mask (bool or uint8; None: all) says which do."""
+    dt, tokens, experts, ld = _matrix(logits, "logits")
+    _dev_here(ids, torch.int32, "ids")
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError("ids must be (tokens, top)")
+    _check_mask(mask, tokens)
+    dev, top = logits.device, ids.shape[1]
+    if out is None:
+        out = Balance(torch.empty((1,), dtype=torch.float32, device=dev), torch.empty((experts + 1,), dtype=torch.int32, device=dev), top)
+    else:
+        _dev_here(out.loss, torch.float32, "out.loss", (1,))
+        _dev_here(out.counts, torch.int32, "out.counts", (experts + 1,))
+        out = out._replace(top=top)
+    lib = load()
+    ws, nb = _workspace(ws, int(lib.gptq_expert_balance_workspace_bytes(tokens, experts)), dev, stream)
+    _check("gptq_expert_balance", lib.gptq_expert_balance(
+        logits.data_ptr(), dt, tokens, experts, ld, ids.data_ptr(), top, _addr(mask), out.loss.data_ptr(), out.counts.data_ptr(),
+        _addr(ws), nb, _raw_stream(stream)))
+    return out
+
+
+def gptq_expert_balance_grad(dloss: Optional[torch.Tensor], logits: torch.Tensor, balance: Balance,
+                             mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of gptq_expert_balance's logits (the counts are constants), zeros in rows that do not count;
+    dloss: the loss's gradient, one fp32 (None: 1). out may be logits itself."""
+    dt, tokens, experts, ld = _matrix(logits, "logits")
+    if dloss is not None:
+        _dev_here(dloss, torch.float32, "dloss")
+        if dloss.numel() != 1:
+            raise ValueError("dloss must hold one number")
+    _dev_here(balance.counts, torch.int32, "balance.counts", (experts + 1,))
+    _check_mask(mask, tokens)
+    dZ = out if out is not None else torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    lddz = experts if out is None else _matrix_like(dZ, "out", logits.dtype, tokens, experts)
+    _check("gptq_expert_balance_grad", load().gptq_expert_balance_grad(
+        _addr(dloss), logits.data_ptr(), dt, tokens, experts, ld, balance.counts.data_ptr(), balance.top, _addr(mask), dZ.data_ptr(),
+        lddz, _raw_stream(stream)))
+    return dZ
+
+
+def gptq_expert_mlp(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, W_up, W_down,
                     up_scale: Optional[torch.Tensor] = None, down_scale: Optional[torch.Tensor] = None):
-    """A layer of experts on microscaled 4-bit weights: y[t] = sum_j weights[t][j] *
-    W_down[e] relu(W_up[e] x[t]) with e = ids[t][j] (negative: dropped), activations quantised
+    """A layer of experts on microscaled 4-bit weights (Fp4) or on 8-bit integers (Int8): y[t] = sum_j
+    weights[t][j] * W_down[e] relu(W_up[e] x[t]) with e = ids[t][j] (negative: dropped), activations quantised
     to the weights' format before each product. X (tokens, d) bf16 or fp32; W_up, W_down: one
-    matrix per expert; up_scale, down_scale: the activations' "nv" tensor scales (None: taken
+    matrix per expert, both Fp4 or both Int8; up_scale, down_scale: the activations' "nv" tensor scales (None: taken
     from the activations). Returns (y bf16, route, the experts' rows ys bf16), what
     gptq_expert_combine_grad needs for the gradients of the router's weights. Host
     orchestration only: every step runs in the library, on the current stream."""
+    if isinstance(W_up, Int8) != isinstance(W_down, Int8):
+        raise ValueError("W_up and W_down must both be Fp4 or both be Int8")
     route = gptq_expert_sort(ids, W_up.codes.shape[0])
     top = ids.shape[1]
+    if isinstance(W_up, Int8):
+        if up_scale is not None or down_scale is not None:
+            raise ValueError("up_scale and down_scale are tensor scales of the 4-bit form")
+        xs = gptq_int8_quantize(X, index=route.src, per=top)
+        h = gptq_int8_matmul(xs, W_up, offsets=route.offsets, relu=True, out_dtype=torch.bfloat16)
+        ys = gptq_int8_matmul(gptq_int8_quantize(h), W_down, offsets=route.offsets, out_dtype=torch.bfloat16)
+        return gptq_expert_combine(ys, route, weights), route, ys
     if W_up.format == "nv" and up_scale is None:
         up_scale = gptq_fp4_tensor_scale(X)
     xs = gptq_fp4_quantize(X, W_up.format, up_scale, index=route.src, per=top)
@@ -867,7 +1125,9 @@ __all__ = [
     "Fp4", "MXFP4", "NVFP4", "gptq_fp4_code_pitch", "gptq_fp4_scale_bytes", "gptq_fp4_tensor_scale", "gptq_fp4_quantize",
     "gptq_fp4_dequantize", "gptq_fp4_tile_scales", "gptq_fp4_matmul", "Route", "gptq_expert_sort",
     "gptq_expert_sort_workspace_bytes", "gptq_expert_gather", "gptq_expert_gather_grad", "gptq_expert_combine",
-    "gptq_expert_combine_grad", "gptq_expert_mlp",
+    "gptq_expert_combine_grad", "Balance", "gptq_expert_balance", "gptq_expert_balance_workspace_bytes", "gptq_expert_balance_grad",
+    "gptq_expert_mlp", "Int8", "gptq_int8_pitch", "gptq_int8_quantize", "gptq_int8_dequantize", "gptq_int8_rms_norm",
+    "gptq_int8_rms_norm_grad", "gptq_int8_rms_norm_grad_workspace_bytes", "gptq_int8_matmul",
     "set_status_mode", "status_sync", "deferred_status", "STATUS_SYNC", "STATUS_DEFERRED",
     "EXPORTS", "LIB_PATH",
 ]

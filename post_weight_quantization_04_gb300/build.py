@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libgptq.so")
 CALL = os.path.join(HERE, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["hessian.cu", "prepare.cu", "quantize.cu", "sgemm.cu", "tc_gemm.cu", "dequant_matmul.cu", "profile.cu",
-           "status.cu", "fp4.cu", "fp4_matmul.cu", "expert.cu"]
+           "status.cu", "fp4.cu", "fp4_matmul.cu", "expert.cu", "int8.cu", "int8_matmul.cu",
+           "balance.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
 

@@ -50,7 +50,8 @@ const char* kNames[K_COUNT] = {
     "tc_gemm_nt_kernel[trailing]", "dequant_matmul_kernel", "merge_status_kernel",
     "tc_gemm_nt_kernel[chain]", "fp4_amax_kernel", "fp4_quantize_kernel", "fp4_dequantize_kernel",
     "fp4_tile_scales_kernel", "fp4_matmul_kernel", "expert_sort_kernel", "expert_gather_kernel",
-    "expert_combine_kernel", "expert_combine_grad_kernel",
+    "expert_combine_kernel", "expert_combine_grad_kernel", "int8_quantize_kernel", "int8_rms_norm_kernel",
+    "int8_rms_norm_grad_kernel", "int8_dequantize_kernel", "int8_matmul_kernel", "balance_kernel",
 };
 
 }  // namespace
