@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "int8.cuh"
+#include "pair.cuh"
 #include "tc_gemm.cuh"
 
 namespace gptq {
@@ -24,7 +25,10 @@ struct IParams {
     int64_t pitch;
     const int32_t* offsets;   // null: one expert, all rows
     int experts;
-    int relu, bf16_out;
+    int ftiles;               // feature tiles
+    int tokens_first;         // neighbouring tiles share their features, not their tokens
+    int splits;               // shares of the columns, each a pair of its own
+    int relu, bf16_out, vec;  // vec: bf16 rows that 16-byte stores can take
     void* Y;
     int64_t ldy;
     int* status;
@@ -43,9 +47,6 @@ __device__ __forceinline__ void expert_rows(const IParams& p, int e, int* lo, in
     *lo = l;
     *hi = h;
 }
-
-// max(x, 0) that keeps a NaN
-__device__ __forceinline__ float relu_of(float x) { return max_nan(x, 0.0f); }
 
 // sum * sx * sw, the smaller scale first: with the sum a whole number that product is exact where it is
 // subnormal, and past fp32 only if the result is
@@ -135,8 +136,569 @@ __global__ void __launch_bounds__(F_THREADS) int8_few_rows_kernel(const IParams 
     }
 }
 
+// ------------------------------------------------------------------------ pairs of SMs, tcgen05
+// There is no integer tensor instruction on sm_103a, but 8-bit integers are exact in fp16, their products and,
+// below 2^24, the sums of them exact in fp32. So the codes stay 8 bits wide up to the SM and are
+// expanded there to what tcgen05.mma kind::f16 multiplies. The weights are the M operand and are expanded into
+// TMEM, the tokens the N operand and are expanded into shared memory, which spares the shared memory one of
+// the two operands' writes and reads.
+//
+// Two CTAs on neighbouring SMs work on a tile of 256 features x up to 256 tokens: each brings and expands
+// its own 128 features and half of the tokens, 128 columns at a time. Roles in each CTA (persistent, one per SM):
+//   warp 0        producer: two TMA copies per stage, 128 x 128 codes of each operand (128-byte swizzle)
+//   warp 1        in the even CTA: the MMAs
+//   warps 2..5    weights: shared memory -> fp16 -> TMEM, a row per lane
+//   warps 6..9    tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), a row per lane
+//   warps 10..17  epilogue: TMEM -> registers -> Y
+// TMEM: 256 columns of sums (tokens), then the expanded weights of W_SLOTS stages, 64 columns each.
+//
+// SPLIT: few tiles, so a cluster of up to 8 CTAs shares the columns of one tile, and its pairs' sums are added
+// through each other's shared memory, each pair for its own part of the tokens.
+// Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits for its own
+// copies, the even one for the MMAs, and all meet before any leaves).
+constexpr int W_F = 128, W_PF = 2 * W_F;   // features per CTA and per tile
+constexpr int W_T = 256;                   // most tokens per tile
+constexpr int W_K = 128;                   // columns per stage
+constexpr int W_RAW = 3, W_SLOTS = 3;      // stages of codes, and of expanded operands
+constexpr int W_THREADS = 32 * 18;
+constexpr int W_CODES = W_F * W_K;         // bytes of one operand's codes per stage
+constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per stage
+constexpr uint32_t W_TMEM = 512, W_A0 = 256;
+constexpr int W_TURN = 32 * 64;            // bytes of a warp's buffer: 32 tokens x 32 features of bf16
+constexpr int W_RING = W_RAW * 2 * W_CODES + W_SLOTS * W_WIDE;
+constexpr int W_BARS = 2 * W_RAW + 2 * W_SLOTS + 3;
+
+struct WMaps {
+    CUtensorMap w, x[3];   // tokens: boxes of 128, 64 and 32 rows
+};
+
+// Token tiles of rows [lo, hi), all of one width: a multiple of 32, so both CTAs have whole groups of 16
+__device__ __forceinline__ int token_tiles(int lo, int hi) { return hi <= lo ? 0 : (hi - lo + W_T - 1) / W_T; }
+
+struct WTile {
+    int e, f0;        // expert, first feature
+    int t0, n;        // first token, tokens (a multiple of 32, the last of which may be past hi)
+    int hi;           // the end of the expert's tokens
+};
+
+__device__ __forceinline__ WTile find_tile(const IParams& p, const int32_t* start, uint32_t i) {
+    WTile t;
+    const uint32_t ttiles = (uint32_t)start[p.experts];
+    const int tt = (int)(p.tokens_first ? i % ttiles : i / (uint32_t)p.ftiles);
+    t.f0 = (int)(p.tokens_first ? i / ttiles : i % (uint32_t)p.ftiles) * W_PF;
+    int a = 0, b = p.experts;   // start[a] <= tt < start[b]
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (start[m] <= tt) a = m;
+        else b = m;
+    }
+    t.e = a;
+    int lo = 0;
+    t.hi = p.T;
+    if (p.offsets) {
+        lo = min(max(p.offsets[a], 0), p.T);
+        t.hi = min(max(p.offsets[a + 1], lo), p.T);
+    }
+    const int tiles = start[a + 1] - start[a];
+    const int width = ((t.hi - lo + tiles - 1) / tiles + 31) & ~31;
+    t.t0 = lo + (tt - start[a]) * width;
+    t.n = min(max(t.hi - t.t0 + 31, 32) & ~31, width);
+    return t;
+}
+
+// four codes to four fp16 numbers: code + 128 in the low bits of 1024, less 1152
+__device__ __forceinline__ void to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// a shared-memory address in another CTA of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// An arrival that orders this thread's shared memory before the MMAs of the pair's even CTA, and that
+// CTA's wait for it
+__device__ __forceinline__ void arrive_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_all_cluster(uint32_t bar, uint32_t parity, uint64_t limit) {
+    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 >= limit)) return false;
+        if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+    }
+}
+
+__device__ __forceinline__ void commit_to(uint32_t bar, uint32_t ctas) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)ctas)
+        : "memory");
+}
+
+// D (+)= A B with A in TMEM, fp16, by both CTAs
+__device__ __forceinline__ void umma_half(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::f16: [4,6) sums (1 = fp32) | [7,10), [10,13) operands (0 = fp16), both K-major |
+// [17,23) N >> 3 | [24,29) M >> 4
+__device__ __forceinline__ uint32_t half_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(W_PF >> 4) << 24); }
+
+// 32 tokens of one feature to Y: the lanes of a warp hold consecutive features, so each token is one store of 64 or
+// 128 consecutive bytes. sx: the tokens' scales
+template <typename T>
+__device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (&v)[32], float sw, const float* sx, bool far, bool relu,
+                                             int last) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (j < last) {
+            const float s = __uint_as_float(v[j]), x = far ? scaled(s, sw, sx[j]) : s * sw * sx[j], z = relu ? relu_of(x) : x;
+            if constexpr (sizeof(T) == 2) *y = __float2bfloat16_rn(z);
+            else *y = z;
+        }
+        y += ldy;
+    }
+}
+
+__device__ __forceinline__ uint32_t pair_bf16(uint32_t a, uint32_t b, float sw, float s0, float s1, bool far, bool relu) {
+    float x = __uint_as_float(a), y = __uint_as_float(b);
+    x = far ? scaled(x, sw, s0) : x * sw * s0;
+    y = far ? scaled(y, sw, s1) : y * sw * s1;
+    if (relu) {
+        x = relu_of(x);
+        y = relu_of(y);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 tokens x 32 features, packed for stmatrix (v[j][..]: tokens 8 j ..), to Y through the warp's 2 KB of shared
+// memory: rows of 64 bytes, one per token, whose 16-byte pieces are permuted so that neither side has conflicts
+__device__ __forceinline__ void turn_tokens(const IParams& p, const uint32_t (&v)[4][4], int tok, int hi, int f0, uint32_t buf) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 8 * j + (lane & 7);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         buf + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4)),
+                     "r"(v[j][0]), "r"(v[j][1]), "r"(v[j][2]), "r"(v[j][3])
+                     : "memory");
+    }
+    __syncwarp();
+    const int f = f0 + 8 * (lane & 3);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y) + f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int row = 8 * j + (lane >> 2), r = tok + row;
+        const uint4 w = lds128(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+        if (f < p.N && r < hi) *reinterpret_cast<uint4*>(y + (int64_t)r * p.ldy) = w;
+    }
+    __syncwarp();
+}
+
+template <bool SPLIT>
+__global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_constant__ WMaps m, const IParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W_RING + 8 * W_TURN);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W_BARS);
+    float* token_scales = reinterpret_cast<float*>(tmem_slot + 1);              // [8][W_T / 2]
+    int32_t* start = reinterpret_cast<int32_t*>(token_scales + 4 * W_T);            // [experts + 1]
+
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t rank = uniform(cluster_rank()), half = rank & 1u, even = rank & ~1u;
+    const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+    auto raw_full = [&](int s) { return bar0 + 8u * s; };                                 // copies landed
+    auto raw_free = [&](int s) { return bar0 + 8u * (W_RAW + s); };                       // all 8 warps have read them
+    auto wide_full = [&](int s) { return bar0 + 8u * (2 * W_RAW + s); };                  // even CTA: both have expanded
+    auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_RAW + W_SLOTS + s); };        // the stage's MMAs are done
+    const uint32_t tfull = bar0 + 8u * (2 * W_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
+    const int per_tile = SPLIT ? 2 * p.splits : 2;
+    const uint32_t first = blockIdx.x / per_tile, step = gridDim.x / per_tile;
+    // this pair's stages
+    const int all = (p.K + W_K - 1) / W_K, share = (int)(rank >> 1);
+    const int k0 = SPLIT ? all * share / p.splits : 0, k1 = SPLIT ? all * (share + 1) / p.splits : all;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < W_RAW; ++s) {
+            mbar_init(raw_full(s), 1);
+            mbar_init(raw_free(s), 8);
+        }
+        for (int s = 0; s < W_SLOTS; ++s) {
+            mbar_init(wide_full(s), 16);
+            mbar_init(wide_free(s), 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tfree, 16);
+        mbar_init(drain_bar, 1);
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&m.w);
+        tma_prefetch_desc(&m.x[0]);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(W_TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();   // from here on memory that the kernel before writes or reads is touched
+    if (warp == 0) {
+        // token tiles before each expert
+        int carry = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            int lo = 0, hi = 0;
+            if (e0 + lane < p.experts) expert_rows(p, e0 + lane, &lo, &hi);
+            const int n = token_tiles(lo, hi);
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (e0 + lane < p.experts) start[e0 + lane] = carry + inc - n;
+            carry += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) start[p.experts] = carry;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // all CTAs' barriers are ready before any signals another's
+    tc_fence_after();
+    const uint32_t tmem = uniform(*tmem_slot);
+    const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_pipeline_wait_limit_ns);
+    bool ok = true;   // false: a wait gave up
+    const uint32_t ntiles = uniform((uint32_t)start[p.experts] * (uint32_t)p.ftiles);
+
+    if (warp == 0) {
+        // ------------------------------- producer -----------------------------------
+        const bool leader = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, issued_par = 0;
+        for (uint32_t i = first; i < ntiles && ok; i += step) {
+            const WTile t = find_tile(p, start, i);
+            const int n = (int)uniform(t.n), e = (int)uniform(t.e);
+            const int box = n > 128 ? 0 : n > 64 ? 1 : 2;
+            const uint32_t bytes = W_CODES + (W_CODES >> box);
+            const int wrow = e * p.N + (int)uniform(t.f0) + (int)half * W_F, xrow = (int)uniform(t.t0) + (int)half * (n >> 1);
+            for (int k = k0; k < k1; ++k) {
+                ok = wait_all(raw_free(stage), phase ^ 1u, limit);
+                if (!ok) break;
+                if (leader) {
+                    const uint32_t base = sbase + stage * 2 * W_CODES, bar = raw_full(stage);
+                    mbar_expect_tx(bar, bytes);
+                    tma_load_2d(base, &m.w, bar, k * W_K, wrow);
+                    tma_load_2d(base + W_CODES, &m.x[box], bar, k * W_K, xrow);
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == W_RAW) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (leader)
+            for (int s = 0; s < W_RAW; ++s)
+                if (issued & (1u << s)) drain(raw_full(s), (issued_par >> s) & 1u);
+        __syncwarp();
+    } else if (warp == 1) {
+        // --------------------------- MMA issuer (even CTA) --------------------------
+        if (half == 0) {
+            int slot = 0;
+            uint32_t phase = 0, tile = 0;
+            for (uint32_t i = first; i < ntiles && ok; i += step, ++tile) {
+                const WTile t = find_tile(p, start, i);
+                const uint32_t idesc = half_idesc((int)uniform(t.n));
+                ok = wait_all(tfree, (tile & 1u) ^ 1u, limit);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = k0; k < k1; ++k) {
+                    ok = wait_all_cluster(wide_full(slot), phase, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const int ksteps = (p.K - k * W_K + 15) / 16;
+                        const uint32_t a = tmem + W_A0 + slot * (W_K / 2);
+                        const uint64_t b = smem_desc(sbase + W_RAW * 2 * W_CODES + slot * W_WIDE, 16, 1024, kSwizzle128B);
+#pragma unroll
+                        for (int j = 0; j < W_K / 16; ++j)
+                            if (j < ksteps)
+                                umma_half(tmem, a + 8 * j, b + (j >> 2) * (W_WIDE / 2 / 16) + 2 * (j & 3), idesc, (k > k0 || j > 0) ? 1u : 0u);
+                        commit_to(wide_free(slot), 3u << even);
+                        if (k == k1 - 1) commit_to(tfull, 3u << even);
+                    }
+                    __syncwarp();
+                    if (++slot == W_SLOTS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (elect_one()) {
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_bar) : "memory");
+                drain(drain_bar, 0);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 10) {
+        // -------------------------- expansion, a row per lane -----------------------
+        const bool weights = warp < 6;
+        const int q = weights ? warp & 3 : warp - 6, r = 32 * q + lane, x = r & 7;
+        int stage = 0, slot = 0;
+        uint32_t rphase = 0, sphase = 0;
+        for (uint32_t i = first; i < ntiles && ok; i += step) {
+            const WTile t = find_tile(p, start, i);
+            const bool live = weights || 64 * q < (int)uniform(t.n);
+            for (int k = k0; k < k1; ++k) {
+                ok = wait_all(raw_full(stage), rphase, limit);
+                if (!ok) break;
+                const uint32_t src = sbase + stage * 2 * W_CODES + (weights ? 0 : W_CODES) + r * W_K;
+                const uint32_t dst = sbase + W_RAW * 2 * W_CODES + slot * W_WIDE + r * 128;
+                bool waited = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+                    if (live) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 w = lds128(src + (((4 * h + c) ^ x) << 4));
+                            to_half(w.x, v[8 * c], v[8 * c + 1]);
+                            to_half(w.y, v[8 * c + 2], v[8 * c + 3]);
+                            to_half(w.z, v[8 * c + 4], v[8 * c + 5]);
+                            to_half(w.w, v[8 * c + 6], v[8 * c + 7]);
+                        }
+                    }
+                    if (h == 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_free(stage));
+                    }
+                    if (!waited) {
+                        ok = wait_all(wide_free(slot), sphase ^ 1u, limit);
+                        if (!ok) break;
+                        waited = true;
+                    }
+                    if (weights) {
+                        if (h == 0) tc_fence_after();
+                        tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + W_A0 + slot * (W_K / 2) + 32 * h, v);
+                    } else if (live) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) sts128(dst + h * (W_WIDE / 2) + ((c ^ x) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                    }
+                }
+                if (!ok) break;
+                if (weights) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else {
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) arrive_release(in_cta(wide_full(slot), even));
+                if (++stage == W_RAW) {
+                    stage = 0;
+                    rphase ^= 1u;
+                }
+                if (++slot == W_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ------------------------------- epilogue -----------------------------------
+        const int q = warp & 3;
+        const int c0 = W_T / 2 * ((warp - 10) >> 2);   // its half of the columns
+        const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + c0;
+        const uint32_t turn = sbase + W_RING + (warp - 10) * W_TURN;
+        uint32_t tile = 0;
+        for (uint32_t i = first; i < ntiles; i += step, ++tile) {
+            const WTile t = find_tile(p, start, i);
+            const int f0 = t.f0 + (int)half * W_F + 32 * q;
+            float* sx = token_scales + (warp - 10) * (W_T / 2);   // the scales of its tokens
+            if (!SPLIT) {
+                __syncwarp();
+#pragma unroll
+                for (int c = lane; c < W_T / 2; c += 32) sx[c] = t.t0 + c0 + c < t.hi ? p.xs[t.t0 + c0 + c] : 0.0f;
+                __syncwarp();
+            }
+            ok = wait_all(tfull, tile & 1u, limit);
+            if (!ok) break;
+            tc_fence_after();
+            if constexpr (SPLIT) {
+                // its sums to its own shared memory, [token][feature], which no copy or MMA uses any more
+                for (int c = c0; c < min(c0 + W_T / 2, t.n); c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) reinterpret_cast<uint32_t*>(smem)[(c + j) * W_F + 32 * q + lane] = v[j];
+                }
+                break;   // (one tile per cluster)
+            }
+            const float* ws = p.ws + (int64_t)t.e * p.N;
+            const bool relu = p.relu != 0;
+            if (p.vec) {
+                // packed before the buffer is free, stored after it
+                uint32_t v[4][4][4];
+                float sw[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) sw[g] = ws[min(f0 + 8 * g + (lane >> 2), p.N - 1)];
+                // (an ordinary weight's scale first cannot overflow: below 2^96 times a sum below 2^31)
+                const bool far = __any_sync(0xffffffffu, fmaxf(fmaxf(sw[0], sw[1]), fmaxf(sw[2], sw[3])) > 0x1p96f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c0 + 32 * c < t.n) {
+                        uint32_t a[2][16];
+                        tmem_ld_16x256b_x4(sums + 32 * c, a[0]);
+                        tmem_ld_16x256b_x4(sums + (16u << 16) + 32 * c, a[1]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float s0 = sx[32 * c + 8 * j + 2 * (lane & 3)], s1 = sx[32 * c + 8 * j + 2 * (lane & 3) + 1];
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                v[c][j][g] = pair_bf16(a[g >> 1][4 * j + 2 * (g & 1)], a[g >> 1][4 * j + 2 * (g & 1) + 1], sw[g], s0, s1, far, relu);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_cta(tfree, even));
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c0 + 32 * c < t.n) turn_tokens(p, v[c], t.t0 + c0 + 32 * c, t.hi, f0, turn);
+            } else {
+                const int f = f0 + lane;
+                const float sw = ws[min(f, p.N - 1)];
+                const bool far = __any_sync(0xffffffffu, sw > 0x1p96f);
+                for (int c = 0; c < W_T / 2 && c0 + c < t.n; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(sums + c, v);
+                    tmem_ld_wait();
+                    const int tok = t.t0 + c0 + c;
+                    const int64_t at = (int64_t)tok * p.ldy + f;
+                    if (f >= p.N) continue;
+                    if (p.bf16_out) store_tokens(static_cast<__nv_bfloat16*>(p.Y) + at, p.ldy, v, sw, sx + c, far, relu, t.hi - tok);
+                    else store_tokens(static_cast<float*>(p.Y) + at, p.ldy, v, sw, sx + c, far, relu, t.hi - tok);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_cta(tfree, even));
+            }
+        }
+    }
+
+    if (!ok && lane == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA leaves, or frees TMEM, while another may still use it
+    if constexpr (SPLIT) {
+        if (first < ntiles) {
+            const WTile t = find_tile(p, start, first);
+            const int a = t.n * share / p.splits, b = t.n * (share + 1) / p.splits;   // this pair's tokens
+            const uint32_t mine = sbase + 4 * (threadIdx.x & (W_F - 1));
+            const int f = t.f0 + (int)half * W_F + (int)(threadIdx.x & (W_F - 1));
+            const float sw = p.ws[(int64_t)t.e * p.N + min(f, p.N - 1)];
+            for (int c = a + (int)(threadIdx.x / W_F); c < min(b, t.hi - t.t0) && threadIdx.x < W_THREADS / W_F * W_F; c += W_THREADS / W_F) {
+                float s = 0.0f;
+                for (int j = 0; j < p.splits; ++j) s += ld_cluster(in_cta(mine + 4 * c * W_F, 2 * j + half));
+                if (f < p.N) store_result(p, t.t0 + c, f, scaled(s, sw, p.xs[t.t0 + c]));
+            }
+        }
+        __syncthreads();
+        cluster_sync();   // nor while another reads its sums
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(W_TMEM) : "memory");
+    }
+    if (p.offsets) zero_rest(p, blockIdx.x, gridDim.x);
+}
+
+bool code_map(CUtensorMap* m, const int8_t* codes, int64_t rows, int64_t cols, int box_rows) {
+    auto enc = tma_encoder();
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)int8_pitch(cols)};
+    cuuint32_t box[2] = {(cuuint32_t)W_K, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(codes), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool SPLIT>
+int launch_pairs(const WMaps& m, const IParams& p, int64_t most_tiles, cudaStream_t s) {
+    constexpr int kFixed = 1024 + W_RING + 8 * W_TURN + 8 * W_BARS + 4 + 16 * W_T;
+    constexpr int kMost = kFixed + 4 * (I_MAX_EXPERTS + 1);
+    static_assert(kMost <= 227 * 1024, "an SM's shared memory");
+    static_assert(W_T * W_F * 4 <= W_RING, "a split tile's sums take the place of the stages");
+    // the limit is the kernel's and not the call's: every thread's calls set it to the same number
+    GPTQ_CUDA_TRY(cudaFuncSetAttribute(int8_matmul_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
+    const unsigned per = 2 * (SPLIT ? p.splits : 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(SPLIT ? (unsigned)most_tiles * per : 2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2));
+    cfg.blockDim = dim3(W_THREADS);
+    cfg.dynamicSmemBytes = kFixed + 4 * (p.experts + 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = per;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaSuccess;
+    GPTQ_LAUNCH(K_INT8_MM, s, e = cudaLaunchKernelEx(&cfg, int8_matmul_kernel<SPLIT>, m, p));
+    GPTQ_CUDA_TRY(e);
+    return GPTQ_OK;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int64_t kMaxDim = (1ll << 31) - 512;
+
+bool few_rows_pay(int64_t T, int64_t N, int64_t K, int64_t experts) { return T <= 8 * experts; }
 
 }  // namespace
 }  // namespace gptq
@@ -150,6 +712,8 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
         (flags & ~(GPTQ_DQ_RELU | GPTQ_DQ_BF16_OUT)) || (!offsets && experts != 1))
         return GPTQ_ERR_INVALID_ARG;
     if (experts > I_MAX_EXPERTS || N > kMaxDim / experts || K > I_MAX_K) return GPTQ_ERR_UNSUPPORTED;
+    // tile numbers have 31 bits (a Y beyond that is larger than the device)
+    if ((ceil_div(T, W_T) + experts) * ceil_div(N, W_PF) > kMaxDim) return GPTQ_ERR_UNSUPPORTED;
     if (T == 0 || N == 0) return GPTQ_OK;
     if (!Y || ldy < N || !x_scales || !w_scales || (K > 0 && (!x_codes || !w_codes || !aligned16(x_codes) || !aligned16(w_codes))))
         return GPTQ_ERR_INVALID_ARG;
@@ -172,9 +736,29 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
     p.Y = Y;
     p.ldy = ldy;
     p.status = st.word;
-    cudaError_t e = cudaSuccess;
-    const dim3 grid((unsigned)ceil_div(N, F_FEATURES), (unsigned)(experts + (offsets ? 1 : 0)));
-    GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(int8_few_rows_kernel, grid, dim3(F_THREADS), 0, s, p));
-    GPTQ_CUDA_TRY(e);
-    return st.finish(s);
+    p.ftiles = (int)ceil_div(N, W_PF);
+    p.tokens_first = experts * N > T ? 1 : 0;   // the larger operand is walked through once
+    p.vec = p.bf16_out && N % 8 == 0 && ldy % 8 == 0 && aligned16(Y) ? 1 : 0;
+    if (K == 0 || few_rows_pay(T, N, K, experts)) {
+        cudaError_t e = cudaSuccess;
+        const dim3 grid((unsigned)ceil_div(N, F_FEATURES), (unsigned)(experts + (offsets ? 1 : 0)));
+        GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(int8_few_rows_kernel, grid, dim3(F_THREADS), 0, s, p));
+        GPTQ_CUDA_TRY(e);
+        return st.finish(s);
+    }
+    WMaps m;
+    if (!code_map(&m.w, w_codes, experts * N, K, W_F)) return GPTQ_ERR_CUDA;
+    for (int i = 0; i < 3; ++i)
+        if (!code_map(&m.x[i], x_codes, T, K, W_F >> i)) return GPTQ_ERR_CUDA;
+    // an expert's last tile may be partial
+    const int64_t most = (ceil_div(T, W_T) + (offsets ? std::min(experts, T) : 0)) * p.ftiles, pairs = device_sm_count() / 2;
+    p.splits = 1;
+    while (p.splits < 4 && most * p.splits * 2 <= pairs && ceil_div(K, W_K) >= p.splits * 4) p.splits *= 2;
+    const int rc = p.splits > 1 ? launch_pairs<true>(m, p, most, s) : launch_pairs<false>(m, p, most, s);
+    return rc != GPTQ_OK ? rc : st.finish(s);
 }
+
+namespace gptq {
+// this file's copy of the pipeline-wait limit (the library's test hook sets every copy)
+cudaError_t int8_set_wait_limit(unsigned long long ns) { return set_pipeline_wait_limit_this_unit(ns); }
+}  // namespace gptq
