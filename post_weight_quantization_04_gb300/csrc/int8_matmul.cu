@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "int8.cuh"
@@ -27,7 +28,8 @@ struct IParams {
     int experts;
     int ftiles;               // feature tiles
     int tokens_first;         // neighbouring tiles share their features, not their tokens
-    int splits;               // shares of the columns, each a pair of its own
+    int splits;               // SPLIT: shares of the columns, each a pair of its own
+    int box, raw;             // SPLIT: rows of a token box, and stages of codes
     int relu, bf16_out, vec;  // vec: bf16 rows that 16-byte stores can take
     void* Y;
     int64_t ldy;
@@ -153,20 +155,23 @@ __global__ void __launch_bounds__(F_THREADS) int8_few_rows_kernel(const IParams 
 // TMEM: 256 columns of sums (tokens), then the expanded weights of W_SLOTS stages, 64 columns each.
 //
 // SPLIT: few tiles, so a cluster of up to 8 CTAs shares the columns of one tile, and its pairs' sums are added
-// through each other's shared memory, each pair for its own part of the tokens.
+// through each other's shared memory, each pair for its own part of the tokens. Such tiles are mostly narrow,
+// bound by the weights and the time that one stage takes, so more stages of codes are in flight, two
+// groups of warps expand the weights in turn, and 4 warps are the epilogue (10..13 tokens, 14..17 epilogue).
 // Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits for its own
 // copies, the even one for the MMAs, and all meet before any leaves).
 constexpr int W_F = 128, W_PF = 2 * W_F;   // features per CTA and per tile
 constexpr int W_T = 256;                   // most tokens per tile
 constexpr int W_K = 128;                   // columns per stage
 constexpr int W_RAW = 3, W_SLOTS = 3;      // stages of codes, and of expanded operands
+constexpr int W_MOST_RAW = 8;              // the former where token boxes are small
 constexpr int W_THREADS = 32 * 18;
 constexpr int W_CODES = W_F * W_K;         // bytes of one operand's codes per stage
 constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per stage
 constexpr uint32_t W_TMEM = 512, W_A0 = 256;
 constexpr int W_TURN = 32 * 64;            // bytes of a warp's buffer: 32 tokens x 32 features of bf16
 constexpr int W_RING = W_RAW * 2 * W_CODES + W_SLOTS * W_WIDE;
-constexpr int W_BARS = 2 * W_RAW + 2 * W_SLOTS + 3;
+constexpr int W_BARS = 2 * W_MOST_RAW + 2 * W_SLOTS + 3;
 
 struct WMaps {
     CUtensorMap w, x[3];   // tokens: boxes of 128, 64 and 32 rows
@@ -229,35 +234,10 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
-}
-
-// An arrival that orders this thread's shared memory before the MMAs of the pair's even CTA, and that
-// CTA's wait for it
-__device__ __forceinline__ void arrive_release(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool wait_all_cluster(uint32_t bar, uint32_t parity, uint64_t limit) {
-    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 >= limit)) return false;
-        if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
-    }
 }
 
 __device__ __forceinline__ void commit_to(uint32_t bar, uint32_t ctas) {
@@ -284,12 +264,12 @@ __device__ __forceinline__ uint32_t half_idesc(int n) { return (1u << 4) | ((uin
 // 32 tokens of one feature to Y: the lanes of a warp hold consecutive features, so each token is one store of 64 or
 // 128 consecutive bytes. sx: the tokens' scales
 template <typename T>
-__device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (&v)[32], float sw, const float* sx, bool far, bool relu,
+__device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (&v)[32], float sw, const float* sx, bool relu,
                                              int last) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
         if (j < last) {
-            const float s = __uint_as_float(v[j]), x = far ? scaled(s, sw, sx[j]) : s * sw * sx[j], z = relu ? relu_of(x) : x;
+            const float x = scaled(__uint_as_float(v[j]), sw, sx[j]), z = relu ? relu_of(x) : x;
             if constexpr (sizeof(T) == 2) *y = __float2bfloat16_rn(z);
             else *y = z;
         }
@@ -297,16 +277,21 @@ __device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (
     }
 }
 
-__device__ __forceinline__ uint32_t pair_bf16(uint32_t a, uint32_t b, float sw, float s0, float s1, bool far, bool relu) {
-    float x = __uint_as_float(a), y = __uint_as_float(b);
-    x = far ? scaled(x, sw, s0) : x * sw * s0;
-    y = far ? scaled(y, sw, s1) : y * sw * s1;
-    if (relu) {
-        x = relu_of(x);
-        y = relu_of(y);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
+// two sums times a feature's scale and their tokens' scales, as a pair of bf16
+__device__ __forceinline__ uint32_t pair_bf16(uint32_t a, uint32_t b, float sw, float2 sx) {
+    uint32_t r;
+    asm("{\n\t.reg .b64 v, w, x;\n\t.reg .b32 lo, hi;\n\t"
+        "mov.b64 v, {%1, %2};\n\tmov.b64 w, {%3, %3};\n\tmov.b64 x, {%4, %5};\n\t"
+        "mul.rn.f32x2 v, v, w;\n\tmul.rn.f32x2 v, v, x;\n\t"
+        "mov.b64 {lo, hi}, v;\n\tcvt.rn.bf16x2.f32 %0, hi, lo;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b), "r"(__float_as_uint(sw)), "r"(__float_as_uint(sx.x)), "r"(__float_as_uint(sx.y)));
+    return r;
+}
+__device__ __forceinline__ uint32_t relu_bf16(uint32_t v) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0u));
+    return r;
 }
 
 // 32 tokens x 32 features, packed for stmatrix (v[j][..]: tokens 8 j ..), to Y through the warp's 2 KB of shared
@@ -339,25 +324,30 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W_RING + 8 * W_TURN);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W_BARS);
-    float* token_scales = reinterpret_cast<float*>(tmem_slot + 1);              // [8][W_T / 2]
-    int32_t* start = reinterpret_cast<int32_t*>(token_scales + 4 * W_T);            // [experts + 1]
+    float* token_scales = reinterpret_cast<float*>(tmem_slot + 2);              // [8][W_T / 2]
+    int32_t* start = reinterpret_cast<int32_t*>(token_scales + 4 * W_T);        // [experts + 1]
 
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = uniform(cluster_rank()), half = rank & 1u, even = rank & ~1u;
     const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
-    auto raw_full = [&](int s) { return bar0 + 8u * s; };                                 // copies landed
-    auto raw_free = [&](int s) { return bar0 + 8u * (W_RAW + s); };                       // all 8 warps have read them
-    auto wide_full = [&](int s) { return bar0 + 8u * (2 * W_RAW + s); };                  // even CTA: both have expanded
-    auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_RAW + W_SLOTS + s); };        // the stage's MMAs are done
-    const uint32_t tfull = bar0 + 8u * (2 * W_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
+    auto raw_full = [&](int s) { return bar0 + 8u * s; };                                      // copies landed
+    auto raw_free = [&](int s) { return bar0 + 8u * (W_MOST_RAW + s); };                       // all 8 warps have read them
+    auto wide_full = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + s); };                  // even CTA: both have expanded
+    auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + W_SLOTS + s); };        // the stage's MMAs are done
+    const uint32_t tfull = bar0 + 8u * (2 * W_MOST_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
+    // the expanded tokens first, then the stages of codes
+    const int box_rows = SPLIT ? p.box : W_F, raws = SPLIT ? p.raw : W_RAW;
+    const uint32_t wide_bytes = box_rows * 2 * W_K, raw_bytes = W_CODES + box_rows * W_K;
+    const uint32_t rbase = sbase + W_SLOTS * wide_bytes;
     const int per_tile = SPLIT ? 2 * p.splits : 2;
     const uint32_t first = blockIdx.x / per_tile, step = gridDim.x / per_tile;
     // this pair's stages
     const int all = (p.K + W_K - 1) / W_K, share = (int)(rank >> 1);
     const int k0 = SPLIT ? all * share / p.splits : 0, k1 = SPLIT ? all * (share + 1) / p.splits : all;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < W_RAW; ++s) {
+    // (each in a warp of its own, side by side)
+    if (warp == 2 && elect_one()) {
+        for (int s = 0; s < raws; ++s) {
             mbar_init(raw_full(s), 1);
             mbar_init(raw_free(s), 8);
         }
@@ -370,7 +360,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
         mbar_init(drain_bar, 1);
         fence_barrier_init();
     }
-    if (warp == 0 && lane == 0) {
+    if (warp == 3 && elect_one()) {
         tma_prefetch_desc(&m.w);
         tma_prefetch_desc(&m.x[0]);
     }
@@ -415,14 +405,14 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
         for (uint32_t i = first; i < ntiles && ok; i += step) {
             const WTile t = find_tile(p, start, i);
             const int n = (int)uniform(t.n), e = (int)uniform(t.e);
-            const int box = n > 128 ? 0 : n > 64 ? 1 : 2;
+            const int box = n > 128 ? 0 : n > 64 ? 1 : 2;   // (its rows are at most SPLIT's)
             const uint32_t bytes = W_CODES + (W_CODES >> box);
             const int wrow = e * p.N + (int)uniform(t.f0) + (int)half * W_F, xrow = (int)uniform(t.t0) + (int)half * (n >> 1);
             for (int k = k0; k < k1; ++k) {
                 ok = wait_all(raw_free(stage), phase ^ 1u, limit);
                 if (!ok) break;
                 if (leader) {
-                    const uint32_t base = sbase + stage * 2 * W_CODES, bar = raw_full(stage);
+                    const uint32_t base = rbase + stage * raw_bytes, bar = raw_full(stage);
                     mbar_expect_tx(bar, bytes);
                     tma_load_2d(base, &m.w, bar, k * W_K, wrow);
                     tma_load_2d(base + W_CODES, &m.x[box], bar, k * W_K, xrow);
@@ -430,14 +420,14 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                 __syncwarp();
                 issued |= 1u << stage;
                 issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-                if (++stage == W_RAW) {
+                if (++stage == raws) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
         }
         if (leader)
-            for (int s = 0; s < W_RAW; ++s)
+            for (int s = 0; s < raws; ++s)
                 if (issued & (1u << s)) drain(raw_full(s), (issued_par >> s) & 1u);
         __syncwarp();
     } else if (warp == 1) {
@@ -452,17 +442,17 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                 if (!ok) break;
                 tc_fence_after();
                 for (int k = k0; k < k1; ++k) {
-                    ok = wait_all_cluster(wide_full(slot), phase, limit);
+                    ok = wait_all(wide_full(slot), phase, limit);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const int ksteps = (p.K - k * W_K + 15) / 16;
                         const uint32_t a = tmem + W_A0 + slot * (W_K / 2);
-                        const uint64_t b = smem_desc(sbase + W_RAW * 2 * W_CODES + slot * W_WIDE, 16, 1024, kSwizzle128B);
+                        const uint64_t b = smem_desc(sbase + slot * wide_bytes, 16, 1024, kSwizzle128B);
 #pragma unroll
                         for (int j = 0; j < W_K / 16; ++j)
                             if (j < ksteps)
-                                umma_half(tmem, a + 8 * j, b + (j >> 2) * (W_WIDE / 2 / 16) + 2 * (j & 3), idesc, (k > k0 || j > 0) ? 1u : 0u);
+                                umma_half(tmem, a + 8 * j, b + (j >> 2) * (wide_bytes / 2 / 16) + 2 * (j & 3), idesc, (k > k0 || j > 0) ? 1u : 0u);
                         commit_to(wide_free(slot), 3u << even);
                         if (k == k1 - 1) commit_to(tfull, 3u << even);
                     }
@@ -479,61 +469,66 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
             }
             __syncwarp();
         }
-    } else if (warp < 10) {
+    } else if (warp < (SPLIT ? 14 : 10)) {
         // -------------------------- expansion, a row per lane -----------------------
-        const bool weights = warp < 6;
-        const int q = weights ? warp & 3 : warp - 6, r = 32 * q + lane, x = r & 7;
-        int stage = 0, slot = 0;
+        const bool weights = warp < (SPLIT ? 10 : 6);
+        const int q = weights ? warp & 3 : warp - (SPLIT ? 10 : 6), r = 32 * q + lane, x = r & 7;
+        // (SPLIT: the two groups of the weights' warps take every other stage)
+        const bool turns = SPLIT && weights;
+        int stage = 0, slot = 0, turn = turns ? (warp - 2) >> 2 : 0;
         uint32_t rphase = 0, sphase = 0;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
             const WTile t = find_tile(p, start, i);
             const bool live = weights || 64 * q < (int)uniform(t.n);
             for (int k = k0; k < k1; ++k) {
-                ok = wait_all(raw_full(stage), rphase, limit);
-                if (!ok) break;
-                const uint32_t src = sbase + stage * 2 * W_CODES + (weights ? 0 : W_CODES) + r * W_K;
-                const uint32_t dst = sbase + W_RAW * 2 * W_CODES + slot * W_WIDE + r * 128;
-                bool waited = false;
+                if (turn == 0) {
+                    ok = wait_all(raw_full(stage), rphase, limit);
+                    if (!ok) break;
+                    const uint32_t src = rbase + stage * raw_bytes + (weights ? 0 : W_CODES) + r * W_K;
+                    const uint32_t dst = sbase + slot * wide_bytes + r * 128;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[32];
-                    if (live) {
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+                        if (live) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint4 w = lds128(src + (((4 * h + c) ^ x) << 4));
-                            to_half(w.x, v[8 * c], v[8 * c + 1]);
-                            to_half(w.y, v[8 * c + 2], v[8 * c + 3]);
-                            to_half(w.z, v[8 * c + 4], v[8 * c + 5]);
-                            to_half(w.w, v[8 * c + 6], v[8 * c + 7]);
+                            for (int c = 0; c < 4; ++c) {
+                                const uint4 w = lds128(src + (((4 * h + c) ^ x) << 4));
+                                to_half(w.x, v[8 * c], v[8 * c + 1]);
+                                to_half(w.y, v[8 * c + 2], v[8 * c + 3]);
+                                to_half(w.z, v[8 * c + 4], v[8 * c + 5]);
+                                to_half(w.w, v[8 * c + 6], v[8 * c + 7]);
+                            }
+                        }
+                        if (h == 0) {
+                            ok = wait_all(wide_free(slot), sphase ^ 1u, limit);
+                            if (!ok) break;
+                            if (weights) tc_fence_after();
+                        } else {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(raw_free(stage));
+                        }
+                        if (weights) {
+                            tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + W_A0 + slot * (W_K / 2) + 32 * h, v);
+                        } else if (live) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                sts128(dst + h * (wide_bytes / 2) + ((c ^ x) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                         }
                     }
-                    if (h == 1) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_free(stage));
-                    }
-                    if (!waited) {
-                        ok = wait_all(wide_free(slot), sphase ^ 1u, limit);
-                        if (!ok) break;
-                        waited = true;
-                    }
+                    if (!ok) break;
                     if (weights) {
-                        if (h == 0) tc_fence_after();
-                        tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + W_A0 + slot * (W_K / 2) + 32 * h, v);
-                    } else if (live) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) sts128(dst + h * (W_WIDE / 2) + ((c ^ x) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                        tmem_st_wait();
+                        tc_fence_before();
+                    } else {
+                        fence_proxy_async_smem();
                     }
+                    __syncwarp();
+                    // (arrive_cluster's CTA scope: each SM's tensor core reads what its own CTA wrote, which the fence
+                    // above has put before the arrival; .release.cluster held a warp up for 900 to 1500 cycles a stage)
+                    if (lane == 0) arrive_cluster(in_cta(wide_full(slot), even));
                 }
-                if (!ok) break;
-                if (weights) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                } else {
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) arrive_release(in_cta(wide_full(slot), even));
-                if (++stage == W_RAW) {
+                if (turns) turn ^= 1;
+                if (++stage == raws) {
                     stage = 0;
                     rphase ^= 1u;
                 }
@@ -543,47 +538,52 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                 }
             }
         }
-    } else {
-        // ------------------------------- epilogue -----------------------------------
-        const int q = warp & 3;
-        const int c0 = W_T / 2 * ((warp - 10) >> 2);   // its half of the columns
-        const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + c0;
-        const uint32_t turn = sbase + W_RING + (warp - 10) * W_TURN;
-        uint32_t tile = 0;
-        for (uint32_t i = first; i < ntiles; i += step, ++tile) {
-            const WTile t = find_tile(p, start, i);
-            const int f0 = t.f0 + (int)half * W_F + 32 * q;
-            float* sx = token_scales + (warp - 10) * (W_T / 2);   // the scales of its tokens
-            if (!SPLIT) {
-                __syncwarp();
-#pragma unroll
-                for (int c = lane; c < W_T / 2; c += 32) sx[c] = t.t0 + c0 + c < t.hi ? p.xs[t.t0 + c0 + c] : 0.0f;
-                __syncwarp();
-            }
-            ok = wait_all(tfull, tile & 1u, limit);
-            if (!ok) break;
+    } else if constexpr (SPLIT) {
+        // ---- the sums to this CTA's shared memory, [token][feature], which no copy or MMA uses any more
+        if (first < ntiles) {   // (one tile per cluster)
+            const WTile t = find_tile(p, start, first);
+            ok = wait_all(tfull, 0, limit);
             tc_fence_after();
-            if constexpr (SPLIT) {
-                // its sums to its own shared memory, [token][feature], which no copy or MMA uses any more
-                for (int c = c0; c < min(c0 + W_T / 2, t.n); c += 32) {
+            if (ok) {
+                const int q = warp & 3;
+                for (int c = 0; c < t.n; c += 32) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) reinterpret_cast<uint32_t*>(smem)[(c + j) * W_F + 32 * q + lane] = v[j];
                 }
-                break;   // (one tile per cluster)
             }
+        }
+    } else {
+        // ------------------------------- epilogue -----------------------------------
+        const int q = warp & 3;
+        const int c0 = W_T / 2 * ((warp - 10) >> 2);   // its half of the columns
+        const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + c0;
+        const uint32_t turn = sbase + W_RING + (warp - 10) * W_TURN;
+        float* sx = token_scales + (warp - 10) * (W_T / 2);   // the scales of its tokens
+        const bool relu = p.relu != 0;
+        uint32_t tile = 0;
+        for (uint32_t i = first; i < ntiles; i += step, ++tile) {
+            const WTile t = find_tile(p, start, i);
+            const int f0 = t.f0 + (int)half * W_F + 32 * q;
             const float* ws = p.ws + (int64_t)t.e * p.N;
-            const bool relu = p.relu != 0;
-            if (p.vec) {
+            __syncwarp();
+#pragma unroll
+            for (int c = lane; c < W_T / 2; c += 32) sx[c] = t.t0 + c0 + c < t.hi ? p.xs[t.t0 + c0 + c] : 0.0f;
+            __syncwarp();
+            const float mine = ws[min(f0 + lane, p.N - 1)];
+            // (an ordinary weight's scale first cannot overflow: below 2^96 times a sum below 2^31)
+            const bool far = __any_sync(0xffffffffu, mine > 0x1p96f);
+            ok = wait_all(tfull, tile & 1u, limit);
+            if (!ok) break;
+            tc_fence_after();
+            if (p.vec && !far) {
                 // packed before the buffer is free, stored after it
                 uint32_t v[4][4][4];
                 float sw[4];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) sw[g] = ws[min(f0 + 8 * g + (lane >> 2), p.N - 1)];
-                // (an ordinary weight's scale first cannot overflow: below 2^96 times a sum below 2^31)
-                const bool far = __any_sync(0xffffffffu, fmaxf(fmaxf(sw[0], sw[1]), fmaxf(sw[2], sw[3])) > 0x1p96f);
+                for (int g = 0; g < 4; ++g) sw[g] = __shfl_sync(0xffffffffu, mine, 8 * g + (lane >> 2));
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c0 + 32 * c < t.n) {
@@ -593,10 +593,10 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float s0 = sx[32 * c + 8 * j + 2 * (lane & 3)], s1 = sx[32 * c + 8 * j + 2 * (lane & 3) + 1];
+                            const float2 s = *reinterpret_cast<const float2*>(sx + 32 * c + 8 * j + 2 * (lane & 3));
 #pragma unroll
                             for (int g = 0; g < 4; ++g)
-                                v[c][j][g] = pair_bf16(a[g >> 1][4 * j + 2 * (g & 1)], a[g >> 1][4 * j + 2 * (g & 1) + 1], sw[g], s0, s1, far, relu);
+                                v[c][j][g] = pair_bf16(a[g >> 1][4 * j + 2 * (g & 1)], a[g >> 1][4 * j + 2 * (g & 1) + 1], sw[g], s);
                         }
                     }
                 }
@@ -604,12 +604,17 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_cta(tfree, even));
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c0 + 32 * c < t.n) turn_tokens(p, v[c], t.t0 + c0 + 32 * c, t.hi, f0, turn);
+                for (int c = 0; c < 4; ++c) {
+                    if (c0 + 32 * c < t.n) {
+                        if (relu) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[c][j >> 2][j & 3] = relu_bf16(v[c][j >> 2][j & 3]);
+                        }
+                        turn_tokens(p, v[c], t.t0 + c0 + 32 * c, t.hi, f0, turn);
+                    }
+                }
             } else {
                 const int f = f0 + lane;
-                const float sw = ws[min(f, p.N - 1)];
-                const bool far = __any_sync(0xffffffffu, sw > 0x1p96f);
                 for (int c = 0; c < W_T / 2 && c0 + c < t.n; c += 32) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(sums + c, v);
@@ -617,8 +622,8 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                     const int tok = t.t0 + c0 + c;
                     const int64_t at = (int64_t)tok * p.ldy + f;
                     if (f >= p.N) continue;
-                    if (p.bf16_out) store_tokens(static_cast<__nv_bfloat16*>(p.Y) + at, p.ldy, v, sw, sx + c, far, relu, t.hi - tok);
-                    else store_tokens(static_cast<float*>(p.Y) + at, p.ldy, v, sw, sx + c, far, relu, t.hi - tok);
+                    if (p.bf16_out) store_tokens(static_cast<__nv_bfloat16*>(p.Y) + at, p.ldy, v, mine, sx + c, relu, t.hi - tok);
+                    else store_tokens(static_cast<float*>(p.Y) + at, p.ldy, v, mine, sx + c, relu, t.hi - tok);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -635,13 +640,34 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
         if (first < ntiles) {
             const WTile t = find_tile(p, start, first);
             const int a = t.n * share / p.splits, b = t.n * (share + 1) / p.splits;   // this pair's tokens
-            const uint32_t mine = sbase + 4 * (threadIdx.x & (W_F - 1));
-            const int f = t.f0 + (int)half * W_F + (int)(threadIdx.x & (W_F - 1));
-            const float sw = p.ws[(int64_t)t.e * p.N + min(f, p.N - 1)];
-            for (int c = a + (int)(threadIdx.x / W_F); c < min(b, t.hi - t.t0) && threadIdx.x < W_THREADS / W_F * W_F; c += W_THREADS / W_F) {
-                float s = 0.0f;
-                for (int j = 0; j < p.splits; ++j) s += ld_cluster(in_cta(mine + 4 * c * W_F, 2 * j + half));
-                if (f < p.N) store_result(p, t.t0 + c, f, scaled(s, sw, p.xs[t.t0 + c]));
+            const int f = t.f0 + (int)half * W_F + 4 * lane;   // four features per lane, a token per warp
+            const uint32_t mine = sbase + 16 * lane;
+            float sw[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) sw[g] = p.ws[(int64_t)t.e * p.N + min(f + g, p.N - 1)];
+#pragma unroll 2
+            for (int c = a + warp; c < min(b, t.hi - t.t0); c += W_THREADS / 32) {
+                const float sx = p.xs[t.t0 + c];
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int j = 0; j < p.splits; ++j) {
+                    const float4 u = ld_cluster(in_cta(mine + 4 * c * W_F, 2 * j + half));
+                    s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+                }
+                float v[4] = {scaled(s.x, sw[0], sx), scaled(s.y, sw[1], sx), scaled(s.z, sw[2], sx), scaled(s.w, sw[3], sx)};
+                if (p.vec) {
+                    if (f >= p.N) continue;
+                    if (p.relu) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) v[g] = relu_of(v[g]);
+                    }
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.Y) + (int64_t)(t.t0 + c) * p.ldy + f) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if (f + g < p.N) store_result(p, t.t0 + c, f + g, v[g]);
+                }
             }
         }
         __syncthreads();
@@ -667,28 +693,56 @@ bool code_map(CUtensorMap* m, const int8_t* codes, int64_t rows, int64_t cols, i
 }
 
 template <bool SPLIT>
-int launch_pairs(const WMaps& m, const IParams& p, int64_t most_tiles, cudaStream_t s) {
-    constexpr int kFixed = 1024 + W_RING + 8 * W_TURN + 8 * W_BARS + 4 + 16 * W_T;
+cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2]) {
+    constexpr int kFixed = 1024 + W_RING + 8 * W_TURN + 8 * W_BARS + 8 + 16 * W_T;
     constexpr int kMost = kFixed + 4 * (I_MAX_EXPERTS + 1);
     static_assert(kMost <= 227 * 1024, "an SM's shared memory");
     static_assert(W_T * W_F * 4 <= W_RING, "a split tile's sums take the place of the stages");
-    // the limit is the kernel's and not the call's: every thread's calls set it to the same number
-    GPTQ_CUDA_TRY(cudaFuncSetAttribute(int8_matmul_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
-    const unsigned per = 2 * (SPLIT ? p.splits : 1);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(SPLIT ? (unsigned)most_tiles * per : 2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2));
-    cfg.blockDim = dim3(W_THREADS);
-    cfg.dynamicSmemBytes = kFixed + 4 * (p.experts + 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
+    *cfg = {};
+    cfg->gridDim = dim3(ctas);
+    cfg->blockDim = dim3(W_THREADS);
+    cfg->dynamicSmemBytes = kFixed + 4 * (p.experts + 1);
+    cfg->stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = per;
+    attr[0].val.clusterDim.x = 2 * (SPLIT ? p.splits : 1);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+    // the limit is the kernel's and not the call's: every thread's calls set it to the same number
+    return cudaFuncSetAttribute(int8_matmul_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+}
+
+// How many clusters of 2 * splits CTAs the device holds at once (its GPCs are not all multiples of 8 SMs)
+int clusters_at_once(int splits) {
+    static std::atomic<int> known[16][2];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int>* k = dev < 16 ? &known[dev][splits > 2] : nullptr;
+    if (k && k->load(std::memory_order_relaxed)) return k->load(std::memory_order_relaxed);
+    IParams p{};
+    p.splits = splits;
+    p.experts = I_MAX_EXPERTS;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (configure<true>(p, 2 * splits, nullptr, &cfg, attr) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, int8_matmul_kernel<true>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    if (k) k->store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <bool SPLIT>
+int launch_pairs(const WMaps& m, const IParams& p, int64_t most_tiles, cudaStream_t s) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    const unsigned ctas = SPLIT ? (unsigned)most_tiles * 2 * p.splits : 2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2);
+    GPTQ_CUDA_TRY(configure<SPLIT>(p, ctas, s, &cfg, attr));
     cudaError_t e = cudaSuccess;
     GPTQ_LAUNCH(K_INT8_MM, s, e = cudaLaunchKernelEx(&cfg, int8_matmul_kernel<SPLIT>, m, p));
     GPTQ_CUDA_TRY(e);
@@ -751,9 +805,16 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
     for (int i = 0; i < 3; ++i)
         if (!code_map(&m.x[i], x_codes, T, K, W_F >> i)) return GPTQ_ERR_CUDA;
     // an expert's last tile may be partial
-    const int64_t most = (ceil_div(T, W_T) + (offsets ? std::min(experts, T) : 0)) * p.ftiles, pairs = device_sm_count() / 2;
+    const int64_t most = (ceil_div(T, W_T) + (offsets ? std::min(experts, T) : 0)) * p.ftiles;
+    // few tiles: as many shares of the columns as the device holds at once, of four stages or more each
     p.splits = 1;
-    while (p.splits < 4 && most * p.splits * 2 <= pairs && ceil_div(K, W_K) >= p.splits * 4) p.splits *= 2;
+    for (int k = 4; k > 1 && p.splits == 1; k >>= 1)
+        if (most * k <= device_sm_count() / 2 && ceil_div(K, W_K) >= 4 * k && most <= clusters_at_once(k)) p.splits = k;
+    if (p.splits > 1) {
+        const int64_t rows = offsets ? std::min<int64_t>(T, W_T) : ceil_div(T, ceil_div(T, W_T));   // of the widest tile
+        p.box = rows <= 64 ? 32 : rows <= 128 ? 64 : 128;
+        p.raw = std::min(W_MOST_RAW, (W_RING - W_SLOTS * p.box * 2 * W_K) / (W_CODES + p.box * W_K));
+    }
     const int rc = p.splits > 1 ? launch_pairs<true>(m, p, most, s) : launch_pairs<false>(m, p, most, s);
     return rc != GPTQ_OK ? rc : st.finish(s);
 }
