@@ -148,16 +148,18 @@ __global__ void __launch_bounds__(F_THREADS) int8_few_rows_kernel(const IParams 
 // Two CTAs on neighbouring SMs work on a tile of 256 features x up to 256 tokens: each brings and expands
 // its own 128 features and half of the tokens, 128 columns at a time. Roles in each CTA (persistent, one per SM):
 //   warp 0        producer: two TMA copies per stage, 128 x 128 codes of each operand (128-byte swizzle)
-//   warp 1        in the even CTA: the MMAs
-//   warps 2..5    weights: shared memory -> fp16 -> TMEM, a row per lane
-//   warps 6..9    tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), a row per lane
-//   warps 10..17  epilogue: TMEM -> registers -> Y
+//   warp 1        in the even CTA: the MMAs (warps 2 and 3 help with the set-up)
+//   warps 4..7    weights: shared memory -> fp16 -> TMEM, a row per lane
+//   warps 8..15   tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), a row per lane; two groups
+//                 that take every other stage
+//   warps 16..23  epilogue: TMEM -> registers -> Y; they take registers that the other warps give up
 // TMEM: 256 columns of sums (tokens), then the expanded weights of W_SLOTS stages, 64 columns each.
 //
 // SPLIT: few tiles, so a cluster of up to 8 CTAs shares the columns of one tile, and its pairs' sums are added
 // through each other's shared memory, each pair for its own part of the tokens. Such tiles are mostly narrow,
-// bound by the weights and the time that one stage takes, so more stages of codes are in flight, two
-// groups of warps expand the weights in turn, and 4 warps are the epilogue (10..13 tokens, 14..17 epilogue).
+// bound by the weights and the time that one stage takes: more stages of codes are in flight, three groups of
+// warps (4..15) expand the weights in turn, the tokens' warps (16..19) are as many groups as a stage's tokens
+// leave free, and 4 warps (20..23) are the epilogue.
 // Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits for its own
 // copies, the even one for the MMAs, and all meet before any leaves).
 constexpr int W_F = 128, W_PF = 2 * W_F;   // features per CTA and per tile
@@ -165,7 +167,7 @@ constexpr int W_T = 256;                   // most tokens per tile
 constexpr int W_K = 128;                   // columns per stage
 constexpr int W_RAW = 3, W_SLOTS = 3;      // stages of codes, and of expanded operands
 constexpr int W_MOST_RAW = 8;              // the former where token boxes are small
-constexpr int W_THREADS = 32 * 18;
+constexpr int W_THREADS = 32 * 24;
 constexpr int W_CODES = W_F * W_K;         // bytes of one operand's codes per stage
 constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per stage
 constexpr uint32_t W_TMEM = 512, W_A0 = 256;
@@ -186,27 +188,30 @@ struct WTile {
     int hi;           // the end of the expert's tokens
 };
 
-__device__ __forceinline__ WTile find_tile(const IParams& p, const int32_t* start, uint32_t i) {
+// What finding a tile takes, in shared memory: token tiles before each expert, and each one's rows
+struct WRows {
+    int32_t* start;   // [experts + 1]
+    int2* rows;       // [experts]
+};
+
+__device__ __forceinline__ WTile find_tile(const IParams& p, const WRows& w, uint32_t i) {
     WTile t;
-    const uint32_t ttiles = (uint32_t)start[p.experts];
-    const int tt = (int)(p.tokens_first ? i % ttiles : i / (uint32_t)p.ftiles);
-    t.f0 = (int)(p.tokens_first ? i / ttiles : i % (uint32_t)p.ftiles) * W_PF;
+    const uint32_t ttiles = (uint32_t)w.start[p.experts], by = p.tokens_first ? ttiles : (uint32_t)p.ftiles;
+    const uint32_t major = i / by, minor = i - major * by;
+    const int tt = (int)(p.tokens_first ? minor : major);
+    t.f0 = (int)(p.tokens_first ? major : minor) * W_PF;
     int a = 0, b = p.experts;   // start[a] <= tt < start[b]
     while (b - a > 1) {
         const int m = (a + b) >> 1;
-        if (start[m] <= tt) a = m;
+        if (w.start[m] <= tt) a = m;
         else b = m;
     }
     t.e = a;
-    int lo = 0;
-    t.hi = p.T;
-    if (p.offsets) {
-        lo = min(max(p.offsets[a], 0), p.T);
-        t.hi = min(max(p.offsets[a + 1], lo), p.T);
-    }
-    const int tiles = start[a + 1] - start[a];
-    const int width = ((t.hi - lo + tiles - 1) / tiles + 31) & ~31;
-    t.t0 = lo + (tt - start[a]) * width;
+    const int first = w.start[a], tiles = w.start[a + 1] - first;
+    const int2 r = w.rows[a];
+    t.hi = r.y;
+    const int width = ((int)((uint32_t)(r.y - r.x + tiles - 1) / (uint32_t)tiles) + 31) & ~31;
+    t.t0 = r.x + (tt - first) * width;
     t.n = min(max(t.hi - t.t0 + 31, 32) & ~31, width);
     return t;
 }
@@ -277,6 +282,13 @@ __device__ __forceinline__ void store_tokens(T* y, int64_t ldy, const uint32_t (
     }
 }
 
+// half of tmem_ld_16x256b_x4
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
 // two sums times a feature's scale and their tokens' scales, as a pair of bf16
 __device__ __forceinline__ uint32_t pair_bf16(uint32_t a, uint32_t b, float sw, float2 sx) {
     uint32_t r;
@@ -325,16 +337,20 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W_RING + 8 * W_TURN);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W_BARS);
     float* token_scales = reinterpret_cast<float*>(tmem_slot + 2);              // [8][W_T / 2]
-    int32_t* start = reinterpret_cast<int32_t*>(token_scales + 4 * W_T);        // [experts + 1]
+    WRows w;
+    w.rows = reinterpret_cast<int2*>(token_scales + 4 * W_T);
+    w.start = reinterpret_cast<int32_t*>(w.rows + p.experts);
 
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = uniform(cluster_rank()), half = rank & 1u, even = rank & ~1u;
     const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
     auto raw_full = [&](int s) { return bar0 + 8u * s; };                                      // copies landed
-    auto raw_free = [&](int s) { return bar0 + 8u * (W_MOST_RAW + s); };                       // all 8 warps have read them
+    auto raw_free = [&](int s) { return bar0 + 8u * (W_MOST_RAW + s); };                       // all have read them
     auto wide_full = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + s); };                  // even CTA: both have expanded
     auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + W_SLOTS + s); };        // the stage's MMAs are done
     const uint32_t tfull = bar0 + 8u * (2 * W_MOST_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
+    // warps that expand one stage's tokens, and the groups of them
+    const int token_warps = SPLIT ? p.box / 32 : 4, token_groups = SPLIT ? 4 / token_warps : 2;
     // the expanded tokens first, then the stages of codes
     const int box_rows = SPLIT ? p.box : W_F, raws = SPLIT ? p.raw : W_RAW;
     const uint32_t wide_bytes = box_rows * 2 * W_K, raw_bytes = W_CODES + box_rows * W_K;
@@ -349,10 +365,10 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     if (warp == 2 && elect_one()) {
         for (int s = 0; s < raws; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_free(s), 8);
+            mbar_init(raw_free(s), 4 + token_warps);
         }
         for (int s = 0; s < W_SLOTS; ++s) {
-            mbar_init(wide_full(s), 16);
+            mbar_init(wide_full(s), 2 * (4 + token_warps));
             mbar_init(wide_free(s), 1);
         }
         mbar_init(tfull, 1);
@@ -383,102 +399,113 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                 const int v = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += v;
             }
-            if (e0 + lane < p.experts) start[e0 + lane] = carry + inc - n;
+            if (e0 + lane < p.experts) {
+                w.start[e0 + lane] = carry + inc - n;
+                w.rows[e0 + lane] = make_int2(lo, hi);
+            }
             carry += __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (lane == 0) start[p.experts] = carry;
+        if (lane == 0) w.start[p.experts] = carry;
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // all CTAs' barriers are ready before any signals another's
+    // all CTAs' barriers are ready before any signals another's (the producer signals only its own)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (warp != 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
     const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_pipeline_wait_limit_ns);
     bool ok = true;   // false: a wait gave up
-    const uint32_t ntiles = uniform((uint32_t)start[p.experts] * (uint32_t)p.ftiles);
+    const uint32_t ntiles = uniform((uint32_t)w.start[p.experts] * (uint32_t)p.ftiles);
 
-    if (warp == 0) {
-        // ------------------------------- producer -----------------------------------
-        const bool leader = elect_one();
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, issued_par = 0;
-        for (uint32_t i = first; i < ntiles && ok; i += step) {
-            const WTile t = find_tile(p, start, i);
-            const int n = (int)uniform(t.n), e = (int)uniform(t.e);
-            const int box = n > 128 ? 0 : n > 64 ? 1 : 2;   // (its rows are at most SPLIT's)
-            const uint32_t bytes = W_CODES + (W_CODES >> box);
-            const int wrow = e * p.N + (int)uniform(t.f0) + (int)half * W_F, xrow = (int)uniform(t.t0) + (int)half * (n >> 1);
-            for (int k = k0; k < k1; ++k) {
-                ok = wait_all(raw_free(stage), phase ^ 1u, limit);
-                if (!ok) break;
-                if (leader) {
-                    const uint32_t base = rbase + stage * raw_bytes, bar = raw_full(stage);
-                    mbar_expect_tx(bar, bytes);
-                    tma_load_2d(base, &m.w, bar, k * W_K, wrow);
-                    tma_load_2d(base + W_CODES, &m.x[box], bar, k * W_K, xrow);
-                }
-                __syncwarp();
-                issued |= 1u << stage;
-                issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-                if (++stage == raws) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (leader)
-            for (int s = 0; s < raws; ++s)
-                if (issued & (1u << s)) drain(raw_full(s), (issued_par >> s) & 1u);
-        __syncwarp();
-    } else if (warp == 1) {
-        // --------------------------- MMA issuer (even CTA) --------------------------
-        if (half == 0) {
-            int slot = 0;
-            uint32_t phase = 0, tile = 0;
-            for (uint32_t i = first; i < ntiles && ok; i += step, ++tile) {
-                const WTile t = find_tile(p, start, i);
-                const uint32_t idesc = half_idesc((int)uniform(t.n));
-                ok = wait_all(tfree, (tile & 1u) ^ 1u, limit);
-                if (!ok) break;
-                tc_fence_after();
+    // registers of 6 groups of 4 warps: the CTA starts with 6 x 80 a lane, and 40 + 3 x 64 + 2 x 120 is 472
+    if (warp < 4) {
+        if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            // ------------------------------- producer -----------------------------------
+            const bool leader = elect_one();
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_par = 0;
+            for (uint32_t i = first; i < ntiles && ok; i += step) {
+                const WTile t = find_tile(p, w, i);
+                const int n = (int)uniform(t.n), e = (int)uniform(t.e);
+                const int box = n > 128 ? 0 : n > 64 ? 1 : 2;   // (its rows are at most SPLIT's)
+                const uint32_t bytes = W_CODES + (W_CODES >> box);
+                const int wrow = e * p.N + (int)uniform(t.f0) + (int)half * W_F, xrow = (int)uniform(t.t0) + (int)half * (n >> 1);
                 for (int k = k0; k < k1; ++k) {
-                    ok = wait_all(wide_full(slot), phase, limit);
+                    ok = wait_all(raw_free(stage), phase ^ 1u, limit);
                     if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const int ksteps = (p.K - k * W_K + 15) / 16;
-                        const uint32_t a = tmem + W_A0 + slot * (W_K / 2);
-                        const uint64_t b = smem_desc(sbase + slot * wide_bytes, 16, 1024, kSwizzle128B);
-#pragma unroll
-                        for (int j = 0; j < W_K / 16; ++j)
-                            if (j < ksteps)
-                                umma_half(tmem, a + 8 * j, b + (j >> 2) * (wide_bytes / 2 / 16) + 2 * (j & 3), idesc, (k > k0 || j > 0) ? 1u : 0u);
-                        commit_to(wide_free(slot), 3u << even);
-                        if (k == k1 - 1) commit_to(tfull, 3u << even);
+                    if (leader) {
+                        const uint32_t base = rbase + stage * raw_bytes, bar = raw_full(stage);
+                        mbar_expect_tx(bar, bytes);
+                        tma_load_2d(base, &m.w, bar, k * W_K, wrow);
+                        tma_load_2d(base + W_CODES, &m.x[box], bar, k * W_K, xrow);
                     }
                     __syncwarp();
-                    if (++slot == W_SLOTS) {
-                        slot = 0;
+                    issued |= 1u << stage;
+                    issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == raws) {
+                        stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (elect_one()) {
-                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_bar) : "memory");
-                drain(drain_bar, 0);
-            }
+            if (leader)
+                for (int s = 0; s < raws; ++s)
+                    if (issued & (1u << s)) drain(raw_full(s), (issued_par >> s) & 1u);
             __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else if (warp == 1) {
+            // --------------------------- MMA issuer (even CTA) --------------------------
+            if (half == 0) {
+                int slot = 0;
+                uint32_t phase = 0, tile = 0;
+                for (uint32_t i = first; i < ntiles && ok; i += step, ++tile) {
+                    const WTile t = find_tile(p, w, i);
+                    const uint32_t idesc = half_idesc((int)uniform(t.n));
+                    ok = wait_all(tfree, (tile & 1u) ^ 1u, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int k = k0; k < k1; ++k) {
+                        ok = wait_all(wide_full(slot), phase, limit);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const int ksteps = (p.K - k * W_K + 15) / 16;
+                            const uint32_t a = tmem + W_A0 + slot * (W_K / 2);
+                            const uint64_t b = smem_desc(sbase + slot * wide_bytes, 16, 1024, kSwizzle128B);
+    #pragma unroll
+                            for (int j = 0; j < W_K / 16; ++j)
+                                if (j < ksteps)
+                                    umma_half(tmem, a + 8 * j, b + (j >> 2) * (wide_bytes / 2 / 16) + 2 * (j & 3), idesc, (k > k0 || j > 0) ? 1u : 0u);
+                            commit_to(wide_free(slot), 3u << even);
+                            if (k == k1 - 1) commit_to(tfull, 3u << even);
+                        }
+                        __syncwarp();
+                        if (++slot == W_SLOTS) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                if (elect_one()) {
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_bar) : "memory");
+                    drain(drain_bar, 0);
+                }
+                __syncwarp();
+            }
         }
-    } else if (warp < (SPLIT ? 14 : 10)) {
+    } else if (warp < (SPLIT ? 20 : 16)) {
         // -------------------------- expansion, a row per lane -----------------------
-        const bool weights = warp < (SPLIT ? 10 : 6);
-        const int q = weights ? warp & 3 : warp - (SPLIT ? 10 : 6), r = 32 * q + lane, x = r & 7;
-        // (SPLIT: the two groups of the weights' warps take every other stage)
-        const bool turns = SPLIT && weights;
-        int stage = 0, slot = 0, turn = turns ? (warp - 2) >> 2 : 0;
+        if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        const bool weights = warp < (SPLIT ? 16 : 8);
+        const int member = warp - (weights ? 4 : SPLIT ? 16 : 8), size = weights ? 4 : token_warps;
+        const int q = member % size, groups = weights ? (SPLIT ? 3 : 1) : token_groups;
+        const int r = 32 * q + lane, x = r & 7;
+        int stage = 0, slot = 0, turn = member / size;   // stages until this group's next one
         uint32_t rphase = 0, sphase = 0;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
-            const WTile t = find_tile(p, start, i);
+            const WTile t = find_tile(p, w, i);
             const bool live = weights || 64 * q < (int)uniform(t.n);
             for (int k = k0; k < k1; ++k) {
                 if (turn == 0) {
@@ -527,7 +554,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                     // above has put before the arrival; .release.cluster held a warp up for 900 to 1500 cycles a stage)
                     if (lane == 0) arrive_cluster(in_cta(wide_full(slot), even));
                 }
-                if (turns) turn ^= 1;
+                turn = turn == 0 ? groups - 1 : turn - 1;
                 if (++stage == raws) {
                     stage = 0;
                     rphase ^= 1u;
@@ -541,7 +568,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     } else if constexpr (SPLIT) {
         // ---- the sums to this CTA's shared memory, [token][feature], which no copy or MMA uses any more
         if (first < ntiles) {   // (one tile per cluster)
-            const WTile t = find_tile(p, start, first);
+            const WTile t = find_tile(p, w, first);
             ok = wait_all(tfull, 0, limit);
             tc_fence_after();
             if (ok) {
@@ -557,15 +584,16 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
         }
     } else {
         // ------------------------------- epilogue -----------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int q = warp & 3;
-        const int c0 = W_T / 2 * ((warp - 10) >> 2);   // its half of the columns
+        const int c0 = W_T / 2 * ((warp - 16) >> 2);   // its half of the columns
         const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + c0;
-        const uint32_t turn = sbase + W_RING + (warp - 10) * W_TURN;
-        float* sx = token_scales + (warp - 10) * (W_T / 2);   // the scales of its tokens
+        const uint32_t turn = sbase + W_RING + (warp - 16) * W_TURN;
+        float* sx = token_scales + (warp - 16) * (W_T / 2);   // the scales of its tokens
         const bool relu = p.relu != 0;
         uint32_t tile = 0;
         for (uint32_t i = first; i < ntiles; i += step, ++tile) {
-            const WTile t = find_tile(p, start, i);
+            const WTile t = find_tile(p, w, i);
             const int f0 = t.f0 + (int)half * W_F + 32 * q;
             const float* ws = p.ws + (int64_t)t.e * p.N;
             __syncwarp();
@@ -587,16 +615,19 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c0 + 32 * c < t.n) {
-                        uint32_t a[2][16];
-                        tmem_ld_16x256b_x4(sums + 32 * c, a[0]);
-                        tmem_ld_16x256b_x4(sums + (16u << 16) + 32 * c, a[1]);
-                        tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 s = *reinterpret_cast<const float2*>(sx + 32 * c + 8 * j + 2 * (lane & 3));
+                        for (int j = 0; j < 4; j += 2) {
+                            uint32_t a[2][8];
+                            tmem_ld_16x256b_x2(sums + 32 * c + 8 * j, a[0]);
+                            tmem_ld_16x256b_x2(sums + (16u << 16) + 32 * c + 8 * j, a[1]);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                v[c][j][g] = pair_bf16(a[g >> 1][4 * j + 2 * (g & 1)], a[g >> 1][4 * j + 2 * (g & 1) + 1], sw[g], s);
+                            for (int u = 0; u < 2; ++u) {
+                                const float2 s = *reinterpret_cast<const float2*>(sx + 32 * c + 8 * (j + u) + 2 * (lane & 3));
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    v[c][j + u][g] = pair_bf16(a[g >> 1][4 * u + 2 * (g & 1)], a[g >> 1][4 * u + 2 * (g & 1) + 1], sw[g], s);
+                            }
                         }
                     }
                 }
@@ -638,7 +669,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     cluster_sync();   // no CTA leaves, or frees TMEM, while another may still use it
     if constexpr (SPLIT) {
         if (first < ntiles) {
-            const WTile t = find_tile(p, start, first);
+            const WTile t = find_tile(p, w, first);
             const int a = t.n * share / p.splits, b = t.n * (share + 1) / p.splits;   // this pair's tokens
             const int f = t.f0 + (int)half * W_F + 4 * lane;   // four features per lane, a token per warp
             const uint32_t mine = sbase + 16 * lane;
@@ -695,13 +726,13 @@ bool code_map(CUtensorMap* m, const int8_t* codes, int64_t rows, int64_t cols, i
 template <bool SPLIT>
 cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2]) {
     constexpr int kFixed = 1024 + W_RING + 8 * W_TURN + 8 * W_BARS + 8 + 16 * W_T;
-    constexpr int kMost = kFixed + 4 * (I_MAX_EXPERTS + 1);
+    constexpr int kMost = kFixed + 12 * I_MAX_EXPERTS + 4;
     static_assert(kMost <= 227 * 1024, "an SM's shared memory");
     static_assert(W_T * W_F * 4 <= W_RING, "a split tile's sums take the place of the stages");
     *cfg = {};
     cfg->gridDim = dim3(ctas);
     cfg->blockDim = dim3(W_THREADS);
-    cfg->dynamicSmemBytes = kFixed + 4 * (p.experts + 1);
+    cfg->dynamicSmemBytes = kFixed + 12 * p.experts + 4;
     cfg->stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * (SPLIT ? p.splits : 1);
