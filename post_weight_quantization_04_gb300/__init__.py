@@ -141,10 +141,12 @@ def _setup_call(lib: ctypes.CDLL) -> None:
     """Hands the C module of the serving calls what it needs: torch's types and the library's entry points."""
     from . import _call
     names = ("gptq_fp4_quantize", "gptq_fp4_dequantize", "gptq_fp4_matmul", "gptq_expert_sort_workspace_bytes",
-             "gptq_expert_sort", "gptq_expert_gather", "gptq_expert_combine", "gptq_expert_combine_grad")
-    _call.setup({"float32": torch.float32, "bfloat16": torch.bfloat16, "uint8": torch.uint8, "int32": torch.int32,
-                 "empty": torch.empty, "raw_stream": _current_raw_stream, "current_device": _current_device,
-                 "Fp4": Fp4, "Route": Route, "check": _check},
+             "gptq_expert_sort", "gptq_expert_gather", "gptq_expert_combine", "gptq_expert_combine_grad", "gptq_int8_quantize",
+             "gptq_int8_dequantize", "gptq_int8_matmul", "gptq_int8_rms_norm", "gptq_int8_rms_norm_grad_workspace_bytes",
+             "gptq_int8_rms_norm_grad", "gptq_expert_balance_workspace_bytes", "gptq_expert_balance", "gptq_expert_balance_grad")
+    _call.setup({"float32": torch.float32, "bfloat16": torch.bfloat16, "uint8": torch.uint8, "int8": torch.int8, "bool": torch.bool,
+                 "int32": torch.int32, "empty": torch.empty, "raw_stream": _current_raw_stream, "current_device": _current_device,
+                 "Fp4": Fp4, "Int8": Int8, "Route": Route, "Balance": Balance, "check": _check},
                 {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names})
     globals()["_fast"] = _call
 
@@ -750,6 +752,10 @@ def gptq_int8_quantize(X: torch.Tensor, index: Optional[torch.Tensor] = None, pe
     """X (bf16 or fp32, any stride between rows that do not overlap) in 8-bit integers, scale = max|x| / 127 of each
     row. index (int32): row r is X row index[r] // per, zeros where index[r] < 0 (a Route's src with per = top
     gathers the experts' rows in the same pass)."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).int8_quantize(X, index, per)
+        if r is not NotImplemented:
+            return r
     dt, n, cols, ld = _matrix(X, "X")
     rows = n
     if index is not None:
@@ -763,6 +769,10 @@ def gptq_int8_quantize(X: torch.Tensor, index: Optional[torch.Tensor] = None, pe
 
 def gptq_int8_dequantize(q: Int8, dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values that q's codes and scales stand for."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).int8_dequantize(q, dtype)
+        if r is not NotImplemented:
+            return r
     _check_int8(q, "q")
     dt = _DTYPES.get(dtype)
     if dt is None:
@@ -781,6 +791,10 @@ def gptq_int8_rms_norm(X: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, r
     """(q, h, rstd): h = X + residual in X's type (X itself without a residual), rstd = 1 / sqrt(mean h^2 + eps) per
     row, and q = (h rstd) gain in 8-bit integers. gain fp32 (cols). h and rstd are what gptq_int8_rms_norm_grad needs.
     out: (q, h, rstd) to write to; its h may be X or residual itself."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).rms_norm(X, gain, eps, residual)
+        if r is not NotImplemented:
+            return r
     dt, rows, cols, ld = _matrix(X, "X")
     _dev_here(gain, torch.float32, "gain", (cols,))
     ldr = _matrix_like(residual, "residual", X.dtype, rows, cols) if residual is not None else 0
@@ -828,6 +842,10 @@ def gptq_int8_rms_norm_grad(dY: torch.Tensor, h: torch.Tensor, gain: torch.Tenso
     """(dX, dgain) of gptq_int8_rms_norm, straight through the rounding: dY is the gradient of q's values, dh (None: 0)
     the one that reaches h past the norm. dX, of X's type, is residual's gradient too; it may be written to dY, h or dh
     (out). dgain is fp32."""
+    if out is None and ws is None and stream is None:
+        r = (_fast or _load_fast()).rms_norm_grad(dY, h, gain, rstd, dh)
+        if r is not NotImplemented:
+            return r
     dt, rows, cols, ldh = _matrix(h, "h")
     lddy = _matrix_like(dY, "dY", h.dtype, rows, cols)
     lddh = _matrix_like(dh, "dh", h.dtype, rows, cols) if dh is not None else 0
@@ -853,6 +871,10 @@ def gptq_int8_matmul(X: Int8, W: Int8, offsets: Optional[torch.Tensor] = None, r
     """Y = X W^T (optionally max(., 0)) of two matrices in 8-bit integers, times the scales of X's row and of W's. With
     offsets (int32, experts + 1, a Route's) W holds one weight per expert and rows offsets[e]..offsets[e+1] of X use
     weight e; rows in no expert's range give zeros."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).int8_matmul(X, W, offsets, relu, out_dtype)
+        if r is not NotImplemented:
+            return r
     _check_int8(X, "X")
     experts = 1
     if offsets is None:
@@ -1025,6 +1047,10 @@ def gptq_expert_balance(logits: torch.Tensor, ids: torch.Tensor, mask: Optional[
     """The balance loss experts / (top n^2) sum_e c[e] sum_t softmax(logits[t])[e] of a router's logits (tokens,
     experts; bf16 or fp32) and choice ids (tokens, top; int32, negative: dropped), with c[e] the slots of expert e
     and n the tokens that count; mask (bool or uint8; None: all) says which do."""
+    if out is None and ws is None and stream is None:
+        r = (_fast or _load_fast()).balance(logits, ids, mask)
+        if r is not NotImplemented:
+            return r
     dt, tokens, experts, ld = _matrix(logits, "logits")
     _dev_here(ids, torch.int32, "ids")
     if ids.dim() != 2 or ids.shape[0] != tokens:
@@ -1049,6 +1075,10 @@ def gptq_expert_balance_grad(dloss: Optional[torch.Tensor], logits: torch.Tensor
                              mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient of gptq_expert_balance's logits (the counts are constants), zeros in rows that do not count;
     dloss: the loss's gradient, one fp32 (None: 1). out may be logits itself."""
+    if out is None and stream is None:
+        r = (_fast or _load_fast()).balance_grad(dloss, logits, balance, mask)
+        if r is not NotImplemented:
+            return r
     dt, tokens, experts, ld = _matrix(logits, "logits")
     if dloss is not None:
         _dev_here(dloss, torch.float32, "dloss")

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
     __shared__ float sum_part[32];
     __shared__ uint32_t max_part[32];
     const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    pdl_trigger();   // the product's prologue may begin
     pdl_wait();
     if (r >= p.rows) return;   // (a whole warp, of a CTA without barriers)
     int64_t sr = r;

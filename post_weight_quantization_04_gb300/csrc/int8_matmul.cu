@@ -71,55 +71,93 @@ __device__ __forceinline__ void zero_rest(const IParams& p, int cta, int ctas) {
     }
 }
 
-// ------------------------------------------------------------------------------- few rows
-// A CTA of 128 threads computes 8 features of up to 8 tokens: a thread takes 16 columns of each, every 128th
-// such piece, and four products at a time go into 32-bit whole numbers (dp4a), which are exact. The
-// sums are then added over the CTA.
-constexpr int F_THREADS = 128, F_FEATURES = 8, F_TOKENS = 8;
+// four codes to four fp16 numbers: code + 128 in the low bits of 1024, less 1152
+__device__ __forceinline__ void to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
 
+// ------------------------------------------------------------------------------- few rows
+// With a handful of tokens the product is the stream of the weights, and what counts is to have all of it in
+// flight at once. A CTA computes 16 features, its warps the columns in turn, 64 at a time: each thread loads 16 bytes
+// of two features and of a token out of eight, expands them to fp16 in its registers and multiplies them with
+// mma.sync (m16n8k16; any order of the columns will do if both operands have the same), 8 tokens at a time. No shared
+// memory, barriers or TMEM lie between the loads and the products; the warps' sums are added at the end.
+constexpr int F_WARPS = 8, F_FEATURES = 16;
+
+__device__ __forceinline__ void mma_half(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// (Plain loads: this kernel starts while the one before may still be writing its operands, so they are not
+// read-only for as long as it runs, which is what the read-only path asks for.)
+// tokens t0 .. t0 + n - 1 (n <= 8 NT) of expert e times features f0 .. f0 + 15
 template <int NT>
-__device__ __forceinline__ void few_rows(const IParams& p, int e, int t0, int n, int f0, int (*part)[F_FEATURES * F_TOKENS]) {
-    const int8_t* wc = p.wc + (int64_t)e * p.N * p.pitch;
-    int acc[F_FEATURES][NT] = {};
-    for (int64_t c = threadIdx.x * 16; c < p.pitch; c += F_THREADS * 16) {
-        uint4 w[F_FEATURES], x[NT];
+__device__ __forceinline__ void few_rows(const IParams& p, int e, int t0, int n, int f0, float* part) {
+    constexpr int AHEAD = NT == 4 ? 2 : 4;   // steps of 64 columns in flight
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, col = 16 * (lane & 3);
+    const int8_t* wc = p.wc + (int64_t)e * p.N * p.pitch + col;
+    const int8_t* w0 = wc + min(f0 + g, p.N - 1) * p.pitch;
+    const int8_t* w1 = wc + min(f0 + g + 8, p.N - 1) * p.pitch;
+    const int8_t* x[NT];
 #pragma unroll
-        for (int i = 0; i < F_FEATURES; ++i) w[i] = *reinterpret_cast<const uint4*>(wc + min(f0 + i, p.N - 1) * p.pitch + c);
+    for (int j = 0; j < NT; ++j) x[j] = p.xc + (t0 + min(8 * j + g, n - 1)) * p.pitch + col;
+    float acc[NT][4] = {};
+    for (int64_t c0 = warp * 64; c0 < p.pitch; c0 += AHEAD * F_WARPS * 64) {
+        uint4 a[AHEAD][2], b[AHEAD][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = *reinterpret_cast<const uint4*>(p.xc + (t0 + min(t, n - 1)) * p.pitch + c);
+        for (int u = 0; u < AHEAD; ++u) {
+            const int64_t c = c0 + u * F_WARPS * 64;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const bool in = c + col < p.pitch;
+            a[u][0] = in ? *reinterpret_cast<const uint4*>(w0 + c) : zero;
+            a[u][1] = in ? *reinterpret_cast<const uint4*>(w1 + c) : zero;
 #pragma unroll
-        for (int i = 0; i < F_FEATURES; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                int a = acc[i][t];
-                a = __dp4a((int)w[i].x, (int)x[t].x, a);
-                a = __dp4a((int)w[i].y, (int)x[t].y, a);
-                a = __dp4a((int)w[i].z, (int)x[t].z, a);
-                acc[i][t] = __dp4a((int)w[i].w, (int)x[t].w, a);
-            }
-    }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < F_FEATURES; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int v = __reduce_add_sync(0xffffffffu, acc[i][t]);
-            if (lane == 0) part[warp][i * NT + t] = v;
+            for (int j = 0; j < NT; ++j) b[u][j] = in ? *reinterpret_cast<const uint4*>(x[j] + c) : zero;
         }
-    __syncthreads();
-    if (threadIdx.x < F_FEATURES * NT) {
-        const int i = threadIdx.x / NT, t = threadIdx.x % NT, f = f0 + i;
-        int v = 0;
 #pragma unroll
-        for (int k = 0; k < F_THREADS / 32; ++k) v += part[k][threadIdx.x];
-        if (f < p.N && t < n) store_result(p, t0 + t, f, scaled((float)v, p.xs[t0 + t], p.ws[(int64_t)e * p.N + f]));
+        for (int u = 0; u < AHEAD; ++u) {
+            const uint32_t r0[4] = {a[u][0].x, a[u][0].y, a[u][0].z, a[u][0].w}, r1[4] = {a[u][1].x, a[u][1].y, a[u][1].z, a[u][1].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t lo0, hi0, lo1, hi1;
+                to_half(r0[q], lo0, hi0);
+                to_half(r1[q], lo1, hi1);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t lo, hi;
+                    to_half(q == 0 ? b[u][j].x : q == 1 ? b[u][j].y : q == 2 ? b[u][j].z : b[u][j].w, lo, hi);
+                    mma_half(acc[j], lo0, lo1, hi0, hi1, lo, hi);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)   // feature g (+ 8), token 8 j + 2 (lane % 4) (+ 1)
+            part[(warp * 8 * NT + 8 * j + 2 * (lane & 3) + (i & 1)) * F_FEATURES + g + 8 * (i >> 1)] = acc[j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < F_FEATURES * n; i += 32 * F_WARPS) {
+        const int t = t0 + i / F_FEATURES, f = f0 + i % F_FEATURES;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < F_WARPS; ++k) v += part[k * 8 * NT * F_FEATURES + i];
+        if (f < p.N) store_result(p, t, f, scaled(v, p.xs[t], p.ws[(int64_t)e * p.N + f]));
     }
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(F_THREADS) int8_few_rows_kernel(const IParams p) {
-    __shared__ int part[F_THREADS / 32][F_FEATURES * F_TOKENS];
-    const int e = blockIdx.y;
+// MOST: groups of 8 tokens at a time; with fewer, more CTAs fit an SM
+template <int MOST>
+__global__ void __launch_bounds__(32 * F_WARPS, MOST == 1 ? 3 : 2) int8_few_rows_kernel(const IParams p) {
+    __shared__ float part[F_WARPS][F_FEATURES * 8 * MOST];
+    const int e = blockIdx.y, f0 = blockIdx.x * F_FEATURES;
+    pdl_trigger();
     pdl_wait();
     if (e == p.experts) {   // (only with offsets)
         zero_rest(p, blockIdx.x, gridDim.x);
@@ -127,14 +165,11 @@ __global__ void __launch_bounds__(F_THREADS) int8_few_rows_kernel(const IParams 
     }
     int lo, hi;
     expert_rows(p, e, &lo, &hi);
-    const int f0 = blockIdx.x * F_FEATURES;
-    for (int t = lo; t < hi;) {
-        const int n = hi - t;
-        if (n > 4) few_rows<8>(p, e, t, min(n, 8), f0, part);
-        else if (n > 2) few_rows<4>(p, e, t, n, f0, part);
-        else if (n == 2) few_rows<2>(p, e, t, 2, f0, part);
-        else few_rows<1>(p, e, t, 1, f0, part);
-        t += min(n, 8);
+    for (int t = lo; t < hi; t += 8 * MOST) {
+        const int n = min(hi - t, 8 * MOST);
+        if (MOST >= 4 && n > 16) few_rows<MOST >= 4 ? 4 : 1>(p, e, t, n, f0, part[0]);
+        else if (MOST >= 2 && n > 8) few_rows<MOST >= 2 ? 2 : 1>(p, e, t, n, f0, part[0]);
+        else few_rows<1>(p, e, t, n, f0, part[0]);
     }
 }
 
@@ -149,17 +184,17 @@ __global__ void __launch_bounds__(F_THREADS) int8_few_rows_kernel(const IParams 
 // its own 128 features and half of the tokens, 128 columns at a time. Roles in each CTA (persistent, one per SM):
 //   warp 0        producer: two TMA copies per stage, 128 x 128 codes of each operand (128-byte swizzle)
 //   warp 1        in the even CTA: the MMAs (warps 2 and 3 help with the set-up)
-//   warps 4..7    weights: shared memory -> fp16 -> TMEM, a row per lane
-//   warps 8..15   tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), a row per lane; two groups
-//                 that take every other stage
-//   warps 16..23  epilogue: TMEM -> registers -> Y; they take registers that the other warps give up
+//   warps 4..11   weights: shared memory -> fp16 -> TMEM, half a row per lane
+//   warps 12..19  tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), half a row per lane
+//   warps 20..27  epilogue: TMEM -> registers -> Y; they take registers that the other warps give up
+// All the warps that expand take part in every stage: groups that take stages in turn can be two phases of a barrier
+// behind, which its parity does not tell from none.
 // TMEM: 256 columns of sums (tokens), then the expanded weights of W_SLOTS stages, 64 columns each.
 //
 // SPLIT: few tiles, so a cluster of up to 8 CTAs shares the columns of one tile, and its pairs' sums are added
 // through each other's shared memory, each pair for its own part of the tokens. Such tiles are mostly narrow,
-// bound by the weights and the time that one stage takes: more stages of codes are in flight, three groups of
-// warps (4..15) expand the weights in turn, the tokens' warps (16..19) are as many groups as a stage's tokens
-// leave free, and 4 warps (20..23) are the epilogue.
+// bound by the weights and the time that one stage takes: more stages of codes are in flight, the tokens have 4 warps
+// (12..15, of which each takes a part of the columns where there are fewer rows), the epilogue 4 (16..19).
 // Every mbarrier wait is bounded (GPTQ_ERR_TIMEOUT into the status word, then unwind: each CTA waits for its own
 // copies, the even one for the MMAs, and all meet before any leaves).
 constexpr int W_F = 128, W_PF = 2 * W_F;   // features per CTA and per tile
@@ -167,7 +202,8 @@ constexpr int W_T = 256;                   // most tokens per tile
 constexpr int W_K = 128;                   // columns per stage
 constexpr int W_RAW = 3, W_SLOTS = 3;      // stages of codes, and of expanded operands
 constexpr int W_MOST_RAW = 8;              // the former where token boxes are small
-constexpr int W_THREADS = 32 * 24;
+constexpr int w_expand(bool split) { return split ? 12 : 16; }   // warps that expand: 8 + 4 or 8 + 8
+constexpr int w_threads(bool split) { return 32 * (split ? 20 : 28); }
 constexpr int W_CODES = W_F * W_K;         // bytes of one operand's codes per stage
 constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per stage
 constexpr uint32_t W_TMEM = 512, W_A0 = 256;
@@ -216,14 +252,6 @@ __device__ __forceinline__ WTile find_tile(const IParams& p, const WRows& w, uin
     return t;
 }
 
-// four codes to four fp16 numbers: code + 128 in the low bits of 1024, less 1152
-__device__ __forceinline__ void to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    w ^= 0x80808080u;
-    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -231,6 +259,42 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void to_half8(const uint4& c, uint32_t* v) {
+    to_half(c.x, v[0], v[1]);
+    to_half(c.y, v[2], v[3]);
+    to_half(c.z, v[4], v[5]);
+    to_half(c.w, v[6], v[7]);
+}
+
+// N pieces of 32 columns of a row (x: its number modulo 8) of codes in the 128-byte swizzle, from piece `at` on
+template <int N>
+__device__ __forceinline__ void load_codes(uint32_t row, int at, int x, uint4 (&code)[2 * N]) {
+#pragma unroll
+    for (int c = 0; c < 2 * N; ++c) code[c] = lds128(row + (((2 * at + c) ^ x) << 4));
+}
+
+// the same pieces as fp16, in slabs of 64 columns
+template <int N>
+__device__ __forceinline__ void store_wide(uint32_t row, uint32_t slab, int at, int x, const uint4 (&code)[2 * N]) {
+#pragma unroll
+    for (int c = 0; c < 2 * N; ++c) {
+        uint32_t v[8];
+        to_half8(code[c], v);
+        const int to = 4 * at + 2 * c;
+        sts128(row + (to >> 3) * slab + (((to & 7) ^ x) << 4), v[0], v[1], v[2], v[3]);
+        sts128(row + (to >> 3) * slab + (((to & 7) ^ x ^ 1) << 4), v[4], v[5], v[6], v[7]);
+    }
+}
+
+// thread t writes lane (base + t), columns c..c+15
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 
 // a shared-memory address in another CTA of the cluster
@@ -331,7 +395,7 @@ __device__ __forceinline__ void turn_tokens(const IParams& p, const uint32_t (&v
 }
 
 template <bool SPLIT>
-__global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_constant__ WMaps m, const IParams p) {
+__global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const __grid_constant__ WMaps m, const IParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W_RING + 8 * W_TURN);
@@ -349,8 +413,6 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     auto wide_full = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + s); };                  // even CTA: both have expanded
     auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + W_SLOTS + s); };        // the stage's MMAs are done
     const uint32_t tfull = bar0 + 8u * (2 * W_MOST_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
-    // warps that expand one stage's tokens, and the groups of them
-    const int token_warps = SPLIT ? p.box / 32 : 4, token_groups = SPLIT ? 4 / token_warps : 2;
     // the expanded tokens first, then the stages of codes
     const int box_rows = SPLIT ? p.box : W_F, raws = SPLIT ? p.raw : W_RAW;
     const uint32_t wide_bytes = box_rows * 2 * W_K, raw_bytes = W_CODES + box_rows * W_K;
@@ -365,10 +427,10 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     if (warp == 2 && elect_one()) {
         for (int s = 0; s < raws; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_free(s), 4 + token_warps);
+            mbar_init(raw_free(s), w_expand(SPLIT));
         }
         for (int s = 0; s < W_SLOTS; ++s) {
-            mbar_init(wide_full(s), 2 * (4 + token_warps));
+            mbar_init(wide_full(s), 2 * w_expand(SPLIT));
             mbar_init(wide_free(s), 1);
         }
         mbar_init(tfull, 1);
@@ -385,6 +447,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    pdl_trigger();   // (the next kernel's CTAs find no room before this one's leave)
     pdl_wait();   // from here on memory that the kernel before writes or reads is touched
     if (warp == 0) {
         // token tiles before each expert
@@ -418,7 +481,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
     bool ok = true;   // false: a wait gave up
     const uint32_t ntiles = uniform((uint32_t)w.start[p.experts] * (uint32_t)p.ftiles);
 
-    // registers of 6 groups of 4 warps: the CTA starts with 6 x 80 a lane, and 40 + 3 x 64 + 2 x 120 is 472
+    // registers of 7 groups of 4 warps: the CTA starts with 7 x 72 a lane, and so is 40 + 4 x 56 + 2 x 120
     if (warp < 4) {
         if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
@@ -455,6 +518,16 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                     if (issued & (1u << s)) drain(raw_full(s), (issued_par >> s) & 1u);
             __syncwarp();
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else if (SPLIT && warp >= 2) {
+            // the scales, for the end
+            if (first < ntiles) {
+                const WTile t = find_tile(p, w, first);
+                if (warp == 2)
+                    for (int c = lane; c < t.n; c += 32) token_scales[c] = t.t0 + c < t.hi ? p.xs[t.t0 + c] : 0.0f;
+                else
+                    for (int c = lane; c < W_F; c += 32)
+                        token_scales[W_T + c] = p.ws[(int64_t)t.e * p.N + min(t.f0 + (int)half * W_F + c, p.N - 1)];
+            }
         } else if (warp == 1) {
             // --------------------------- MMA issuer (even CTA) --------------------------
             if (half == 0) {
@@ -495,66 +568,70 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
                 __syncwarp();
             }
         }
-    } else if (warp < (SPLIT ? 20 : 16)) {
-        // -------------------------- expansion, a row per lane -----------------------
-        if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        const bool weights = warp < (SPLIT ? 16 : 8);
-        const int member = warp - (weights ? 4 : SPLIT ? 16 : 8), size = weights ? 4 : token_warps;
-        const int q = member % size, groups = weights ? (SPLIT ? 3 : 1) : token_groups;
-        const int r = 32 * q + lane, x = r & 7;
-        int stage = 0, slot = 0, turn = member / size;   // stages until this group's next one
+    } else if (warp < 4 + w_expand(SPLIT)) {
+        // ------------- expansion: a row per lane, some of the stage's four pieces of 32 columns -------------
+        if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const bool weights = warp < 12;
+        const int member = warp - (weights ? 4 : 12), row_warps = weights ? 4 : box_rows / 32;
+        const int q = member % row_warps, r = 32 * q + lane;
+        // (SPLIT: four warps share the tokens' rows and columns)
+        const int pieces = !SPLIT || weights ? 2 : row_warps, first_piece = member / row_warps * pieces;
+        const uint32_t column = tmem + ((uint32_t)(32 * q) << 16) + W_A0 + 16 * first_piece;
+        int stage = 0, slot = 0;
         uint32_t rphase = 0, sphase = 0;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
             const WTile t = find_tile(p, w, i);
-            const bool live = weights || 64 * q < (int)uniform(t.n);
+            const bool live = 64 * q < (int)uniform(t.n);
             for (int k = k0; k < k1; ++k) {
-                if (turn == 0) {
-                    ok = wait_all(raw_full(stage), rphase, limit);
-                    if (!ok) break;
-                    const uint32_t src = rbase + stage * raw_bytes + (weights ? 0 : W_CODES) + r * W_K;
-                    const uint32_t dst = sbase + slot * wide_bytes + r * 128;
+                ok = wait_all(raw_full(stage), rphase, limit);
+                if (!ok) break;
+                const uint32_t src = rbase + stage * raw_bytes + (weights ? 0 : W_CODES) + r * W_K;
+                const uint32_t dst = sbase + slot * wide_bytes + r * 128;
+                auto freed = [&] { return ok = wait_all(wide_free(slot), sphase ^ 1u, limit); };
+                // (only once what depends on the codes has been issued: the copy that follows this arrival has overtaken
+                // loads whose values nothing had asked for yet)
+                auto taken = [&] {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_free(stage));
+                };
+                if (weights) {
+                    uint4 code[4];
+                    load_codes<2>(src, first_piece, r & 7, code);
+                    if (!freed()) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t v[32];
-                        if (live) {
+                        uint32_t v[16];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint4 w = lds128(src + (((4 * h + c) ^ x) << 4));
-                                to_half(w.x, v[8 * c], v[8 * c + 1]);
-                                to_half(w.y, v[8 * c + 2], v[8 * c + 3]);
-                                to_half(w.z, v[8 * c + 4], v[8 * c + 5]);
-                                to_half(w.w, v[8 * c + 6], v[8 * c + 7]);
-                            }
-                        }
-                        if (h == 0) {
-                            ok = wait_all(wide_free(slot), sphase ^ 1u, limit);
-                            if (!ok) break;
-                            if (weights) tc_fence_after();
-                        } else {
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(raw_free(stage));
-                        }
-                        if (weights) {
-                            tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + W_A0 + slot * (W_K / 2) + 32 * h, v);
-                        } else if (live) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                sts128(dst + h * (wide_bytes / 2) + ((c ^ x) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-                        }
+                        for (int c = 0; c < 2; ++c) to_half8(code[2 * h + c], &v[8 * c]);
+                        tmem_st_32x32b_x16(column + slot * (W_K / 2) + 16 * h, v);
                     }
-                    if (!ok) break;
-                    if (weights) {
-                        tmem_st_wait();
-                        tc_fence_before();
+                    taken();
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else {
+                    if (SPLIT && pieces == 1) {
+                        uint4 code[2];
+                        if (live) load_codes<1>(src, first_piece, r & 7, code);
+                        if (!freed()) break;
+                        if (live) store_wide<1>(dst, wide_bytes / 2, first_piece, r & 7, code);
+                        taken();
                     } else {
-                        fence_proxy_async_smem();
+                        for (int h = 0; h < (SPLIT ? pieces : 2); h += 2) {
+                            uint4 code[4];
+                            if (live) load_codes<2>(src, first_piece + h, r & 7, code);
+                            if (h == 0 && !freed()) break;
+                            if (live) store_wide<2>(dst, wide_bytes / 2, first_piece + h, r & 7, code);
+                            if (h + 2 >= pieces) taken();
+                        }
+                        if (!ok) break;
                     }
-                    __syncwarp();
-                    // (arrive_cluster's CTA scope: each SM's tensor core reads what its own CTA wrote, which the fence
-                    // above has put before the arrival; .release.cluster held a warp up for 900 to 1500 cycles a stage)
-                    if (lane == 0) arrive_cluster(in_cta(wide_full(slot), even));
+                    fence_proxy_async_smem();
                 }
-                turn = turn == 0 ? groups - 1 : turn - 1;
+                __syncwarp();
+                // (arrive_cluster's CTA scope: each SM's tensor core reads what its own CTA wrote, which the fence
+                // above has put before the arrival; .release.cluster held a warp up for 900 to 1500 cycles a stage)
+                if (lane == 0) arrive_cluster(in_cta(wide_full(slot), even));
                 if (++stage == raws) {
                     stage = 0;
                     rphase ^= 1u;
@@ -586,10 +663,10 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
         // ------------------------------- epilogue -----------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int q = warp & 3;
-        const int c0 = W_T / 2 * ((warp - 16) >> 2);   // its half of the columns
+        const int c0 = W_T / 2 * ((warp - 20) >> 2);   // its half of the columns
         const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + c0;
-        const uint32_t turn = sbase + W_RING + (warp - 16) * W_TURN;
-        float* sx = token_scales + (warp - 16) * (W_T / 2);   // the scales of its tokens
+        const uint32_t turn = sbase + W_RING + (warp - 20) * W_TURN;
+        float* sx = token_scales + (warp - 20) * (W_T / 2);   // the scales of its tokens
         const bool relu = p.relu != 0;
         uint32_t tile = 0;
         for (uint32_t i = first; i < ntiles; i += step, ++tile) {
@@ -673,18 +750,16 @@ __global__ void __launch_bounds__(W_THREADS, 1) int8_matmul_kernel(const __grid_
             const int a = t.n * share / p.splits, b = t.n * (share + 1) / p.splits;   // this pair's tokens
             const int f = t.f0 + (int)half * W_F + 4 * lane;   // four features per lane, a token per warp
             const uint32_t mine = sbase + 16 * lane;
-            float sw[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) sw[g] = p.ws[(int64_t)t.e * p.N + min(f + g, p.N - 1)];
+            const float4 sw = *reinterpret_cast<const float4*>(token_scales + W_T + 4 * lane);
 #pragma unroll 2
-            for (int c = a + warp; c < min(b, t.hi - t.t0); c += W_THREADS / 32) {
-                const float sx = p.xs[t.t0 + c];
+            for (int c = a + warp; c < min(b, t.hi - t.t0); c += w_threads(true) / 32) {
+                const float sx = token_scales[c];
                 float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int j = 0; j < p.splits; ++j) {
                     const float4 u = ld_cluster(in_cta(mine + 4 * c * W_F, 2 * j + half));
                     s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
                 }
-                float v[4] = {scaled(s.x, sw[0], sx), scaled(s.y, sw[1], sx), scaled(s.z, sw[2], sx), scaled(s.w, sw[3], sx)};
+                float v[4] = {scaled(s.x, sw.x, sx), scaled(s.y, sw.y, sx), scaled(s.z, sw.z, sx), scaled(s.w, sw.w, sx)};
                 if (p.vec) {
                     if (f >= p.N) continue;
                     if (p.relu) {
@@ -731,7 +806,7 @@ cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunc
     static_assert(W_T * W_F * 4 <= W_RING, "a split tile's sums take the place of the stages");
     *cfg = {};
     cfg->gridDim = dim3(ctas);
-    cfg->blockDim = dim3(W_THREADS);
+    cfg->blockDim = dim3(w_threads(SPLIT));
     cfg->dynamicSmemBytes = kFixed + 12 * p.experts + 4;
     cfg->stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -783,7 +858,21 @@ int launch_pairs(const WMaps& m, const IParams& p, int64_t most_tiles, cudaStrea
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int64_t kMaxDim = (1ll << 31) - 512;
 
-bool few_rows_pay(int64_t T, int64_t N, int64_t K, int64_t experts) { return T <= 8 * experts; }
+// Whether the kernel for few rows is the faster one. Measured (us, few rows / pairs; weights from memory, features x
+// columns):
+//                   1 token     16 tokens    32 tokens    64 tokens
+//    4096 x 4096    6.3 / 11.0   6.9 / 11.3   9.0 / 11.4  15.2 / 12.3
+//   14336 x 4096   14.1 / 21.7  18.7 / 21.7  25.5 / 21.9  43.5 / 22.6
+//    4096 x 14336  15.0 / 23.8  17.6 / 24.1  25.1 / 24.1  44.6 / 25.2
+//    1024 x 4096    4.7 /  8.1   5.5 /  8.2   7.7 /  8.3  13.1 /  9.1
+//    4096 x 1024                                          7.0 /  8.3 (96 tokens 9.4 / 9.0)
+//     512 x 512                                           4.2 /  6.5
+//   experts, rows at random: 16 of 1024 x 4096, 32 rows 16.6 / 22.7, 64 rows 18.5 / 22.9, 128 rows 21 / 23.0, 256 rows
+//   27 / 23.0; 8 of 14336 x 4096, 16 rows 80 / 106, 64 rows 115 / 108
+bool few_rows_pay(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts) {
+    if (by_expert) return T <= 4 * experts;
+    return T <= 16 || (T <= 32 && N * K <= 24000000) || (T <= 64 && K <= 1024 && N * K <= 5000000);
+}
 
 }  // namespace
 }  // namespace gptq
@@ -824,10 +913,15 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
     p.ftiles = (int)ceil_div(N, W_PF);
     p.tokens_first = experts * N > T ? 1 : 0;   // the larger operand is walked through once
     p.vec = p.bf16_out && N % 8 == 0 && ldy % 8 == 0 && aligned16(Y) ? 1 : 0;
-    if (K == 0 || few_rows_pay(T, N, K, experts)) {
+    if (K == 0 || few_rows_pay(T, N, K, offsets != nullptr, experts)) {
         cudaError_t e = cudaSuccess;
         const dim3 grid((unsigned)ceil_div(N, F_FEATURES), (unsigned)(experts + (offsets ? 1 : 0)));
-        GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(int8_few_rows_kernel, grid, dim3(F_THREADS), 0, s, p));
+        auto go = [&](auto kern) { GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(kern, grid, dim3(32 * F_WARPS), 0, s, p)); };
+        // (with experts the rows of each are not known here: mostly a share of them)
+        const int64_t rows = offsets ? T / experts : T;
+        if (rows <= 8) go(int8_few_rows_kernel<1>);
+        else if (rows <= 16) go(int8_few_rows_kernel<2>);
+        else go(int8_few_rows_kernel<4>);
         GPTQ_CUDA_TRY(e);
         return st.finish(s);
     }

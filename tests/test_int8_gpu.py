@@ -322,6 +322,24 @@ def test_product_of_far_scales(lib, T):
     assert torch.isnan(y[-1]).all() and torch.isfinite(y[:-1]).all()
 
 
+@pytest.mark.parametrize("T,N,K", [(40, 256, 8192), (64, 256, 4096), (100, 300, 6000), (200, 512, 4096), (300, 2048, 4096), (2048, 2048, 2048)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_product_is_the_same_every_time(lib, T, N, K, dt):
+    """stages in flight, with other work's traffic between the calls"""
+    xc, xs, wc, ws = _operands(np.random.default_rng(T), T, N, K)
+    X, W = _stored(lib, xc, xs), _stored(lib, wc, ws)
+    y = lib.gptq_int8_matmul(X, W, out_dtype=DT[dt])
+    if T <= 300:
+        _check(y, I.matmul(xc, xs, wc, ws), dt)
+    noise = torch.empty(1 << 26, device=DEV)
+    with lib.deferred_status():
+        for i in range(300):
+            if i % 3 == 0:
+                noise.add_(1)
+            assert torch.equal(lib.gptq_int8_matmul(X, W, out_dtype=DT[dt]), y)
+        lib.status_sync()
+
+
 @pytest.mark.parametrize("T,N", [(1, 3), (3, 50), (40, 300), (300, 300)])
 def test_product_over_no_columns_or_of_nothing(lib, T, N):
     none = lambda r: lib.Int8(torch.empty(r, 0, dtype=torch.int8, device=DEV), torch.ones(r, device=DEV), 0)   # noqa: E731
