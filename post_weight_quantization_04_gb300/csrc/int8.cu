@@ -19,9 +19,9 @@ namespace gptq {
 namespace {
 
 // --------------------------------------------------------------------- sums over a row's threads
-// A row has blockDim.x threads (whole warps); a CTA has blockDim.y rows, more than one only where a
-// warp takes a whole row. The sum is the same in all its threads. `part` [32]: one slot per warp,
-// another one each time it is used between two barriers.
+// A row has blockDim.x threads (whole warps); a CTA has blockDim.y rows at a time, more than one only where a
+// warp takes a whole row. The sum is the same in all its threads. `part` [32]: one slot per warp, not the
+// ones of the sum before.
 template <typename V, typename Op>
 __device__ __forceinline__ V row_reduce(V v, V* part, Op op) {
 #pragma unroll
@@ -46,22 +46,160 @@ struct Max {
     __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
 };
 
-// the gain of N columns (16-byte aligned where N is 4 or 8)
-template <int N>
-__device__ __forceinline__ void load_gain(const float* p, float (&g)[N]) {
-    if constexpr (N < 4) {
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// ------------------------------------------------------------------------------------ units of a row
+// A thread works on units of N = 16 / sizeof(T) neighbouring columns, unit j being columns N j .. N j + N - 1
+// whatever the row's address. Memory is read and written in aligned 16-byte granules: a row that starts
+// `o` elements into a granule has its unit j in granules j and j + 1, and the second one is the next lane's
+// first (the last lane of a warp loads it itself). Granules that are not the row's alone, at its ends, are read
+// and written element by element. All lanes of a warp take part. ANY = false: rows of whole granules.
+template <typename T>
+constexpr int kUnit = 16 / sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ int row_start(const T* row) {   // elements
+    return (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
+}
+
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+
+template <typename T>
+__device__ __forceinline__ uint4 load_granule(const T* row, int64_t cols, int o, int64_t g) {
+    constexpr int N = kUnit<T>;
+    const int64_t c = g * N - o;   // its first column
+    if (c >= 0 && c + N <= cols) return *reinterpret_cast<const uint4*>(row + c);
+    uint32_t w[4] = {};
 #pragma unroll
-        for (int e = 0; e < N; ++e) g[e] = p[e];
-    } else {
+    for (int e = 0; e < N; ++e)
+        if (c + e >= 0 && c + e < cols) w[e * (int)sizeof(T) / 4] |= bits(row[c + e]) << (sizeof(T) == 2 ? 16 * (e & 1) : 0);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// words of (a, b) from `bytes` on (0 .. 15, a multiple of 2)
+__device__ __forceinline__ uint4 from_byte(const uint4& a, const uint4& b, int bytes) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (bytes & 8) {
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p + e);
-            g[e] = v.x, g[e + 1] = v.y, g[e + 2] = v.z, g[e + 3] = v.w;
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (bytes & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Granule j of a row, to be made unit j by to_words
+template <typename T, bool ANY>
+__device__ __forceinline__ uint4 load_raw(const T* row, int64_t cols, int64_t j) {
+    if constexpr (ANY) return load_granule(row, cols, row_start(row), j);
+    return j * kUnit<T> < cols ? *reinterpret_cast<const uint4*>(row + j * kUnit<T>) : make_uint4(0, 0, 0, 0);
+}
+
+// Unit j from the granules that the lanes have loaded, zeros past the columns. (The last lane reads the next warp's first granule
+// here, most likely from L1: before any barrier behind which that warp may write to it.)
+template <typename T, bool ANY>
+__device__ __forceinline__ uint4 to_words(const T* row, int64_t cols, int64_t j, const uint4& a) {
+    if constexpr (ANY) {
+        const int o = row_start(row);
+        if (o != 0) {
+            uint4 n;
+            n.x = __shfl_down_sync(0xffffffffu, a.x, 1), n.y = __shfl_down_sync(0xffffffffu, a.y, 1);
+            n.z = __shfl_down_sync(0xffffffffu, a.z, 1), n.w = __shfl_down_sync(0xffffffffu, a.w, 1);
+            if ((threadIdx.x & 31) == 31) n = load_granule(row, cols, o, j + 1);
+            return from_byte(a, n, o * (int)sizeof(T));
+        }
+    }
+    return a;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& w, float (&v)[kUnit<T>]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+            v[2 * e] = __uint_as_float(u[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        } else {
+            v[e] = __uint_as_float(u[e]);
         }
     }
 }
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&v)[kUnit<T>]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            u[e] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            u[e] = __float_as_uint(v[e]);
+        }
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ void put(float* p, const uint32_t (&w)[4], int e) { *p = __uint_as_float(w[e]); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const uint32_t (&w)[4], int e) {
+    *p = __ushort_as_bfloat16((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+}
+
+template <typename T, bool ANY>
+__device__ __forceinline__ void store_unit_at(T* row, int64_t cols, int64_t j, const float (&v)[kUnit<T>]) {
+    constexpr int N = kUnit<T>;
+    const uint4 p = pack<T>(v);
+    if constexpr (!ANY) {
+        if (j * N < cols) *reinterpret_cast<uint4*>(row + j * N) = p;
+    } else {
+        const int o = row_start(row), lane = threadIdx.x & 31;
+        const uint32_t own[4] = {p.x, p.y, p.z, p.w};
+        const int64_t c = j * N - o;   // the first column of granule j
+        uint4 g = p;
+        if (o != 0) {
+            uint4 q;
+            q.x = __shfl_up_sync(0xffffffffu, p.x, 1), q.y = __shfl_up_sync(0xffffffffu, p.y, 1);
+            q.z = __shfl_up_sync(0xffffffffu, p.z, 1), q.w = __shfl_up_sync(0xffffffffu, p.w, 1);
+            g = from_byte(q, p, 16 - o * (int)sizeof(T));
+        }
+        // (of its first granule lane 0 has only its own elements, and of the one after its last, the last lane)
+        const bool whole = c >= 0 && c + N <= cols && (o == 0 || lane != 0);
+        if (whole) *reinterpret_cast<uint4*>(row + c) = g;
+        if (!whole || (o != 0 && lane == 31)) {
+            const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (!whole && (o == 0 || lane != 0 || e >= o) && c + e >= 0 && c + e < cols) put(row + c + e, w, e);
+                if (o != 0 && lane == 31 && e >= N - o && j * N + e < cols) put(row + j * N + e, own, e);
+            }
+        }
+    }
+}
+
+// the gain of a unit's columns, zeros past them
+template <int N, bool ANY>
+__device__ __forceinline__ void load_gain(const float* gain, int64_t cols, int64_t c, float (&g)[N]) {
+    if (!ANY || ((reinterpret_cast<uintptr_t>(gain) & 15) == 0 && c + N <= cols)) {
+        if (c < cols) {
+#pragma unroll
+            for (int e = 0; e < N; e += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(gain + c + e);
+                g[e] = v.x, g[e + 1] = v.y, g[e + 2] = v.z, g[e + 3] = v.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) g[e] = c + e < cols ? gain[c + e] : 0.0f;
+}
 
 // ------------------------------------------------------------------------------- the quotient
 // code = rint(x / s), exactly as the fp32 quotient rounds: with the divisor's reciprocal correctly
@@ -80,32 +218,33 @@ __device__ __forceinline__ Step step_of(float s) {
     t.inv = s > 0.0f ? 1.0f / t.d : 0.0f;   // (a NaN scale has codes of zero)
     return t;
 }
-__device__ __forceinline__ uint32_t code_of(float x, const Step& t) {
+__device__ __forceinline__ uint32_t code_of(float x, const Step& t) {   // in the low byte
     if (!t.usual) x *= t.f;
     float q = x * t.inv;
     q = fmaf(fmaf(-q, t.d, x), t.inv, q);
     // (a subnormal scale is rounded, up to half of it, so a quotient may be past 127)
     if (!t.usual) q = t.inv > 0.0f ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
-    return __float_as_uint(q + 12582912.0f) & 0xFFu;
+    return __float_as_uint(q + 12582912.0f);
 }
 
 template <int N>
 __device__ __forceinline__ void store_codes(int8_t* y, const float (&v)[N], const Step& t) {
-    uint32_t u[N];
+    uint32_t u[N], w[N / 4];
+    if (t.usual) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) u[e] = code_of(v[e], t);
-    if constexpr (N == 1) {
-        *y = (int8_t)u[0];
-    } else if constexpr (N == 2) {
-        *reinterpret_cast<uint16_t*>(y) = (uint16_t)(u[0] | u[1] << 8);
+        for (int e = 0; e < N; ++e) {
+            const float q = v[e] * t.inv;
+            u[e] = __float_as_uint(fmaf(fmaf(-q, t.d, v[e]), t.inv, q) + 12582912.0f);
+        }
     } else {
-        uint32_t w[N / 4];
 #pragma unroll
-        for (int e = 0; e < N / 4; ++e)
-            w[e] = __byte_perm(__byte_perm(u[4 * e], u[4 * e + 1], 0x0040), __byte_perm(u[4 * e + 2], u[4 * e + 3], 0x0040), 0x5410);
-        if constexpr (N == 4) *reinterpret_cast<uint32_t*>(y) = w[0];
-        else *reinterpret_cast<uint2*>(y) = make_uint2(w[0], w[1]);
+        for (int e = 0; e < N; ++e) u[e] = code_of(v[e], t);
     }
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e)
+        w[e] = __byte_perm(__byte_perm(u[4 * e], u[4 * e + 1], 0x0040), __byte_perm(u[4 * e + 2], u[4 * e + 3], 0x0040), 0x5410);
+    if constexpr (N == 4) *reinterpret_cast<uint32_t*>(y) = w[0];
+    else *reinterpret_cast<uint2*>(y) = make_uint2(w[0], w[1]);
 }
 
 // ----------------------------------------------------------------------------------- the rows
@@ -137,99 +276,107 @@ __device__ __forceinline__ float rstd_of(float sum, float n, float eps, F again)
     return rsqrtf(again(f) / n + eps * f * f) * f;
 }
 
-// One row in the registers of its threads, UNITS units of N columns each. The row is read once and
-// everything written once.
-template <typename T, int N, int UNITS, bool NORM>
+// the row of X that row r is, or -1
+__device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
+    if (!p.index) return r;
+    const int k = p.index[r];
+    const int64_t sr = k < 0 ? -1 : k / p.per;
+    if (sr < p.src_rows) return sr;
+    set_status(p.status, GPTQ_ERR_INVALID_ARG);
+    return -1;
+}
+
+// Rows in the registers of their threads, UNITS units each: a row is read once and everything written once. CTAs
+// are persistent, and the next row's loads are under way (AHEAD) while this one is reduced and written.
+template <typename T, int UNITS, bool NORM, bool ANY>
 __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
-    __shared__ float sum_part[32];
-    __shared__ uint32_t max_part[32];
-    const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    constexpr int N = kUnit<T>;
+    constexpr bool AHEAD = UNITS <= 2;
+    __shared__ float sum_part[2][32];
+    __shared__ uint32_t max_part[2][32];
     pdl_trigger();   // the product's prologue may begin
     pdl_wait();
-    if (r >= p.rows) return;   // (a whole warp, of a CTA without barriers)
-    int64_t sr = r;
-    if (!NORM && p.index) {
-        const int k = p.index[r];
-        sr = k < 0 ? -1 : k / p.per;
-        if (sr >= p.src_rows) {
-            sr = -1;
-            set_status(p.status, GPTQ_ERR_INVALID_ARG);
+    const int64_t j0 = threadIdx.x, units = blockDim.x;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    uint4 x[UNITS], res[UNITS];
+    const T *row = nullptr, *rrow = nullptr;
+    int64_t n = 0;
+    auto load = [&](int64_t r) {
+        const int64_t sr = NORM ? r : source_row(p, r);
+        n = sr < 0 ? 0 : p.cols;
+        row = static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx);
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) x[i] = load_raw<T, ANY>(row, n, j0 + i * units);
+        if (NORM && p.R) {
+            rrow = static_cast<const T*>(p.R) + r * p.ldr;
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) res[i] = load_raw<T, ANY>(rrow, n, j0 + i * units);
         }
-    }
-    float v[UNITS][N];
-    const T* x = static_cast<const T*>(p.X) + max(sr, (int64_t)0) * p.ldx;
-    const int64_t n = sr < 0 ? 0 : p.cols;
-    int64_t c = (int64_t)threadIdx.x * N;
-    const int64_t step = (int64_t)blockDim.x * N;
+    };
+    int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (AHEAD && r < p.rows) load(r);
+    int turn = 0;
+    for (; r < p.rows; r += step, turn ^= 1) {
+        if (!AHEAD) load(r);
+        float v[UNITS][N];
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        if (c + i * step < n) {
-            load_unit<T, N>(x + c + i * step, v[i]);
-        } else {
+        for (int i = 0; i < UNITS; ++i) {
+            unpack<T>(to_words<T, ANY>(row, n, j0 + i * units, x[i]), v[i]);
+            if (NORM && p.R) {
+                float w[N];
+                unpack<T>(to_words<T, ANY>(rrow, n, j0 + i * units, res[i]), w);
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[i][e] = 0.0f;
-        }
-    }
-    if constexpr (NORM) {
-        if (p.R) {
-            const T* res = static_cast<const T*>(p.R) + r * p.ldr;
-            T* h = static_cast<T*>(p.H) + r * p.ldh;
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                if (c + i * step < n) {
-                    float w[N];
-                    load_unit<T, N>(res + c + i * step, w);
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        v[i][e] += w[e];
-                        if constexpr (sizeof(T) == 2) v[i][e] = __bfloat162float(__float2bfloat16_rn(v[i][e]));
-                    }
-                    store_unit<T, N>(h + c + i * step, v[i]);
-                }
+                for (int e = 0; e < N; ++e) v[i][e] += w[e];
+                if constexpr (sizeof(T) == 2) unpack<T>(pack<T>(v[i]), v[i]);   // h as it is stored
             }
         }
-        auto squares = [&](float f) {
-            float s = 0.0f;
+        if (AHEAD && r + step < p.rows) load(r + step);
+        if constexpr (NORM) {
+            auto squares = [&](float f) {
+                float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i)
+                for (int i = 0; i < UNITS; ++i)
 #pragma unroll
-                for (int e = 0; e < N; ++e) s = fmaf(v[i][e] * f, v[i][e] * f, s);
-            return s;
-        };
-        const float sum = row_reduce(squares(1.0f), sum_part, Add());
-        const float rstd = rstd_of(sum, (float)p.cols, p.eps, [&](float f) {
-            if (blockDim.x > 32) __syncthreads();
-            return row_reduce(squares(f), sum_part, Add());
-        });
-        if (threadIdx.x == 0) p.rstd[r] = rstd;
+                    for (int e = 0; e < N; ++e) s = fmaf(v[i][e] * f, v[i][e] * f, s);
+                return s;
+            };
+            const float sum = row_reduce(squares(1.0f), sum_part[turn], Add());
+            const float rstd = rstd_of(sum, (float)p.cols, p.eps, [&](float f) {
+                if (blockDim.x > 32) __syncthreads();
+                return row_reduce(squares(f), sum_part[turn], Add());
+            });
+            if (threadIdx.x == 0) p.rstd[r] = rstd;
+            if (p.R) {   // (H may be X or R: all of the row's threads have read it by now)
+                T* h = static_cast<T*>(p.H) + r * p.ldh;
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i)
-            if (c + i * step < n) {
+                for (int i = 0; i < UNITS; ++i) store_unit_at<T, ANY>(h, p.cols, j0 + i * units, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
                 float g[N];
-                load_gain<N>(p.gain + c + i * step, g);
+                load_gain<N, ANY>(p.gain, p.cols, (j0 + i * units) * N, g);
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * rstd * g[e];
             }
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) m = max(m, magnitude(v[i][e]));
+        m = row_reduce(m, max_part[turn], Max());
+        const bool bad = m >= 0x7F800000u;
+        const float s = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.0f;
+        if (threadIdx.x == 0) {
+            p.scales[r] = s;
+            if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
+        }
+        const Step t = step_of(s);
+        int8_t* y = p.codes + r * p.pitch;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+            if ((j0 + i * units) * N < p.pitch) store_codes<N>(y + (j0 + i * units) * N, v[i], t);
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i)
-#pragma unroll
-        for (int e = 0; e < N; ++e) m = max(m, magnitude(v[i][e]));
-    m = row_reduce(m, max_part, Max());
-    const bool bad = m >= 0x7F800000u;
-    const float s = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.0f;
-    if (threadIdx.x == 0) {
-        p.scales[r] = s;
-        if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
-    }
-    const Step t = step_of(s);
-    int8_t* y = p.codes + r * p.pitch;
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i)
-        if (c + i * step < p.cols) store_codes<N>(y + c + i * step, v[i], t);
-    const int64_t pad = p.cols + threadIdx.x;
-    if (pad < p.pitch) y[pad] = 0;
 }
 
 // The same for rows of any length: passes over the row, of which all but the first find it in L2. (The norm's
@@ -239,16 +386,7 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
     __shared__ float sum_part[32];
     __shared__ uint32_t max_part[32];
     pdl_wait();
-    const int64_t r = blockIdx.x;
-    int64_t sr = r;
-    if (!NORM && p.index) {
-        const int k = p.index[r];
-        sr = k < 0 ? -1 : k / p.per;
-        if (sr >= p.src_rows) {
-            sr = -1;
-            set_status(p.status, GPTQ_ERR_INVALID_ARG);
-        }
-    }
+    const int64_t r = blockIdx.x, sr = NORM ? r : source_row(p, r);
     const T* x = static_cast<const T*>(p.X) + max(sr, (int64_t)0) * p.ldx;
     const int64_t n = sr < 0 ? 0 : p.cols;
     float rstd = 1.0f;
@@ -303,7 +441,7 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
     for (int64_t c = threadIdx.x; c < p.pitch; c += blockDim.x) {
         float a[1] = {0.0f};
         if (c < n) value(c, a);
-        store_codes<1>(y + c, a, t);
+        y[c] = (int8_t)code_of(a[0], t);
     }
 }
 
@@ -317,25 +455,26 @@ struct BackParams {
 };
 constexpr int B_THREADS = 128, B_ROWS = 4;   // rows in flight per thread
 
-template <typename T, int N>
+template <typename T, bool ANY>
 __global__ void __launch_bounds__(B_THREADS) int8_dequantize_kernel(const BackParams p) {
-    const int64_t c = ((int64_t)blockIdx.x * B_THREADS + threadIdx.x) * N;
-    if (c >= p.cols) return;
+    constexpr int N = kUnit<T>;
+    const int64_t j = (int64_t)blockIdx.x * B_THREADS + threadIdx.x;
+    if ((j & ~(int64_t)31) * N >= p.cols) return;   // (whole warps)
+    pdl_trigger();
     pdl_wait();
+    const int64_t at = min(j * N, p.pitch - N);   // (lanes past the row: any)
     for (int64_t r0 = (int64_t)blockIdx.y * B_ROWS; r0 < p.rows; r0 += (int64_t)gridDim.y * B_ROWS) {
-        uint32_t w[B_ROWS][N <= 4 ? 1 : 2];
+        uint32_t w[B_ROWS][N / 4];
         float s[B_ROWS];
 #pragma unroll
         for (int i = 0; i < B_ROWS; ++i) {
             const int64_t r = min(r0 + i, p.rows - 1);
-            const int8_t* src = p.codes + r * p.pitch + c;
+            const int8_t* src = p.codes + r * p.pitch + at;
             if constexpr (N == 8) {
                 const uint2 u = *reinterpret_cast<const uint2*>(src);
                 w[i][0] = u.x, w[i][1] = u.y;
-            } else if constexpr (N == 4) {
-                w[i][0] = *reinterpret_cast<const uint32_t*>(src);
             } else {
-                w[i][0] = *reinterpret_cast<const uint8_t*>(src);
+                w[i][0] = *reinterpret_cast<const uint32_t*>(src);
             }
             s[i] = p.scales[r];
         }
@@ -345,7 +484,7 @@ __global__ void __launch_bounds__(B_THREADS) int8_dequantize_kernel(const BackPa
             float v[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] = (float)(int8_t)(w[i][e >> 2] >> (8 * (e & 3))) * s[i];
-            store_unit<T, N>(static_cast<T*>(p.Y) + (r0 + i) * p.ldy + c, v);
+            store_unit_at<T, ANY>(static_cast<T*>(p.Y) + (r0 + i) * p.ldy, p.cols, j, v);
         }
     }
 }
@@ -361,54 +500,109 @@ struct GradParams {
     int64_t per;               // rows per CTA
 };
 
-// A CTA takes a contiguous share of the rows, a thread the same UNITS units of N columns of each: dgain's
-// sums over the rows stay in its registers. Rows are read once.
-template <typename T, int N, int UNITS>
-__global__ void __launch_bounds__(1024) int8_norm_grad_kernel(const GradParams p) {
+// the sum over the warps of one of a CTA's groups of threads, which has `warps` of them and a barrier of its own
+__device__ __forceinline__ float group_sum(float v, float* part, int warps, int barrier) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;   // (threadIdx.x is the thread's number within its group)
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * warps) : "memory");
+    v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A CTA takes a contiguous share of the rows, each of its blockDim.y groups of threads every so many of them, and a thread
+// the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added in turn at the
+// end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written.
+template <typename T, int UNITS, bool ANY>
+__global__ void __launch_bounds__(UNITS == 1 ? 512 : 1024, UNITS == 1 ? 2 : 1) int8_norm_grad_kernel(const GradParams p) {
+    constexpr int N = kUnit<T>;
+    constexpr bool AHEAD = UNITS == 1;
+    extern __shared__ float sums[];   // [columns of the units], where there are several groups
     __shared__ float part[2][32];
+    pdl_trigger();
     pdl_wait();
     const int64_t first = (int64_t)blockIdx.x * p.per, last = min(first + p.per, p.rows);
-    const int64_t c = (int64_t)threadIdx.x * N, step = (int64_t)blockDim.x * N;
-    float acc[UNITS][N] = {};
+    const int64_t j0 = threadIdx.x, units = blockDim.x, step = blockDim.y;
+    const int warps = blockDim.x >> 5, group = threadIdx.y;
     const float inv_n = 1.0f / (float)p.cols;
-    for (int64_t r = first; r < last; ++r) {
-        const T* dy = static_cast<const T*>(p.dY) + r * p.lddy + c;
-        const T* h = static_cast<const T*>(p.H) + r * p.ldh + c;
-        const float rstd = p.rstd[r];
-        float u[UNITS][N], v[UNITS][N], dot = 0.0f;
+    float acc[UNITS][N] = {};
+    uint4 dy[UNITS], h[UNITS], dh[UNITS];
+    const T *ry = nullptr, *rh = nullptr, *rd = nullptr;
+    float rstd = 0.0f;
+    auto load = [&](int64_t r) {
+        ry = static_cast<const T*>(p.dY) + r * p.lddy;
+        rh = static_cast<const T*>(p.H) + r * p.ldh;
+        rd = static_cast<const T*>(p.dH) + r * p.lddh;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            if (c + i * step < p.cols) {
-                load_unit<T, N>(h + i * step, u[i]);
-                load_unit<T, N>(dy + i * step, v[i]);
-                float g[N];
-                load_gain<N>(p.gain + c + i * step, g);
+            dy[i] = load_raw<T, ANY>(ry, p.cols, j0 + i * units);
+            h[i] = load_raw<T, ANY>(rh, p.cols, j0 + i * units);
+            if (p.dH) dh[i] = load_raw<T, ANY>(rd, p.cols, j0 + i * units);
+        }
+        rstd = p.rstd[r];
+    };
+    int64_t r = first + group;
+    if (AHEAD && r < last) load(r);
+    int turn = 0;
+    for (; r < last; r += step, turn ^= 1) {
+        if (!AHEAD) load(r);
+        // what is needed behind the barrier stays as the words it was read as: dX may be written over any input
+        uint4 yw[UNITS], hw[UNITS], dw[UNITS];
+        const float rs = rstd;
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    u[i][e] *= rstd;
-                    acc[i][e] = fmaf(v[i][e], u[i][e], acc[i][e]);
-                    v[i][e] *= g[e];
-                    dot = fmaf(u[i][e], v[i][e], dot);
-                }
+        for (int i = 0; i < UNITS; ++i) {
+            yw[i] = to_words<T, ANY>(ry, p.cols, j0 + i * units, dy[i]);
+            hw[i] = to_words<T, ANY>(rh, p.cols, j0 + i * units, h[i]);
+            if (p.dH) dw[i] = to_words<T, ANY>(rd, p.cols, j0 + i * units, dh[i]);
+        }
+        if (AHEAD && r + step < last) load(r + step);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            float g[N], u[N], v[N];
+            load_gain<N, ANY>(p.gain, p.cols, (j0 + i * units) * N, g);
+            unpack<T>(hw[i], u);
+            unpack<T>(yw[i], v);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                u[e] *= rs;
+                acc[i][e] = fmaf(v[e], u[e], acc[i][e]);
+                dot = fmaf(u[e], v[e] * g[e], dot);
             }
         }
-        dot = row_reduce(dot, part[(r - first) & 1], Add()) * inv_n;
+        dot = group_sum(dot, part[turn] + group * warps, warps, 1 + group) * inv_n;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            if (c + i * step < p.cols) {
-                float d[N];
-                if (p.dH) load_unit<T, N>(static_cast<const T*>(p.dH) + r * p.lddh + c + i * step, d);
+            float g[N], u[N], v[N], d[N] = {};
+            load_gain<N, ANY>(p.gain, p.cols, (j0 + i * units) * N, g);
+            unpack<T>(hw[i], u);
+            unpack<T>(yw[i], v);
+            if (p.dH) unpack<T>(dw[i], d);
 #pragma unroll
-                for (int e = 0; e < N; ++e) d[e] = fmaf(rstd, v[i][e] - u[i][e] * dot, p.dH ? d[e] : 0.0f);
-                store_unit<T, N>(static_cast<T*>(p.dX) + r * p.lddx + c + i * step, d);
-            }
+            for (int e = 0; e < N; ++e) d[e] = fmaf(rs, v[e] * g[e] - u[e] * rs * dot, d[e]);
+            store_unit_at<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, p.cols, j0 + i * units, d);
         }
     }
+    float* out = p.part + blockIdx.x * p.cols;
+    for (int g = 0; g < (int)blockDim.y; ++g) {
+        if (group == g) {
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i)
+            for (int i = 0; i < UNITS; ++i)
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (c + i * step < p.cols) p.part[blockIdx.x * p.cols + c + i * step + e] = acc[i][e];
+                for (int e = 0; e < N; ++e) {
+                    const int64_t c = (j0 + i * units) * N + e;
+                    if (c >= p.cols) continue;
+                    const float s = g > 0 ? sums[c] + acc[i][e] : acc[i][e];
+                    if (g == (int)blockDim.y - 1) out[c] = s;
+                    else sums[c] = s;
+                }
+        }
+        if (blockDim.y > 1) __syncthreads();
+    }
 }
 
 // Rows of any length: the row's mean is taken in one pass over it, and its gradient in a second one, which finds
@@ -471,51 +665,47 @@ struct Rows {
     const void* p;
     int64_t ld;
 };
-// bytes of the units that all these rows of `cols` elements can move in
-int unit_of(int64_t es, int64_t cols, std::initializer_list<Rows> rows) {
+// whether all these rows of `cols` elements are whole aligned granules of 16 bytes
+bool whole_granules(int64_t es, int64_t cols, std::initializer_list<Rows> rows) {
     uint64_t all = (uint64_t)(cols * es);
     for (const Rows& r : rows)
         if (r.p) all |= reinterpret_cast<uintptr_t>(r.p) | (uint64_t)(r.ld * es);
-    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)es;
+    return all % 16 == 0;
 }
 
 template <int V>
 using Const = std::integral_constant<int, V>;
 
-// Calls f(T(), columns per unit, units per thread); a thread takes the units that the row's threads need it
-// to. False: the row does not fit into the registers of a CTA.
-template <typename F>
-bool with_units(int dtype, int unit_bytes, int64_t cols, unsigned* threads, F f) {
-    const int n = unit_bytes / (dtype == GPTQ_BF16 ? 2 : 4);
-    const int64_t units = cols / n;
-    auto go = [&](auto t, auto n, auto wide, auto most) {
-        // `wide` units per thread while a row has few of them, `most` for the longest rows
-        const int per = ceil_div(units, decltype(wide)::value) <= 512 ? decltype(wide)::value : decltype(most)::value;
-        const int64_t need = ceil_div(ceil_div(units, per), 32) * 32;
-        if (need > 1024) return false;
-        *threads = (unsigned)std::max<int64_t>(need, 32);
-        if (per == decltype(wide)::value) f(t, n, wide);
-        else f(t, n, most);
+// Calls f(T(), units per thread, whether rows start anywhere) after setting the threads that a row of `units` units takes: FEW units
+// per thread while they need no more than `most` threads, MANY up to 1024. False: the row does not fit into a CTA's registers.
+template <typename T, int FEW, int MANY, typename F>
+bool with_units(bool any, int64_t units, int most, unsigned* threads, F f) {
+    auto go = [&](auto u) {
+        const int64_t n = ceil_div(ceil_div(units, decltype(u)::value), 32) * 32;
+        *threads = (unsigned)std::max<int64_t>(n, 32);
+        any ? f(T(), u, Const<1>()) : f(T(), u, Const<0>());
         return true;
     };
-    if (dtype == GPTQ_BF16) {
-        if (unit_bytes == 16) return go(__nv_bfloat16(), Const<8>(), Const<2>(), Const<4>());
-        if (unit_bytes == 4) return go(__nv_bfloat16(), Const<2>(), Const<4>(), Const<16>());
-        return go(__nv_bfloat16(), Const<1>(), Const<8>(), Const<16>());
-    }
-    if (unit_bytes == 16) return go(float(), Const<4>(), Const<2>(), Const<8>());
-    return go(float(), Const<1>(), Const<8>(), Const<16>());
+    if (units <= FEW * most) return go(Const<FEW>());
+    if (units <= MANY * 1024) return go(Const<MANY>());
+    return false;
 }
 
 template <bool NORM>
-int launch_rows(const RowParams& p, int dtype, int unit_bytes, int id, cudaStream_t s) {
+int launch_rows(const RowParams& p, int dtype, bool any, int id, cudaStream_t s) {
     unsigned threads = 0;
     cudaError_t e = cudaSuccess;
-    const bool fits = with_units(dtype, unit_bytes, p.cols, &threads, [&](auto t, auto n, auto u) {
-        auto kern = int8_rows_kernel<decltype(t), decltype(n)::value, decltype(u)::value, NORM>;
-        const unsigned rows = threads == 32 ? 4 : 1;
-        GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3((unsigned)ceil_div(p.rows, rows)), dim3(threads, rows), 0, s, p));
-    });
+    const int64_t units = p.pitch / (dtype == GPTQ_BF16 ? 8 : 4);
+    auto go = [&](auto t, auto u, auto a) {
+        auto kern = int8_rows_kernel<decltype(t), decltype(u)::value, NORM, decltype(a)::value != 0>;
+        // a warp takes a whole row where it can; about 1024 threads per SM
+        const unsigned rows = threads == 32 ? 8 : 1;
+        const int64_t most = (int64_t)device_sm_count() * std::max(1u, 1024 / (threads * rows));
+        const unsigned ctas = (unsigned)std::min<int64_t>(ceil_div(p.rows, rows), most);
+        GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, rows), 0, s, p));
+    };
+    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2, 4>(any, units, 1024, &threads, go)
+                                         : with_units<float, 2, 4>(any, units, 1024, &threads, go);
     if (!fits) {
         auto kern = dtype == GPTQ_BF16 ? int8_long_rows_kernel<__nv_bfloat16, NORM> : int8_long_rows_kernel<float, NORM>;
         GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3((unsigned)p.rows), dim3(1024), 0, s, p));
@@ -557,7 +747,7 @@ extern "C" int gptq_int8_quantize(const void* X, int dtype, int64_t src_rows, in
     p.pitch = int8_pitch(cols);
     p.scales = scales;
     p.status = st.word;
-    const int rc = launch_rows<false>(p, dtype, unit_of(dtype == GPTQ_BF16 ? 2 : 4, cols, {{X, ldx}}), K_INT8_QUANT, s);
+    const int rc = launch_rows<false>(p, dtype, !whole_granules(dtype == GPTQ_BF16 ? 2 : 4, cols, {{X, ldx}}), K_INT8_QUANT, s);
     return rc != GPTQ_OK ? rc : st.finish(s);
 }
 
@@ -589,8 +779,9 @@ extern "C" int gptq_int8_rms_norm(const void* X, int64_t ldx, const void* residu
     p.ldh = ldh;
     p.rstd = rstd;
     p.status = st.word;
-    const int unit = unit_of(dtype == GPTQ_BF16 ? 2 : 4, cols, {{X, ldx}, {residual, ldr}, {residual ? H : nullptr, ldh}, {gain, 0}});
-    const int rc = launch_rows<true>(p, dtype, unit, K_INT8_NORM, s);
+    const bool any =
+        !whole_granules(dtype == GPTQ_BF16 ? 2 : 4, cols, {{X, ldx}, {residual, ldr}, {residual ? H : nullptr, ldh}, {gain, 0}});
+    const int rc = launch_rows<true>(p, dtype, any, K_INT8_NORM, s);
     return rc != GPTQ_OK ? rc : st.finish(s);
 }
 
@@ -611,16 +802,23 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
     if (!dY || !H || !gain || !rstd || !dX || lddy < cols || ldh < cols || lddx < cols || (dH && lddh < cols)) return GPTQ_ERR_INVALID_ARG;
     if (!ws || ws_bytes < gptq_int8_rms_norm_grad_workspace_bytes(rows, cols)) return GPTQ_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(ws) % 4 != 0) return GPTQ_ERR_INVALID_ARG;
-    const int unit = unit_of(dtype == GPTQ_BF16 ? 2 : 4, cols, {{dY, lddy}, {H, ldh}, {dH, lddh}, {dX, lddx}, {gain, 0}});
+    const int64_t es = dtype == GPTQ_BF16 ? 2 : 4, units = ceil_div(cols, 16 / es);
+    const bool any = !whole_granules(es, cols, {{dY, lddy}, {H, ldh}, {dH, lddh}, {dX, lddx}, {gain, 0}});
     GradParams p{dY, H, dH, gain, rstd, rows, cols, lddy, ldh, lddh, dX, lddx, static_cast<float*>(ws), 0};
     p.per = ceil_div(rows, grad_ctas(rows));
     const unsigned ctas = (unsigned)ceil_div(rows, p.per);
     unsigned threads = 0;
     cudaError_t e = cudaSuccess;
-    const bool fits = with_units(dtype, unit, cols, &threads, [&](auto t, auto n, auto u) {
-        auto kern = int8_norm_grad_kernel<decltype(t), decltype(n)::value, decltype(u)::value>;
-        GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(threads), 0, s, p));
-    });
+    auto go = [&](auto t, auto u, auto a) {
+        auto kern = int8_norm_grad_kernel<decltype(t), decltype(u)::value, decltype(a)::value != 0>;
+        // groups of threads up to 512, each with a barrier (15 of them besides the CTA's), none idle
+        const unsigned groups = (unsigned)std::max<int64_t>(1, std::min<int64_t>(std::min(15u, 512 / threads), p.per));
+        const size_t smem = groups > 1 ? sizeof(float) * cols : 0;   // (at most 256 threads of 8 columns: 8 KB)
+        GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, groups), smem, s, p));
+    };
+    // (bf16 units are 8 columns: with 4 of them the registers would not do)
+    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 1, 2>(any, units, 512, &threads, go)
+                                         : with_units<float, 1, 4>(any, units, 512, &threads, go);
     if (!fits) {
         auto kern = dtype == GPTQ_BF16 ? int8_norm_grad_long_kernel<__nv_bfloat16> : int8_norm_grad_long_kernel<float>;
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(1024), 0, s, p));
@@ -639,13 +837,13 @@ extern "C" int gptq_int8_dequantize(const int8_t* codes, const float* scales, in
     if (!codes || !scales || !Y || ldy < cols || reinterpret_cast<uintptr_t>(codes) % 16 != 0) return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const BackParams p{codes, scales, rows, cols, int8_pitch(cols), Y, ldy};
-    const bool vec = unit_of(dtype == GPTQ_BF16 ? 2 : 4, cols, {{Y, ldy}}) == 16;
-    const int n = vec ? (dtype == GPTQ_BF16 ? 8 : 4) : 1;
+    const bool any = !whole_granules(dtype == GPTQ_BF16 ? 2 : 4, cols, {{Y, ldy}});
+    const int n = dtype == GPTQ_BF16 ? 8 : 4;
     const dim3 grid((unsigned)ceil_div(ceil_div(cols, n), B_THREADS), (unsigned)std::min<int64_t>(ceil_div(rows, B_ROWS), 65535));
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kern) { GPTQ_LAUNCH(K_INT8_DEQUANT, s, e = launch_pdl(kern, grid, dim3(B_THREADS), 0, s, p)); };
-    if (dtype == GPTQ_BF16) vec ? go(int8_dequantize_kernel<__nv_bfloat16, 8>) : go(int8_dequantize_kernel<__nv_bfloat16, 1>);
-    else vec ? go(int8_dequantize_kernel<float, 4>) : go(int8_dequantize_kernel<float, 1>);
+    if (dtype == GPTQ_BF16) any ? go(int8_dequantize_kernel<__nv_bfloat16, true>) : go(int8_dequantize_kernel<__nv_bfloat16, false>);
+    else any ? go(int8_dequantize_kernel<float, true>) : go(int8_dequantize_kernel<float, false>);
     GPTQ_CUDA_TRY(e);
     return GPTQ_OK;
 }
