@@ -8,6 +8,7 @@
 //   gradient  with u = h rstd, v = dy gain: dx = dh + rstd (v - u mean(u v)), dgain = sum over rows of dy u
 // Sums are fp32 in a fixed order.
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -22,29 +23,38 @@ namespace {
 // A row has blockDim.x threads (whole warps); a CTA has blockDim.y rows at a time, more than one only where a
 // warp takes a whole row. The sum is the same in all its threads. `part` [32]: one slot per warp, not the
 // ones of the sum before.
-template <typename V, typename Op>
-__device__ __forceinline__ V row_reduce(V v, V* part, Op op) {
+__device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (blockDim.x == 32) return v;
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = part[(threadIdx.x & 31) < warps ? threadIdx.x & 31 : 0];
+    v = lane < warps ? part[lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const V w = __shfl_down_sync(0xffffffffu, v, o);
-        if ((int)(threadIdx.x & 31) + o < warps) v = op(v, w);
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < warps) v += __shfl_xor_sync(0xffffffffu, v, o);
     return __shfl_sync(0xffffffffu, v, 0);
 }
 
-struct Add {
-    __device__ float operator()(float a, float b) const { return a + b; }
-};
-struct Max {
-    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
-};
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (blockDim.x == 32) return v;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, part[lane < warps ? lane : 0]);
+}
+
+// a / 127, correctly rounded (see the quotient below); m: a's bits. NaN for what is not finite
+__device__ __forceinline__ float scale_of(uint32_t m) {
+    if (m >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    const float a = __uint_as_float(m);
+    if (a < 0x1p-60f) return a / 127.0f;
+    constexpr float inv = 1.0f / 127.0f;
+    const float q = a * inv;
+    return fmaf(fmaf(-q, 127.0f, a), inv, q);
+}
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
@@ -66,9 +76,9 @@ __device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
 __device__ __forceinline__ uint32_t bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 
 template <typename T>
-__device__ __forceinline__ uint4 load_granule(const T* row, int64_t cols, int o, int64_t g) {
+__device__ __forceinline__ uint4 load_granule(const T* row, int cols, int o, int g) {
     constexpr int N = kUnit<T>;
-    const int64_t c = g * N - o;   // its first column
+    const int c = g * N - o;   // its first column
     if (c >= 0 && c + N <= cols) return *reinterpret_cast<const uint4*>(row + c);
     uint32_t w[4] = {};
 #pragma unroll
@@ -97,7 +107,7 @@ __device__ __forceinline__ uint4 from_byte(const uint4& a, const uint4& b, int b
 
 // Granule j of a row, to be made unit j by to_words
 template <typename T, bool ANY>
-__device__ __forceinline__ uint4 load_raw(const T* row, int64_t cols, int64_t j) {
+__device__ __forceinline__ uint4 load_raw(const T* row, int cols, int j) {
     if constexpr (ANY) return load_granule(row, cols, row_start(row), j);
     return j * kUnit<T> < cols ? *reinterpret_cast<const uint4*>(row + j * kUnit<T>) : make_uint4(0, 0, 0, 0);
 }
@@ -105,7 +115,7 @@ __device__ __forceinline__ uint4 load_raw(const T* row, int64_t cols, int64_t j)
 // Unit j from the granules that the lanes have loaded, zeros past the columns. (The last lane reads the next warp's first granule
 // here, most likely from L1: before any barrier behind which that warp may write to it.)
 template <typename T, bool ANY>
-__device__ __forceinline__ uint4 to_words(const T* row, int64_t cols, int64_t j, const uint4& a) {
+__device__ __forceinline__ uint4 to_words(const T* row, int cols, int j, const uint4& a) {
     if constexpr (ANY) {
         const int o = row_start(row);
         if (o != 0) {
@@ -154,7 +164,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const uint32_t (&w)[4], in
 }
 
 template <typename T, bool ANY>
-__device__ __forceinline__ void store_unit_at(T* row, int64_t cols, int64_t j, const float (&v)[kUnit<T>]) {
+__device__ __forceinline__ void store_unit_at(T* row, int cols, int j, const float (&v)[kUnit<T>]) {
     constexpr int N = kUnit<T>;
     const uint4 p = pack<T>(v);
     if constexpr (!ANY) {
@@ -162,7 +172,7 @@ __device__ __forceinline__ void store_unit_at(T* row, int64_t cols, int64_t j, c
     } else {
         const int o = row_start(row), lane = threadIdx.x & 31;
         const uint32_t own[4] = {p.x, p.y, p.z, p.w};
-        const int64_t c = j * N - o;   // the first column of granule j
+        const int c = j * N - o;   // the first column of granule j
         uint4 g = p;
         if (o != 0) {
             uint4 q;
@@ -186,7 +196,7 @@ __device__ __forceinline__ void store_unit_at(T* row, int64_t cols, int64_t j, c
 
 // the gain of a unit's columns, zeros past them
 template <int N, bool ANY>
-__device__ __forceinline__ void load_gain(const float* gain, int64_t cols, int64_t c, float (&g)[N]) {
+__device__ __forceinline__ void load_gain(const float* gain, int cols, int c, float (&g)[N]) {
     if (!ANY || ((reinterpret_cast<uintptr_t>(gain) & 15) == 0 && c + N <= cols)) {
         if (c < cols) {
 #pragma unroll
@@ -215,7 +225,7 @@ __device__ __forceinline__ Step step_of(float s) {
     t.usual = s >= 0x1p-60f && s <= 0x1p60f;
     t.f = t.usual ? 1.0f : s < 1.0f ? 0x1p64f : 0x1p-64f;
     t.d = s * t.f;
-    t.inv = s > 0.0f ? 1.0f / t.d : 0.0f;   // (a NaN scale has codes of zero)
+    t.inv = s > 0.0f ? __frcp_rn(t.d) : 0.0f;   // (a NaN scale has codes of zero)
     return t;
 }
 __device__ __forceinline__ uint32_t code_of(float x, const Step& t) {   // in the low byte
@@ -269,11 +279,17 @@ struct RowParams {
 // 1 / sqrt(mean h^2 + eps) from the sum of squares; where the squares leave fp32's normal numbers the sum is
 // taken again of scaled values (a row apart, so nothing is lost elsewhere)
 template <typename F>
-__device__ __forceinline__ float rstd_of(float sum, float n, float eps, F again) {
-    const float v = sum / n + eps;
+__device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps, F again) {
+    const float v = fmaf(sum, inv_n, eps);
     if (v >= 0x1p-80f && v <= 0x1.fffffep127f) return rsqrtf(v);
     const float f = v < 1.0f ? 0x1p100f : 0x1p-80f;
-    return rsqrtf(again(f) / n + eps * f * f) * f;
+    return rsqrtf(again(f) * inv_n + eps * f * f) * f;
+}
+
+// the most threads of a row: bf16 units, of 8 columns, take more registers than 1024 threads have
+template <typename T>
+constexpr int row_threads() {
+    return sizeof(T) == 2 ? 512 : 1024;
 }
 
 // the row of X that row r is, or -1
@@ -287,23 +303,24 @@ __device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
 }
 
 // Rows in the registers of their threads, UNITS units each: a row is read once and everything written once. CTAs
-// are persistent, and the next row's loads are under way (AHEAD) while this one is reduced and written.
+// are persistent, and the next row's loads are under way while this one is reduced and written. Four units per thread, so
+// that what every warp does for a row (its sums, scale and reciprocals) is shared by more columns.
 template <typename T, int UNITS, bool NORM, bool ANY>
-__global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
+__global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const RowParams p) {
     constexpr int N = kUnit<T>;
-    constexpr bool AHEAD = UNITS <= 2;
     __shared__ float sum_part[2][32];
     __shared__ uint32_t max_part[2][32];
     pdl_trigger();   // the product's prologue may begin
     pdl_wait();
-    const int64_t j0 = threadIdx.x, units = blockDim.x;
+    const int j0 = threadIdx.x, units = blockDim.x, cols = (int)p.cols;
+    const float inv_n = 1.0f / (float)cols;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     uint4 x[UNITS], res[UNITS];
     const T *row = nullptr, *rrow = nullptr;
-    int64_t n = 0;
+    int n = 0;
     auto load = [&](int64_t r) {
         const int64_t sr = NORM ? r : source_row(p, r);
-        n = sr < 0 ? 0 : p.cols;
+        n = sr < 0 ? 0 : cols;
         row = static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx);
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) x[i] = load_raw<T, ANY>(row, n, j0 + i * units);
@@ -314,10 +331,9 @@ __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
         }
     };
     int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (AHEAD && r < p.rows) load(r);
+    if (r < p.rows) load(r);
     int turn = 0;
     for (; r < p.rows; r += step, turn ^= 1) {
-        if (!AHEAD) load(r);
         float v[UNITS][N];
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
@@ -330,7 +346,7 @@ __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
                 if constexpr (sizeof(T) == 2) unpack<T>(pack<T>(v[i]), v[i]);   // h as it is stored
             }
         }
-        if (AHEAD && r + step < p.rows) load(r + step);
+        if (r + step < p.rows) load(r + step);
         if constexpr (NORM) {
             auto squares = [&](float f) {
                 float s = 0.0f;
@@ -340,21 +356,21 @@ __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
                     for (int e = 0; e < N; ++e) s = fmaf(v[i][e] * f, v[i][e] * f, s);
                 return s;
             };
-            const float sum = row_reduce(squares(1.0f), sum_part[turn], Add());
-            const float rstd = rstd_of(sum, (float)p.cols, p.eps, [&](float f) {
+            const float sum = row_sum(squares(1.0f), sum_part[turn]);
+            const float rstd = rstd_of(sum, inv_n, p.eps, [&](float f) {
                 if (blockDim.x > 32) __syncthreads();
-                return row_reduce(squares(f), sum_part[turn], Add());
+                return row_sum(squares(f), sum_part[turn]);
             });
             if (threadIdx.x == 0) p.rstd[r] = rstd;
             if (p.R) {   // (H may be X or R: all of the row's threads have read it by now)
                 T* h = static_cast<T*>(p.H) + r * p.ldh;
 #pragma unroll
-                for (int i = 0; i < UNITS; ++i) store_unit_at<T, ANY>(h, p.cols, j0 + i * units, v[i]);
+                for (int i = 0; i < UNITS; ++i) store_unit_at<T, ANY>(h, cols, j0 + i * units, v[i]);
             }
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
                 float g[N];
-                load_gain<N, ANY>(p.gain, p.cols, (j0 + i * units) * N, g);
+                load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, g);
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * rstd * g[e];
             }
@@ -364,9 +380,9 @@ __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
         for (int i = 0; i < UNITS; ++i)
 #pragma unroll
             for (int e = 0; e < N; ++e) m = max(m, magnitude(v[i][e]));
-        m = row_reduce(m, max_part[turn], Max());
+        m = row_max(m, max_part[turn]);
         const bool bad = m >= 0x7F800000u;
-        const float s = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.0f;
+        const float s = scale_of(m);
         if (threadIdx.x == 0) {
             p.scales[r] = s;
             if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
@@ -375,7 +391,7 @@ __global__ void __launch_bounds__(1024) int8_rows_kernel(const RowParams p) {
         int8_t* y = p.codes + r * p.pitch;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i)
-            if ((j0 + i * units) * N < p.pitch) store_codes<N>(y + (j0 + i * units) * N, v[i], t);
+            if ((j0 + i * units) * N < (int)p.pitch) store_codes<N>(y + (j0 + i * units) * N, v[i], t);
     }
 }
 
@@ -406,8 +422,8 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
             s = fmaf(a[0], a[0], s);
         }
         if (res) x = h;
-        const float sum = row_reduce(s, sum_part, Add());
-        rstd = rstd_of(sum, (float)p.cols, p.eps, [&](float f) {
+        const float sum = row_sum(s, sum_part);
+        rstd = rstd_of(sum, 1.0f / (float)p.cols, p.eps, [&](float f) {
             __syncthreads();
             float q = 0.0f;
             for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
                 load_unit<T, 1>(x + c, a);
                 q = fmaf(a[0] * f, a[0] * f, q);
             }
-            return row_reduce(q, sum_part, Add());
+            return row_sum(q, sum_part);
         });
         if (threadIdx.x == 0) p.rstd[r] = rstd;
     }
@@ -429,9 +445,9 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
         value(c, a);
         m = max(m, magnitude(a[0]));
     }
-    m = row_reduce(m, max_part, Max());
+    m = row_max(m, max_part);
     const bool bad = m >= 0x7F800000u;
-    const float s = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float(m) / 127.0f;
+    const float s = scale_of(m);
     if (threadIdx.x == 0) {
         p.scales[r] = s;
         if (bad) set_status(p.status, GPTQ_ERR_NONFINITE);
@@ -458,11 +474,11 @@ constexpr int B_THREADS = 128, B_ROWS = 4;   // rows in flight per thread
 template <typename T, bool ANY>
 __global__ void __launch_bounds__(B_THREADS) int8_dequantize_kernel(const BackParams p) {
     constexpr int N = kUnit<T>;
-    const int64_t j = (int64_t)blockIdx.x * B_THREADS + threadIdx.x;
-    if ((j & ~(int64_t)31) * N >= p.cols) return;   // (whole warps)
+    const int j = blockIdx.x * B_THREADS + threadIdx.x, cols = (int)p.cols;
+    if ((j & ~31) * N >= cols) return;   // (whole warps)
     pdl_trigger();
     pdl_wait();
-    const int64_t at = min(j * N, p.pitch - N);   // (lanes past the row: any)
+    const int at = min(j * N, (int)p.pitch - N);   // (lanes past the row: any)
     for (int64_t r0 = (int64_t)blockIdx.y * B_ROWS; r0 < p.rows; r0 += (int64_t)gridDim.y * B_ROWS) {
         uint32_t w[B_ROWS][N / 4];
         float s[B_ROWS];
@@ -484,7 +500,7 @@ __global__ void __launch_bounds__(B_THREADS) int8_dequantize_kernel(const BackPa
             float v[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] = (float)(int8_t)(w[i][e >> 2] >> (8 * (e & 3))) * s[i];
-            store_unit_at<T, ANY>(static_cast<T*>(p.Y) + (r0 + i) * p.ldy, p.cols, j, v);
+            store_unit_at<T, ANY>(static_cast<T*>(p.Y) + (r0 + i) * p.ldy, cols, j, v);
         }
     }
 }
@@ -518,17 +534,22 @@ __device__ __forceinline__ float group_sum(float v, float* part, int warps, int 
 // the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added in turn at the
 // end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written.
 template <typename T, int UNITS, bool ANY>
-__global__ void __launch_bounds__(UNITS == 1 ? 512 : 1024, UNITS == 1 ? 2 : 1) int8_norm_grad_kernel(const GradParams p) {
+__global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_norm_grad_kernel(const GradParams p) {
     constexpr int N = kUnit<T>;
-    constexpr bool AHEAD = UNITS == 1;
+    constexpr bool AHEAD = UNITS <= 2;   // (and the gain stays in registers)
     extern __shared__ float sums[];   // [columns of the units], where there are several groups
     __shared__ float part[2][32];
     pdl_trigger();
     pdl_wait();
     const int64_t first = (int64_t)blockIdx.x * p.per, last = min(first + p.per, p.rows);
-    const int64_t j0 = threadIdx.x, units = blockDim.x, step = blockDim.y;
+    const int j0 = threadIdx.x, units = blockDim.x, step = blockDim.y, cols = (int)p.cols;
     const int warps = blockDim.x >> 5, group = threadIdx.y;
-    const float inv_n = 1.0f / (float)p.cols;
+    const float inv_n = 1.0f / (float)cols;
+    float gain[UNITS][N];
+    if (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, gain[i]);
+    }
     float acc[UNITS][N] = {};
     uint4 dy[UNITS], h[UNITS], dh[UNITS];
     const T *ry = nullptr, *rh = nullptr, *rd = nullptr;
@@ -539,9 +560,9 @@ __global__ void __launch_bounds__(UNITS == 1 ? 512 : 1024, UNITS == 1 ? 2 : 1) i
         rd = static_cast<const T*>(p.dH) + r * p.lddh;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            dy[i] = load_raw<T, ANY>(ry, p.cols, j0 + i * units);
-            h[i] = load_raw<T, ANY>(rh, p.cols, j0 + i * units);
-            if (p.dH) dh[i] = load_raw<T, ANY>(rd, p.cols, j0 + i * units);
+            dy[i] = load_raw<T, ANY>(ry, cols, j0 + i * units);
+            h[i] = load_raw<T, ANY>(rh, cols, j0 + i * units);
+            if (p.dH) dh[i] = load_raw<T, ANY>(rd, cols, j0 + i * units);
         }
         rstd = p.rstd[r];
     };
@@ -555,36 +576,36 @@ __global__ void __launch_bounds__(UNITS == 1 ? 512 : 1024, UNITS == 1 ? 2 : 1) i
         const float rs = rstd;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            yw[i] = to_words<T, ANY>(ry, p.cols, j0 + i * units, dy[i]);
-            hw[i] = to_words<T, ANY>(rh, p.cols, j0 + i * units, h[i]);
-            if (p.dH) dw[i] = to_words<T, ANY>(rd, p.cols, j0 + i * units, dh[i]);
+            yw[i] = to_words<T, ANY>(ry, cols, j0 + i * units, dy[i]);
+            hw[i] = to_words<T, ANY>(rh, cols, j0 + i * units, h[i]);
+            if (p.dH) dw[i] = to_words<T, ANY>(rd, cols, j0 + i * units, dh[i]);
         }
         if (AHEAD && r + step < last) load(r + step);
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            float g[N], u[N], v[N];
-            load_gain<N, ANY>(p.gain, p.cols, (j0 + i * units) * N, g);
+            float u[N], v[N];
+            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, gain[i]);
             unpack<T>(hw[i], u);
             unpack<T>(yw[i], v);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 u[e] *= rs;
                 acc[i][e] = fmaf(v[e], u[e], acc[i][e]);
-                dot = fmaf(u[e], v[e] * g[e], dot);
+                dot = fmaf(u[e], v[e] * gain[i][e], dot);
             }
         }
-        dot = group_sum(dot, part[turn] + group * warps, warps, 1 + group) * inv_n;
+        const float k = group_sum(dot, part[turn] + group * warps, warps, 1 + group) * inv_n * rs;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            float g[N], u[N], v[N], d[N] = {};
-            load_gain<N, ANY>(p.gain, p.cols, (j0 + i * units) * N, g);
+            float u[N], v[N], d[N] = {};
+            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, gain[i]);
             unpack<T>(hw[i], u);
             unpack<T>(yw[i], v);
             if (p.dH) unpack<T>(dw[i], d);
 #pragma unroll
-            for (int e = 0; e < N; ++e) d[e] = fmaf(rs, v[e] * g[e] - u[e] * rs * dot, d[e]);
-            store_unit_at<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, p.cols, j0 + i * units, d);
+            for (int e = 0; e < N; ++e) d[e] = fmaf(rs, fmaf(-u[e], k, v[e] * gain[i][e]), d[e]);
+            store_unit_at<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, cols, j0 + i * units, d);
         }
     }
     float* out = p.part + blockIdx.x * p.cols;
@@ -594,8 +615,8 @@ __global__ void __launch_bounds__(UNITS == 1 ? 512 : 1024, UNITS == 1 ? 2 : 1) i
             for (int i = 0; i < UNITS; ++i)
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const int64_t c = (j0 + i * units) * N + e;
-                    if (c >= p.cols) continue;
+                    const int c = (j0 + i * units) * N + e;
+                    if (c >= cols) continue;
                     const float s = g > 0 ? sums[c] + acc[i][e] : acc[i][e];
                     if (g == (int)blockDim.y - 1) out[c] = s;
                     else sums[c] = s;
@@ -625,7 +646,7 @@ __global__ void __launch_bounds__(1024) int8_norm_grad_long_kernel(const GradPar
             load_unit<T, 1>(dy + c, v);
             dot = fmaf(u[0] * rstd, v[0] * p.gain[c], dot);
         }
-        dot = row_reduce(dot, part[(r - first) & 1], Add()) * inv_n;
+        dot = row_sum(dot, part[(r - first) & 1]) * inv_n;
         for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
             float d[1] = {0.0f};
             load_unit<T, 1>(h + c, u);
@@ -676,9 +697,10 @@ bool whole_granules(int64_t es, int64_t cols, std::initializer_list<Rows> rows) 
 template <int V>
 using Const = std::integral_constant<int, V>;
 
-// Calls f(T(), units per thread, whether rows start anywhere) after setting the threads that a row of `units` units takes: FEW units
-// per thread while they need no more than `most` threads, MANY up to 1024. False: the row does not fit into a CTA's registers.
-template <typename T, int FEW, int MANY, typename F>
+// Calls f(T(), units per thread, whether rows start anywhere) after setting the threads that a row of `units` units takes:
+// one or two units per thread where a warp can take it so, MOST (2 or more) while it needs up to `threads`, then 4.
+// False: the row does not fit into a CTA's registers.
+template <typename T, int MOST, typename F>
 bool with_units(bool any, int64_t units, int most, unsigned* threads, F f) {
     auto go = [&](auto u) {
         const int64_t n = ceil_div(ceil_div(units, decltype(u)::value), 32) * 32;
@@ -686,9 +708,24 @@ bool with_units(bool any, int64_t units, int most, unsigned* threads, F f) {
         any ? f(T(), u, Const<1>()) : f(T(), u, Const<0>());
         return true;
     };
-    if (units <= FEW * most) return go(Const<FEW>());
-    if (units <= MANY * 1024) return go(Const<MANY>());
+    if (units <= 32) return go(Const<1>());
+    if (units <= 64 || (MOST == 2 && units <= 2 * most)) return go(Const<2>());
+    if (units <= 4 * row_threads<T>()) return go(Const<4>());
     return false;
+}
+
+// CTAs of a kernel that an SM holds at once, asked once for each number of threads
+template <typename K>
+int ctas_per_sm(K kern, unsigned threads, std::atomic<int> (&known)[33]) {
+    std::atomic<int>& k = known[threads / 32];
+    int n = k.load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, (int)threads, 0) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 1;
+    }
+    k.store(n, std::memory_order_relaxed);
+    return n;
 }
 
 template <bool NORM>
@@ -698,14 +735,14 @@ int launch_rows(const RowParams& p, int dtype, bool any, int id, cudaStream_t s)
     const int64_t units = p.pitch / (dtype == GPTQ_BF16 ? 8 : 4);
     auto go = [&](auto t, auto u, auto a) {
         auto kern = int8_rows_kernel<decltype(t), decltype(u)::value, NORM, decltype(a)::value != 0>;
-        // a warp takes a whole row where it can; about 1024 threads per SM
-        const unsigned rows = threads == 32 ? 8 : 1;
-        const int64_t most = (int64_t)device_sm_count() * std::max(1u, 1024 / (threads * rows));
+        static std::atomic<int> known[33];
+        const unsigned rows = threads == 32 ? 8 : 1;   // a warp takes a whole row where it can
+        const int64_t most = (int64_t)device_sm_count() * ctas_per_sm(kern, threads * rows, known);
         const unsigned ctas = (unsigned)std::min<int64_t>(ceil_div(p.rows, rows), most);
         GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, rows), 0, s, p));
     };
-    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2, 4>(any, units, 1024, &threads, go)
-                                         : with_units<float, 2, 4>(any, units, 1024, &threads, go);
+    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 4>(any, units, 0, &threads, go)
+                                         : with_units<float, 4>(any, units, 0, &threads, go);
     if (!fits) {
         auto kern = dtype == GPTQ_BF16 ? int8_long_rows_kernel<__nv_bfloat16, NORM> : int8_long_rows_kernel<float, NORM>;
         GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3((unsigned)p.rows), dim3(1024), 0, s, p));
@@ -714,7 +751,7 @@ int launch_rows(const RowParams& p, int dtype, bool any, int id, cudaStream_t s)
     return GPTQ_OK;
 }
 
-// CTAs of the gradient, each with a row of partial sums
+// The most CTAs of the gradient, each with a row of partial sums
 int64_t grad_ctas(int64_t rows) { return std::min<int64_t>(rows, 2 * kSMs); }
 
 }  // namespace
@@ -805,21 +842,26 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
     const int64_t es = dtype == GPTQ_BF16 ? 2 : 4, units = ceil_div(cols, 16 / es);
     const bool any = !whole_granules(es, cols, {{dY, lddy}, {H, ldh}, {dH, lddh}, {dX, lddx}, {gain, 0}});
     GradParams p{dY, H, dH, gain, rstd, rows, cols, lddy, ldh, lddh, dX, lddx, static_cast<float*>(ws), 0};
-    p.per = ceil_div(rows, grad_ctas(rows));
-    const unsigned ctas = (unsigned)ceil_div(rows, p.per);
-    unsigned threads = 0;
+    unsigned threads = 0, ctas = 0;
     cudaError_t e = cudaSuccess;
+    auto share = [&](int64_t most) {   // each CTA's rows, and the CTAs
+        p.per = ceil_div(rows, std::min(most, grad_ctas(rows)));
+        ctas = (unsigned)ceil_div(rows, p.per);
+    };
     auto go = [&](auto t, auto u, auto a) {
         auto kern = int8_norm_grad_kernel<decltype(t), decltype(u)::value, decltype(a)::value != 0>;
+        static std::atomic<int> known[33];
         // groups of threads up to 512, each with a barrier (15 of them besides the CTA's), none idle
-        const unsigned groups = (unsigned)std::max<int64_t>(1, std::min<int64_t>(std::min(15u, 512 / threads), p.per));
-        const size_t smem = groups > 1 ? sizeof(float) * cols : 0;   // (at most 256 threads of 8 columns: 8 KB)
+        unsigned groups = std::max(1u, std::min(15u, 512 / threads));
+        share((int64_t)device_sm_count() * ctas_per_sm(kern, threads * groups, known));
+        groups = (unsigned)std::min<int64_t>(groups, p.per);
+        const size_t smem = groups > 1 ? sizeof(float) * cols : 0;   // (at most 256 threads of 16 columns: 16 KB)
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, groups), smem, s, p));
     };
-    // (bf16 units are 8 columns: with 4 of them the registers would not do)
-    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 1, 2>(any, units, 512, &threads, go)
-                                         : with_units<float, 1, 4>(any, units, 512, &threads, go);
+    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2>(any, units, 512, &threads, go)
+                                         : with_units<float, 2>(any, units, 512, &threads, go);
     if (!fits) {
+        share(grad_ctas(rows));
         auto kern = dtype == GPTQ_BF16 ? int8_norm_grad_long_kernel<__nv_bfloat16> : int8_norm_grad_long_kernel<float>;
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(1024), 0, s, p));
     }
