@@ -61,9 +61,11 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 // ------------------------------------------------------------------------------------ units of a row
 // A thread works on units of N = 16 / sizeof(T) neighbouring columns, unit j being columns N j .. N j + N - 1
 // whatever the row's address. Memory is read and written in aligned 16-byte granules: a row that starts
-// `o` elements into a granule has its unit j in granules j and j + 1, and the second one is the next lane's
-// first (the last lane of a warp loads it itself). Granules that are not the row's alone, at its ends, are read
-// and written element by element. All lanes of a warp take part. ANY = false: rows of whole granules.
+// `o` elements into a granule has its unit j in granules j and j + 1, and the second one is the next unit's
+// first. A warp's units are neighbours (its lane l has units 32 i + l past the warp's first one), so they come by
+// shuffles but for the last one's, which its lane loads itself. Granules that are not the row's alone, at its ends, or
+// not the warp's, are read and written element by element. All lanes of a warp take part. ANY = false: rows of whole
+// granules.
 template <typename T>
 constexpr int kUnit = 16 / sizeof(T);
 
@@ -112,21 +114,37 @@ __device__ __forceinline__ uint4 load_raw(const T* row, int cols, int j) {
     return j * kUnit<T> < cols ? *reinterpret_cast<const uint4*>(row + j * kUnit<T>) : make_uint4(0, 0, 0, 0);
 }
 
-// Unit j from the granules that the lanes have loaded, zeros past the columns. (The last lane reads the next warp's first granule
-// here, most likely from L1: before any barrier behind which that warp may write to it.)
-template <typename T, bool ANY>
-__device__ __forceinline__ uint4 to_words(const T* row, int cols, int j, const uint4& a) {
+// a lane's neighbour along the warp's units: the next lane's, and for the last lane the first lane's next one
+__device__ __forceinline__ uint4 next_of(const uint4& a, const uint4& after) {
+    const int lane = threadIdx.x & 31, from = (lane + 1) & 31;
+    uint4 n;
+    n.x = __shfl_sync(0xffffffffu, lane == 0 ? after.x : a.x, from), n.y = __shfl_sync(0xffffffffu, lane == 0 ? after.y : a.y, from);
+    n.z = __shfl_sync(0xffffffffu, lane == 0 ? after.z : a.z, from), n.w = __shfl_sync(0xffffffffu, lane == 0 ? after.w : a.w, from);
+    return n;
+}
+
+// The warp's units from j on (this lane's first one; 32 apart) from the granules that the lanes have loaded, in place; zeros past the
+// columns. (The last lane reads the next warp's first granule here, most likely from L1: before any barrier behind which that
+// warp may write to it.)
+template <typename T, bool ANY, int UNITS>
+__device__ __forceinline__ void to_words(const T* row, int cols, int j, uint4 (&a)[UNITS]) {
     if constexpr (ANY) {
         const int o = row_start(row);
-        if (o != 0) {
+        if (o == 0) return;
+        uint4 past = make_uint4(0, 0, 0, 0);   // what follows the warp's last granule
+        if ((threadIdx.x & 31) == 31) past = load_granule(row, cols, o, j + 32 * (UNITS - 1) + 1);
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
             uint4 n;
-            n.x = __shfl_down_sync(0xffffffffu, a.x, 1), n.y = __shfl_down_sync(0xffffffffu, a.y, 1);
-            n.z = __shfl_down_sync(0xffffffffu, a.z, 1), n.w = __shfl_down_sync(0xffffffffu, a.w, 1);
-            if ((threadIdx.x & 31) == 31) n = load_granule(row, cols, o, j + 1);
-            return from_byte(a, n, o * (int)sizeof(T));
+            if (i + 1 < UNITS) {
+                n = next_of(a[i], a[i + 1]);
+            } else {
+                n = next_of(a[i], a[i]);
+                if ((threadIdx.x & 31) == 31) n = past;
+            }
+            a[i] = from_byte(a[i], n, o * (int)sizeof(T));
         }
     }
-    return a;
 }
 
 template <typename T>
@@ -163,32 +181,44 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const uint32_t (&w)[4], in
     *p = __ushort_as_bfloat16((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
 }
 
-template <typename T, bool ANY>
-__device__ __forceinline__ void store_unit_at(T* row, int cols, int j, const float (&v)[kUnit<T>]) {
+// writes the warp's units from j on (see to_words)
+template <typename T, bool ANY, int UNITS>
+__device__ __forceinline__ void store_units(T* row, int cols, int j, const uint4 (&p)[UNITS]) {
     constexpr int N = kUnit<T>;
-    const uint4 p = pack<T>(v);
     if constexpr (!ANY) {
-        if (j * N < cols) *reinterpret_cast<uint4*>(row + j * N) = p;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+            if ((j + 32 * i) * N < cols) *reinterpret_cast<uint4*>(row + (j + 32 * i) * N) = p[i];
     } else {
         const int o = row_start(row), lane = threadIdx.x & 31;
-        const uint32_t own[4] = {p.x, p.y, p.z, p.w};
-        const int c = j * N - o;   // the first column of granule j
-        uint4 g = p;
-        if (o != 0) {
-            uint4 q;
-            q.x = __shfl_up_sync(0xffffffffu, p.x, 1), q.y = __shfl_up_sync(0xffffffffu, p.y, 1);
-            q.z = __shfl_up_sync(0xffffffffu, p.z, 1), q.w = __shfl_up_sync(0xffffffffu, p.w, 1);
-            g = from_byte(q, p, 16 - o * (int)sizeof(T));
-        }
-        // (of its first granule lane 0 has only its own elements, and of the one after its last, the last lane)
-        const bool whole = c >= 0 && c + N <= cols && (o == 0 || lane != 0);
-        if (whole) *reinterpret_cast<uint4*>(row + c) = g;
-        if (!whole || (o != 0 && lane == 31)) {
-            const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (!whole && (o == 0 || lane != 0 || e >= o) && c + e >= 0 && c + e < cols) put(row + c + e, w, e);
-                if (o != 0 && lane == 31 && e >= N - o && j * N + e < cols) put(row + j * N + e, own, e);
+        for (int i = 0; i < UNITS; ++i) {
+            const int c = (j + 32 * i) * N - o;   // the first column of this unit's granule
+            uint4 g = p[i];
+            if (o != 0) {
+                // the unit before: the lane before's, and for the first lane the last one's before
+                const int from = (lane + 31) & 31;
+                const uint4 b = p[i > 0 ? i - 1 : 0];
+                uint4 q;
+                q.x = __shfl_sync(0xffffffffu, lane == 31 ? b.x : p[i].x, from), q.y = __shfl_sync(0xffffffffu, lane == 31 ? b.y : p[i].y, from);
+                q.z = __shfl_sync(0xffffffffu, lane == 31 ? b.z : p[i].z, from), q.w = __shfl_sync(0xffffffffu, lane == 31 ? b.w : p[i].w, from);
+                g = from_byte(q, p[i], 16 - o * (int)sizeof(T));
+            }
+            // of its first granule the warp has only the elements from o on, and of the one after its last, o
+            const bool first = o != 0 && i == 0 && lane == 0, last = o != 0 && i == UNITS - 1 && lane == 31;
+            const bool whole = !first && c >= 0 && c + N <= cols;
+            if (whole) *reinterpret_cast<uint4*>(row + c) = g;
+            if (!whole) {
+                const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if ((!first || e >= o) && c + e >= 0 && c + e < cols) put(row + c + e, w, e);
+            }
+            if (last) {
+                const uint32_t w[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (e >= N - o && c + o + e < cols) put(row + c + o + e, w, e);
             }
         }
     }
@@ -312,7 +342,8 @@ __global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const Ro
     __shared__ uint32_t max_part[2][32];
     pdl_trigger();   // the product's prologue may begin
     pdl_wait();
-    const int j0 = threadIdx.x, units = blockDim.x, cols = (int)p.cols;
+    // this lane's first unit, the others 32 apart
+    const int j0 = (int)(threadIdx.x >> 5) * 32 * UNITS + (int)(threadIdx.x & 31), cols = (int)p.cols;
     const float inv_n = 1.0f / (float)cols;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     uint4 x[UNITS], res[UNITS];
@@ -323,11 +354,11 @@ __global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const Ro
         n = sr < 0 ? 0 : cols;
         row = static_cast<const T*>(p.X) + (sr < 0 ? 0 : sr * p.ldx);
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) x[i] = load_raw<T, ANY>(row, n, j0 + i * units);
+        for (int i = 0; i < UNITS; ++i) x[i] = load_raw<T, ANY>(row, n, j0 + 32 * i);
         if (NORM && p.R) {
             rrow = static_cast<const T*>(p.R) + r * p.ldr;
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i) res[i] = load_raw<T, ANY>(rrow, n, j0 + i * units);
+            for (int i = 0; i < UNITS; ++i) res[i] = load_raw<T, ANY>(rrow, n, j0 + 32 * i);
         }
     };
     int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -335,12 +366,14 @@ __global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const Ro
     int turn = 0;
     for (; r < p.rows; r += step, turn ^= 1) {
         float v[UNITS][N];
+        to_words<T, ANY>(row, n, j0, x);
+        if (NORM && p.R) to_words<T, ANY>(rrow, n, j0, res);
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            unpack<T>(to_words<T, ANY>(row, n, j0 + i * units, x[i]), v[i]);
+            unpack<T>(x[i], v[i]);
             if (NORM && p.R) {
                 float w[N];
-                unpack<T>(to_words<T, ANY>(rrow, n, j0 + i * units, res[i]), w);
+                unpack<T>(res[i], w);
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[i][e] += w[e];
                 if constexpr (sizeof(T) == 2) unpack<T>(pack<T>(v[i]), v[i]);   // h as it is stored
@@ -364,13 +397,15 @@ __global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const Ro
             if (threadIdx.x == 0) p.rstd[r] = rstd;
             if (p.R) {   // (H may be X or R: all of the row's threads have read it by now)
                 T* h = static_cast<T*>(p.H) + r * p.ldh;
+                uint4 w[UNITS];
 #pragma unroll
-                for (int i = 0; i < UNITS; ++i) store_unit_at<T, ANY>(h, cols, j0 + i * units, v[i]);
+                for (int i = 0; i < UNITS; ++i) w[i] = pack<T>(v[i]);
+                store_units<T, ANY>(h, cols, j0, w);
             }
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
                 float g[N];
-                load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, g);
+                load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, g);
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * rstd * g[e];
             }
@@ -391,7 +426,7 @@ __global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const Ro
         int8_t* y = p.codes + r * p.pitch;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i)
-            if ((j0 + i * units) * N < (int)p.pitch) store_codes<N>(y + (j0 + i * units) * N, v[i], t);
+            if ((j0 + 32 * i) * N < (int)p.pitch) store_codes<N>(y + (j0 + 32 * i) * N, v[i], t);
     }
 }
 
@@ -469,39 +504,36 @@ struct BackParams {
     void* Y;
     int64_t ldy;
 };
-constexpr int B_THREADS = 128, B_ROWS = 4;   // rows in flight per thread
+constexpr int B_WARPS = 4;   // rows per CTA at a time
 
-template <typename T, bool ANY>
-__global__ void __launch_bounds__(B_THREADS) int8_dequantize_kernel(const BackParams p) {
+// A warp takes UNITS units per lane of a row
+template <typename T, int UNITS, bool ANY>
+__global__ void __launch_bounds__(32 * B_WARPS) int8_dequantize_kernel(const BackParams p) {
     constexpr int N = kUnit<T>;
-    const int j = blockIdx.x * B_THREADS + threadIdx.x, cols = (int)p.cols;
-    if ((j & ~31) * N >= cols) return;   // (whole warps)
+    const int j0 = blockIdx.x * 32 * UNITS + threadIdx.x, cols = (int)p.cols;
     pdl_trigger();
     pdl_wait();
-    const int at = min(j * N, (int)p.pitch - N);   // (lanes past the row: any)
-    for (int64_t r0 = (int64_t)blockIdx.y * B_ROWS; r0 < p.rows; r0 += (int64_t)gridDim.y * B_ROWS) {
-        uint32_t w[B_ROWS][N / 4];
-        float s[B_ROWS];
+    for (int64_t r = (int64_t)blockIdx.y * B_WARPS + threadIdx.y; r < p.rows; r += (int64_t)gridDim.y * B_WARPS) {
+        uint2 w[UNITS];
+        uint4 out[UNITS];
 #pragma unroll
-        for (int i = 0; i < B_ROWS; ++i) {
-            const int64_t r = min(r0 + i, p.rows - 1);
-            const int8_t* src = p.codes + r * p.pitch + at;
-            if constexpr (N == 8) {
-                const uint2 u = *reinterpret_cast<const uint2*>(src);
-                w[i][0] = u.x, w[i][1] = u.y;
-            } else {
-                w[i][0] = *reinterpret_cast<const uint32_t*>(src);
+        for (int i = 0; i < UNITS; ++i) {
+            const int8_t* src = p.codes + r * p.pitch + (j0 + 32 * i) * N;
+            w[i] = make_uint2(0, 0);
+            if ((j0 + 32 * i) * N < cols) {
+                if constexpr (N == 8) w[i] = *reinterpret_cast<const uint2*>(src);
+                else w[i].x = *reinterpret_cast<const uint32_t*>(src);
             }
-            s[i] = p.scales[r];
         }
+        const float s = p.scales[r];
 #pragma unroll
-        for (int i = 0; i < B_ROWS; ++i) {
-            if (r0 + i >= p.rows) break;
+        for (int i = 0; i < UNITS; ++i) {
             float v[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = (float)(int8_t)(w[i][e >> 2] >> (8 * (e & 3))) * s[i];
-            store_unit_at<T, ANY>(static_cast<T*>(p.Y) + (r0 + i) * p.ldy, cols, j, v);
+            for (int e = 0; e < N; ++e) v[e] = (float)(int8_t)((e < 4 ? w[i].x : w[i].y) >> (8 * (e & 3))) * s;
+            out[i] = pack<T>(v);
         }
+        store_units<T, ANY>(static_cast<T*>(p.Y) + r * p.ldy, cols, j0, out);
     }
 }
 
@@ -542,13 +574,13 @@ __global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_n
     pdl_trigger();
     pdl_wait();
     const int64_t first = (int64_t)blockIdx.x * p.per, last = min(first + p.per, p.rows);
-    const int j0 = threadIdx.x, units = blockDim.x, step = blockDim.y, cols = (int)p.cols;
+    const int j0 = (int)(threadIdx.x >> 5) * 32 * UNITS + (int)(threadIdx.x & 31), step = blockDim.y, cols = (int)p.cols;
     const int warps = blockDim.x >> 5, group = threadIdx.y;
     const float inv_n = 1.0f / (float)cols;
     float gain[UNITS][N];
     if (AHEAD) {
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, gain[i]);
+        for (int i = 0; i < UNITS; ++i) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, gain[i]);
     }
     float acc[UNITS][N] = {};
     uint4 dy[UNITS], h[UNITS], dh[UNITS];
@@ -560,9 +592,9 @@ __global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_n
         rd = static_cast<const T*>(p.dH) + r * p.lddh;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
-            dy[i] = load_raw<T, ANY>(ry, cols, j0 + i * units);
-            h[i] = load_raw<T, ANY>(rh, cols, j0 + i * units);
-            if (p.dH) dh[i] = load_raw<T, ANY>(rd, cols, j0 + i * units);
+            dy[i] = load_raw<T, ANY>(ry, cols, j0 + 32 * i);
+            h[i] = load_raw<T, ANY>(rh, cols, j0 + 32 * i);
+            if (p.dH) dh[i] = load_raw<T, ANY>(rd, cols, j0 + 32 * i);
         }
         rstd = p.rstd[r];
     };
@@ -574,18 +606,17 @@ __global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_n
         // what is needed behind the barrier stays as the words it was read as: dX may be written over any input
         uint4 yw[UNITS], hw[UNITS], dw[UNITS];
         const float rs = rstd;
+        to_words<T, ANY>(ry, cols, j0, dy);
+        to_words<T, ANY>(rh, cols, j0, h);
+        if (p.dH) to_words<T, ANY>(rd, cols, j0, dh);
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            yw[i] = to_words<T, ANY>(ry, cols, j0 + i * units, dy[i]);
-            hw[i] = to_words<T, ANY>(rh, cols, j0 + i * units, h[i]);
-            if (p.dH) dw[i] = to_words<T, ANY>(rd, cols, j0 + i * units, dh[i]);
-        }
+        for (int i = 0; i < UNITS; ++i) yw[i] = dy[i], hw[i] = h[i], dw[i] = dh[i];
         if (AHEAD && r + step < last) load(r + step);
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             float u[N], v[N];
-            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, gain[i]);
+            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, gain[i]);
             unpack<T>(hw[i], u);
             unpack<T>(yw[i], v);
 #pragma unroll
@@ -599,14 +630,15 @@ __global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_n
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             float u[N], v[N], d[N] = {};
-            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + i * units) * N, gain[i]);
+            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, gain[i]);
             unpack<T>(hw[i], u);
             unpack<T>(yw[i], v);
             if (p.dH) unpack<T>(dw[i], d);
 #pragma unroll
             for (int e = 0; e < N; ++e) d[e] = fmaf(rs, fmaf(-u[e], k, v[e] * gain[i][e]), d[e]);
-            store_unit_at<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, cols, j0 + i * units, d);
+            dw[i] = pack<T>(d);
         }
+        store_units<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, cols, j0, dw);
     }
     float* out = p.part + blockIdx.x * p.cols;
     for (int g = 0; g < (int)blockDim.y; ++g) {
@@ -615,7 +647,7 @@ __global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_n
             for (int i = 0; i < UNITS; ++i)
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const int c = (j0 + i * units) * N + e;
+                    const int c = (j0 + 32 * i) * N + e;
                     if (c >= cols) continue;
                     const float s = g > 0 ? sums[c] + acc[i][e] : acc[i][e];
                     if (g == (int)blockDim.y - 1) out[c] = s;
@@ -880,12 +912,19 @@ extern "C" int gptq_int8_dequantize(const int8_t* codes, const float* scales, in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const BackParams p{codes, scales, rows, cols, int8_pitch(cols), Y, ldy};
     const bool any = !whole_granules(dtype == GPTQ_BF16 ? 2 : 4, cols, {{Y, ldy}});
-    const int n = dtype == GPTQ_BF16 ? 8 : 4;
-    const dim3 grid((unsigned)ceil_div(ceil_div(cols, n), B_THREADS), (unsigned)std::min<int64_t>(ceil_div(rows, B_ROWS), 65535));
+    const int64_t units = ceil_div(cols, dtype == GPTQ_BF16 ? 8 : 4);
     cudaError_t e = cudaSuccess;
-    auto go = [&](auto kern) { GPTQ_LAUNCH(K_INT8_DEQUANT, s, e = launch_pdl(kern, grid, dim3(B_THREADS), 0, s, p)); };
-    if (dtype == GPTQ_BF16) any ? go(int8_dequantize_kernel<__nv_bfloat16, true>) : go(int8_dequantize_kernel<__nv_bfloat16, false>);
-    else any ? go(int8_dequantize_kernel<float, true>) : go(int8_dequantize_kernel<float, false>);
+    auto go = [&](auto kern, int per) {
+        const dim3 grid((unsigned)ceil_div(units, 32 * per), (unsigned)std::min<int64_t>(ceil_div(rows, B_WARPS), 65535));
+        GPTQ_LAUNCH(K_INT8_DEQUANT, s, e = launch_pdl(kern, grid, dim3(32, B_WARPS), 0, s, p));
+    };
+    auto typed = [&](auto t) {
+        using T = decltype(t);
+        if (units <= 32) any ? go(int8_dequantize_kernel<T, 1, true>, 1) : go(int8_dequantize_kernel<T, 1, false>, 1);
+        else any ? go(int8_dequantize_kernel<T, 4, true>, 4) : go(int8_dequantize_kernel<T, 4, false>, 4);
+    };
+    if (dtype == GPTQ_BF16) typed(__nv_bfloat16());
+    else typed(float());
     GPTQ_CUDA_TRY(e);
     return GPTQ_OK;
 }
