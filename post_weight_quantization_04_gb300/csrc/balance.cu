@@ -3,21 +3,29 @@
 //   p[t] = softmax(z[t]) over the E experts, n = the tokens that count (mask), c[e] = their slots with
 //   ids = e:   L = E / (top n^2) sum_e c[e] sum_t p[t][e]     (1 where both are even)
 //   dz[t][e] = dL E / (top n^2) p[t][e] (c[e] - sum_j p[t][j] c[j])
+// (with counts taken from their mean, which changes nothing but the rounding: even counts give zeros)
 // Sums are fp32 in a fixed order; counts are whole numbers, so their atomics (in shared memory) give the same in any
 // order.
 #include <algorithm>
 
 #include "common.cuh"
 #include "int8.cuh"
+#include "pair.cuh"
 
 namespace gptq {
 
 namespace {
 
-constexpr int L_THREADS = 256;          // 8 warps
+constexpr int L_THREADS = 256;          // of the gradient
+constexpr int L_COUNTERS = 128;         // threads of the first kernel that count, besides those that take the softmax
+constexpr int L_ALONE = 128;            // tokens up to which one CTA does all in one launch
+// threads of the first kernel that take the softmax (their sums are in shared memory, by lanes and experts)
+constexpr int summing_threads(int v) { return v <= 8 ? 512 : 256; }
 constexpr int L_MAX_EXPERTS = 1024;
-constexpr int L_MAX_CTAS = 152;
-constexpr int L_AHEAD = 4;              // tokens in flight per group of lanes
+constexpr int L_MAX_CTAS = 304;
+constexpr int L_SUMMERS = 1024;         // threads of a CTA of the second kernel
+// tokens in flight per group of lanes, of V values per lane each
+constexpr int ahead(int v) { return v <= 4 ? 4 : v <= 8 ? 2 : 1; }
 
 struct LParams {
     const void* Z;
@@ -28,6 +36,7 @@ struct LParams {
     const uint8_t* mask;     // null: every token counts
     float* sums;             // [cta][expert] sums of p
     int32_t* counts;         // [cta][expert + 1]; forward: per CTA; gradient: the call's
+    int32_t* total;          // the call's counts
     const float* dloss;      // gradient
     void* dZ;
     int64_t lddz;
@@ -37,6 +46,18 @@ struct LParams {
 
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// a word of another CTA's shared memory
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
+                 : "=r"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
 
 // The softmax of a token over G lanes with V values each, lane l's v-th being expert l + G v (past the experts: 0).
 // A row of nothing but -inf is 0. Returns the largest value's test: false where a NaN or +inf is among them.
@@ -71,126 +92,175 @@ __device__ __forceinline__ void load_logits(const LParams& p, int64_t t, bool li
     for (int v = 0; v < V; ++v) z[v] = live && l + G * v < p.experts ? load_one(row + l + G * v) : -INFINITY;
 }
 
+__device__ __forceinline__ float loss_of(const LParams& p, float dot, int32_t tokens) {
+    const float n = (float)max(tokens, 1);
+    return (float)p.experts / (float)p.top * (dot / n / n);
+}
+
+// Each CTA's sums of p and counts over a contiguous share of the tokens. Bound by latency: two loads and two trees of shuffles
+// one after another for each few tokens of a warp.
 template <typename T, int G, int V>
-__global__ void __launch_bounds__(L_THREADS) balance_sums_kernel(const LParams p) {
+__global__ void __launch_bounds__(summing_threads(V) + L_COUNTERS) balance_sums_kernel(const LParams p) {
     extern __shared__ float sh[];                               // [groups][experts], then counts [experts + 1]
-    constexpr int GROUPS = L_THREADS / G;
+    constexpr int THREADS = summing_threads(V), ALL = THREADS + L_COUNTERS, GROUPS = THREADS / G, AHEAD = ahead(V);
+    __shared__ float warp_dot[ALL / 32];
     int32_t* cnt = reinterpret_cast<int32_t*>(sh + GROUPS * p.experts);
-    for (int e = threadIdx.x; e <= p.experts; e += L_THREADS) cnt[e] = 0;
+    for (int e = threadIdx.x; e <= p.experts; e += ALL) cnt[e] = 0;
+    pdl_trigger();
     pdl_wait();
     __syncthreads();
     const int64_t share = (p.tokens + gridDim.x - 1) / gridDim.x;
     const int64_t first = blockIdx.x * share, last = min(first + share, p.tokens);
-    const int group = threadIdx.x / G, l = threadIdx.x & (G - 1);
-    float acc[V] = {};
-    int live_tokens = 0;
-    bool fine = true;
-    for (int64_t t0 = first; t0 < last; t0 += GROUPS * L_AHEAD) {   // (the same for the whole CTA)
-        float z[L_AHEAD][V];
-        bool live[L_AHEAD];
-#pragma unroll
-        for (int u = 0; u < L_AHEAD; ++u) {
-            const int64_t t = t0 + u * GROUPS + group;
-            live[u] = t < last && (!p.mask || p.mask[t]);
-            load_logits<T, G, V>(p, t, live[u], z[u]);
+    if (threadIdx.x >= THREADS) {
+        int live = 0;
+        for (int64_t t = first + (threadIdx.x - THREADS); t < last; t += L_COUNTERS) {
+            if (p.mask && !p.mask[t]) continue;
+            ++live;
+#pragma unroll 4
+            for (int j = 0; j < p.top; ++j) {
+                const int e = p.ids[t * p.top + j];
+                if (e >= 0 && e < p.experts) atomicAdd(cnt + e, 1);
+                else if (e >= 0) set_status(p.status, GPTQ_ERR_INVALID_ARG);
+            }
         }
+        if (live) atomicAdd(cnt + p.experts, live);
+    } else {
+        const int group = threadIdx.x / G, l = threadIdx.x & (G - 1);
+        float acc[V] = {};
+        bool fine = true;
+        for (int64_t t0 = first; t0 < last; t0 += GROUPS * AHEAD) {   // (the same for all these threads)
+            float z[AHEAD][V];
 #pragma unroll
-        for (int u = 0; u < L_AHEAD; ++u) {
-            fine &= softmax<G, V>(z[u]);
-            live_tokens += live[u] ? 1 : 0;
+            for (int u = 0; u < AHEAD; ++u) {
+                const int64_t t = t0 + u * GROUPS + group;
+                load_logits<T, G, V>(p, t, t < last && (!p.mask || p.mask[t]), z[u]);
+            }
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] += z[u][v];
+            for (int u = 0; u < AHEAD; ++u) {
+                fine &= softmax<G, V>(z[u]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] += z[u][v];
+            }
         }
-    }
-    if (!fine) set_status(p.status, GPTQ_ERR_NONFINITE);
-    if (l == 0 && live_tokens) atomicAdd(cnt + p.experts, live_tokens);
-    for (int64_t i = first * p.top + threadIdx.x; i < last * p.top; i += L_THREADS) {
-        const int e = p.ids[i];
-        if (e < 0 || (p.mask && !p.mask[i / p.top])) continue;
-        if (e < p.experts) atomicAdd(cnt + e, 1);
-        else set_status(p.status, GPTQ_ERR_INVALID_ARG);
-    }
+        if (!fine) set_status(p.status, GPTQ_ERR_NONFINITE);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (l + G * v < p.experts) sh[group * p.experts + l + G * v] = acc[v];
+        for (int v = 0; v < V; ++v)
+            if (l + G * v < p.experts) sh[group * p.experts + l + G * v] = acc[v];
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e <= p.experts; e += L_THREADS) {
+    float dot = 0.0f;
+    for (int e = threadIdx.x; e <= p.experts; e += ALL) {
+        float s = 0.0f;
         if (e < p.experts) {
-            float s = 0.0f;
 #pragma unroll 8
             for (int g = 0; g < GROUPS; ++g) s += sh[g * p.experts + e];
-            p.sums[(int64_t)blockIdx.x * p.experts + e] = s;
         }
-        p.counts[(int64_t)blockIdx.x * (p.experts + 1) + e] = cnt[e];
+        if (gridDim.x > 1) {
+            if (e < p.experts) p.sums[(int64_t)blockIdx.x * p.experts + e] = s;
+            p.counts[(int64_t)blockIdx.x * (p.experts + 1) + e] = cnt[e];
+        } else {
+            p.total[e] = cnt[e];
+            if (e < p.experts) dot = fmaf((float)cnt[e], s, dot);
+        }
+    }
+    if (gridDim.x > 1) return;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if ((threadIdx.x & 31) == 0) warp_dot[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        dot = 0.0f;
+        for (int w = 0; w < ALL / 32; ++w) dot += warp_dot[w];
+        *p.loss = loss_of(p, dot, cnt[p.experts]);
     }
 }
 
-// the CTAs' sums and counts to the loss and the counts: 32 experts x 32 shares of the CTAs at a time
-__global__ void __launch_bounds__(1024) balance_loss_kernel(const LParams p, int ctas, int32_t* counts) {
-    __shared__ float sums[32][33];
-    __shared__ int32_t cnts[32][33];
-    __shared__ float dots[32];
+// The CTAs' sums and counts to the counts and the loss. The CTAs of the cluster share the experts (and, as one more, the
+// tokens), `wide` threads of each one's columns; its other threads share the rows. What they find is added in a
+// fixed order.
+__global__ void __launch_bounds__(L_SUMMERS) balance_loss_kernel(const LParams p, int rows, int wide) {
+    __shared__ float sums[L_SUMMERS];
+    __shared__ int32_t cnts[L_SUMMERS];
+    __shared__ float warp_dot[L_SUMMERS / 32];
+    __shared__ float dot;
     __shared__ int32_t live;
     pdl_wait();
-    float dot = 0.0f;
-    for (int e0 = 0; e0 <= p.experts; e0 += 32) {
-        const int e = e0 + threadIdx.x;
-        float s = 0.0f;
-        int32_t n = 0;
-        if (e <= p.experts) {
-#pragma unroll 4
-            for (int k = threadIdx.y; k < ctas; k += 32) {
-                if (e < p.experts) s += p.sums[(int64_t)k * p.experts + e];
-                n += p.counts[(int64_t)k * (p.experts + 1) + e];
-            }
+    const int share = (p.experts + gridDim.x) / gridDim.x;   // of experts + 1 columns, rounded up
+    const int c = threadIdx.x & (wide - 1), e = blockIdx.x * share + c, groups = L_SUMMERS / wide;
+    const bool mine = c < share && e <= p.experts;
+    float s = 0.0f;
+    int32_t n = 0;
+    if (mine) {
+#pragma unroll 8
+        for (int k = threadIdx.x / wide; k < rows; k += groups) {
+            if (e < p.experts) s += p.sums[(int64_t)k * p.experts + e];
+            n += p.counts[(int64_t)k * (p.experts + 1) + e];
         }
-        sums[threadIdx.y][threadIdx.x] = s;
-        cnts[threadIdx.y][threadIdx.x] = n;
-        __syncthreads();
-        s = sums[threadIdx.x][threadIdx.y];
-        n = __reduce_add_sync(0xffffffffu, cnts[threadIdx.x][threadIdx.y]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const int mine = e0 + threadIdx.y;
-        if (threadIdx.x == 0 && mine <= p.experts) {
-            counts[mine] = n;
-            if (mine == p.experts) live = n;
-        }
-        if (mine < p.experts) dot = fmaf((float)n, s, dot);
-        __syncthreads();
     }
-    if (threadIdx.x == 0) dots[threadIdx.y] = dot;
+    sums[threadIdx.x] = s;
+    cnts[threadIdx.x] = n;
     __syncthreads();
-    if (threadIdx.y == 0) {
-        dot = dots[threadIdx.x];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float n = (float)max(live, 1);
-        if (threadIdx.x == 0) *p.loss = (float)p.experts / (float)p.top * (dot / n / n);
+    float d = 0.0f;
+    if (threadIdx.x < wide && mine) {
+        for (int g = 1; g < groups; ++g) {
+            s += sums[g * wide + c];
+            n += cnts[g * wide + c];
+        }
+        p.total[e] = n;
+        if (e < p.experts) d = (float)n * s;
+        else live = n;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if ((threadIdx.x & 31) == 0) warp_dot[threadIdx.x >> 5] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        d = 0.0f;
+        for (int w = 0; w < (wide + 31) / 32; ++w) d += warp_dot[w];
+        dot = d;
+    }
+    if (gridDim.x > 1) cluster_sync();
+    else __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        float all = dot;
+        for (uint32_t r = 1; r < gridDim.x; ++r) all += __uint_as_float(ld_cluster_u32(smem_u32(&dot), r));
+        const int32_t tokens = gridDim.x > 1 ? (int32_t)ld_cluster_u32(smem_u32(&live), p.experts / share) : live;
+        *p.loss = loss_of(p, all, tokens);
+    }
+    if (gridDim.x > 1) cluster_sync();   // no CTA leaves while its sum is read
 }
 
 template <typename T, int G, int V>
 __global__ void __launch_bounds__(L_THREADS) balance_grad_kernel(const LParams p) {
     constexpr int GROUPS = L_THREADS / G;
     pdl_wait();
+    constexpr int AHEAD = ahead(V);
     const int group = threadIdx.x / G, l = threadIdx.x & (G - 1);
+    int n[V], sum = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        n[v] = l + G * v < p.experts ? p.counts[l + G * v] : 0;
+        sum += n[v];
+    }
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int mean_count = sum / p.experts;
     float c[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = l + G * v < p.experts ? (float)p.counts[l + G * v] : 0.0f;
-    const float n = (float)max(p.counts[p.experts], 1);
-    const float k = (p.dloss ? *p.dloss : 1.0f) * ((float)p.experts / (float)p.top / n / n);
-    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * L_AHEAD; t0 < p.tokens; t0 += (int64_t)gridDim.x * GROUPS * L_AHEAD) {
-        float z[L_AHEAD][V];
-        bool live[L_AHEAD];
+    for (int v = 0; v < V; ++v) c[v] = l + G * v < p.experts ? (float)(n[v] - mean_count) : 0.0f;
+    const float tokens = (float)max(p.counts[p.experts], 1);
+    const float k = (p.dloss ? *p.dloss : 1.0f) * ((float)p.experts / (float)p.top / tokens / tokens);
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS * AHEAD; t0 < p.tokens; t0 += (int64_t)gridDim.x * GROUPS * AHEAD) {
+        float z[AHEAD][V];
+        bool live[AHEAD];
 #pragma unroll
-        for (int u = 0; u < L_AHEAD; ++u) {
+        for (int u = 0; u < AHEAD; ++u) {
             const int64_t t = t0 + u * GROUPS + group;
             live[u] = t < p.tokens && (!p.mask || p.mask[t]);
             load_logits<T, G, V>(p, t, live[u], z[u]);
         }
 #pragma unroll
-        for (int u = 0; u < L_AHEAD; ++u) {
+        for (int u = 0; u < AHEAD; ++u) {
             const int64_t t = t0 + u * GROUPS + group;
             if (!softmax<G, V>(z[u])) set_status(p.status, GPTQ_ERR_NONFINITE);
             float mean = 0.0f;
@@ -203,8 +273,7 @@ __global__ void __launch_bounds__(L_THREADS) balance_grad_kernel(const LParams p
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (l + G * v >= p.experts) continue;
-                const float d[1] = {live[u] ? k * z[u][v] * (c[v] - mean) : 0.0f};
-                store_unit<T, 1>(out + l + G * v, d);
+                store_one(out + l + G * v, live[u] ? k * z[u][v] * (c[v] - mean) : 0.0f);
             }
         }
     }
@@ -233,7 +302,9 @@ constexpr int64_t kMaxSlots = (1ll << 31) - 4096;
 bool bad_shape(int64_t tokens, int64_t experts, int64_t top) {
     return tokens < 0 || experts < 1 || top < 1 || top > 65535 || tokens > kMaxSlots / top;
 }
-int64_t sum_ctas(int64_t tokens) { return std::min<int64_t>(std::max<int64_t>(ceil_div(tokens, 32), 1), L_MAX_CTAS); }
+int64_t sum_ctas(int64_t tokens) { return tokens <= L_ALONE ? 1 : std::min<int64_t>(ceil_div(tokens, 32), L_MAX_CTAS); }
+// CTAs of the second kernel
+unsigned summers(int64_t experts) { return experts >= 256 ? 8 : experts >= 32 ? 4 : 1; }
 
 }  // namespace
 }  // namespace gptq
@@ -267,17 +338,35 @@ extern "C" int gptq_expert_balance(const void* Z, int dtype, int64_t tokens, int
     p.mask = mask;
     p.sums = static_cast<float*>(ws);
     p.counts = reinterpret_cast<int32_t*>(p.sums + ctas * experts);
+    p.total = counts;
     p.loss = loss;
     p.status = st.word;
     cudaError_t e = cudaSuccess;
     with_lanes(experts, [&](auto gv) {
         constexpr int G = decltype(gv)::G, V = decltype(gv)::V;
-        const size_t smem = 4 * ((size_t)(L_THREADS / G) * experts + experts + 1);   // at most 8 x 1024 words and 1025
+        // at most 16 x 256 or 8 x 1024 words, and 1025
+        const size_t smem = 4 * ((size_t)(summing_threads(V) / G) * experts + experts + 1);
         auto kern = dtype == GPTQ_BF16 ? balance_sums_kernel<__nv_bfloat16, G, V> : balance_sums_kernel<float, G, V>;
-        GPTQ_LAUNCH(K_BALANCE, s, e = launch_pdl(kern, dim3((unsigned)ctas), dim3(L_THREADS), smem, s, p));
+        GPTQ_LAUNCH(K_BALANCE, s, e = launch_pdl(kern, dim3((unsigned)ctas), dim3(summing_threads(V) + L_COUNTERS), smem, s, p));
     });
     GPTQ_CUDA_TRY(e);
-    GPTQ_LAUNCH(K_BALANCE, s, e = launch_pdl(balance_loss_kernel, dim3(1), dim3(32, 32), 0, s, p, (int)ctas, counts));
+    if (ctas == 1) return st.finish(s);
+    int wide = 1;
+    while (wide < ceil_div(experts + 1, summers(experts))) wide <<= 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(summers(experts));
+    cfg.blockDim = dim3(L_SUMMERS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = summers(experts);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    GPTQ_LAUNCH(K_BALANCE, s, e = cudaLaunchKernelEx(&cfg, balance_loss_kernel, p, (int)ctas, wide));
     GPTQ_CUDA_TRY(e);
     return st.finish(s);
 }
@@ -306,7 +395,7 @@ extern "C" int gptq_expert_balance_grad(const float* dloss, const void* Z, int d
     cudaError_t e = cudaSuccess;
     with_lanes(experts, [&](auto gv) {
         constexpr int G = decltype(gv)::G, V = decltype(gv)::V;
-        const int64_t ctas = std::min<int64_t>(ceil_div(tokens, L_THREADS / G * L_AHEAD), 8 * kSMs);
+        const int64_t ctas = std::min<int64_t>(ceil_div(tokens, L_THREADS / G * ahead(V)), 8 * kSMs);
         auto kern = dtype == GPTQ_BF16 ? balance_grad_kernel<__nv_bfloat16, G, V> : balance_grad_kernel<float, G, V>;
         GPTQ_LAUNCH(K_BALANCE, s, e = launch_pdl(kern, dim3((unsigned)ctas), dim3(L_THREADS), 0, s, p));
     });
