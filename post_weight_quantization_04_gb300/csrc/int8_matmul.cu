@@ -28,6 +28,7 @@ struct IParams {
     int experts;
     int ftiles;               // feature tiles
     int tokens_first;         // neighbouring tiles share their features, not their tokens
+    int width;                // the widest tile: a multiple of 16 up to W_T
     int splits;               // SPLIT: shares of the columns, each a pair of its own
     int box, raw;             // SPLIT: rows of a token box, and stages of codes
     int relu, bf16_out, vec;  // vec: bf16 rows that 16-byte stores can take
@@ -203,7 +204,7 @@ constexpr int W_K = 128;                   // columns per stage
 constexpr int W_RAW = 3, W_SLOTS = 3;      // stages of codes, and of expanded operands
 constexpr int W_MOST_RAW = 8;              // the former where token boxes are small
 constexpr int w_expand(bool split) { return split ? 12 : 16; }   // warps that expand: 8 + 4 or 8 + 8
-constexpr int w_threads(bool split) { return 32 * (split ? 20 : 28); }
+constexpr int w_threads(bool split) { return 32 * (split ? 20 : 28); }   // (whole groups of 4 warps: see the end)
 constexpr int W_CODES = W_F * W_K;         // bytes of one operand's codes per stage
 constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per stage
 constexpr uint32_t W_TMEM = 512, W_A0 = 256;
@@ -215,13 +216,13 @@ struct WMaps {
     CUtensorMap w, x[3];   // tokens: boxes of 128, 64 and 32 rows
 };
 
-// Token tiles of rows [lo, hi), all of one width: a multiple of 32, so both CTAs have whole groups of 16
-__device__ __forceinline__ int token_tiles(int lo, int hi) { return hi <= lo ? 0 : (hi - lo + W_T - 1) / W_T; }
+// Token tiles of rows [lo, hi), all of one width: a multiple of 16, as the MMA wants it
+__device__ __forceinline__ int token_tiles(int lo, int hi, int width) { return hi <= lo ? 0 : (hi - lo + width - 1) / width; }
 
 struct WTile {
     int e, f0;        // expert, first feature
-    int t0, n;        // first token, tokens (a multiple of 32, the last of which may be past hi)
-    int hi;           // the end of the expert's tokens
+    int t0, n;        // first token, tokens (a multiple of 16, the last of which may be past hi)
+    int hi;           // the end of its tokens, and of the expert's
 };
 
 // What finding a tile takes, in shared memory: token tiles before each expert, and each one's rows
@@ -246,9 +247,10 @@ __device__ __forceinline__ WTile find_tile(const IParams& p, const WRows& w, uin
     const int first = w.start[a], tiles = w.start[a + 1] - first;
     const int2 r = w.rows[a];
     t.hi = r.y;
-    const int width = ((int)((uint32_t)(r.y - r.x + tiles - 1) / (uint32_t)tiles) + 31) & ~31;
+    const int width = max(((int)((uint32_t)(r.y - r.x + tiles - 1) / (uint32_t)tiles) + 15) & ~15, 32);
     t.t0 = r.x + (tt - first) * width;
-    t.n = min(max(t.hi - t.t0 + 31, 32) & ~31, width);
+    t.n = min(max(t.hi - t.t0 + 15, 32) & ~15, width);
+    t.hi = min(t.hi, t.t0 + t.n);
     return t;
 }
 
@@ -303,12 +305,6 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-    return v;
-}
-
 __device__ __forceinline__ void commit_to(uint32_t bar, uint32_t ctas) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
@@ -455,7 +451,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             int lo = 0, hi = 0;
             if (e0 + lane < p.experts) expert_rows(p, e0 + lane, &lo, &hi);
-            const int n = token_tiles(lo, hi);
+            const int n = token_tiles(lo, hi, p.width);
             int inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -577,6 +573,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         // (SPLIT: four warps share the tokens' rows and columns)
         const int pieces = !SPLIT || weights ? 2 : row_warps, first_piece = member / row_warps * pieces;
         const uint32_t column = tmem + ((uint32_t)(32 * q) << 16) + W_A0 + 16 * first_piece;
+        const uint32_t wide_remote = in_cta(wide_full(0), even);   // (mapa in the loop cost 5 %)
         int stage = 0, slot = 0;
         uint32_t rphase = 0, sphase = 0;
         for (uint32_t i = first; i < ntiles && ok; i += step) {
@@ -631,7 +628,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
                 __syncwarp();
                 // (arrive_cluster's CTA scope: each SM's tensor core reads what its own CTA wrote, which the fence
                 // above has put before the arrival; .release.cluster held a warp up for 900 to 1500 cycles a stage)
-                if (lane == 0) arrive_cluster(in_cta(wide_full(slot), even));
+                if (lane == 0) arrive_cluster(wide_remote + 8u * slot);
                 if (++stage == raws) {
                     stage = 0;
                     rphase ^= 1u;
@@ -643,22 +640,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
             }
         }
     } else if constexpr (SPLIT) {
-        // ---- the sums to this CTA's shared memory, [token][feature], which no copy or MMA uses any more
-        if (first < ntiles) {   // (one tile per cluster)
-            const WTile t = find_tile(p, w, first);
-            ok = wait_all(tfull, 0, limit);
-            tc_fence_after();
-            if (ok) {
-                const int q = warp & 3;
-                for (int c = 0; c < t.n; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) reinterpret_cast<uint32_t*>(smem)[(c + j) * W_F + 32 * q + lane] = v[j];
-                }
-            }
-        }
+        if (first < ntiles) ok = wait_all(tfull, 0, limit);   // (one tile per cluster)
     } else {
         // ------------------------------- epilogue -----------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
@@ -684,7 +666,8 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
             if (!ok) break;
             tc_fence_after();
             if (p.vec && !far) {
-                // packed before the buffer is free, stored after it
+                // packed before the buffer is free, stored after it; a last tile, that nobody waits for, as it is packed
+                const bool final = i + step >= ntiles;
                 uint32_t v[4][4][4];
                 float sw[4];
 #pragma unroll
@@ -702,24 +685,22 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
                             for (int u = 0; u < 2; ++u) {
                                 const float2 s = *reinterpret_cast<const float2*>(sx + 32 * c + 8 * (j + u) + 2 * (lane & 3));
 #pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    v[c][j + u][g] = pair_bf16(a[g >> 1][4 * u + 2 * (g & 1)], a[g >> 1][4 * u + 2 * (g & 1) + 1], sw[g], s);
+                                for (int g = 0; g < 4; ++g) {
+                                    const uint32_t y = pair_bf16(a[g >> 1][4 * u + 2 * (g & 1)], a[g >> 1][4 * u + 2 * (g & 1) + 1], sw[g], s);
+                                    v[c][j + u][g] = relu ? relu_bf16(y) : y;
+                                }
                             }
                         }
+                        if (final) turn_tokens(p, v[c], t.t0 + c0 + 32 * c, t.hi, f0, turn);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_cta(tfree, even));
+                if (!final) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c0 + 32 * c < t.n) {
-                        if (relu) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[c][j >> 2][j & 3] = relu_bf16(v[c][j >> 2][j & 3]);
-                        }
-                        turn_tokens(p, v[c], t.t0 + c0 + 32 * c, t.hi, f0, turn);
-                    }
+                    for (int c = 0; c < 4; ++c)
+                        if (c0 + 32 * c < t.n) turn_tokens(p, v[c], t.t0 + c0 + 32 * c, t.hi, f0, turn);
                 }
             } else {
                 const int f = f0 + lane;
@@ -745,39 +726,53 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
     __syncthreads();
     cluster_sync();   // no CTA leaves, or frees TMEM, while another may still use it
     if constexpr (SPLIT) {
-        if (first < ntiles) {
-            const WTile t = find_tile(p, w, first);
-            const int a = t.n * share / p.splits, b = t.n * (share + 1) / p.splits;   // this pair's tokens
-            const int f = t.f0 + (int)half * W_F + 4 * lane;   // four features per lane, a token per warp
-            const uint32_t mine = sbase + 16 * lane;
-            const float4 sw = *reinterpret_cast<const float4*>(token_scales + W_T + 4 * lane);
-#pragma unroll 2
-            for (int c = a + warp; c < min(b, t.hi - t.t0); c += w_threads(true) / 32) {
-                const float sx = token_scales[c];
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int j = 0; j < p.splits; ++j) {
-                    const float4 u = ld_cluster(in_cta(mine + 4 * c * W_F, 2 * j + half));
-                    s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
-                }
-                float v[4] = {scaled(s.x, sw.x, sx), scaled(s.y, sw.y, sx), scaled(s.z, sw.z, sx), scaled(s.w, sw.w, sx)};
-                if (p.vec) {
-                    if (f >= p.N) continue;
-                    if (p.relu) {
+        // No copy or MMA of the cluster uses its shared memory any more. Each pair sends the others their parts of its sums and
+        // adds what it got to its own; all warps take part, each in its quarter of the lanes. ([source][token / 4][feature][4])
+        tc_fence_after();
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int feature = 32 * (warp & 3) + lane, mover = warp >> 2;
+        const WTile t = first < ntiles ? find_tile(p, w, first) : WTile{0, 0, 0, 0, 0};
+        const int own = t.n / p.splits, blocks = (own + 31) / 32;   // (n is a multiple of 16)
+        for (int b = mover; b < blocks * (p.splits - 1); b += w_threads(true) / 128) {
+            const int other = b / blocks, to = other < share ? other : other + 1, c = b % blocks * 32;
+            const uint32_t dst = in_cta(sbase, 2 * to + half) + (uint32_t)((share < to ? share : share - 1) * own + c) * (W_F * 4) + feature * 16;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(lanes + to * own + c, v);
+            tmem_ld_wait();
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) v[g] = relu_of(v[g]);
-                    }
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.Y) + (int64_t)(t.t0 + c) * p.ldy + f) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                } else {
+            for (int u = 0; u < 8; ++u)
+                if (c + 4 * u < own)
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + u * (W_F * 16)), "r"(v[4 * u]),
+                                 "r"(v[4 * u + 1]), "r"(v[4 * u + 2]), "r"(v[4 * u + 3])
+                                 : "memory");
+        }
+        cluster_sync();   // all have what they wait for, and nobody's shared memory is touched any more
+        for (int b = mover; b < blocks; b += w_threads(true) / 128) {
+            const int c = 32 * b, tok = share * own + c;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(lanes + tok, v);
+            tmem_ld_wait();
+            for (int j = 0; j < p.splits - 1; ++j) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if (f + g < p.N) store_result(p, t.t0 + c, f + g, v[g]);
+                for (int u = 0; u < 8; ++u) {
+                    if (c + 4 * u >= own) break;
+                    const uint4 a = lds128(sbase + (uint32_t)(j * own + c + 4 * u) * (W_F * 4) + feature * 16);
+                    v[4 * u] = __float_as_uint(__uint_as_float(v[4 * u]) + __uint_as_float(a.x));
+                    v[4 * u + 1] = __float_as_uint(__uint_as_float(v[4 * u + 1]) + __uint_as_float(a.y));
+                    v[4 * u + 2] = __float_as_uint(__uint_as_float(v[4 * u + 2]) + __uint_as_float(a.z));
+                    v[4 * u + 3] = __float_as_uint(__uint_as_float(v[4 * u + 3]) + __uint_as_float(a.w));
                 }
             }
+            const int f = t.f0 + (int)half * W_F + feature, last = min(t.hi - t.t0, share * own + own) - tok;
+            if (f < p.N) {
+                const int64_t at = (int64_t)(t.t0 + tok) * p.ldy + f;
+                const float sw = token_scales[W_T + feature];
+                if (p.bf16_out) store_tokens(static_cast<__nv_bfloat16*>(p.Y) + at, p.ldy, v, sw, token_scales + tok, p.relu != 0, last);
+                else store_tokens(static_cast<float*>(p.Y) + at, p.ldy, v, sw, token_scales + tok, p.relu != 0, last);
+            }
         }
+        tc_fence_before();
         __syncthreads();
-        cluster_sync();   // nor while another reads its sums
     }
     if (warp == 1) {
         __syncwarp();
@@ -855,6 +850,36 @@ int launch_pairs(const WMaps& m, const IParams& p, int64_t most_tiles, cudaStrea
     return GPTQ_OK;
 }
 
+struct Plan {
+    int width, splits;
+};
+// The width of token tiles, and in how many shares the columns are split: what takes the fewest cycles by what was measured.
+// A stage takes 1080 whatever the width (an MMA of 16 columns with its weights in TMEM takes 128, with 256 tokens or fewer),
+// a round of tiles 1700 more, a launch 10000; where the columns are split a launch takes 6500 and the sums' exchange 64 for
+// each token. With experts their rows are not known here, so tiles are as wide as can be. *most: the most tiles.
+// Features x columns 4096 x 4096, us: 512 tokens as 256 x 2 shares 20.1, as 256 and 128 in whole 25.1 and 24.5; 256 tokens as 128 x 2
+// 15.7, as 256 x 2 19.7, as 64 x 2 in two rounds 26.3; 64 tokens as 64 x 2 13.4, as 256 x 2 16.6.
+Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, int64_t pairs, int64_t* most) {
+    const int64_t ftiles = ceil_div(N, W_PF), stages = ceil_div(K, W_K);
+    Plan best = {W_T, 1};
+    int64_t least = -1;
+    for (int64_t tt = ceil_div(T, W_T);; ++tt) {
+        const int width = by_expert ? W_T : (int)std::max<int64_t>(ceil_div(ceil_div(T, tt), 16) * 16, 32);
+        const int64_t tiles = (ceil_div(T, width) + (by_expert ? std::min(experts, T) : 0)) * ftiles;
+        for (int k = 1; k <= 4; k <<= 1) {
+            if (k > 1 && (tiles * k > pairs || stages < 2 * k || tiles > clusters_at_once(k))) break;
+            const int64_t cycles = k > 1 ? ceil_div(stages, k) * 1080 + 6500 + 64 * width
+                                         : ceil_div(tiles, pairs) * (stages * 1080 + 1700) + 10000;
+            if (least < 0 || cycles < least) {
+                least = cycles;
+                best = {width, k};
+                *most = tiles;
+            }
+        }
+        if (by_expert || width == 32 || tiles > pairs) return best;   // (narrower tiles only pay while all run at once)
+    }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int64_t kMaxDim = (1ll << 31) - 512;
 
@@ -929,15 +954,12 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
     if (!code_map(&m.w, w_codes, experts * N, K, W_F)) return GPTQ_ERR_CUDA;
     for (int i = 0; i < 3; ++i)
         if (!code_map(&m.x[i], x_codes, T, K, W_F >> i)) return GPTQ_ERR_CUDA;
-    // an expert's last tile may be partial
-    const int64_t most = (ceil_div(T, W_T) + (offsets ? std::min(experts, T) : 0)) * p.ftiles;
-    // few tiles: as many shares of the columns as the device holds at once, of four stages or more each
-    p.splits = 1;
-    for (int k = 4; k > 1 && p.splits == 1; k >>= 1)
-        if (most * k <= device_sm_count() / 2 && ceil_div(K, W_K) >= 4 * k && most <= clusters_at_once(k)) p.splits = k;
+    int64_t most;
+    const Plan plan = plan_of(T, N, K, offsets != nullptr, experts, device_sm_count() / 2, &most);
+    p.width = plan.width;
+    p.splits = plan.splits;
     if (p.splits > 1) {
-        const int64_t rows = offsets ? std::min<int64_t>(T, W_T) : ceil_div(T, ceil_div(T, W_T));   // of the widest tile
-        p.box = rows <= 64 ? 32 : rows <= 128 ? 64 : 128;
+        p.box = p.width <= 64 ? 32 : p.width <= 128 ? 64 : 128;
         p.raw = std::min(W_MOST_RAW, (W_RING - W_SLOTS * p.box * 2 * W_K) / (W_CODES + p.box * W_K));
     }
     const int rc = p.splits > 1 ? launch_pairs<true>(m, p, most, s) : launch_pairs<false>(m, p, most, s);
