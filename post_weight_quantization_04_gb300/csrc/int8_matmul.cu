@@ -66,9 +66,18 @@ __device__ __forceinline__ void store_result(const IParams& p, int64_t row, int 
 // (ranges that were clamped are an error)
 __device__ __forceinline__ void zero_rest(const IParams& p, int cta, int ctas) {
     const int first = min(max(p.offsets[0], 0), p.T), last = max(min(p.offsets[p.experts], p.T), first);
+    const int64_t size = p.bf16_out ? 2 : 4;
     for (int r = cta; r < p.T - (last - first); r += ctas) {
         const int64_t row = r < first ? r : r + (last - first);
-        for (int f = threadIdx.x; f < p.N; f += blockDim.x) store_result(p, row, f, 0.0f);
+        char* y = static_cast<char*>(p.Y) + row * p.ldy * size;
+        const int64_t bytes = p.N * size;
+        if ((reinterpret_cast<uintptr_t>(y) & 15) == 0) {
+            for (int64_t b = threadIdx.x * 16; b < (bytes & ~(int64_t)15); b += blockDim.x * 16)
+                *reinterpret_cast<uint4*>(y + b) = make_uint4(0, 0, 0, 0);
+            for (int64_t b = (bytes & ~(int64_t)15) + threadIdx.x * 2; b < bytes; b += blockDim.x * 2) *reinterpret_cast<uint16_t*>(y + b) = 0;
+        } else {
+            for (int64_t b = threadIdx.x * 2; b < bytes; b += blockDim.x * 2) *reinterpret_cast<uint16_t*>(y + b) = 0;
+        }
     }
 }
 
@@ -86,7 +95,10 @@ __device__ __forceinline__ void to_half(uint32_t w, uint32_t& lo, uint32_t& hi) 
 // of two features and of a token out of eight, expands them to fp16 in its registers and multiplies them with
 // mma.sync (m16n8k16; any order of the columns will do if both operands have the same), 8 tokens at a time. No shared
 // memory, barriers or TMEM lie between the loads and the products; the warps' sums are added at the end.
-constexpr int F_WARPS = 8, F_FEATURES = 16;
+// While all CTAs run at once, what counts is one row's loads in flight: 8 warps with 8 steps each (4096 x 4096, one token: 5.7 us; 4
+// steps 6.3). With more CTAs than that small ones that follow each other closely do better: 4 warps with 2 steps (8 experts of
+// 14336 x 4096, 16 rows: 67 us, 7.0 TB/s; the others 81 and 90. 14336 x 4096, one token: 13.5 and 15.2).
+constexpr int F_FEATURES = 16;
 
 __device__ __forceinline__ void mma_half(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -97,9 +109,9 @@ __device__ __forceinline__ void mma_half(float (&c)[4], uint32_t a0, uint32_t a1
 // (Plain loads: this kernel starts while the one before may still be writing its operands, so they are not
 // read-only for as long as it runs, which is what the read-only path asks for.)
 // tokens t0 .. t0 + n - 1 (n <= 8 NT) of expert e times features f0 .. f0 + 15
-template <int NT>
+// AHEAD: steps of 64 columns in flight
+template <int NT, int WARPS, int AHEAD>
 __device__ __forceinline__ void few_rows(const IParams& p, int e, int t0, int n, int f0, float* part) {
-    constexpr int AHEAD = NT == 4 ? 2 : 4;   // steps of 64 columns in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, col = 16 * (lane & 3);
     const int8_t* wc = p.wc + (int64_t)e * p.N * p.pitch + col;
     const int8_t* w0 = wc + min(f0 + g, p.N - 1) * p.pitch;
@@ -108,11 +120,11 @@ __device__ __forceinline__ void few_rows(const IParams& p, int e, int t0, int n,
 #pragma unroll
     for (int j = 0; j < NT; ++j) x[j] = p.xc + (t0 + min(8 * j + g, n - 1)) * p.pitch + col;
     float acc[NT][4] = {};
-    for (int64_t c0 = warp * 64; c0 < p.pitch; c0 += AHEAD * F_WARPS * 64) {
+    for (int64_t c0 = warp * 64; c0 < p.pitch; c0 += AHEAD * WARPS * 64) {
         uint4 a[AHEAD][2], b[AHEAD][NT];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
-            const int64_t c = c0 + u * F_WARPS * 64;
+            const int64_t c = c0 + u * WARPS * 64;
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const bool in = c + col < p.pitch;
             a[u][0] = in ? *reinterpret_cast<const uint4*>(w0 + c) : zero;
@@ -143,20 +155,21 @@ __device__ __forceinline__ void few_rows(const IParams& p, int e, int t0, int n,
         for (int i = 0; i < 4; ++i)   // feature g (+ 8), token 8 j + 2 (lane % 4) (+ 1)
             part[(warp * 8 * NT + 8 * j + 2 * (lane & 3) + (i & 1)) * F_FEATURES + g + 8 * (i >> 1)] = acc[j][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < F_FEATURES * n; i += 32 * F_WARPS) {
+    for (int i = threadIdx.x; i < F_FEATURES * n; i += 32 * WARPS) {
         const int t = t0 + i / F_FEATURES, f = f0 + i % F_FEATURES;
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < F_WARPS; ++k) v += part[k * 8 * NT * F_FEATURES + i];
+        for (int k = 0; k < WARPS; ++k) v += part[k * 8 * NT * F_FEATURES + i];
         if (f < p.N) store_result(p, t, f, scaled(v, p.xs[t], p.ws[(int64_t)e * p.N + f]));
     }
     __syncthreads();
 }
 
 // MOST: groups of 8 tokens at a time; with fewer, more CTAs fit an SM
-template <int MOST>
-__global__ void __launch_bounds__(32 * F_WARPS, MOST == 1 ? 3 : 2) int8_few_rows_kernel(const IParams p) {
-    __shared__ float part[F_WARPS][F_FEATURES * 8 * MOST];
+template <int MOST, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 2 : 8) int8_few_rows_kernel(const IParams p) {
+    constexpr int AHEAD = WARPS == 8 ? 8 / MOST : 2;
+    __shared__ float part[WARPS][F_FEATURES * 8 * MOST];
     const int e = blockIdx.y, f0 = blockIdx.x * F_FEATURES;
     pdl_trigger();
     pdl_wait();
@@ -168,9 +181,9 @@ __global__ void __launch_bounds__(32 * F_WARPS, MOST == 1 ? 3 : 2) int8_few_rows
     expert_rows(p, e, &lo, &hi);
     for (int t = lo; t < hi; t += 8 * MOST) {
         const int n = min(hi - t, 8 * MOST);
-        if (MOST >= 4 && n > 16) few_rows<MOST >= 4 ? 4 : 1>(p, e, t, n, f0, part[0]);
-        else if (MOST >= 2 && n > 8) few_rows<MOST >= 2 ? 2 : 1>(p, e, t, n, f0, part[0]);
-        else few_rows<1>(p, e, t, n, f0, part[0]);
+        if (MOST >= 4 && n > 16) few_rows<MOST >= 4 ? 4 : 1, WARPS, AHEAD>(p, e, t, n, f0, part[0]);
+        else if (MOST >= 2 && n > 8) few_rows<MOST >= 2 ? 2 : 1, WARPS, AHEAD>(p, e, t, n, f0, part[0]);
+        else few_rows<1, WARPS, AHEAD>(p, e, t, n, f0, part[0]);
     }
 }
 
@@ -941,12 +954,13 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
     if (K == 0 || few_rows_pay(T, N, K, offsets != nullptr, experts)) {
         cudaError_t e = cudaSuccess;
         const dim3 grid((unsigned)ceil_div(N, F_FEATURES), (unsigned)(experts + (offsets ? 1 : 0)));
-        auto go = [&](auto kern) { GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(kern, grid, dim3(32 * F_WARPS), 0, s, p)); };
+        auto go = [&](auto kern, int warps) { GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(kern, grid, dim3(32 * warps), 0, s, p)); };
         // (with experts the rows of each are not known here: mostly a share of them)
         const int64_t rows = offsets ? T / experts : T;
-        if (rows <= 8) go(int8_few_rows_kernel<1>);
-        else if (rows <= 16) go(int8_few_rows_kernel<2>);
-        else go(int8_few_rows_kernel<4>);
+        if (rows > 16) go(int8_few_rows_kernel<4, 8>, 8);
+        else if (rows > 8) go(int8_few_rows_kernel<2, 8>, 8);
+        else if ((int64_t)grid.x * experts <= 2 * device_sm_count()) go(int8_few_rows_kernel<1, 8>, 8);
+        else go(int8_few_rows_kernel<1, 4>, 4);
         GPTQ_CUDA_TRY(e);
         return st.finish(s);
     }
