@@ -899,16 +899,16 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 // Whether the kernel for few rows is the faster one. Measured (us, few rows / pairs; weights from memory, features x
 // columns):
 //                   1 token     16 tokens    32 tokens    64 tokens
-//    4096 x 4096    6.3 / 11.0   6.9 / 11.3   9.0 / 11.4  15.2 / 12.3
-//   14336 x 4096   14.1 / 21.7  18.7 / 21.7  25.5 / 21.9  43.5 / 22.6
-//    4096 x 14336  15.0 / 23.8  17.6 / 24.1  25.1 / 24.1  44.6 / 25.2
-//    1024 x 4096    4.7 /  8.1   5.5 /  8.2   7.7 /  8.3  13.1 /  9.1
+//    4096 x 4096    5.7 / 11.0   7.0 / 11.3   9.4 / 12.9  15.2 / 13.0
+//   14336 x 4096   13.7 / 21.7  18.7 / 21.7  25.5 / 21.9  43.5 / 22.6
+//    4096 x 14336  14.5 / 23.8  17.7 / 24.1  25.1 / 24.1  44.6 / 25.2
+//    1024 x 4096    4.2 /  8.1   5.7 /  8.2   7.7 /  8.3  13.1 /  9.1
 //    4096 x 1024                                          7.0 /  8.3 (96 tokens 9.4 / 9.0)
 //     512 x 512                                           4.2 /  6.5
-//   experts, rows at random: 16 of 1024 x 4096, 32 rows 16.6 / 22.7, 64 rows 18.5 / 22.9, 128 rows 21 / 23.0, 256 rows
-//   27 / 23.0; 8 of 14336 x 4096, 16 rows 80 / 106, 64 rows 115 / 108
+// Experts, rows at random: 16 of 1024 x 4096, 32 rows 14.4 / 22.7, 96 rows 19.3 / 22.6, 128 rows 21.1 / 22.6, 192 rows 25.1 / 22.6;
+// 8 of 14336 x 4096, 16 rows 69 / 106, 64 rows 91 / 106; 16 of 512 x 1024, 256 rows 9.2 / 10.1; 32 of 700 x 300, 400 rows 7.3 / 13.0
 bool few_rows_pay(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts) {
-    if (by_expert) return T <= 4 * experts;
+    if (by_expert) return T <= 8 * experts || (T <= 16 * experts && N * K <= 600000);
     return T <= 16 || (T <= 32 && N * K <= 24000000) || (T <= 64 && K <= 1024 && N * K <= 5000000);
 }
 
