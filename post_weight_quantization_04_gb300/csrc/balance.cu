@@ -44,11 +44,6 @@ struct LParams {
     int* status;
 };
 
-__device__ __forceinline__ float load_one(const float* p) { return *p; }
-__device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // a word of another CTA's shared memory
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
     uint32_t v;
@@ -97,8 +92,9 @@ __device__ __forceinline__ float loss_of(const LParams& p, float dot, int32_t to
     return (float)p.experts / (float)p.top * (dot / n / n);
 }
 
-// Each CTA's sums of p and counts over a contiguous share of the tokens. Bound by latency: two loads and two trees of shuffles
-// one after another for each few tokens of a warp.
+// Each CTA's sums of p and counts over a contiguous share of the tokens; with one CTA the loss too. Bound by latency: a load, two
+// trees of shuffles and a sum over the warps, then (in a second launch) one over the CTAs. 16384 tokens x 64 experts fp32 11.5 us for
+// both, 33 x 64 3.1, 16384 x 1024 61; with counting and softmax one after another in half the CTAs 16.7, 6.0 and 91.
 template <typename T, int G, int V>
 __global__ void __launch_bounds__(summing_threads(V) + L_COUNTERS) balance_sums_kernel(const LParams p) {
     extern __shared__ float sh[];                               // [groups][experts], then counts [experts + 1]
@@ -230,6 +226,7 @@ __global__ void __launch_bounds__(L_SUMMERS) balance_loss_kernel(const LParams p
     if (gridDim.x > 1) cluster_sync();   // no CTA leaves while its sum is read
 }
 
+// 16384 tokens x 64 experts fp32 5.8 us, x 1024 32 us (4.2 TB/s): latency, then instructions.
 template <typename T, int G, int V>
 __global__ void __launch_bounds__(L_THREADS) balance_grad_kernel(const LParams p) {
     constexpr int GROUPS = L_THREADS / G;
