@@ -89,22 +89,42 @@ __device__ __forceinline__ uint4 load_granule(const T* row, int cols, int o, int
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// words of (a, b) from `bytes` on (0 .. 15, a multiple of 2)
-__device__ __forceinline__ uint4 from_byte(const uint4& a, const uint4& b, int bytes) {
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (bytes & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+// Calls f(whole words) with a constant for the words of a byte offset (0 .. 15) of bf16: the shift below then takes one
+// permutation per word, and no selection. fp32 takes two selections per word instead and FOR_ALL words: the branches made the
+// gradient's loads of four rows wait for one another (16384 x 4095 203 us so, 241 with them).
+template <typename T, int FOR_ALL, typename F>
+__device__ __forceinline__ void with_words(int bytes, F f) {
+    if constexpr (sizeof(T) == 4) {
+        f(std::integral_constant<int, FOR_ALL>());
+    } else {
+        switch (bytes >> 2) {
+            case 0: f(std::integral_constant<int, 0>()); break;
+            case 1: f(std::integral_constant<int, 1>()); break;
+            case 2: f(std::integral_constant<int, 2>()); break;
+            default: f(std::integral_constant<int, 3>()); break;
+        }
     }
-    if (bytes & 4) {
+}
+
+// the four words of w from `bytes` on, of which WORDS are whole words (bf16)
+template <typename T, int WORDS>
+__device__ __forceinline__ uint4 shifted(uint32_t (&w)[8], int bytes) {
+    if constexpr (sizeof(T) == 4) {
+        if (bytes & 8) {
 #pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    if (bytes & 2) {
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+        }
+        if (bytes & 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            for (int i = 0; i < 4; ++i) w[i] = w[i + 1];
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+        const uint32_t selector = bytes & 2 ? 0x5432u : 0x3210u;
+        const uint32_t* v = w + WORDS;
+        return make_uint4(__byte_perm(v[0], v[1], selector), __byte_perm(v[1], v[2], selector), __byte_perm(v[2], v[3], selector),
+                          __byte_perm(v[3], v[4], selector));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Granule j of a row, to be made unit j by to_words
@@ -114,36 +134,33 @@ __device__ __forceinline__ uint4 load_raw(const T* row, int cols, int j) {
     return j * kUnit<T> < cols ? *reinterpret_cast<const uint4*>(row + j * kUnit<T>) : make_uint4(0, 0, 0, 0);
 }
 
-// a lane's neighbour along the warp's units: the next lane's, and for the last lane the first lane's next one
-__device__ __forceinline__ uint4 next_of(const uint4& a, const uint4& after) {
-    const int lane = threadIdx.x & 31, from = (lane + 1) & 31;
-    uint4 n;
-    n.x = __shfl_sync(0xffffffffu, lane == 0 ? after.x : a.x, from), n.y = __shfl_sync(0xffffffffu, lane == 0 ? after.y : a.y, from);
-    n.z = __shfl_sync(0xffffffffu, lane == 0 ? after.z : a.z, from), n.w = __shfl_sync(0xffffffffu, lane == 0 ? after.w : a.w, from);
-    return n;
-}
-
 // The warp's units from j on (this lane's first one; 32 apart) from the granules that the lanes have loaded, in place; zeros past the
 // columns. (The last lane reads the next warp's first granule here, most likely from L1: before any barrier behind which that
 // warp may write to it.)
 template <typename T, bool ANY, int UNITS>
 __device__ __forceinline__ void to_words(const T* row, int cols, int j, uint4 (&a)[UNITS]) {
     if constexpr (ANY) {
-        const int o = row_start(row);
+        const int o = row_start(row), lane = threadIdx.x & 31;
         if (o == 0) return;
         uint4 past = make_uint4(0, 0, 0, 0);   // what follows the warp's last granule
-        if ((threadIdx.x & 31) == 31) past = load_granule(row, cols, o, j + 32 * (UNITS - 1) + 1);
+        if (lane == 31) past = load_granule(row, cols, o, j + 32 * (UNITS - 1) + 1);
+        const int bytes = o * (int)sizeof(T);
+        with_words<T, 2>(bytes, [&](auto words) {
+            constexpr int W = decltype(words)::value;
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            uint4 n;
-            if (i + 1 < UNITS) {
-                n = next_of(a[i], a[i + 1]);
-            } else {
-                n = next_of(a[i], a[i]);
-                if ((threadIdx.x & 31) == 31) n = past;
+            for (int i = 0; i < UNITS; ++i) {
+                // the next lane's granule behind this one's, and for the last lane the first lane's next
+                uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w};
+                const uint4 after = i + 1 < UNITS ? a[i + 1 < UNITS ? i + 1 : i] : past;
+                const uint32_t first[4] = {after.x, after.y, after.z, after.w};
+#pragma unroll
+                for (int k = 0; k <= W; ++k) {
+                    w[4 + k] = __shfl_sync(0xffffffffu, i + 1 < UNITS && lane == 0 ? first[k] : w[k], (lane + 1) & 31);
+                    if (i + 1 == UNITS && lane == 31) w[4 + k] = first[k];
+                }
+                a[i] = shifted<T, W>(w, bytes);
             }
-            a[i] = from_byte(a[i], n, o * (int)sizeof(T));
-        }
+        });
     }
 }
 
@@ -191,35 +208,48 @@ __device__ __forceinline__ void store_units(T* row, int cols, int j, const uint4
             if ((j + 32 * i) * N < cols) *reinterpret_cast<uint4*>(row + (j + 32 * i) * N) = p[i];
     } else {
         const int o = row_start(row), lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            const int c = (j + 32 * i) * N - o;   // the first column of this unit's granule
-            uint4 g = p[i];
-            if (o != 0) {
-                // the unit before: the lane before's, and for the first lane the last one's before
-                const int from = (lane + 31) & 31;
-                const uint4 b = p[i > 0 ? i - 1 : 0];
-                uint4 q;
-                q.x = __shfl_sync(0xffffffffu, lane == 31 ? b.x : p[i].x, from), q.y = __shfl_sync(0xffffffffu, lane == 31 ? b.y : p[i].y, from);
-                q.z = __shfl_sync(0xffffffffu, lane == 31 ? b.z : p[i].z, from), q.w = __shfl_sync(0xffffffffu, lane == 31 ? b.w : p[i].w, from);
-                g = from_byte(q, p[i], 16 - o * (int)sizeof(T));
-            }
-            // of its first granule the warp has only the elements from o on, and of the one after its last, o
-            const bool first = o != 0 && i == 0 && lane == 0, last = o != 0 && i == UNITS - 1 && lane == 31;
-            const bool whole = !first && c >= 0 && c + N <= cols;
-            if (whole) *reinterpret_cast<uint4*>(row + c) = g;
-            if (!whole) {
+        // writes granule i, or those of its elements from `from` on that are the row's
+        auto put_granule = [&](int i, const uint4& g, int from) {
+            const int c = (j + 32 * i) * N - o;   // its first column
+            if (from == 0 && c >= 0 && c + N <= cols) {
+                *reinterpret_cast<uint4*>(row + c) = g;
+            } else {
                 const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
                 for (int e = 0; e < N; ++e)
-                    if ((!first || e >= o) && c + e >= 0 && c + e < cols) put(row + c + e, w, e);
+                    if (e >= from && c + e >= 0 && c + e < cols) put(row + c + e, w, e);
             }
-            if (last) {
-                const uint32_t w[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+        };
+        if (o == 0) {
 #pragma unroll
-                for (int e = 0; e < N; ++e)
-                    if (e >= N - o && c + o + e < cols) put(row + c + o + e, w, e);
+            for (int i = 0; i < UNITS; ++i) put_granule(i, p[i], 0);
+            return;
+        }
+        const int bytes = 16 - o * (int)sizeof(T);   // of the unit before that a granule does not have
+        with_words<T, 1>(bytes, [&](auto words) {
+            constexpr int W = decltype(words)::value;
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
+                // the unit before in front of this one: the lane before's, and for the first lane the last one's before
+                const uint32_t own[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+                const uint4 b = p[i > 0 ? i - 1 : 0];
+                const uint32_t before[4] = {b.x, b.y, b.z, b.w};
+                uint32_t w[8] = {};
+#pragma unroll
+                for (int k = W; k < 4; ++k) w[k] = __shfl_sync(0xffffffffu, lane == 31 ? before[k] : own[k], (lane + 31) & 31);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[4 + k] = own[k];
+                // (of its first granule the warp has only the elements from o on)
+                put_granule(i, shifted<T, W>(w, bytes), i == 0 && lane == 0 ? o : 0);
             }
+        });
+        if (lane == 31) {   // and of the one after its last, the first o
+            const uint4 l = p[UNITS - 1];
+            const uint32_t w[4] = {l.x, l.y, l.z, l.w};
+            const int c = (j + 32 * (UNITS - 1)) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (e >= N - o && c + e < cols) put(row + c + e, w, e);
         }
     }
 }
@@ -316,12 +346,6 @@ __device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps, F ag
     return rsqrtf(again(f) * inv_n + eps * f * f) * f;
 }
 
-// the most threads of a row: bf16 units, of 8 columns, take more registers than 1024 threads have
-template <typename T>
-constexpr int row_threads() {
-    return sizeof(T) == 2 ? 512 : 1024;
-}
-
 // the row of X that row r is, or -1
 __device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
     if (!p.index) return r;
@@ -336,11 +360,12 @@ __device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
 // are persistent, and the next row's loads are under way while this one is reduced and written. Four units per thread, so
 // that what every warp does for a row (its sums, scale and reciprocals) is shared by more columns.
 // Bound by memory, and for bf16 nearly as much by instructions (52 to 63 % of the issue slots). 16384 x 4096: bf16 37 us
-// (5.4 TB/s), with the norm and a residual 78 (6.0); fp32 51 (6.6) and 146 (6.0). With two units per thread bf16 took 39 and
+// (5.4 TB/s), with the norm and a residual 78 (6.0); fp32 51 (6.6) and 137 (6.4). With two units per thread bf16 took 39 and
 // 91, with a CTA for each row and no loads ahead 52 and 107. Rows at odd addresses pay for the shifting: 16384 x 4095
-// bf16 56 and 138 us (column by column 109 and 278).
-template <typename T, int UNITS, bool NORM, bool ANY>
-__global__ void __launch_bounds__(row_threads<T>(), 1) int8_rows_kernel(const RowParams p) {
+// bf16 54 and 133 us (column by column 109 and 278), fp32 65 and 165. MOST is 512 or, for longer rows of fp32, 1024 threads:
+// the norm of 16384 x 4095 fp32 took 202 us within the 64 registers of the latter, the quantisation 74 instead of 65 with more.
+template <typename T, int UNITS, bool NORM, bool ANY, int MOST>
+__global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_rows_kernel(const RowParams p) {
     constexpr int N = kUnit<T>;
     __shared__ float sum_part[2][32];
     __shared__ uint32_t max_part[2][32];
@@ -559,9 +584,9 @@ __device__ __forceinline__ float group_sum(float v, float* part, int warps, int 
 // the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added in turn at the
 // end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written.
 // Bound by memory: 16384 x 4096 bf16 88 us (6.1 TB/s), fp32 163 (6.6), both with the sum over the CTAs (4 us). Without the
-// loads ahead and with the gain read for every row it took 199.
-template <typename T, int UNITS, bool ANY>
-__global__ void __launch_bounds__(UNITS <= 2 ? 512 : row_threads<T>(), 1) int8_norm_grad_kernel(const GradParams p) {
+// loads ahead and with the gain read for every row it took 199. Rows at odd addresses: 16384 x 4095 bf16 180, fp32 203.
+template <typename T, int UNITS, bool ANY, int MOST>
+__global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParams p) {
     constexpr int N = kUnit<T>;
     constexpr bool AHEAD = UNITS <= 2;   // (and the gain stays in registers)
     extern __shared__ float sums[];   // [columns of the units], where there are several groups
@@ -716,20 +741,22 @@ bool whole_granules(int64_t es, int64_t cols, std::initializer_list<Rows> rows) 
 template <int V>
 using Const = std::integral_constant<int, V>;
 
-// Calls f(T(), units per thread, whether rows start anywhere) after setting the threads that a row of `units` units takes:
-// one or two units per thread where a warp can take it so, MOST (2 or more) while it needs up to `threads`, then 4.
-// False: the row does not fit into a CTA's registers.
-template <typename T, int MOST, typename F>
-bool with_units(bool any, int64_t units, int most, unsigned* threads, F f) {
-    auto go = [&](auto u) {
+// Calls f(T(), units per thread, whether rows start anywhere, the most threads) after setting the threads that a row of
+// `units` units takes: one or two units per thread where a warp can take it so, FEW (2 or 4) with up to 512 threads, then 4.
+// Only rows of fp32, whose units are half as many columns, fit the registers of 1024 threads. False: the row fits none.
+template <typename T, int FEW, typename F>
+bool with_units(bool any, int64_t units, unsigned* threads, F f) {
+    auto go = [&](auto u, auto most) {
         const int64_t n = ceil_div(ceil_div(units, decltype(u)::value), 32) * 32;
         *threads = (unsigned)std::max<int64_t>(n, 32);
-        any ? f(T(), u, Const<1>()) : f(T(), u, Const<0>());
+        any ? f(T(), u, Const<1>(), most) : f(T(), u, Const<0>(), most);
         return true;
     };
-    if (units <= 32) return go(Const<1>());
-    if (units <= 64 || (MOST == 2 && units <= 2 * most)) return go(Const<2>());
-    if (units <= 4 * row_threads<T>()) return go(Const<4>());
+    if (units <= 32) return go(Const<1>(), Const<512>());
+    if (units <= 64 || (FEW == 2 && units <= 2 * 512)) return go(Const<2>(), Const<512>());
+    if (units <= 4 * 512) return go(Const<4>(), Const<512>());
+    if constexpr (sizeof(T) == 4)
+        if (units <= 4 * 1024) return go(Const<4>(), Const<1024>());
     return false;
 }
 
@@ -752,16 +779,16 @@ int launch_rows(const RowParams& p, int dtype, bool any, int id, cudaStream_t s)
     unsigned threads = 0;
     cudaError_t e = cudaSuccess;
     const int64_t units = p.pitch / (dtype == GPTQ_BF16 ? 8 : 4);
-    auto go = [&](auto t, auto u, auto a) {
-        auto kern = int8_rows_kernel<decltype(t), decltype(u)::value, NORM, decltype(a)::value != 0>;
+    auto go = [&](auto t, auto u, auto a, auto m) {
+        auto kern = int8_rows_kernel<decltype(t), decltype(u)::value, NORM, decltype(a)::value != 0, decltype(m)::value>;
         static std::atomic<int> known[33];
         const unsigned rows = threads == 32 ? 8 : 1;   // a warp takes a whole row where it can
         const int64_t most = (int64_t)device_sm_count() * ctas_per_sm(kern, threads * rows, known);
         const unsigned ctas = (unsigned)std::min<int64_t>(ceil_div(p.rows, rows), most);
         GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, rows), 0, s, p));
     };
-    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 4>(any, units, 0, &threads, go)
-                                         : with_units<float, 4>(any, units, 0, &threads, go);
+    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 4>(any, units, &threads, go)
+                                         : with_units<float, 4>(any, units, &threads, go);
     if (!fits) {
         auto kern = dtype == GPTQ_BF16 ? int8_long_rows_kernel<__nv_bfloat16, NORM> : int8_long_rows_kernel<float, NORM>;
         GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3((unsigned)p.rows), dim3(1024), 0, s, p));
@@ -867,8 +894,8 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
         p.per = ceil_div(rows, std::min(most, grad_ctas(rows)));
         ctas = (unsigned)ceil_div(rows, p.per);
     };
-    auto go = [&](auto t, auto u, auto a) {
-        auto kern = int8_norm_grad_kernel<decltype(t), decltype(u)::value, decltype(a)::value != 0>;
+    auto go = [&](auto t, auto u, auto a, auto m) {
+        auto kern = int8_norm_grad_kernel<decltype(t), decltype(u)::value, decltype(a)::value != 0, decltype(m)::value>;
         static std::atomic<int> known[33];
         // groups of threads up to 512, each with a barrier (15 of them besides the CTA's), none idle
         unsigned groups = std::max(1u, std::min(15u, 512 / threads));
@@ -877,8 +904,8 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
         const size_t smem = groups > 1 ? sizeof(float) * cols : 0;   // (at most 256 threads of 16 columns: 16 KB)
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, groups), smem, s, p));
     };
-    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2>(any, units, 512, &threads, go)
-                                         : with_units<float, 2>(any, units, 512, &threads, go);
+    const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2>(any, units, &threads, go)
+                                         : with_units<float, 2>(any, units, &threads, go);
     if (!fits) {
         share(grad_ctas(rows));
         auto kern = dtype == GPTQ_BF16 ? int8_norm_grad_long_kernel<__nv_bfloat16> : int8_norm_grad_long_kernel<float>;
