@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int
 
 // ------------------------------------------------------------------------------------- host side
 bool bad_dtype(int t) { return t != GPTQ_F32 && t != GPTQ_BF16; }
-constexpr int64_t kMaxDim = (1ll << 31) - 512;
+constexpr int64_t kMaxDim = (1ll << 31) - 4096;   // (a warp's last unit is up to 1024 columns past the row's end)
 struct Rows {
     const void* p;
     int64_t ld;

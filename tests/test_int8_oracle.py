@@ -204,3 +204,9 @@ def test_the_expert_layer_takes_one_form(clib):
     i8, f4 = g.Int8(None, None, 4), g.Fp4(None, None, 4, "mx")
     with pytest.raises(ValueError, match="both"):
         g.gptq_expert_mlp(None, None, None, i8, f4)
+
+
+def test_columns_whose_last_unit_passes_31_bits_are_refused(clib):
+    """A warp's units reach up to 1024 columns past the row's end, and their numbers have 31 bits."""
+    for cols in ((1 << 31) - 513, (1 << 31) - 1024):
+        assert clib.gptq_int8_dequantize(P, P, 2, cols, P, 1, cols, Z) == 1
