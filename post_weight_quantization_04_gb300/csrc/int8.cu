@@ -809,11 +809,10 @@ extern "C" int64_t gptq_int8_pitch(int64_t cols) { return int8_pitch(cols); }
 
 extern "C" int gptq_int8_quantize(const void* X, int dtype, int64_t src_rows, int64_t cols, int64_t ldx, const int32_t* index,
                                   int64_t per, int64_t rows, int8_t* codes, float* scales, void* stream) {
-    if (src_rows < 0 || cols < 0 || rows < 0 || rows > kMaxDim || src_rows > kMaxDim || cols > kMaxDim || per < 1 || bad_dtype(dtype) ||
-        (!index && rows != src_rows))
+    if (src_rows < 0 || cols < 0 || rows < 0 || rows > kMaxDim || src_rows > kMaxDim || cols > kMaxDim || per < 1 || bad_dtype(dtype))
         return GPTQ_ERR_INVALID_ARG;
-    if (rows == 0) return GPTQ_OK;
-    if (!scales || (cols > 0 && ((src_rows > 0 && !X) || !codes || ldx < cols || reinterpret_cast<uintptr_t>(codes) % 16 != 0)))
+    if (rows == 0) return GPTQ_OK;   // (an empty index has no address)
+    if ((!index && rows != src_rows) || !scales || (cols > 0 && ((src_rows > 0 && !X) || !codes || ldx < cols || reinterpret_cast<uintptr_t>(codes) % 16 != 0)))
         return GPTQ_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallStatus st;

@@ -210,3 +210,9 @@ def test_columns_whose_last_unit_passes_31_bits_are_refused(clib):
     """A warp's units reach up to 1024 columns past the row's end, and their numbers have 31 bits."""
     for cols in ((1 << 31) - 513, (1 << 31) - 1024):
         assert clib.gptq_int8_dequantize(P, P, 2, cols, P, 1, cols, Z) == 1
+
+
+def test_no_rows_of_a_matrix_that_has_some(clib):
+    """An empty index has no address."""
+    a = dict(X=P, dtype=1, src_rows=4, cols=64, ldx=64, index=Z, per=1, rows=0, codes=Z, scales=Z)
+    assert clib.gptq_int8_quantize(*a.values(), Z) == 0
