@@ -30,7 +30,7 @@ struct IParams {
     int experts;
     int ftiles;               // feature tiles
     int tokens_first;         // neighbouring tiles share their features, not their tokens
-    int width;                // the widest tile: a multiple of 16 up to W_T
+    int width;                // the widest tile: a multiple of 32 up to W_T
     int splits;               // SPLIT: shares of the columns, each a pair of its own
     int box, raw;             // SPLIT: rows of a token box, and stages of codes
     int relu, bf16_out, vec;  // vec: bf16 rows that 16-byte stores can take
@@ -240,12 +240,12 @@ struct WMaps {
     CUtensorMap w, x[3];   // tokens: boxes of 128, 64 and 32 rows
 };
 
-// Token tiles of rows [lo, hi), all of one width: a multiple of 16, as the MMA wants it
+// Token tiles of rows [lo, hi), all of one width: a multiple of 32, as an MMA of two CTAs wants it
 __device__ __forceinline__ int token_tiles(int lo, int hi, int width) { return hi <= lo ? 0 : (hi - lo + width - 1) / width; }
 
 struct WTile {
     int e, f0;        // expert, first feature
-    int t0, n;        // first token, tokens (a multiple of 16, the last of which may be past hi)
+    int t0, n;        // first token, tokens (a multiple of 32, the last of which may be past hi)
     int hi;           // the end of its tokens, and of the expert's
 };
 
@@ -271,9 +271,9 @@ __device__ __forceinline__ WTile find_tile(const IParams& p, const WRows& w, uin
     const int first = w.start[a], tiles = w.start[a + 1] - first;
     const int2 r = w.rows[a];
     t.hi = r.y;
-    const int width = max(((int)((uint32_t)(r.y - r.x + tiles - 1) / (uint32_t)tiles) + 15) & ~15, 32);
+    const int width = ((int)((uint32_t)(r.y - r.x + tiles - 1) / (uint32_t)tiles) + 31) & ~31;
     t.t0 = r.x + (tt - first) * width;
-    t.n = min(max(t.hi - t.t0 + 15, 32) & ~15, width);
+    t.n = min((t.hi - t.t0 + 31) & ~31, width);
     t.hi = min(t.hi, t.t0 + t.n);
     return t;
 }
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int feature = 32 * (warp & 3) + lane, mover = warp >> 2;
         const WTile t = first < ntiles ? find_tile(p, w, first) : WTile{0, 0, 0, 0, 0};
-        const int own = t.n / p.splits, blocks = (own + 31) / 32;   // (n is a multiple of 16)
+        const int own = t.n / p.splits, blocks = (own + 31) / 32;   // (n is a multiple of 32)
         for (int b = mover; b < blocks * (p.splits - 1); b += w_threads(true) / 128) {
             const int other = b / blocks, to = other < share ? other : other + 1, c = b % blocks * 32;
             const uint32_t dst = in_cta(sbase, 2 * to + half) + (uint32_t)((share < to ? share : share - 1) * own + c) * (W_F * 4) + feature * 16;
@@ -888,7 +888,7 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, i
     Plan best = {W_T, 1};
     int64_t least = -1;
     for (int64_t tt = ceil_div(T, W_T);; ++tt) {
-        const int width = by_expert ? W_T : (int)std::max<int64_t>(ceil_div(ceil_div(T, tt), 16) * 16, 32);
+        const int width = by_expert ? W_T : (int)(ceil_div(ceil_div(T, tt), 32) * 32);
         const int64_t tiles = (ceil_div(T, width) + (by_expert ? std::min(experts, T) : 0)) * ftiles;
         for (int k = 1; k <= 4; k <<= 1) {
             if (k > 1 && (tiles * k > pairs || stages < 2 * k || tiles > clusters_at_once(k))) break;
