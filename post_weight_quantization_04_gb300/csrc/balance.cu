@@ -18,7 +18,8 @@ namespace {
 
 constexpr int L_THREADS = 256;          // of the gradient
 constexpr int L_COUNTERS = 128;         // threads of the first kernel that count, besides those that take the softmax
-constexpr int L_ALONE = 128;            // tokens up to which one CTA does all in one launch
+constexpr int L_CLUSTER = 8;            // CTAs of the cluster that does all in one launch
+constexpr int L_FEW = 128;              // tokens that never take two launches
 // threads of the first kernel that take the softmax (their sums are in shared memory, by lanes and experts)
 constexpr int summing_threads(int v) { return v <= 8 ? 512 : 256; }
 constexpr int L_MAX_EXPERTS = 1024;
@@ -41,6 +42,7 @@ struct LParams {
     void* dZ;
     int64_t lddz;
     float* loss;
+    int together;            // the CTAs are one cluster, which leaves the results itself
     int* status;
 };
 
@@ -92,14 +94,16 @@ __device__ __forceinline__ float loss_of(const LParams& p, float dot, int32_t to
     return (float)p.experts / (float)p.top * (dot / n / n);
 }
 
-// Each CTA's sums of p and counts over a contiguous share of the tokens; with one CTA the loss too. Bound by latency: a load, two
-// trees of shuffles and a sum over the warps, then (in a second launch) one over the CTAs. 16384 tokens x 64 experts fp32 11.5 us for
-// both, 33 x 64 3.1, 16384 x 1024 61; with counting and softmax one after another in half the CTAs 16.7, 6.0 and 91.
+// Each CTA's sums of p and counts over a contiguous share of the tokens; with one CTA or one cluster of them the loss too. Bound by
+// latency: a load, two trees of shuffles and a sum over the warps, then one over the CTAs, by their cluster or in a second launch.
+// 16384 tokens x 64 experts fp32 11.3 us in two launches, 500 x 64 4.6 by a cluster (6.8 in two launches), 33 x 64 3.1 by one CTA,
+// 16384 x 1024 48; with counting and softmax one after another in half the CTAs 16.7, 6.0 for 33 x 64, and 91.
 template <typename T, int G, int V>
 __global__ void __launch_bounds__(summing_threads(V) + L_COUNTERS) balance_sums_kernel(const LParams p) {
     extern __shared__ float sh[];                               // [groups][experts], then counts [experts + 1]
     constexpr int THREADS = summing_threads(V), ALL = THREADS + L_COUNTERS, GROUPS = THREADS / G, AHEAD = ahead(V);
     __shared__ float warp_dot[ALL / 32];
+    __shared__ float dots;
     int32_t* cnt = reinterpret_cast<int32_t*>(sh + GROUPS * p.experts);
     for (int e = threadIdx.x; e <= p.experts; e += ALL) cnt[e] = 0;
     pdl_trigger();
@@ -151,7 +155,9 @@ __global__ void __launch_bounds__(summing_threads(V) + L_COUNTERS) balance_sums_
 #pragma unroll 8
             for (int g = 0; g < GROUPS; ++g) s += sh[g * p.experts + e];
         }
-        if (gridDim.x > 1) {
+        if (p.together) {
+            if (e < p.experts) sh[e] = s;   // (this thread's own column, which it has read)
+        } else if (gridDim.x > 1) {
             if (e < p.experts) p.sums[(int64_t)blockIdx.x * p.experts + e] = s;
             p.counts[(int64_t)blockIdx.x * (p.experts + 1) + e] = cnt[e];
         } else {
@@ -159,7 +165,21 @@ __global__ void __launch_bounds__(summing_threads(V) + L_COUNTERS) balance_sums_
             if (e < p.experts) dot = fmaf((float)cnt[e], s, dot);
         }
     }
-    if (gridDim.x > 1) return;
+    if (gridDim.x > 1 && !p.together) return;
+    if (p.together) {
+        // the CTAs of the cluster share the experts (and, as one more, the tokens), each with the others' sums in their order
+        cluster_sync();
+        for (int e = blockIdx.x * ALL + threadIdx.x; e <= p.experts; e += gridDim.x * ALL) {
+            float s = 0.0f;
+            int32_t n = 0;
+            for (uint32_t k = 0; k < gridDim.x; ++k) {
+                if (e < p.experts) s += __uint_as_float(ld_cluster_u32(smem_u32(sh + e), k));
+                n += (int32_t)ld_cluster_u32(smem_u32(cnt + e), k);
+            }
+            p.total[e] = n;
+            if (e < p.experts) dot = fmaf((float)n, s, dot);
+        }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if ((threadIdx.x & 31) == 0) warp_dot[threadIdx.x >> 5] = dot;
@@ -167,7 +187,21 @@ __global__ void __launch_bounds__(summing_threads(V) + L_COUNTERS) balance_sums_
     if (threadIdx.x == 0) {
         dot = 0.0f;
         for (int w = 0; w < ALL / 32; ++w) dot += warp_dot[w];
-        *p.loss = loss_of(p, dot, cnt[p.experts]);
+        dots = dot;
+        if (!p.together) *p.loss = loss_of(p, dot, cnt[p.experts]);
+    }
+    if (p.together) {
+        cluster_sync();
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            int32_t tokens = 0;
+            dot = 0.0f;
+            for (uint32_t k = 0; k < gridDim.x; ++k) {
+                dot += __uint_as_float(ld_cluster_u32(smem_u32(&dots), k));
+                tokens += (int32_t)ld_cluster_u32(smem_u32(cnt + p.experts), k);
+            }
+            *p.loss = loss_of(p, dot, tokens);
+        }
+        cluster_sync();   // no CTA leaves while its sums are read
     }
 }
 
@@ -299,9 +333,40 @@ constexpr int64_t kMaxSlots = (1ll << 31) - 4096;
 bool bad_shape(int64_t tokens, int64_t experts, int64_t top) {
     return tokens < 0 || experts < 1 || top < 1 || top > 65535 || tokens > kMaxSlots / top;
 }
-int64_t sum_ctas(int64_t tokens) { return tokens <= L_ALONE ? 1 : std::min<int64_t>(ceil_div(tokens, 32), L_MAX_CTAS); }
+// CTAs of the first of two launches
+int64_t sum_ctas(int64_t tokens) { return tokens <= L_FEW ? 1 : std::min<int64_t>(ceil_div(tokens, 32), L_MAX_CTAS); }
+// CTAs of a launch that does all by itself: one, or one cluster; 0: too many tokens for that. A CTA takes
+// (threads / lanes per token) x ahead tokens at a time, and more often than two or three times it is better to
+// have all SMs at work and a second launch. (us, two launches / a cluster: 8 experts 2000 tokens 5.7 / 4.9, 4000 5.9 / 6.2; 64 experts 500
+// 6.8 / 4.6, 1000 6.9 / 6.1, 2000 7.1 / 9.2; 256 experts 500 7.0 / 6.4, 1000 7.4 / 9.4; 1024 experts 200 13.6 / 11.3, 500 15.3 / 20.8; a
+// launch less is 2.8 us of the call's time besides. One CTA: 64 experts 33 tokens 3.1.)
+int alone_ctas(int64_t tokens, int64_t experts) {
+    int64_t at_once = 0;
+    with_lanes(experts, [&](auto gv) { at_once = summing_threads(gv.V) / gv.G * ahead(gv.V); });
+    return tokens <= 2 * at_once ? 1 : tokens <= 3 * L_CLUSTER * at_once ? L_CLUSTER : 0;
+}
 // CTAs of the second kernel
 unsigned summers(int64_t experts) { return experts >= 256 ? 8 : experts >= 32 ? 4 : 1; }
+
+// A launch of `ctas` CTAs in clusters of `cluster`, which starts while the kernel before ends
+struct Clustered {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Clustered(unsigned ctas, unsigned cluster, dim3 block, size_t smem, cudaStream_t s) {
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
 
 }  // namespace
 }  // namespace gptq
@@ -324,7 +389,8 @@ extern "C" int gptq_expert_balance(const void* Z, int dtype, int64_t tokens, int
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallStatus st;
     GPTQ_CUDA_TRY(st.begin(s));
-    const int64_t ctas = sum_ctas(tokens);
+    const int alone = alone_ctas(tokens, experts);
+    const int64_t ctas = alone ? alone : sum_ctas(tokens);
     LParams p{};
     p.Z = Z;
     p.tokens = tokens;
@@ -334,9 +400,10 @@ extern "C" int gptq_expert_balance(const void* Z, int dtype, int64_t tokens, int
     p.ids = ids;
     p.mask = mask;
     p.sums = static_cast<float*>(ws);
-    p.counts = reinterpret_cast<int32_t*>(p.sums + ctas * experts);
+    if (!alone) p.counts = reinterpret_cast<int32_t*>(p.sums + ctas * experts);
     p.total = counts;
     p.loss = loss;
+    p.together = alone > 1;
     p.status = st.word;
     cudaError_t e = cudaSuccess;
     with_lanes(experts, [&](auto gv) {
@@ -344,26 +411,20 @@ extern "C" int gptq_expert_balance(const void* Z, int dtype, int64_t tokens, int
         // at most 16 x 256 or 8 x 1024 words, and 1025
         const size_t smem = 4 * ((size_t)(summing_threads(V) / G) * experts + experts + 1);
         auto kern = dtype == GPTQ_BF16 ? balance_sums_kernel<__nv_bfloat16, G, V> : balance_sums_kernel<float, G, V>;
-        GPTQ_LAUNCH(K_BALANCE, s, e = launch_pdl(kern, dim3((unsigned)ctas), dim3(summing_threads(V) + L_COUNTERS), smem, s, p));
+        const dim3 block(summing_threads(V) + L_COUNTERS);
+        if (p.together) {
+            const Clustered l(ctas, L_CLUSTER, block, smem, s);
+            GPTQ_LAUNCH(K_BALANCE, s, e = cudaLaunchKernelEx(&l.cfg, kern, p));
+        } else {
+            GPTQ_LAUNCH(K_BALANCE, s, e = launch_pdl(kern, dim3((unsigned)ctas), block, smem, s, p));
+        }
     });
     GPTQ_CUDA_TRY(e);
-    if (ctas == 1) return st.finish(s);
+    if (alone) return st.finish(s);
     int wide = 1;
     while (wide < ceil_div(experts + 1, summers(experts))) wide <<= 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(summers(experts));
-    cfg.blockDim = dim3(L_SUMMERS);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = summers(experts);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    GPTQ_LAUNCH(K_BALANCE, s, e = cudaLaunchKernelEx(&cfg, balance_loss_kernel, p, (int)ctas, wide));
+    const Clustered l(summers(experts), summers(experts), dim3(L_SUMMERS), 0, s);
+    GPTQ_LAUNCH(K_BALANCE, s, e = cudaLaunchKernelEx(&l.cfg, balance_loss_kernel, p, (int)ctas, wide));
     GPTQ_CUDA_TRY(e);
     return st.finish(s);
 }

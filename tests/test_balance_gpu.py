@@ -132,3 +132,14 @@ def test_gradient_by_differences(lib):
         d = np.zeros((9, 7))
         d[i, j] = 1e-4
         assert abs((loss(f64(z) + d) - loss(f64(z) - d)) / 2e-4 - dz[i, j]) <= 1e-6
+
+
+@pytest.mark.parametrize("T,E,k", [(1024, 3, 2), (1025, 3, 2), (12289, 4, 1), (513, 8, 2), (6144, 7, 3), (6145, 8, 2), (129, 64, 6), (1000, 64, 6),
+                                   (1536, 50, 2), (1537, 64, 1), (65, 256, 8), (768, 200, 8), (17, 1024, 8), (192, 1024, 1), (193, 700, 4)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_loss_by_one_cta_one_cluster_and_two_launches(lib, T, E, k, masked):
+    z, ids, mask = _inputs(T, E, k, "f32", T + E)
+    b, _ = _check(lib, z, ids, mask if masked else None)
+    for _ in range(20):
+        b2 = lib.gptq_expert_balance(z, ids, mask if masked else None)
+        assert torch.equal(b.loss, b2.loss) and torch.equal(b.counts, b2.counts)
