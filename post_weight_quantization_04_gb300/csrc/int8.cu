@@ -581,15 +581,15 @@ __device__ __forceinline__ float group_sum(float v, float* part, int warps, int 
 }
 
 // A CTA takes a contiguous share of the rows, each of its blockDim.y groups of threads every so many of them, and a thread
-// the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added in turn at the
+// the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added at the
 // end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written.
-// Bound by memory: 16384 x 4096 bf16 88 us (6.1 TB/s), fp32 163 (6.6), both with the sum over the CTAs (4 us). Without the
-// loads ahead and with the gain read for every row it took 199. Rows at odd addresses: 16384 x 4095 bf16 180, fp32 203.
+// Bound by memory: 16384 x 4096 bf16 86 us (6.2 TB/s), fp32 163 (6.6), both with the sum over the CTAs (4 us). Without the
+// loads ahead and with the gain read for every row it took 199. Rows at odd addresses: 16384 x 4095 bf16 183, fp32 203.
 template <typename T, int UNITS, bool ANY, int MOST>
 __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParams p) {
     constexpr int N = kUnit<T>;
     constexpr bool AHEAD = UNITS <= 2;   // (and the gain stays in registers)
-    extern __shared__ float sums[];   // [columns of the units], where there are several groups
+    extern __shared__ float sums[];   // [groups][columns], where there are several groups
     __shared__ float part[2][32];
     pdl_trigger();
     pdl_wait();
@@ -661,21 +661,36 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
         store_units<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, cols, j0, dw);
     }
     float* out = p.part + blockIdx.x * p.cols;
-    for (int g = 0; g < (int)blockDim.y; ++g) {
-        if (group == g) {
+    // each group leaves its sums in shared memory, and all add them up; rows at odd addresses are faster where the first group adds
+    // the others' to its own (16384 x 4095 fp32 203 us, else 231; 16384 x 4096 bf16 90 so and 86)
+    const int groups = blockDim.y;
+    auto each = [&](auto f) {
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i)
+        for (int i = 0; i < UNITS; ++i)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const int c = (j0 + 32 * i) * N + e;
-                    if (c >= cols) continue;
-                    const float s = g > 0 ? sums[c] + acc[i][e] : acc[i][e];
-                    if (g == (int)blockDim.y - 1) out[c] = s;
-                    else sums[c] = s;
-                }
+            for (int e = 0; e < N; ++e) {
+                const int c = (j0 + 32 * i) * N + e;
+                if (c < cols) f(c, acc[i][e]);
+            }
+    };
+    if (AHEAD && groups > 1) {
+        each([&](int c, float& v) { sums[group * cols + c] = v; });
+        __syncthreads();
+        if (ANY) {
+            if (group > 0) return;
+            each([&](int c, float& v) {
+                for (int g = 1; g < groups; ++g) v += sums[g * cols + c];
+            });
+        } else {
+            for (int c = group * blockDim.x + threadIdx.x; c < cols; c += groups * blockDim.x) {
+                float s = 0.0f;
+                for (int g = 0; g < groups; ++g) s += sums[g * cols + c];
+                out[c] = s;
+            }
+            return;
         }
-        if (blockDim.y > 1) __syncthreads();
     }
+    each([&](int c, float& v) { out[c] = v; });
 }
 
 // Rows of any length: the row's mean is taken in one pass over it, and its gradient in a second one, which finds
@@ -898,9 +913,11 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
         static std::atomic<int> known[33];
         // groups of threads up to 512, each with a barrier (15 of them besides the CTA's), none idle
         unsigned groups = std::max(1u, std::min(15u, 512 / threads));
-        share((int64_t)device_sm_count() * ctas_per_sm(kern, threads * groups, known));
+        // (one row, or two at a time, are one CTA's, whose sums are dgain: 1 x 4096 bf16 3.6 us, with a launch to add them up 5.5)
+        share(rows <= std::min(groups, 2u) ? 1 : (int64_t)device_sm_count() * ctas_per_sm(kern, threads * groups, known));
+        if (ctas == 1) p.part = dgain;
         groups = (unsigned)std::min<int64_t>(groups, p.per);
-        const size_t smem = groups > 1 ? sizeof(float) * cols : 0;   // (at most 256 threads of 16 columns: 16 KB)
+        const size_t smem = groups > 1 ? sizeof(float) * groups * cols : 0;   // (at most 512 threads of 16 columns: 32 KB)
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, groups), smem, s, p));
     };
     const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2>(any, units, &threads, go)
@@ -911,6 +928,7 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(1024), 0, s, p));
     }
     GPTQ_CUDA_TRY(e);
+    if (p.part == dgain) return GPTQ_OK;
     GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(column_sum_kernel, dim3((unsigned)ceil_div(cols, 32)), dim3(32, 32), 0, s,
                                                (const float*)p.part, (int)ctas, cols, dgain));
     GPTQ_CUDA_TRY(e);
