@@ -582,14 +582,17 @@ __device__ __forceinline__ float group_sum(float v, float* part, int warps, int 
 
 // A CTA takes a contiguous share of the rows, each of its blockDim.y groups of threads every so many of them, and a thread
 // the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added at the
-// end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written.
+// end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written. Wider rows leave no
+// registers for that, and have the sums in shared memory (4096 x 14336 bf16 121 us, 3.9 TB/s, in registers 131; with loads ahead 147).
 // Bound by memory: 16384 x 4096 bf16 86 us (6.2 TB/s), fp32 163 (6.6), both with the sum over the CTAs (4 us). Without the
 // loads ahead and with the gain read for every row it took 199. Rows at odd addresses: 16384 x 4095 bf16 183, fp32 203.
 template <typename T, int UNITS, bool ANY, int MOST>
 __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParams p) {
     constexpr int N = kUnit<T>;
-    constexpr bool AHEAD = UNITS <= 2;   // (and the gain stays in registers)
-    extern __shared__ float sums[];   // [groups][columns], where there are several groups
+    constexpr bool AHEAD = UNITS <= 2;   // (and the gain and the sums stay in registers)
+    extern __shared__ float4 shared_sums[];   // AHEAD: [groups][columns] floats, where there are several groups; else [UNITS N / 4][threads]
+    float* sums = reinterpret_cast<float*>(shared_sums);
+    const int tid = threadIdx.x;
     __shared__ float part[2][32];
     pdl_trigger();
     pdl_wait();
@@ -597,12 +600,14 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
     const int j0 = (int)(threadIdx.x >> 5) * 32 * UNITS + (int)(threadIdx.x & 31), step = blockDim.y, cols = (int)p.cols;
     const int warps = blockDim.x >> 5, group = threadIdx.y;
     const float inv_n = 1.0f / (float)cols;
-    float gain[UNITS][N];
+    float gain[AHEAD ? UNITS : 1][N];
     if (AHEAD) {
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, gain[i]);
     }
-    float acc[UNITS][N] = {};
+    float acc[AHEAD ? UNITS : 1][N] = {};
+    if (!AHEAD)
+        for (int i = 0; i < UNITS * N / 4; ++i) shared_sums[i * blockDim.x + tid] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     uint4 dy[UNITS], h[UNITS], dh[UNITS];
     const T *ry = nullptr, *rh = nullptr, *rd = nullptr;
     float rstd = 0.0f;
@@ -636,26 +641,41 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             float u[N], v[N];
-            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, gain[i]);
+            float(&g)[N] = gain[AHEAD ? i : 0];
+            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, g);
             unpack<T>(hw[i], u);
             unpack<T>(yw[i], v);
+            float(&a)[N] = acc[AHEAD ? i : 0];
+            if (!AHEAD) {
+#pragma unroll
+                for (int e = 0; e < N; e += 4) {
+                    const float4 w = shared_sums[(i * N / 4 + e / 4) * blockDim.x + tid];
+                    a[e] = w.x, a[e + 1] = w.y, a[e + 2] = w.z, a[e + 3] = w.w;
+                }
+            }
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 u[e] *= rs;
-                acc[i][e] = fmaf(v[e], u[e], acc[i][e]);
-                dot = fmaf(u[e], v[e] * gain[i][e], dot);
+                a[e] = fmaf(v[e], u[e], a[e]);
+                dot = fmaf(u[e], v[e] * g[e], dot);
+            }
+            if (!AHEAD) {
+#pragma unroll
+                for (int e = 0; e < N; e += 4)
+                    shared_sums[(i * N / 4 + e / 4) * blockDim.x + tid] = make_float4(a[e], a[e + 1], a[e + 2], a[e + 3]);
             }
         }
         const float k = group_sum(dot, part[turn] + group * warps, warps, 1 + group) * inv_n * rs;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             float u[N], v[N], d[N] = {};
-            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, gain[i]);
+            float(&g)[N] = gain[AHEAD ? i : 0];
+            if (!AHEAD) load_gain<N, ANY>(p.gain, cols, (j0 + 32 * i) * N, g);
             unpack<T>(hw[i], u);
             unpack<T>(yw[i], v);
             if (p.dH) unpack<T>(dw[i], d);
 #pragma unroll
-            for (int e = 0; e < N; ++e) d[e] = fmaf(rs, fmaf(-u[e], k, v[e] * gain[i][e]), d[e]);
+            for (int e = 0; e < N; ++e) d[e] = fmaf(rs, fmaf(-u[e], k, v[e] * g[e]), d[e]);
             dw[i] = pack<T>(d);
         }
         store_units<T, ANY>(static_cast<T*>(p.dX) + r * p.lddx, cols, j0, dw);
@@ -670,7 +690,11 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const int c = (j0 + 32 * i) * N + e;
-                if (c < cols) f(c, acc[i][e]);
+                if (AHEAD) {
+                    if (c < cols) f(c, acc[i][e]);
+                } else if (c < cols) {
+                    f(c, sums[((i * N / 4 + e / 4) * blockDim.x + tid) * 4 + e % 4]);
+                }
             }
     };
     if (AHEAD && groups > 1) {
@@ -917,7 +941,10 @@ extern "C" int gptq_int8_rms_norm_grad(const void* dY, int64_t lddy, const void*
         share(rows <= std::min(groups, 2u) ? 1 : (int64_t)device_sm_count() * ctas_per_sm(kern, threads * groups, known));
         if (ctas == 1) p.part = dgain;
         groups = (unsigned)std::min<int64_t>(groups, p.per);
-        const size_t smem = groups > 1 ? sizeof(float) * groups * cols : 0;   // (at most 512 threads of 16 columns: 32 KB)
+        // (at most 512 threads of 16 columns, 32 KB; 4 units: up to 16384 columns, 64 KB)
+        constexpr int kUnits = decltype(u)::value;
+        const size_t smem = kUnits > 2 ? sizeof(float) * threads * kUnits * kUnit<decltype(t)> : groups > 1 ? sizeof(float) * groups * cols : 0;
+        if (kUnits > 2 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024)) != cudaSuccess) return;
         GPTQ_LAUNCH(K_INT8_GRAD, s, e = launch_pdl(kern, dim3(ctas), dim3(threads, groups), smem, s, p));
     };
     const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 2>(any, units, &threads, go)
