@@ -468,3 +468,42 @@ def test_on_another_stream_and_captured(lib):
             got = [t.clone() for t in held]
             assert all(torch.equal(a, b) for a, b in zip(got, step()))
         lib.status_sync()
+
+
+@pytest.mark.parametrize("rows,cols,dt", [(400, 8200, "bf16"), (400, 8201, "bf16"), (330, 16384, "bf16"), (320, 5001, "f32"), (400, 8192, "f32"),
+                                          (310, 16383, "f32"), (700, 3001, "bf16"), (5000, 250, "f32"), (5000, 251, "bf16"), (1500, 1030, "f32"),
+                                          (1, 5000, "bf16"), (2, 250, "f32"), (2, 251, "bf16"), (3, 250, "bf16")])
+def test_gradient_of_several_rows_per_cta(lib, rows, cols, dt):
+    """dX and dgain against the formula, and the same where dX takes the place of any input at its own address."""
+    h, dy, dh = (rows_of(rows, cols, dt, s, 1) for s in (1, 2, 3))
+    gain, rstd = torch.rand(cols, device=DEV) + 0.5, torch.rand(rows, device=DEV) + 0.5
+    dx, dg = lib.gptq_int8_rms_norm_grad(dy, h, gain, rstd, dh)
+    H, G, R, Y, D = f64(h), f64(gain), f64(rstd)[:, None], f64(dy), f64(dh)
+    ref, refg = I.rms_norm_grad(Y, H, G, R[:, 0], D)
+    u, v = H * R, Y * G
+    mean = np.abs((u * v).mean(1, keepdims=True))
+    off = (cols / 32 + 24) * U * R * np.abs(u) * np.abs(u * v).mean(1, keepdims=True)
+    off = off + 6 * U * (np.abs(D) + R * (np.abs(v) + np.abs(u) * mean)) + (B * np.abs(ref) if dt == "bf16" else 0)
+    assert (np.abs(f64(dx) - ref) <= off).all()
+    assert (np.abs(f64(dg) - refg) <= (rows + 4) * U * np.abs(Y * u).sum(0)).all()
+    for i in range(3):
+        a = [rows_of(rows, cols, dt, s, 1) for s in (2, 1, 3)]
+        dx2, dg2 = lib.gptq_int8_rms_norm_grad(a[0], a[1], gain, rstd, a[2], out=(a[i], torch.empty_like(dg)))
+        assert torch.equal(dx2, dx) and torch.equal(dg2, dg), i
+
+
+@pytest.mark.parametrize("rows,cols,dt", [(700, 4095, "bf16"), (700, 4096, "bf16"), (500, 8201, "bf16"), (600, 2310, "f32"), (400, 9001, "f32"),
+                                          (5000, 251, "bf16"), (5000, 100, "f32"), (310, 16384, "f32")])
+def test_norm_of_several_rows_per_cta(lib, rows, cols, dt):
+    """As row by row, and the same where h takes the place of either input at its own address."""
+    x, r = (rows_of(rows, cols, dt, s, 1) for s in (1, 2))
+    gain = torch.rand(cols, device=DEV) + 0.5
+    q, h, rstd = lib.gptq_int8_rms_norm(x, gain, 1e-5, r)
+    assert torch.equal(h, (x.float() + r.float()).to(DT[dt]))
+    for at in (0, 1, rows // 3, rows - 1):
+        q1, h1, rstd1 = lib.gptq_int8_rms_norm(x[at:at + 1], gain, 1e-5, r[at:at + 1])
+        assert torch.equal(q1.codes, q.codes[at:at + 1]) and torch.equal(q1.scales, q.scales[at:at + 1]) and torch.equal(rstd1, rstd[at:at + 1])
+    for i in range(2):
+        a = [rows_of(rows, cols, dt, s, 1) for s in (1, 2)]
+        q2, _, rstd2 = lib.gptq_int8_rms_norm(a[0], gain, 1e-5, a[1], out=(None, a[i], None))
+        assert torch.equal(a[i], h) and torch.equal(q2.codes, q.codes) and torch.equal(q2.scales, q.scales) and torch.equal(rstd2, rstd), i
