@@ -459,49 +459,95 @@ __global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_
     }
 }
 
-// The same for rows of any length (1024 x 40000 bf16 84 us): passes over the row, of which all but the first find it in L2. (The norm's
-// later passes read h, each thread what it wrote itself.)
-template <typename T, bool NORM>
+// The same for rows of any length: passes over the row, of which all but the first find it in L2, four units of a thread in
+// flight at a time. (The norm's later passes read h, each thread what it wrote itself.) ANY: a warp's units take its columns in
+// turn, element by element. 1024 x 40000 bf16 37 us, with single elements in flight 84; 4096 x 28672 83 (4.2 TB/s).
+template <typename T, bool NORM, bool ANY>
 __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p) {
+    constexpr int N = kUnit<T>, UNITS = 4;
     __shared__ float sum_part[32];
     __shared__ uint32_t max_part[32];
     pdl_wait();
     const int64_t r = blockIdx.x, sr = NORM ? r : source_row(p, r);
     const T* x = static_cast<const T*>(p.X) + max(sr, (int64_t)0) * p.ldx;
-    const int64_t n = sr < 0 ? 0 : p.cols;
+    const uint32_t n = sr < 0 ? 0 : (uint32_t)p.cols, pitch = (uint32_t)p.pitch, units = pitch / N;
+    // column e of unit j (some units past the row's end are asked for, whose columns may not have 31 bits)
+    auto column = [](uint32_t j, int e) { return ANY ? (j & ~31u) * N + 32 * e + (j & 31) : j * N + e; };
+    auto load = [&](const T* row, uint32_t j, float(&v)[N]) {
+        if constexpr (ANY) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = column(j, e) < n ? load_one(row + column(j, e)) : 0.0f;
+        } else {
+            unpack<T>(j * N < n ? *reinterpret_cast<const uint4*>(row + j * N) : make_uint4(0, 0, 0, 0), v);
+        }
+    };
+    // f(unit, its columns) for this thread's units of a row
+    auto sweep = [&](const T* row, auto f) {
+        for (uint32_t j0 = threadIdx.x; j0 < (ANY ? (units + 31) & ~31u : units); j0 += UNITS * 1024) {
+            float v[UNITS][N];
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) load(row, j0 + 1024 * u, v[u]);
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) f(j0 + 1024 * u, v[u]);
+        }
+    };
     float rstd = 1.0f;
     if constexpr (NORM) {
         const T* res = p.R ? static_cast<const T*>(p.R) + r * p.ldr : nullptr;
         T* h = res ? static_cast<T*>(p.H) + r * p.ldh : nullptr;
         float s = 0.0f;
-        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
-            float a = load_one(x + c);
+        sweep(x, [&](uint32_t j, float(&v)[N]) {
             if (res) {
-                a += load_one(res + c);
-                if constexpr (sizeof(T) == 2) a = __bfloat162float(__float2bfloat16_rn(a));
-                store_one(h + c, a);
+                float d[N];
+                load(res, j, d);
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] += d[e];
+                const uint4 w = pack<T>(v);
+                unpack<T>(w, v);   // h as it is stored
+                if constexpr (ANY) {
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (column(j, e) < n) put(h + column(j, e), u, e);
+                } else {
+                    if (j * N < n) *reinterpret_cast<uint4*>(h + j * N) = w;
+                }
             }
-            s = fmaf(a, a, s);
-        }
+#pragma unroll
+            for (int e = 0; e < N; ++e) s = fmaf(v[e], v[e], s);
+        });
         if (res) x = h;
         const float sum = row_sum(s, sum_part);
         rstd = rstd_of(sum, 1.0f / (float)p.cols, p.eps, [&](float f) {
             __syncthreads();
             float q = 0.0f;
-            for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
-                const float a = load_one(x + c) * f;
-                q = fmaf(a, a, q);
-            }
+            sweep(x, [&](uint32_t, float(&v)[N]) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) q = fmaf(v[e] * f, v[e] * f, q);
+            });
             return row_sum(q, sum_part);
         });
         if (threadIdx.x == 0) p.rstd[r] = rstd;
     }
-    auto value = [&](int64_t c) {
-        const float a = load_one(x + c);
-        return NORM ? a * rstd * p.gain[c] : a;
+    auto scaled = [&](uint32_t j, float(&v)[N]) {   // the values that are quantised
+        if constexpr (NORM) {
+            float g[N];
+            if constexpr (ANY) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) g[e] = column(j, e) < n ? p.gain[column(j, e)] : 0.0f;
+            } else {
+                load_gain<N, false>(p.gain, (int)n, (int)min(j * N, n), g);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = v[e] * rstd * g[e];
+        }
     };
     uint32_t m = 0;
-    for (int64_t c = threadIdx.x; c < n; c += blockDim.x) m = max(m, magnitude(value(c)));
+    sweep(x, [&](uint32_t j, float(&v)[N]) {
+        scaled(j, v);
+#pragma unroll
+        for (int e = 0; e < N; ++e) m = max(m, magnitude(v[e]));
+    });
     m = row_max(m, max_part);
     const bool bad = m >= 0x7F800000u;
     const float s = scale_of(m);
@@ -511,7 +557,16 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
     }
     const Step t = step_of(s);
     int8_t* y = p.codes + r * p.pitch;
-    for (int64_t c = threadIdx.x; c < p.pitch; c += blockDim.x) y[c] = (int8_t)code_of(c < n ? value(c) : 0.0f, t);
+    sweep(x, [&](uint32_t j, float(&v)[N]) {
+        scaled(j, v);
+        if constexpr (ANY) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (column(j, e) < pitch) y[column(j, e)] = (int8_t)code_of(v[e], t);
+        } else {
+            if (j < units) store_codes<N>(y + j * N, v, t);
+        }
+    });
 }
 
 // ------------------------------------------------------------------------------------ the inverse
@@ -829,8 +884,12 @@ int launch_rows(const RowParams& p, int dtype, bool any, int id, cudaStream_t s)
     const bool fits = dtype == GPTQ_BF16 ? with_units<__nv_bfloat16, 4>(any, units, &threads, go)
                                          : with_units<float, 4>(any, units, &threads, go);
     if (!fits) {
-        auto kern = dtype == GPTQ_BF16 ? int8_long_rows_kernel<__nv_bfloat16, NORM> : int8_long_rows_kernel<float, NORM>;
-        GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3((unsigned)p.rows), dim3(1024), 0, s, p));
+        auto lengthy = [&](auto t, auto a) {
+            auto kern = int8_long_rows_kernel<decltype(t), NORM, decltype(a)::value != 0>;
+            GPTQ_LAUNCH(id, s, e = launch_pdl(kern, dim3((unsigned)p.rows), dim3(1024), 0, s, p));
+        };
+        if (dtype == GPTQ_BF16) any ? lengthy(__nv_bfloat16(), Const<1>()) : lengthy(__nv_bfloat16(), Const<0>());
+        else any ? lengthy(float(), Const<1>()) : lengthy(float(), Const<0>());
     }
     GPTQ_CUDA_TRY(e);
     return GPTQ_OK;

@@ -209,3 +209,19 @@ def test_a_balance_past_2_31_logits(lib):
     dz0 = lib.gptq_expert_balance_grad(torch.full((1,), n / T, device=DEV), base, b0)
     for i in (0, T - n):
         assert (f64(dz[i:i + n]) - f64(dz0)).__abs__().max() <= 2 * B * np.abs(f64(dz0)).max()
+
+
+@pytest.mark.parametrize("cols", [(1 << 31) - 4096, (1 << 31) - 4099])
+def test_a_row_of_almost_2_31_columns(lib, cols):
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("not enough memory")
+    x = torch.zeros(1, cols, dtype=torch.bfloat16, device=DEV)
+    x[0, 5], x[0, cols // 2], x[0, cols - 1] = 1.0, -2.0, 4.0
+    q = lib.gptq_int8_quantize(x)
+    scale = np.float32(4.0) / np.float32(127.0)
+    assert float(q.scales) == scale
+    for at, value in ((5, 1.0), (cols // 2, -2.0), (cols - 1, 4.0)):
+        assert int(q.codes[0, at]) == np.rint(np.float32(value) / scale)
+    assert int(torch.count_nonzero(q.codes)) == 3
+    y = lib.gptq_int8_dequantize(q, torch.bfloat16)
+    assert int(torch.count_nonzero(y)) == 3 and float(y[0, cols - 1]) == 4.0
