@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 2 : 8) int8_few_rows_
 // behind, which its parity does not tell from none.
 // TMEM: 256 columns of sums (tokens), then the expanded weights of W_SLOTS stages, 64 columns each.
 //
-// SPLIT: few tiles, so a cluster of up to 8 CTAs shares the columns of one tile, and its pairs' sums are added
+// SPLIT: few tiles, so a cluster of up to 4 pairs shares the columns of one tile, and its pairs' sums are added
 // through each other's shared memory, each pair for its own part of the tokens. Such tiles are mostly narrow,
 // bound by the weights and the time that one stage takes: more stages of codes are in flight, the tokens have 4 warps
 // (12..15, of which each takes a part of the columns where there are fewer rows), the epilogue 4 (16..19).
@@ -756,22 +756,26 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int feature = 32 * (warp & 3) + lane, mover = warp >> 2;
         const WTile t = first < ntiles ? find_tile(p, w, first) : WTile{0, 0, 0, 0, 0};
-        const int own = t.n / p.splits, blocks = (own + 31) / 32;   // (n is a multiple of 32)
+        // each pair's tokens, whole fours (n is a multiple of 32); the last ones may have fewer or none
+        const int own = (t.n / 4 + p.splits - 1) / p.splits * 4, blocks = (own + 31) / 32;
+        auto part_of = [&](int s) { return min(max(t.n - s * own, 0), own); };
         for (int b = mover; b < blocks * (p.splits - 1); b += w_threads(true) / 128) {
             const int other = b / blocks, to = other < share ? other : other + 1, c = b % blocks * 32;
+            const int theirs = part_of(to);
             const uint32_t dst = in_cta(sbase, 2 * to + half) + (uint32_t)((share < to ? share : share - 1) * own + c) * (W_F * 4) + feature * 16;
             uint32_t v[32];
             tmem_ld_32x32b_x32(lanes + to * own + c, v);
             tmem_ld_wait();
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (c + 4 * u < own)
+                if (c + 4 * u < theirs)
                     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + u * (W_F * 16)), "r"(v[4 * u]),
                                  "r"(v[4 * u + 1]), "r"(v[4 * u + 2]), "r"(v[4 * u + 3])
                                  : "memory");
         }
         cluster_sync();   // all have what they wait for, and nobody's shared memory is touched any more
-        for (int b = mover; b < blocks; b += w_threads(true) / 128) {
+        const int mine = part_of(share);
+        for (int b = mover; b < (mine + 31) / 32; b += w_threads(true) / 128) {
             const int c = 32 * b, tok = share * own + c;
             uint32_t v[32];
             tmem_ld_32x32b_x32(lanes + tok, v);
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
             for (int j = 0; j < p.splits - 1; ++j) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    if (c + 4 * u >= own) break;
+                    if (c + 4 * u >= mine) break;
                     const uint4 a = lds128(sbase + (uint32_t)(j * own + c + 4 * u) * (W_F * 4) + feature * 16);
                     v[4 * u] = __float_as_uint(__uint_as_float(v[4 * u]) + __uint_as_float(a.x));
                     v[4 * u + 1] = __float_as_uint(__uint_as_float(v[4 * u + 1]) + __uint_as_float(a.y));
@@ -842,10 +846,10 @@ cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunc
 
 // How many clusters of 2 * splits CTAs the device holds at once (its GPCs are not all multiples of 8 SMs)
 int clusters_at_once(int splits) {
-    static std::atomic<int> known[16][2];
+    static std::atomic<int> known[16][5];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::atomic<int>* k = dev < 16 ? &known[dev][splits > 2] : nullptr;
+    std::atomic<int>* k = dev < 16 ? &known[dev][splits] : nullptr;
     if (k && k->load(std::memory_order_relaxed)) return k->load(std::memory_order_relaxed);
     IParams p{};
     p.splits = splits;
@@ -890,7 +894,7 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, i
     for (int64_t tt = ceil_div(T, W_T);; ++tt) {
         const int width = by_expert ? W_T : (int)(ceil_div(ceil_div(T, tt), 32) * 32);
         const int64_t tiles = (ceil_div(T, width) + (by_expert ? std::min(experts, T) : 0)) * ftiles;
-        for (int k = 1; k <= 4; k <<= 1) {
+        for (int k = 1; k <= 4; ++k) {
             if (k > 1 && (tiles * k > pairs || stages < 2 * k || tiles > clusters_at_once(k))) break;
             const int64_t cycles = k > 1 ? ceil_div(stages, k) * 1080 + 6500 + 64 * width
                                          : ceil_div(tiles, pairs) * (stages * 1080 + 1700) + 10000;
