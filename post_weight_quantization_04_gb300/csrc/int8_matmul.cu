@@ -32,7 +32,6 @@ struct IParams {
     int tokens_first;         // neighbouring tiles share their features, not their tokens
     int width;                // the widest tile: a multiple of 32 up to W_T
     int splits;               // SPLIT: shares of the columns, each a pair of its own
-    int box, raw;             // SPLIT: rows of a token box, and stages of codes
     int relu, bf16_out, vec;  // vec: bf16 rows that 16-byte stores can take
     void* Y;
     int64_t ldy;
@@ -201,22 +200,24 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 2 : 8) int8_few_rows_
 //   warp 0        producer: two TMA copies per stage, 128 x 128 codes of each operand (128-byte swizzle)
 //   warp 1        in the even CTA: the MMAs (warps 2 and 3 help with the set-up)
 //   warps 4..11   weights: shared memory -> fp16 -> TMEM, half a row per lane
-//   warps 12..19  tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), half a row per lane
-//   warps 20..27  epilogue: TMEM -> registers -> Y; they take registers that the other warps give up
+//   8 (BOX = 32: 4) warps  tokens: shared memory -> fp16 -> shared memory (128-byte swizzle), half or a quarter of a row per lane
+//   8 warps       epilogue: TMEM -> registers -> Y; they take registers that the other warps give up
 // All the warps that expand take part in every stage: groups that take stages in turn can be two phases of a barrier
 // behind, which its parity does not tell from none.
 // TMEM: 256 columns of sums (tokens), then the expanded weights of W_SLOTS stages, 64 columns each.
 //
-// SPLIT: few tiles, so a cluster of up to 4 pairs shares the columns of one tile, and its pairs' sums are added
-// through each other's shared memory, each pair for its own part of the tokens. Such tiles are mostly narrow,
-// bound by the weights and the time that one stage takes: more stages of codes are in flight, the tokens have 4 warps
-// (12..15, of which each takes a part of the columns where there are fewer rows), the epilogue 4 (16..19).
+// BOX: the tokens that a CTA brings of a tile, 128, 64 or 32. Narrow tiles leave room for more stages of codes (w_raws), and what
+// their tokens take is smaller: a stage of a tile of 64, 128, 256 tokens takes 680, 800, 1060 cycles. (The box was a variable
+// once: 128 tokens then took 950, 256 of a split tile 1310.)
 //
-// What bounds it: the MMAs. With its weights in TMEM an MMA of 16 columns takes 128 cycles with 256 tokens or with fewer, so a
-// stage cannot take less than 1024; it takes 1030 to 1080. 8192 x 8192 x 8192 545 us, 2.02 PFLOP/s, with the tensor pipe
+// SPLIT: few tiles, so a cluster of up to 4 pairs shares the columns of one tile, and its pairs' sums are added
+// through each other's shared memory, each pair for its own part of the tokens, by all warps.
+//
+// What bounds it: with 256 tokens the MMAs, 128 cycles for 16 columns, so that a stage cannot take less than 1024; it takes 1030 to
+// 1080. With fewer the expansion of the weights. 8192 x 8192 x 8192 545 us, 2.02 PFLOP/s, with the tensor pipe
 // busy 89 % of the launch (a bf16 library product of that size takes 546 to 560); 16384 x 4096 x 14336 963 to
 // 1040 us from one card to the next, by the clock that the power limit leaves. Small products are the launch, the first stage's way through all
-// of it (3.5 us), 17 us for each round of 32 stages, and the last tile's stores (2.6 us).
+// of it (3.5 us), 12 to 17 us for each round of 32 stages, and the last tile's stores (2.6 us).
 // Taken back: expanding warps in groups that take stages in turn (no faster once all follow the barriers); two expanded
 // stages and four of codes (10 % slower); codes let go before there is room for them (7 % slower); copies of later stages
 // into L2 ahead (no faster); the arrivals at a stage's two barriers in one place (4 % slower).
@@ -227,13 +228,16 @@ constexpr int W_T = 256;                   // most tokens per tile
 constexpr int W_K = 128;                   // columns per stage
 constexpr int W_RAW = 3, W_SLOTS = 3;      // stages of codes, and of expanded operands
 constexpr int W_MOST_RAW = 8;              // the former where token boxes are small
-constexpr int w_expand(bool split) { return split ? 12 : 16; }   // warps that expand: 8 + 4 or 8 + 8
-constexpr int w_threads(bool split) { return 32 * (split ? 20 : 28); }   // (whole groups of 4 warps: see the end)
+// warps that expand (8 + 8, or 8 + 4 where the tokens are 32 rows of four pieces), threads (whole groups of 4 warps: see the
+// end), and below stages of codes
+constexpr int w_expand(int box) { return box == 32 ? 12 : 16; }
+constexpr int w_threads(int box, bool split) { return 32 * (w_expand(box) + (split ? 8 : 12)); }
 constexpr int W_CODES = W_F * W_K;         // bytes of one operand's codes per stage
 constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per stage
 constexpr uint32_t W_TMEM = 512, W_A0 = 256;
 constexpr int W_TURN = 32 * 64;            // bytes of a warp's buffer: 32 tokens x 32 features of bf16
 constexpr int W_RING = W_RAW * 2 * W_CODES + W_SLOTS * W_WIDE;
+constexpr int w_raws(int box) { return std::min(W_MOST_RAW, (W_RING - W_SLOTS * box * 2 * W_K) / (W_CODES + box * W_K)); }
 constexpr int W_BARS = 2 * W_MOST_RAW + 2 * W_SLOTS + 3;
 
 struct WMaps {
@@ -414,8 +418,8 @@ __device__ __forceinline__ void turn_tokens(const IParams& p, const uint32_t (&v
     __syncwarp();
 }
 
-template <bool SPLIT>
-__global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const __grid_constant__ WMaps m, const IParams p) {
+template <int BOX, bool SPLIT>
+__global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(const __grid_constant__ WMaps m, const IParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W_RING + 8 * W_TURN);
@@ -434,8 +438,8 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
     auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + W_SLOTS + s); };        // the stage's MMAs are done
     const uint32_t tfull = bar0 + 8u * (2 * W_MOST_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
     // the expanded tokens first, then the stages of codes
-    const int box_rows = SPLIT ? p.box : W_F, raws = SPLIT ? p.raw : W_RAW;
-    const uint32_t wide_bytes = box_rows * 2 * W_K, raw_bytes = W_CODES + box_rows * W_K;
+    constexpr int raws = w_raws(BOX), epilogue = 4 + w_expand(BOX);   // (its first warp)
+    constexpr uint32_t wide_bytes = BOX * 2 * W_K, raw_bytes = W_CODES + BOX * W_K;
     const uint32_t rbase = sbase + W_SLOTS * wide_bytes;
     const int per_tile = SPLIT ? 2 * p.splits : 2;
     const uint32_t first = blockIdx.x / per_tile, step = gridDim.x / per_tile;
@@ -447,10 +451,10 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
     if (warp == 2 && elect_one()) {
         for (int s = 0; s < raws; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_free(s), w_expand(SPLIT));
+            mbar_init(raw_free(s), w_expand(BOX));
         }
         for (int s = 0; s < W_SLOTS; ++s) {
-            mbar_init(wide_full(s), 2 * w_expand(SPLIT));
+            mbar_init(wide_full(s), 2 * w_expand(BOX));
             mbar_init(wide_free(s), 1);
         }
         mbar_init(tfull, 1);
@@ -588,14 +592,14 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
                 __syncwarp();
             }
         }
-    } else if (warp < 4 + w_expand(SPLIT)) {
+    } else if (warp < 4 + w_expand(BOX)) {
         // ------------- expansion: a row per lane, some of the stage's four pieces of 32 columns -------------
         if constexpr (!SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const bool weights = warp < 12;
-        const int member = warp - (weights ? 4 : 12), row_warps = weights ? 4 : box_rows / 32;
+        const int member = warp - (weights ? 4 : 12), row_warps = weights ? 4 : BOX / 32;
         const int q = member % row_warps, r = 32 * q + lane;
-        // (SPLIT: four warps share the tokens' rows and columns)
-        const int pieces = !SPLIT || weights ? 2 : row_warps, first_piece = member / row_warps * pieces;
+        // (fewer than 128 rows of tokens: one piece of them for each warp)
+        const int pieces = row_warps == 4 ? 2 : 1, first_piece = member / row_warps * pieces;
         const uint32_t column = tmem + ((uint32_t)(32 * q) << 16) + W_A0 + 16 * first_piece;
         const uint32_t wide_remote = in_cta(wide_full(0), even);   // (mapa in the loop cost 5 %)
         int stage = 0, slot = 0;
@@ -631,21 +635,18 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
                     tmem_st_wait();
                     tc_fence_before();
                 } else {
-                    if (SPLIT && pieces == 1) {
+                    if constexpr (BOX < 128) {
                         uint4 code[2];
                         if (live) load_codes<1>(src, first_piece, r & 7, code);
                         if (!freed()) break;
                         if (live) store_wide<1>(dst, wide_bytes / 2, first_piece, r & 7, code);
                         taken();
                     } else {
-                        for (int h = 0; h < (SPLIT ? pieces : 2); h += 2) {
-                            uint4 code[4];
-                            if (live) load_codes<2>(src, first_piece + h, r & 7, code);
-                            if (h == 0 && !freed()) break;
-                            if (live) store_wide<2>(dst, wide_bytes / 2, first_piece + h, r & 7, code);
-                            if (h + 2 >= pieces) taken();
-                        }
-                        if (!ok) break;
+                        uint4 code[4];
+                        if (live) load_codes<2>(src, first_piece, r & 7, code);
+                        if (!freed()) break;
+                        if (live) store_wide<2>(dst, wide_bytes / 2, first_piece, r & 7, code);
+                        taken();
                     }
                     fence_proxy_async_smem();
                 }
@@ -669,10 +670,10 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         // ------------------------------- epilogue -----------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int q = warp & 3;
-        const int c0 = W_T / 2 * ((warp - 20) >> 2);   // its half of the columns
+        const int c0 = W_T / 2 * ((warp - epilogue) >> 2);   // its half of the columns
         const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + c0;
-        const uint32_t turn = sbase + W_RING + (warp - 20) * W_TURN;
-        float* sx = token_scales + (warp - 20) * (W_T / 2);   // the scales of its tokens
+        const uint32_t turn = sbase + W_RING + (warp - epilogue) * W_TURN;
+        float* sx = token_scales + (warp - epilogue) * (W_T / 2);   // the scales of its tokens
         const bool relu = p.relu != 0;
         uint32_t tile = 0;
         for (uint32_t i = first; i < ntiles; i += step, ++tile) {
@@ -759,7 +760,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         // each pair's tokens, whole fours (n is a multiple of 32); the last ones may have fewer or none
         const int own = (t.n / 4 + p.splits - 1) / p.splits * 4, blocks = (own + 31) / 32;
         auto part_of = [&](int s) { return min(max(t.n - s * own, 0), own); };
-        for (int b = mover; b < blocks * (p.splits - 1); b += w_threads(true) / 128) {
+        for (int b = mover; b < blocks * (p.splits - 1); b += w_threads(BOX, SPLIT) / 128) {
             const int other = b / blocks, to = other < share ? other : other + 1, c = b % blocks * 32;
             const int theirs = part_of(to);
             const uint32_t dst = in_cta(sbase, 2 * to + half) + (uint32_t)((share < to ? share : share - 1) * own + c) * (W_F * 4) + feature * 16;
@@ -775,7 +776,7 @@ __global__ void __launch_bounds__(w_threads(SPLIT), 1) int8_matmul_kernel(const 
         }
         cluster_sync();   // all have what they wait for, and nobody's shared memory is touched any more
         const int mine = part_of(share);
-        for (int b = mover; b < (mine + 31) / 32; b += w_threads(true) / 128) {
+        for (int b = mover; b < (mine + 31) / 32; b += w_threads(BOX, SPLIT) / 128) {
             const int c = 32 * b, tok = share * own + c;
             uint32_t v[32];
             tmem_ld_32x32b_x32(lanes + tok, v);
@@ -821,7 +822,7 @@ bool code_map(CUtensorMap* m, const int8_t* codes, int64_t rows, int64_t cols, i
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool SPLIT>
+template <int BOX, bool SPLIT>
 cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2]) {
     constexpr int kFixed = 1024 + W_RING + 8 * W_TURN + 8 * W_BARS + 8 + 16 * W_T;
     constexpr int kMost = kFixed + 12 * I_MAX_EXPERTS + 4;
@@ -829,7 +830,7 @@ cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunc
     static_assert(W_T * W_F * 4 <= W_RING, "a split tile's sums take the place of the stages");
     *cfg = {};
     cfg->gridDim = dim3(ctas);
-    cfg->blockDim = dim3(w_threads(SPLIT));
+    cfg->blockDim = dim3(w_threads(BOX, SPLIT));
     cfg->dynamicSmemBytes = kFixed + 12 * p.experts + 4;
     cfg->stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -841,7 +842,7 @@ cudaError_t configure(const IParams& p, unsigned ctas, cudaStream_t s, cudaLaunc
     cfg->attrs = attr;
     cfg->numAttrs = 2;
     // the limit is the kernel's and not the call's: every thread's calls set it to the same number
-    return cudaFuncSetAttribute(int8_matmul_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    return cudaFuncSetAttribute(int8_matmul_kernel<BOX, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
 }
 
 // How many clusters of 2 * splits CTAs the device holds at once (its GPCs are not all multiples of 8 SMs)
@@ -857,8 +858,8 @@ int clusters_at_once(int splits) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (configure<true>(p, 2 * splits, nullptr, &cfg, attr) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, int8_matmul_kernel<true>, &cfg) != cudaSuccess) {
+    if (configure<128, true>(p, 2 * splits, nullptr, &cfg, attr) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, int8_matmul_kernel<128, true>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
@@ -866,14 +867,14 @@ int clusters_at_once(int splits) {
     return n;
 }
 
-template <bool SPLIT>
+template <int BOX, bool SPLIT>
 int launch_pairs(const WMaps& m, const IParams& p, int64_t most_tiles, cudaStream_t s) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     const unsigned ctas = SPLIT ? (unsigned)most_tiles * 2 * p.splits : 2 * (unsigned)std::min<int64_t>(most_tiles, device_sm_count() / 2);
-    GPTQ_CUDA_TRY(configure<SPLIT>(p, ctas, s, &cfg, attr));
-    cudaError_t e = cudaSuccess;
-    GPTQ_LAUNCH(K_INT8_MM, s, e = cudaLaunchKernelEx(&cfg, int8_matmul_kernel<SPLIT>, m, p));
+    cudaError_t e = configure<BOX, SPLIT>(p, ctas, s, &cfg, attr);
+    GPTQ_CUDA_TRY(e);
+    GPTQ_LAUNCH(K_INT8_MM, s, e = cudaLaunchKernelEx(&cfg, int8_matmul_kernel<BOX, SPLIT>, m, p));
     GPTQ_CUDA_TRY(e);
     return GPTQ_OK;
 }
@@ -882,22 +883,25 @@ struct Plan {
     int width, splits;
 };
 // The width of token tiles, and in how many shares the columns are split: what takes the fewest cycles by what was measured.
-// A stage takes 1080 whatever the width (an MMA of 16 columns with its weights in TMEM takes 128, with 256 tokens or fewer),
-// a round of tiles 1700 more, a launch 10000; where the columns are split a launch takes 6500 and the sums' exchange 64 for
-// each token. With experts their rows are not known here, so tiles are as wide as can be. *most: the most tiles.
-// Features x columns 4096 x 4096, us: 512 tokens as 256 x 2 shares 20.1, as 256 and 128 in whole 25.1 and 24.5; 256 tokens as 128 x 2
-// 15.7, as 256 x 2 19.7, as 64 x 2 in two rounds 26.3; 64 tokens as 64 x 2 13.4, as 256 x 2 16.6.
+// In cycles: a stage takes 560 and 2 for each token of the width, a round of tiles 1700 more, a launch 5800 and 20 for each token;
+// where the columns are split a launch and the sums' exchange take 9500 and 28 (two shares) or 40 for each token. With experts
+// their rows are not known here: the width is the one for evenly spread ones with room for half as many again or so, and an expert
+// with more rows has several tiles. *most: the most tiles.
+// Features x columns 4096 x 4096, us: 512 tokens as 256 x 2 shares 18.8, as 256 and 128 in whole 25.1 and 20.3; 256 tokens as 128 x 2
+// 14.8, as 64 in whole 17.0, as 256 x 3 17.1; 64 tokens as 64 x 3 12.0, as 64 x 2 13.0. 8 experts of 14336 x 4096, 200 rows in tiles
+// of 64, 128, 256: 82, 85, 107; 320 rows 84, 86, 109; 500 rows 116, 92, 114; 700 rows 153, 96, 116; 1000 rows 171, 129, 120.
 Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, int64_t pairs, int64_t* most) {
     const int64_t ftiles = ceil_div(N, W_PF), stages = ceil_div(K, W_K);
     Plan best = {W_T, 1};
     int64_t least = -1;
     for (int64_t tt = ceil_div(T, W_T);; ++tt) {
-        const int width = by_expert ? W_T : (int)(ceil_div(ceil_div(T, tt), 32) * 32);
+        const int width = by_expert ? (T <= 32 * experts ? 64 : T <= 96 * experts ? 128 : W_T) : (int)(ceil_div(ceil_div(T, tt), 32) * 32);
         const int64_t tiles = (ceil_div(T, width) + (by_expert ? std::min(experts, T) : 0)) * ftiles;
         for (int k = 1; k <= 4; ++k) {
             if (k > 1 && (tiles * k > pairs || stages < 2 * k || tiles > clusters_at_once(k))) break;
-            const int64_t cycles = k > 1 ? ceil_div(stages, k) * 1080 + 6500 + 64 * width
-                                         : ceil_div(tiles, pairs) * (stages * 1080 + 1700) + 10000;
+            const int64_t stage = 560 + 2 * width;
+            const int64_t cycles = k > 1 ? ceil_div(stages, k) * stage + 9500 + (k == 2 ? 28 : 40) * width
+                                         : ceil_div(tiles, pairs) * (stages * stage + 1700) + 5800 + 20 * width;
             if (least < 0 || cycles < least) {
                 least = cycles;
                 best = {width, k};
@@ -914,16 +918,17 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 // Whether the kernel for few rows is the faster one. Measured (us, few rows / pairs; weights from memory, features x
 // columns):
 //                   1 token     16 tokens    32 tokens    64 tokens
-//    4096 x 4096    5.7 / 11.0   7.0 / 11.3   9.4 / 12.9  15.2 / 13.0
-//   14336 x 4096   13.7 / 21.7  18.7 / 21.7  25.5 / 21.9  43.5 / 22.6
-//    4096 x 14336  14.5 / 23.8  17.7 / 24.1  25.1 / 24.1  44.6 / 25.2
-//    1024 x 4096    4.2 /  8.1   5.7 /  8.2   7.7 /  8.3  13.1 /  9.1
-//    4096 x 1024                                          7.0 /  8.3 (96 tokens 9.4 / 9.0)
-//     512 x 512                                           4.2 /  6.5
-// Experts, rows at random: 16 of 1024 x 4096, 32 rows 14.4 / 22.7, 96 rows 19.3 / 22.6, 128 rows 21.1 / 22.6, 192 rows 25.1 / 22.6;
-// 8 of 14336 x 4096, 16 rows 69 / 106, 64 rows 91 / 106; 16 of 512 x 1024, 256 rows 9.2 / 10.1; 32 of 700 x 300, 400 rows 7.3 / 13.0
+//    4096 x 4096    5.7 / 11.0   7.1 / 11.4   9.5 / 11.4  15.2 / 12.0
+//   14336 x 4096   13.7 / 18.0  18.6 / 18.0  25.8 / 18.1  43.5 / 18.9
+//    4096 x 14336  14.5 / 21.2  17.7 / 21.3  25.2 / 21.4  44.6 / 22.1
+//    1024 x 4096    4.2 /  8.1   5.7 /  9.2   8.0 /  9.3  13.4 /  9.4
+//    4096 x 1024                                          6.9 /  8.2 (96 tokens 9.5 / 7.8)
+//     512 x 512                                           4.2 /  5.6 (100 tokens 6.6 / 5.7)
+// Experts, rows at random: 16 of 1024 x 4096, 32 rows 14.1 / 19.2, 64 rows 16.3 / 19.8, 96 rows 19.2 / 19.8, 128 rows 20.7 / 19.9;
+// 8 of 14336 x 4096, 8 rows 51 / 62, 32 rows 78 / 80, 48 rows 82 / 80, 64 rows 98 / 80; 32 of 512 x 1024, 256 rows 7.6 / 10.5, 512 rows
+// 15.6 / 10.4; 32 of 700 x 300, 100 rows 5.1 / 11.5, 400 rows 14.9 / 12.6
 bool few_rows_pay(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts) {
-    if (by_expert) return T <= 8 * experts || (T <= 16 * experts && N * K <= 600000);
+    if (by_expert) return T <= 6 * experts || (T <= 10 * experts && N * K <= 600000);
     return T <= 16 || (T <= 32 && N * K <= 24000000) || (T <= 64 && K <= 1024 && N * K <= 5000000);
 }
 
@@ -987,11 +992,12 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
     const Plan plan = plan_of(T, N, K, offsets != nullptr, experts, device_sm_count() / 2, &most);
     p.width = plan.width;
     p.splits = plan.splits;
-    if (p.splits > 1) {
-        p.box = p.width <= 64 ? 32 : p.width <= 128 ? 64 : 128;
-        p.raw = std::min(W_MOST_RAW, (W_RING - W_SLOTS * p.box * 2 * W_K) / (W_CODES + p.box * W_K));
-    }
-    const int rc = p.splits > 1 ? launch_pairs<true>(m, p, most, s) : launch_pairs<false>(m, p, most, s);
+    const int rc = p.splits == 1 ? (p.width <= 64    ? launch_pairs<32, false>(m, p, most, s)
+                                    : p.width <= 128 ? launch_pairs<64, false>(m, p, most, s)
+                                                     : launch_pairs<128, false>(m, p, most, s))
+                                 : (p.width <= 64    ? launch_pairs<32, true>(m, p, most, s)
+                                    : p.width <= 128 ? launch_pairs<64, true>(m, p, most, s)
+                                                     : launch_pairs<128, true>(m, p, most, s));
     return rc != GPTQ_OK ? rc : st.finish(s);
 }
 
