@@ -32,6 +32,12 @@ def test_bounded_waits_time_out_and_unwind(lib, T, N, K, E):
     assert torch.equal(lib.gptq_int8_matmul(X, W, offsets=o), ref)
 
 
+@pytest.mark.parametrize("T,N,K,E", [(64, 4096, 4096, None), (128, 2000, 3000, None), (40, 10240, 600, None), (100, 10240, 300, None),
+                                     (200, 700, 300, 8), (500, 700, 300, 8)])
+def test_bounded_waits_in_tiles_of_other_widths(lib, T, N, K, E):
+    test_bounded_waits_time_out_and_unwind(lib, T, N, K, E)
+
+
 def test_several_host_threads(lib):
     """Dense and expert products of several kernels, the norm, its gradient and the balance at once, each thread on a stream of its own"""
     rng = np.random.default_rng(3)

@@ -507,3 +507,29 @@ def test_norm_of_several_rows_per_cta(lib, rows, cols, dt):
         a = [rows_of(rows, cols, dt, s, 1) for s in (1, 2)]
         q2, _, rstd2 = lib.gptq_int8_rms_norm(a[0], gain, 1e-5, a[1], out=(None, a[i], None))
         assert torch.equal(a[i], h) and torch.equal(q2.codes, q.codes) and torch.equal(q2.scales, q.scales) and torch.equal(rstd2, rstd), i
+
+
+@pytest.mark.parametrize("T,N,K,E", [(64, 4096, 4096, None), (40, 10240, 600, None), (100, 10240, 300, None), (130, 10241, 200, None),
+                                     (60, 4000, 2000, None), (96, 4000, 3000, None), (128, 4000, 7000, None), (250, 5000, 9000, None),
+                                     (200, 600, 2000, None), (90, 1000, 5000, None), (230, 2600, 6000, None), (250, 3800, 9000, None),
+                                     (200, 700, 300, 8), (500, 700, 300, 8), (150, 300, 500, 16), (90, 300, 2000, 3), (300, 300, 3000, 4),
+                                     (60, 100, 3000, 3), (250, 300, 4000, 2), (1200, 520, 640, 16), (900, 300, 1000, 40)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_product_in_tiles_of_every_width(lib, T, N, K, E, dt):
+    """Tiles of 64, 128 and 256 tokens, whole and with the columns in two to four shares; experts with rows at random and all in
+    one; the same each time. (Codes small enough for sums below 2^24.)"""
+    rng = np.random.default_rng(T + N)
+    xc, wc = rng.integers(-40, 41, (T, K)).astype(np.int8), rng.integers(-40, 41, (E, N, K) if E else (N, K)).astype(np.int8)
+    xs, ws = (np.exp(rng.normal(size=s) - 4).astype(np.float32) for s in ((T,), wc.shape[:-1]))
+    X, W = _stored(lib, xc, xs), _stored(lib, wc, ws)
+    for kind in (("gaps", "one") if E else (None,)):
+        o = _offsets(rng, T, E, kind) if E else None
+        offsets = torch.tensor(o, dtype=torch.int32, device=DEV) if E else None
+        y = lib.gptq_int8_matmul(X, W, offsets=offsets, out_dtype=DT[dt])
+        ref = torch.zeros(T, N, dtype=torch.float64, device=DEV)   # (whole numbers: exact in 64 bits)
+        for e, (a, b) in enumerate(zip(o[:-1], o[1:]) if E else [(0, T)]):
+            w, s = (W.codes[e], W.scales[e]) if E else W[:2]
+            ref[a:b] = (X.codes[a:b].double() @ w.double().T) * X.scales[a:b, None].double() * s.double()
+        _check(y, f64(ref), dt)
+        for _ in range(30):
+            assert torch.equal(lib.gptq_int8_matmul(X, W, offsets=offsets, out_dtype=DT[dt]), y)
