@@ -56,7 +56,10 @@ __device__ __forceinline__ float scale_of(uint32_t m) {
     return fmaf(fmaf(-q, 127.0f, a), inv, q);
 }
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// the larger of a magnitude and |v|, a NaN above all: as bits it is largest too
+__device__ __forceinline__ float larger(float m, float v) { return max_nan(m, fabsf(v)); }
+// the same of two pairs of bf16, as bits
+__device__ __forceinline__ uint32_t larger_pair(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
 
 // ------------------------------------------------------------------------------------ units of a row
 // A thread works on units of N = 16 / sizeof(T) neighbouring columns, unit j being columns N j .. N j + N - 1
@@ -359,10 +362,10 @@ __device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
 // Rows in the registers of their threads, UNITS units each: a row is read once and everything written once. CTAs
 // are persistent, and the next row's loads are under way while this one is reduced and written. Four units per thread, so
 // that what every warp does for a row (its sums, scale and reciprocals) is shared by more columns.
-// Bound by memory, and for bf16 nearly as much by instructions (52 to 63 % of the issue slots). 16384 x 4096: bf16 37 us
-// (5.4 TB/s), with the norm and a residual 78 (6.0); fp32 51 (6.6) and 137 (6.4). With two units per thread bf16 took 39 and
+// Bound by memory, and for bf16 nearly as much by instructions (52 to 63 % of the issue slots). 16384 x 4096: bf16 34 us
+// (5.9 TB/s), with the norm and a residual 78 (6.0); fp32 51 (6.6) and 137 (6.4). With two units per thread bf16 took 39 and
 // 91, with a CTA for each row and no loads ahead 52 and 107. Rows at odd addresses pay for the shifting: 16384 x 4095
-// bf16 54 and 133 us (column by column 109 and 278), fp32 65 and 165. MOST is 512 or, for longer rows of fp32, 1024 threads:
+// bf16 45 and 133 us (column by column 109 and 278), fp32 65 and 165. MOST is 512 or, for longer rows of fp32, 1024 threads:
 // the norm of 16384 x 4095 fp32 took 202 us within the 64 registers of the latter, the quantisation 74 instead of 65 with more.
 template <typename T, int UNITS, bool NORM, bool ANY, int MOST>
 __global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_rows_kernel(const RowParams p) {
@@ -408,6 +411,13 @@ __global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_
                 if constexpr (sizeof(T) == 2) unpack<T>(pack<T>(v[i]), v[i]);   // h as it is stored
             }
         }
+        float top = 0.0f;   // the largest magnitude that is quantised
+        if constexpr (!NORM && sizeof(T) == 2) {
+            uint32_t two = 0;
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) two = larger_pair(larger_pair(larger_pair(larger_pair(two, x[i].x), x[i].y), x[i].z), x[i].w);
+            top = __uint_as_float(max(two << 16, two & 0xFFFF0000u));
+        }
         if (r + step < p.rows) load(r + step);
         if constexpr (NORM) {
             auto squares = [&](float f) {
@@ -439,12 +449,13 @@ __global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_
                 for (int e = 0; e < N; ++e) v[i][e] = v[i][e] * rstd * g[e];
             }
         }
-        uint32_t m = 0;
+        if constexpr (NORM || sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i)
+            for (int i = 0; i < UNITS; ++i)
 #pragma unroll
-            for (int e = 0; e < N; ++e) m = max(m, magnitude(v[i][e]));
-        m = row_max(m, max_part[turn]);
+                for (int e = 0; e < N; ++e) top = larger(top, v[i][e]);
+        }
+        const uint32_t m = row_max(__float_as_uint(top), max_part[turn]);
         const bool bad = m >= 0x7F800000u;
         const float s = scale_of(m);
         if (threadIdx.x == 0) {
@@ -542,13 +553,13 @@ __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p)
             for (int e = 0; e < N; ++e) v[e] = v[e] * rstd * g[e];
         }
     };
-    uint32_t m = 0;
+    float top = 0.0f;
     sweep(x, [&](uint32_t j, float(&v)[N]) {
         scaled(j, v);
 #pragma unroll
-        for (int e = 0; e < N; ++e) m = max(m, magnitude(v[e]));
+        for (int e = 0; e < N; ++e) top = larger(top, v[e]);
     });
-    m = row_max(m, max_part);
+    const uint32_t m = row_max(__float_as_uint(top), max_part);
     const bool bad = m >= 0x7F800000u;
     const float s = scale_of(m);
     if (threadIdx.x == 0) {
