@@ -300,14 +300,35 @@ __device__ __forceinline__ uint32_t code_of(float x, const Step& t) {   // in th
     return __float_as_uint(q + 12582912.0f);
 }
 
+// two fp32 operations at a time
+struct Pair {
+    uint64_t w;
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit Pair(float a) : Pair(a, a) {}
+    __device__ __forceinline__ void get(uint32_t& a, uint32_t& b) const { asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(w)); }
+};
+__device__ __forceinline__ Pair operator*(Pair a, const Pair& b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.w) : "l"(b.w));
+    return a;
+}
+__device__ __forceinline__ Pair operator+(Pair a, const Pair& b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.w) : "l"(b.w));
+    return a;
+}
+__device__ __forceinline__ Pair fma2(Pair a, const Pair& b, const Pair& c) {
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.w) : "l"(b.w), "l"(c.w));
+    return a;
+}
+
 template <int N>
 __device__ __forceinline__ void store_codes(int8_t* y, const float (&v)[N], const Step& t) {
     uint32_t u[N], w[N / 4];
     if (t.usual) {
+        const Pair inv(t.inv), minus(-t.d), one_half(12582912.0f);   // (1.5 * 2^23)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float q = v[e] * t.inv;
-            u[e] = __float_as_uint(fmaf(fmaf(-q, t.d, v[e]), t.inv, q) + 12582912.0f);
+        for (int e = 0; e < N; e += 2) {
+            const Pair x(v[e], v[e + 1]), q = x * inv;
+            (fma2(fma2(q, minus, x), inv, q) + one_half).get(u[e], u[e + 1]);
         }
     } else {
 #pragma unroll
@@ -362,10 +383,10 @@ __device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
 // Rows in the registers of their threads, UNITS units each: a row is read once and everything written once. CTAs
 // are persistent, and the next row's loads are under way while this one is reduced and written. Four units per thread, so
 // that what every warp does for a row (its sums, scale and reciprocals) is shared by more columns.
-// Bound by memory, and for bf16 nearly as much by instructions (52 to 63 % of the issue slots). 16384 x 4096: bf16 34 us
-// (5.9 TB/s), with the norm and a residual 78 (6.0); fp32 51 (6.6) and 137 (6.4). With two units per thread bf16 took 39 and
+// Bound by memory, and for bf16 nearly as much by instructions. 16384 x 4096: bf16 34 us
+// (6.0 TB/s), with the norm and a residual 77 (6.1); fp32 51 (6.6) and 136 (6.4). With two units per thread bf16 took 39 and
 // 91, with a CTA for each row and no loads ahead 52 and 107. Rows at odd addresses pay for the shifting: 16384 x 4095
-// bf16 45 and 133 us (column by column 109 and 278), fp32 65 and 165. MOST is 512 or, for longer rows of fp32, 1024 threads:
+// bf16 44 and 128 us (column by column 109 and 278), fp32 65 and 165. MOST is 512 or, for longer rows of fp32, 1024 threads:
 // the norm of 16384 x 4095 fp32 took 202 us within the 64 registers of the latter, the quantisation 74 instead of 65 with more.
 template <typename T, int UNITS, bool NORM, bool ANY, int MOST>
 __global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_rows_kernel(const RowParams p) {
@@ -472,7 +493,7 @@ __global__ void __launch_bounds__(NORM || sizeof(T) == 2 ? MOST : 1024, 1) int8_
 
 // The same for rows of any length: passes over the row, of which all but the first find it in L2, four units of a thread in
 // flight at a time. (The norm's later passes read h, each thread what it wrote itself.) ANY: a warp's units take its columns in
-// turn, element by element. 1024 x 40000 bf16 37 us, with single elements in flight 84; 4096 x 28672 83 (4.2 TB/s).
+// turn, element by element. 1024 x 40000 bf16 35 us, with single elements in flight 84; 4096 x 28672 81 (4.4 TB/s).
 template <typename T, bool NORM, bool ANY>
 __global__ void __launch_bounds__(1024) int8_long_rows_kernel(const RowParams p) {
     constexpr int N = kUnit<T>, UNITS = 4;
