@@ -894,7 +894,8 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, i
     const int64_t ftiles = ceil_div(N, W_PF), stages = ceil_div(K, W_K);
     Plan best = {W_T, 1};
     int64_t least = -1;
-    for (int64_t tt = ceil_div(T, W_T);; ++tt) {
+    const int64_t fewest = ceil_div(T, W_T);
+    for (int64_t tt = fewest;; ++tt) {
         const int width = by_expert ? (T <= 32 * experts ? 64 : T <= 96 * experts ? 128 : W_T) : (int)(ceil_div(ceil_div(T, tt), 32) * 32);
         const int64_t tiles = (ceil_div(T, width) + (by_expert ? std::min(experts, T) : 0)) * ftiles;
         for (int k = 1; k <= 4; ++k) {
@@ -908,7 +909,8 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, i
                 *most = tiles;
             }
         }
-        if (by_expert || width == 32 || tiles > pairs) return best;   // (narrower tiles only pay while all run at once)
+        // (in several rounds only somewhat narrower tiles pay, and in many rounds none)
+        if (by_expert || width == 32 || (tiles > pairs && (tt > fewest + fewest / 2 || fewest > 64))) return best;
     }
 }
 
