@@ -237,7 +237,14 @@ constexpr int W_WIDE = 2 * W_T / 2 * W_K;  // bytes of the expanded tokens per s
 constexpr uint32_t W_TMEM = 512, W_A0 = 256;
 constexpr int W_TURN = 32 * 64;            // bytes of a warp's buffer: 32 tokens x 32 features of bf16
 constexpr int W_RING = W_RAW * 2 * W_CODES + W_SLOTS * W_WIDE;
-constexpr int w_raws(int box) { return std::min(W_MOST_RAW, (W_RING - W_SLOTS * box * 2 * W_K) / (W_CODES + box * W_K)); }
+// A split tile's sums from its cluster's other pairs (three quarters of its tokens at most) have their own shared memory where
+// there is room, which spares a meeting of the cluster (64 x 4096 x 4096 12.0 -> 11.1 us), and else the stages'. SPLIT has no
+// use for the warps' buffers of the epilogue behind the stages.
+constexpr int w_apart(int box, bool split) { return split && box < W_F ? 2 * box * 3 / 4 * W_F * 4 : 0; }
+constexpr int w_room(bool split) { return W_RING + (split ? 8 * W_TURN : 0); }
+constexpr int w_raws(int box, bool split) {
+    return std::min(W_MOST_RAW, (w_room(split) - w_apart(box, split) - W_SLOTS * box * 2 * W_K) / (W_CODES + box * W_K));
+}
 constexpr int W_BARS = 2 * W_MOST_RAW + 2 * W_SLOTS + 3;
 
 struct WMaps {
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
     auto wide_free = [&](int s) { return bar0 + 8u * (2 * W_MOST_RAW + W_SLOTS + s); };        // the stage's MMAs are done
     const uint32_t tfull = bar0 + 8u * (2 * W_MOST_RAW + 2 * W_SLOTS), tfree = tfull + 8, drain_bar = tfull + 16;
     // the expanded tokens first, then the stages of codes
-    constexpr int raws = w_raws(BOX), epilogue = 4 + w_expand(BOX);   // (its first warp)
+    constexpr int raws = w_raws(BOX, SPLIT), epilogue = 4 + w_expand(BOX);   // (its first warp)
     constexpr uint32_t wide_bytes = BOX * 2 * W_K, raw_bytes = W_CODES + BOX * W_K;
     const uint32_t rbase = sbase + W_SLOTS * wide_bytes;
     const int per_tile = SPLIT ? 2 * p.splits : 2;
@@ -749,13 +756,15 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
     if (!ok && lane == 0) set_status(p.status, GPTQ_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // no CTA leaves, or frees TMEM, while another may still use it
+    constexpr bool APART = w_apart(BOX, SPLIT) > 0;
+    if (!APART) cluster_sync();   // no CTA leaves, or frees TMEM, while another may still use it
     if constexpr (SPLIT) {
-        // No copy or MMA of the cluster uses its shared memory any more. Each pair sends the others their parts of its sums and
+        // No copy or MMA uses the memory that the sums go to (any more). Each pair sends the others their parts of its sums and
         // adds what it got to its own; all warps take part, each in its quarter of the lanes. ([source][token / 4][feature][4])
         tc_fence_after();
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int feature = 32 * (warp & 3) + lane, mover = warp >> 2;
+        const uint32_t sums = sbase + (APART ? w_room(SPLIT) - w_apart(BOX, SPLIT) : 0);
         const WTile t = first < ntiles ? find_tile(p, w, first) : WTile{0, 0, 0, 0, 0};
         // each pair's tokens, whole fours (n is a multiple of 32); the last ones may have fewer or none
         const int own = (t.n / 4 + p.splits - 1) / p.splits * 4, blocks = (own + 31) / 32;
@@ -763,7 +772,7 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
         for (int b = mover; b < blocks * (p.splits - 1); b += w_threads(BOX, SPLIT) / 128) {
             const int other = b / blocks, to = other < share ? other : other + 1, c = b % blocks * 32;
             const int theirs = part_of(to);
-            const uint32_t dst = in_cta(sbase, 2 * to + half) + (uint32_t)((share < to ? share : share - 1) * own + c) * (W_F * 4) + feature * 16;
+            const uint32_t dst = in_cta(sums, 2 * to + half) + (uint32_t)((share < to ? share : share - 1) * own + c) * (W_F * 4) + feature * 16;
             uint32_t v[32];
             tmem_ld_32x32b_x32(lanes + to * own + c, v);
             tmem_ld_wait();
@@ -774,7 +783,7 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
                                  "r"(v[4 * u + 1]), "r"(v[4 * u + 2]), "r"(v[4 * u + 3])
                                  : "memory");
         }
-        cluster_sync();   // all have what they wait for, and nobody's shared memory is touched any more
+        cluster_sync();   // all have what they wait for, nobody's shared memory is touched any more, nor TMEM by another's MMAs
         const int mine = part_of(share);
         for (int b = mover; b < (mine + 31) / 32; b += w_threads(BOX, SPLIT) / 128) {
             const int c = 32 * b, tok = share * own + c;
@@ -785,7 +794,7 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     if (c + 4 * u >= mine) break;
-                    const uint4 a = lds128(sbase + (uint32_t)(j * own + c + 4 * u) * (W_F * 4) + feature * 16);
+                    const uint4 a = lds128(sums + (uint32_t)(j * own + c + 4 * u) * (W_F * 4) + feature * 16);
                     v[4 * u] = __float_as_uint(__uint_as_float(v[4 * u]) + __uint_as_float(a.x));
                     v[4 * u + 1] = __float_as_uint(__uint_as_float(v[4 * u + 1]) + __uint_as_float(a.y));
                     v[4 * u + 2] = __float_as_uint(__uint_as_float(v[4 * u + 2]) + __uint_as_float(a.z));
@@ -884,11 +893,11 @@ struct Plan {
 };
 // The width of token tiles, and in how many shares the columns are split: what takes the fewest cycles by what was measured.
 // In cycles: a stage takes 560 and 2 for each token of the width, a round of tiles 1700 more, a launch 5800 and 20 for each token;
-// where the columns are split a launch and the sums' exchange take 9500 and 28 (two shares) or 40 for each token. With experts
+// where the columns are split a launch and the sums' exchange take 8100 (256 tokens: 9500) and 28 (two shares) or 40 for each token. With experts
 // their rows are not known here: the width is the one for evenly spread ones with room for half as many again or so, and an expert
 // with more rows has several tiles. *most: the most tiles.
 // Features x columns 4096 x 4096, us: 512 tokens as 256 x 2 shares 18.8, as 256 and 128 in whole 25.1 and 20.3; 256 tokens as 128 x 2
-// 14.8, as 64 in whole 17.0, as 256 x 3 17.1; 64 tokens as 64 x 3 12.0, as 64 x 2 13.0. 8 experts of 14336 x 4096, 200 rows in tiles
+// 14.8, as 64 in whole 17.0, as 256 x 3 17.1; 64 tokens as 64 x 3 12.0, as 64 x 2 13.0 (11.1 with the sums apart). 8 experts of 14336 x 4096, 200 rows in tiles
 // of 64, 128, 256: 82, 85, 107; 320 rows 84, 86, 109; 500 rows 116, 92, 114; 700 rows 153, 96, 116; 1000 rows 171, 129, 120.
 Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, int64_t pairs, int64_t* most) {
     const int64_t ftiles = ceil_div(N, W_PF), stages = ceil_div(K, W_K);
@@ -901,7 +910,7 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, i
         for (int k = 1; k <= 4; ++k) {
             if (k > 1 && (tiles * k > pairs || stages < 2 * k || tiles > clusters_at_once(k))) break;
             const int64_t stage = 560 + 2 * width;
-            const int64_t cycles = k > 1 ? ceil_div(stages, k) * stage + 9500 + (k == 2 ? 28 : 40) * width
+            const int64_t cycles = k > 1 ? ceil_div(stages, k) * stage + (width > 128 ? 9500 : 8100) + (k == 2 ? 28 : 40) * width
                                          : ceil_div(tiles, pairs) * (stages * stage + 1700) + 5800 + 20 * width;
             if (least < 0 || cycles < least) {
                 least = cycles;
@@ -920,10 +929,10 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 // Whether the kernel for few rows is the faster one. Measured (us, few rows / pairs; weights from memory, features x
 // columns):
 //                   1 token     16 tokens    32 tokens    64 tokens
-//    4096 x 4096    5.7 / 11.0   7.1 / 11.4   9.5 / 11.4  15.2 / 12.0
+//    4096 x 4096    5.7 / 11.0   7.1 / 11.4   9.5 / 11.4  15.2 / 11.1
 //   14336 x 4096   13.7 / 18.0  18.6 / 18.0  25.8 / 18.1  43.5 / 18.9
 //    4096 x 14336  14.5 / 21.2  17.7 / 21.3  25.2 / 21.4  44.6 / 22.1
-//    1024 x 4096    4.2 /  8.1   5.7 /  9.2   8.0 /  9.3  13.4 /  9.4
+//    1024 x 4096    4.2 /  8.1   5.7 /  9.2   8.0 /  9.3  13.4 /  8.7
 //    4096 x 1024                                          6.9 /  8.2 (96 tokens 9.5 / 7.8)
 //     512 x 512                                           4.2 /  5.6 (100 tokens 6.6 / 5.7)
 // Experts, rows at random: 16 of 1024 x 4096, 32 rows 14.1 / 19.2, 64 rows 16.3 / 19.8, 96 rows 19.2 / 19.8, 128 rows 20.7 / 19.9;
