@@ -248,8 +248,9 @@ constexpr int w_raws(int box, bool split) {
 constexpr int W_BARS = 2 * W_MOST_RAW + 2 * W_SLOTS + 3;
 
 struct WMaps {
-    CUtensorMap w, x[3];   // tokens: boxes of 128, 64 and 32 rows
+    CUtensorMap w, x[3];   // tokens: boxes of 128, 64 and 32 rows, those that the width of the tiles can need
 };
+__host__ __device__ __forceinline__ int first_box(int tokens) { return tokens > 128 ? 0 : tokens > 64 ? 1 : 2; }
 
 // Token tiles of rows [lo, hi), all of one width: a multiple of 32, as an MMA of two CTAs wants it
 __device__ __forceinline__ int token_tiles(int lo, int hi, int width) { return hi <= lo ? 0 : (hi - lo + width - 1) / width; }
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
     }
     if (warp == 3 && elect_one()) {
         tma_prefetch_desc(&m.w);
-        tma_prefetch_desc(&m.x[0]);
+        tma_prefetch_desc(&m.x[first_box(2 * BOX)]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(W_TMEM)
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
             for (uint32_t i = first; i < ntiles && ok; i += step) {
                 const WTile t = find_tile(p, w, i);
                 const int n = (int)uniform(t.n), e = (int)uniform(t.e);
-                const int box = n > 128 ? 0 : n > 64 ? 1 : 2;   // (its rows are at most SPLIT's)
+                const int box = first_box(n);   // (its rows are at most BOX)
                 const uint32_t bytes = W_CODES + (W_CODES >> box);
                 const int wrow = e * p.N + (int)uniform(t.f0) + (int)half * W_F, xrow = (int)uniform(t.t0) + (int)half * (n >> 1);
                 for (int k = k0; k < k1; ++k) {
@@ -995,14 +996,14 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
         GPTQ_CUDA_TRY(e);
         return st.finish(s);
     }
-    WMaps m;
-    if (!code_map(&m.w, w_codes, experts * N, K, W_F)) return GPTQ_ERR_CUDA;
-    for (int i = 0; i < 3; ++i)
-        if (!code_map(&m.x[i], x_codes, T, K, W_F >> i)) return GPTQ_ERR_CUDA;
     int64_t most;
     const Plan plan = plan_of(T, N, K, offsets != nullptr, experts, device_sm_count() / 2, &most);
     p.width = plan.width;
     p.splits = plan.splits;
+    WMaps m;
+    if (!code_map(&m.w, w_codes, experts * N, K, W_F)) return GPTQ_ERR_CUDA;
+    for (int i = first_box(p.width); i < 3; ++i)
+        if (!code_map(&m.x[i], x_codes, T, K, W_F >> i)) return GPTQ_ERR_CUDA;
     const int rc = p.splits == 1 ? (p.width <= 64    ? launch_pairs<32, false>(m, p, most, s)
                                     : p.width <= 128 ? launch_pairs<64, false>(m, p, most, s)
                                                      : launch_pairs<128, false>(m, p, most, s))
