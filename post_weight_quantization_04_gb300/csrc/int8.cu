@@ -677,6 +677,7 @@ template <typename T, int UNITS, bool ANY, int MOST>
 __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParams p) {
     constexpr int N = kUnit<T>;
     constexpr bool AHEAD = UNITS <= 2;   // (and the gain and the sums stay in registers)
+    constexpr bool LATE = MOST > 512;    // 64 registers: dH is read once the others are used (4096 x 16384 fp32 216 us, else 245)
     extern __shared__ float4 shared_sums[];   // AHEAD: [groups][columns] floats, where there are several groups; else [UNITS N / 4][threads]
     float* sums = reinterpret_cast<float*>(shared_sums);
     const int tid = threadIdx.x;
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
         for (int i = 0; i < UNITS; ++i) {
             dy[i] = load_raw<T, ANY>(ry, cols, j0 + 32 * i);
             h[i] = load_raw<T, ANY>(rh, cols, j0 + 32 * i);
-            if (p.dH) dh[i] = load_raw<T, ANY>(rd, cols, j0 + 32 * i);
+            if (!LATE && p.dH) dh[i] = load_raw<T, ANY>(rd, cols, j0 + 32 * i);
         }
         rstd = p.rstd[r];
     };
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
         const float rs = rstd;
         to_words<T, ANY>(ry, cols, j0, dy);
         to_words<T, ANY>(rh, cols, j0, h);
-        if (p.dH) to_words<T, ANY>(rd, cols, j0, dh);
+        if (!LATE && p.dH) to_words<T, ANY>(rd, cols, j0, dh);
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) yw[i] = dy[i], hw[i] = h[i], dw[i] = dh[i];
         if (AHEAD && r + step < last) load(r + step);
@@ -751,6 +752,11 @@ __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParam
                 for (int e = 0; e < N; e += 4)
                     shared_sums[(i * N / 4 + e / 4) * blockDim.x + tid] = make_float4(a[e], a[e + 1], a[e + 2], a[e + 3]);
             }
+        }
+        if (LATE && p.dH) {
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) dw[i] = load_raw<T, ANY>(rd, cols, j0 + 32 * i);
+            to_words<T, ANY>(rd, cols, j0, dw);
         }
         const float k = group_sum(dot, part[turn] + group * warps, warps, 1 + group) * inv_n * rs;
 #pragma unroll
