@@ -166,10 +166,9 @@ __device__ __forceinline__ void few_rows(const IParams& p, int e, int t0, int n,
     __syncthreads();
 }
 
-// MOST: groups of 8 tokens at a time; with fewer, more CTAs fit an SM
-template <int MOST, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 2 : 8) int8_few_rows_kernel(const IParams p) {
-    constexpr int AHEAD = WARPS == 8 ? 8 / MOST : 2;
+// MOST: groups of 8 tokens at a time; with fewer, more CTAs fit an SM. CTAS: of an SM, by registers
+template <int MOST, int WARPS, int AHEAD, int CTAS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) int8_few_rows_kernel(const IParams p) {
     __shared__ float part[WARPS][F_FEATURES * 8 * MOST];
     const int e = blockIdx.y, f0 = blockIdx.x * F_FEATURES;
     pdl_trigger();
@@ -930,10 +929,10 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 // Whether the kernel for few rows is the faster one. Measured (us, few rows / pairs; weights from memory, features x
 // columns):
 //                   1 token     16 tokens    32 tokens    64 tokens
-//    4096 x 4096    5.7 / 11.0   7.1 / 11.4   9.5 / 11.4  15.2 / 11.1
+//    4096 x 4096    5.7 / 11.0   7.1 / 11.4   9.0 / 11.1  15.2 / 11.1
 //   14336 x 4096   13.7 / 18.0  18.6 / 18.0  25.8 / 18.1  43.5 / 18.9
 //    4096 x 14336  14.5 / 21.2  17.7 / 21.3  25.2 / 21.4  44.6 / 22.1
-//    1024 x 4096    4.2 /  8.1   5.7 /  9.2   8.0 /  9.3  13.4 /  8.7
+//    1024 x 4096    4.2 /  8.1   5.7 /  9.2   7.0 /  8.7  13.4 /  8.7
 //    4096 x 1024                                          6.9 /  8.2 (96 tokens 9.5 / 7.8)
 //     512 x 512                                           4.2 /  5.6 (100 tokens 6.6 / 5.7)
 // Experts, rows at random: 16 of 1024 x 4096, 32 rows 14.1 / 19.2, 64 rows 16.3 / 19.8, 96 rows 19.2 / 19.8, 128 rows 20.7 / 19.9;
@@ -989,10 +988,15 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
         auto go = [&](auto kern, int warps) { GPTQ_LAUNCH(K_INT8_MM, s, e = launch_pdl(kern, grid, dim3(32 * warps), 0, s, p)); };
         // (with experts the rows of each are not known here: mostly a share of them)
         const int64_t rows = offsets ? T / experts : T;
-        if (rows > 16) go(int8_few_rows_kernel<4, 8>, 8);
-        else if (rows > 8) go(int8_few_rows_kernel<2, 8>, 8);
-        else if ((int64_t)grid.x * experts <= 2 * device_sm_count()) go(int8_few_rows_kernel<1, 8>, 8);
-        else go(int8_few_rows_kernel<1, 4>, 4);
+        const int64_t ctas = (int64_t)grid.x * experts, sms = device_sm_count();
+        // (four steps ahead are 2048 columns of the CTA; 32 tokens, us with two, four, and four steps and all registers: 1024 x 4096 8.0, 7.2,
+        // 7.0; 2048 x 4096 8.9, 8.4, 7.5; 4096 x 4096 9.5, 9.0, 13.6; 64 tokens 4096 x 1024 6.9, 8.8)
+        if (rows > 16 && p.pitch < 2048) go(int8_few_rows_kernel<4, 8, 2, 2>, 8);
+        else if (rows > 16 && ctas > sms) go(int8_few_rows_kernel<4, 8, 4, 2>, 8);
+        else if (rows > 16) go(int8_few_rows_kernel<4, 8, 4, 1>, 8);
+        else if (rows > 8) go(int8_few_rows_kernel<2, 8, 4, 2>, 8);
+        else if (ctas <= 2 * sms) go(int8_few_rows_kernel<1, 8, 8, 2>, 8);
+        else go(int8_few_rows_kernel<1, 4, 2, 8>, 4);
         GPTQ_CUDA_TRY(e);
         return st.finish(s);
     }
