@@ -990,10 +990,12 @@ extern "C" int gptq_int8_matmul(const int8_t* x_codes, const float* x_scales, in
         const int64_t rows = offsets ? T / experts : T;
         const int64_t ctas = (int64_t)grid.x * experts, sms = device_sm_count();
         // (four steps ahead are 2048 columns of the CTA; 32 tokens, us with two, four, and four steps and all registers: 1024 x 4096 8.0, 7.2,
-        // 7.0; 2048 x 4096 8.9, 8.4, 7.5; 4096 x 4096 9.5, 9.0, 13.6; 64 tokens 4096 x 1024 6.9, 8.8)
+        // 7.0; 2048 x 4096 8.9, 8.4, 7.5; 4096 x 4096 9.5, 9.0, 13.6; 64 tokens 4096 x 1024 6.9, 8.8. 16 tokens, four steps and eight:
+        // 2048 x 4096 6.5 and 6.1, 1024 x 2500 4.3 and 3.9)
         if (rows > 16 && p.pitch < 2048) go(int8_few_rows_kernel<4, 8, 2, 2>, 8);
         else if (rows > 16 && ctas > sms) go(int8_few_rows_kernel<4, 8, 4, 2>, 8);
         else if (rows > 16) go(int8_few_rows_kernel<4, 8, 4, 1>, 8);
+        else if (rows > 8 && ctas <= sms && p.pitch > 2048) go(int8_few_rows_kernel<2, 8, 8, 1>, 8);
         else if (rows > 8) go(int8_few_rows_kernel<2, 8, 4, 2>, 8);
         else if (ctas <= 2 * sms) go(int8_few_rows_kernel<1, 8, 8, 2>, 8);
         else go(int8_few_rows_kernel<1, 4, 2, 8>, 4);

@@ -514,7 +514,7 @@ def test_norm_of_several_rows_per_cta(lib, rows, cols, dt):
                                      (200, 600, 2000, None), (90, 1000, 5000, None), (230, 2600, 6000, None), (250, 3800, 9000, None),
                                      (200, 700, 300, 8), (500, 700, 300, 8), (150, 300, 500, 16), (90, 300, 2000, 3), (300, 300, 3000, 4),
                                      (60, 100, 3000, 3), (250, 300, 4000, 2), (1200, 520, 640, 16), (900, 300, 1000, 40), (24, 2500, 2100, None), (32, 40, 2048, None),
-                                     (20, 300, 2032, None)])
+                                     (20, 300, 2032, None), (13, 400, 2100, None)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_product_in_tiles_of_every_width(lib, T, N, K, E, dt):
     """Tiles of 64, 128 and 256 tokens, whole and with the columns in two to four shares; experts with rows at random and all in
