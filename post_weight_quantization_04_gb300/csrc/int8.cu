@@ -361,12 +361,14 @@ struct RowParams {
 };
 
 // 1 / sqrt(mean h^2 + eps) from the sum of squares; where the squares leave fp32's normal numbers the sum is
-// taken again of scaled values (a row apart, so nothing is lost elsewhere)
+// taken again of scaled values (a row apart, so nothing is lost elsewhere). A mean below 2^-80 times 2^160 is the mean of less than
+// 2^31 squares, so their sum is below 2^111, and what counts next to eps >= 2^-149 (2^11) stays normal. Squares past
+// fp32 are below 2^256 times 2^-160, and 2^31 of them below 2^127.
 template <typename F>
 __device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps, F again) {
     const float v = fmaf(sum, inv_n, eps);
     if (v >= 0x1p-80f && v <= 0x1.fffffep127f) return rsqrtf(v);
-    const float f = v < 1.0f ? 0x1p100f : 0x1p-80f;
+    const float f = v < 1.0f ? 0x1p80f : 0x1p-80f;
     return rsqrtf(again(f) * inv_n + eps * f * f) * f;
 }
 
