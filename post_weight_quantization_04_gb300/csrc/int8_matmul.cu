@@ -482,10 +482,22 @@ __global__ void __launch_bounds__(w_threads(BOX, SPLIT), 1) int8_matmul_kernel(c
     pdl_wait();   // from here on memory that the kernel before writes or reads is touched
     if (warp == 0) {
         // token tiles before each expert
-        int carry = 0;
+        int carry = 0, end = 0;   // the tiles, and the end of the rows, of the experts before
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
-            int lo = 0, hi = 0;
+            int lo = 0x7FFFFFFF, hi = lo;
             if (e0 + lane < p.experts) expert_rows(p, e0 + lane, &lo, &hi);
+            // Offsets out of order (reported above): a row counts for the first expert that has it, so that there are no more
+            // tiles than the host has counted. A split tile's cluster takes no second one: its MMAs would wait for the first
+            // one's sums to be read until the wait gives up.
+            const int up = __shfl_up_sync(0xffffffffu, hi, 1), before = lane ? up : end;
+            if (__any_sync(0xffffffffu, lo < before)) {
+                int most = before;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) most = max(most, __shfl_up_sync(0xffffffffu, most, o));
+                lo = max(lo, most);
+                hi = max(hi, lo);
+            }
+            end = __shfl_sync(0xffffffffu, hi, 31);
             const int n = token_tiles(lo, hi, p.width);
             int inc = n;
 #pragma unroll
