@@ -1,4 +1,5 @@
-"""The 8-bit integer operators at the ends of their ranges: rows and eps whose squares leave fp32's middle.
+"""The 8-bit integer operators at the ends of their ranges: rows and eps whose squares leave fp32's middle, scales whose products do,
+offsets out of order, codes and gradients of rows at every address.
 
 Bounds as in test_int8_gpu.py (u = 2^-24): rstd is off by r = (cols / 32 + 24) u / 2 + 4 u of it, and |q - y| <= s (1/2 + 127 (2 r + 8 u)).
 """
@@ -9,7 +10,7 @@ import pytest
 import torch
 
 from oracle import int8_oracle as I
-from test_int8_gpu import B, DEV, DT, U, _offsets, _operands, _stored, f64, rows_of
+from test_int8_gpu import B, DEV, DT, U, _check, _offsets, _operands, _stored, f64, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,67 @@ def test_offsets_out_of_order(lib, T, E, N, K, kind):
         lib.gptq_int8_matmul(X, W, offsets=b)
     assert e.value.status == 1 and time.perf_counter() - t < 1
     assert torch.equal(lib.gptq_int8_matmul(X, W, offsets=o), ref)
+
+
+@pytest.mark.parametrize("T,K,experts", [(4, 100, None), (20, 300, None), (40, 1500, None), (64, 1500, None), (120, 2000, None), (250, 4000, None),
+                                         (300, 100, None), (100, 100, None), (300, 100, 3), (90, 1500, 3)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_product_of_far_scales_in_every_epilogue(lib, T, K, experts, dt):
+    """Few rows, pairs with the columns whole and split, 64 features (packed pairs of bf16 where the type allows it). A weight's scale times
+    the sum is exact where it is subnormal, so the bound is _check's and half the last subnormal step: 2^-150 of fp32, 2^-134 of bf16."""
+    rng = np.random.default_rng(T)
+    xc, _, wc, _ = _operands(rng, T, 64, K, experts)
+    o = None if experts is None else _offsets(rng, T, experts, "even")
+    off = None if o is None else torch.tensor(o, dtype=torch.int32, device=DEV)
+    last = 2.0 ** -149 if dt == "f32" else 2.0 ** -149 + 2.0 ** -134
+    for a, b in ((1e-30, 1e30), (1e30, 1e-30), (1e-44, 1e38), (1e38, 1e-44), (1e-20, 1e-22), (1e20, 1e12), (1e12, 1e20), (1e-40, 1.0), (1.0, 1e-40),
+                 (1e-45, 1.0), (0.0, 1e38), (1e38, 0.0)):
+        xs, ws = np.full(T, a, np.float32), np.full(wc.shape[:-1], b, np.float32)
+        y = lib.gptq_int8_matmul(_stored(lib, xc, xs), _stored(lib, wc, ws), offsets=off, out_dtype=DT[dt])
+        _check(y, I.matmul(xc, xs, wc, ws, o), dt, last)
+    # one feature in nine far above the others, tokens far below
+    xs, ws = np.full(T, 1e-36, np.float32), np.ones(wc.shape[:-1], np.float32)
+    ws[..., ::9] = 1e37
+    y = lib.gptq_int8_matmul(_stored(lib, xc, xs), _stored(lib, wc, ws), offsets=off, out_dtype=DT[dt])
+    _check(y, I.matmul(xc, xs, wc, ws, o), dt, last)
+    # a row that was not finite
+    xs, ws = np.ones(T, np.float32), np.ones(wc.shape[:-1], np.float32)
+    xs[-1] = np.nan
+    for relu in (False, True):
+        y = lib.gptq_int8_matmul(_stored(lib, xc, xs), _stored(lib, wc, ws), offsets=off, relu=relu, out_dtype=DT[dt])
+        assert torch.isnan(y[-1]).all() and torch.isfinite(y[:-1]).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(9, 333), (5, 2310), (40, 17), (3, 8195), (6, 1001), (4, 17000)])
+def test_codes_and_gains_gradient_at_every_address(lib, dt, rows, cols):
+    """q of the norm and dgain of its gradient (and plain codes) for inputs that start anywhere within 16 bytes, against 64 bits."""
+    x, r, dy = (rows_of(rows, cols, dt, i) for i in (1, 2, 3))
+    gain = torch.rand(cols, generator=torch.Generator().manual_seed(cols)).to(DEV) + 0.5
+    h = (x.float() + r.float()).to(x.dtype)
+    y, _ = I.rms_norm(f64(h), f64(gain), np.float64(np.float32(1e-5)))
+    off = (cols / 32 + 24) * U / 2 + 4 * U
+    s = np.abs(y).max(1) / 127
+    codes, scales = I.quantise(x.float().cpu().numpy())
+    _, _, rstd = lib.gptq_int8_rms_norm(x, gain, 1e-5, r)
+    u = f64(h) * f64(rstd)[:, None]
+    _, refg = I.rms_norm_grad(f64(dy), f64(h), f64(gain), f64(rstd), f64(r))
+
+    def moved(t, start, more):
+        flat = torch.full((rows * (cols + more) + start + 40,), 3, dtype=t.dtype, device=DEV)
+        m = flat[start:start + rows * (cols + more)].view(rows, cols + more)[:, :cols]
+        m.copy_(t)
+        return m
+    for start in range(16 * 8 // torch.finfo(DT[dt]).bits):
+        for more in (0, 1, 3):
+            x2, r2 = moved(x, start, more), moved(r, (start + 1) % 8, more + 1)
+            gain2 = torch.cat((gain[:start % 4], gain))[start % 4:]
+            q, _, _ = lib.gptq_int8_rms_norm(x2, gain2, 1e-5, r2, out=(None, moved(h, (start + 3) % 8, more), None))
+            assert (np.abs(f64(q.scales) - s) <= (off + 4 * U) * s).all()
+            v = q.codes[:, :cols].cpu().numpy() * f64(q.scales)[:, None]
+            assert (np.abs(v - y) <= s[:, None] * (0.5 + 127 * (2 * off + 8 * U))).all() and not q.codes[:, cols:].any()
+            p = lib.gptq_int8_quantize(x2)
+            np.testing.assert_array_equal(p.codes.cpu().numpy(), I.stored(codes))
+            np.testing.assert_array_equal(p.scales.cpu().numpy(), scales)
+            _, dg = lib.gptq_int8_rms_norm_grad(moved(dy, start, 0), moved(h, (start + 2) % 8, more + 2), gain2, rstd, r2)
+            assert (np.abs(f64(dg) - refg) <= (rows + 4) * U * np.abs(f64(dy) * u).sum(0)).all()
