@@ -385,9 +385,10 @@ __device__ __forceinline__ int64_t source_row(const RowParams& p, int64_t r) {
 // Rows in the registers of their threads, UNITS units each: a row is read once and everything written once. CTAs
 // are persistent, and the next row's loads are under way while this one is reduced and written. Four units per thread, so
 // that what every warp does for a row (its sums, scale and reciprocals) is shared by more columns.
-// Bound by memory, and for bf16 nearly as much by instructions. 16384 x 4096: bf16 34 us
-// (6.0 TB/s), with the norm and a residual 77 (6.1); fp32 51 (6.6) and 136 (6.4). With two units per thread bf16 took 39 and
-// 91, with a CTA for each row and no loads ahead 52 and 107. Rows at odd addresses pay for the shifting: 16384 x 4095
+// Bound by memory, and for bf16 nearly as much by instructions, the quantisation and the norm with a residual: 16384 x 4096
+// bf16 34 us (6.0 TB/s) and 77 (6.1); fp32 51 (6.6) and 136 (6.4). The norm without a residual is not: bf16 53 (3.8), fp32 87 (3.9). For each row
+// it reads the gain again (as many bytes as an fp32 row) and has two barriers, one after the other, as with a residual, but for less than
+// half of the bytes. With two units per thread bf16 took 39 (quantisation) and 91 (norm with a residual), with a CTA for each row and no loads ahead 52 and 107. Rows at odd addresses pay for the shifting: 16384 x 4095
 // bf16 44 and 128 us (column by column 109 and 278), fp32 65 and 165. MOST is 512 or, for longer rows of fp32, 1024 threads:
 // the norm of 16384 x 4095 fp32 took 202 us within the 64 registers of the latter, the quantisation 74 instead of 65 with more.
 template <typename T, int UNITS, bool NORM, bool ANY, int MOST>
@@ -672,8 +673,9 @@ __device__ __forceinline__ float group_sum(float v, float* part, int warps, int 
 // A CTA takes a contiguous share of the rows, each of its blockDim.y groups of threads every so many of them, and a thread
 // the same UNITS units of each: dgain's sums over the rows stay in its registers, and the groups' are added at the
 // end. Rows are read once, the next one's loads under way (AHEAD) while this one is reduced and written. Wider rows leave no
-// registers for that, and have the sums in shared memory (4096 x 14336 bf16 121 us, 3.9 TB/s, in registers 131; with loads ahead 147).
-// Bound by memory: 16384 x 4096 bf16 86 us (6.2 TB/s), fp32 163 (6.6), both with the sum over the CTAs (4 us). Without the
+// registers for that, and have the sums in shared memory (4096 x 14336 bf16 121 us, 3.9 TB/s, in registers 131; with loads ahead 147): there each
+// row's loads start behind the last row's stores, which costs 1.4 to 1.75 times the time of the bytes.
+// Narrower rows are bound by memory: 16384 x 4096 bf16 86 us (6.2 TB/s), fp32 163 (6.6), both with the sum over the CTAs (4 us). Without the
 // loads ahead and with the gain read for every row it took 199. Rows at odd addresses: 16384 x 4095 bf16 183, fp32 203.
 template <typename T, int UNITS, bool ANY, int MOST>
 __global__ void __launch_bounds__(MOST, 1) int8_norm_grad_kernel(const GradParams p) {

@@ -18,7 +18,8 @@ namespace gptq {
 namespace {
 
 constexpr int I_MAX_EXPERTS = 1024;
-// a sum of K products, each up to 2^14, has to fit 32 bits
+// K products, each up to 2^14, sum to less than 2^31, which the packed epilogue relies on (weights' scales up to 2^96 times
+// a sum stay within fp32). Sums are fp32 and rounded past 2^24, which takes more than 1024 products of the largest codes.
 constexpr int64_t I_MAX_K = (1 << 17) - 1;
 
 struct IParams {
@@ -188,8 +189,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int8_few_rows_kernel(const I
 }
 
 // ------------------------------------------------------------------------ pairs of SMs, tcgen05
-// There is no integer tensor instruction on sm_103a, but 8-bit integers are exact in fp16, their products and,
-// below 2^24, the sums of them exact in fp32. So the codes stay 8 bits wide up to the SM and are
+// tcgen05.mma has no integer kind on sm_103a, and mma.sync on 8-bit integers runs at a quarter of its rate on fp16. But 8-bit
+// integers are exact in fp16, their products and, below 2^24, the sums of them exact in fp32. So the codes stay 8 bits wide up to the SM and are
 // expanded there to what tcgen05.mma kind::f16 multiplies. The weights are the M operand and are expanded into
 // TMEM, the tokens the N operand and are expanded into shared memory, which spares the shared memory one of
 // the two operands' writes and reads.
@@ -909,7 +910,9 @@ struct Plan {
 // their rows are not known here: the width is the one for evenly spread ones with room for half as many again or so, and an expert
 // with more rows has several tiles. *most: the most tiles.
 // Features x columns 4096 x 4096, us: 512 tokens as 256 x 2 shares 18.8, as 256 and 128 in whole 25.1 and 20.3; 256 tokens as 128 x 2
-// 14.8, as 64 in whole 17.0, as 256 x 3 17.1; 64 tokens as 64 x 3 12.0, as 64 x 2 13.0 (11.1 with the sums apart). 8 experts of 14336 x 4096, 200 rows in tiles
+// 14.8, as 64 in whole 17.0, as 256 x 3 17.1; 64 tokens as 64 x 3 12.0, as 64 x 2 13.0. (These and the
+// constants are from before narrow split tiles had memory apart for their sums: 64 x 3 takes 11.1 to 11.6 now, so the fixed part of split tiles
+// up to 128 wide is counted 0.4 to 0.9 us too high.) 8 experts of 14336 x 4096, 200 rows in tiles
 // of 64, 128, 256: 82, 85, 107; 320 rows 84, 86, 109; 500 rows 116, 92, 114; 700 rows 153, 96, 116; 1000 rows 171, 129, 120.
 Plan plan_of(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts, int64_t pairs, int64_t* most) {
     const int64_t ftiles = ceil_div(N, W_PF), stages = ceil_div(K, W_K);
@@ -950,6 +953,9 @@ constexpr int64_t kMaxDim = (1ll << 31) - 512;
 // Experts, rows at random: 16 of 1024 x 4096, 32 rows 14.1 / 19.2, 64 rows 16.3 / 19.8, 96 rows 19.2 / 19.8, 128 rows 20.7 / 19.9;
 // 8 of 14336 x 4096, 8 rows 51 / 62, 32 rows 78 / 80, 48 rows 82 / 80, 64 rows 98 / 80; 32 of 512 x 1024, 256 rows 7.6 / 10.5, 512 rows
 // 15.6 / 10.4; 32 of 700 x 300, 100 rows 5.1 / 11.5, 400 rows 14.9 / 12.6
+// The host does not know how the rows are spread: all on one expert they take that expert's weights in turns of 8 or 16 rows. At random / on
+// one, by this rule: 16 of 1024 x 4096, 32 rows 12.5 / 15.7, 96 rows 17 / 44; 8 of 14336 x 4096, 16 rows 68 / 24, 48 rows 81 / 57;
+// 32 of 512 x 1024, 192 rows 6.5 / 27; 256 of 1024 x 2048, 1536 rows 97 / 424
 bool few_rows_pay(int64_t T, int64_t N, int64_t K, bool by_expert, int64_t experts) {
     if (by_expert) return T <= 6 * experts || (T <= 10 * experts && N * K <= 600000);
     return T <= 16 || (T <= 32 && N * K <= 24000000) || (T <= 64 && K <= 1024 && N * K <= 5000000);
